@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -69,9 +70,17 @@ class Tensors(ctypes.Structure):
         "slot_ids", "initial_state", "final_state", "gate_scale", "seq_lens")]
 
 
+class GradientPointers(ctypes.Structure):
+    """gdr_gradients"""
+    _fields_ = [(name, ctypes.c_void_p) for name in (
+        "d_o", "d_final_state", "d_q", "d_k", "d_v", "d_gate", "d_beta", "d_initial_state", "d_a_log",
+        "d_dt_bias", "d_gate_scale")]
+
+
 EXPORTS = ("gdr_abi_version", "gdr_status_str", "gdr_last_error", "gdr_validate",
-           "gdr_workspace_size", "gdr_select_algo", "gdr_forward", "gdr_forward_noalloc", "gdr_gate",
-           "gdr_slab_stream")
+           "gdr_workspace_size", "gdr_select_algo", "gdr_forward", "gdr_forward_noalloc",
+           "gdr_backward_workspace_size", "gdr_backward", "gdr_gate", "gdr_gate_backward_workspace_size",
+           "gdr_gate_backward", "gdr_slab_stream")
 NOALLOC_SCRATCH_BYTES = 256 << 20  # GDR_NOALLOC_SCRATCH_BYTES of include/gdr.h
 
 
@@ -110,6 +119,18 @@ def load_library():
                                  ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                  ctypes.c_void_p, ctypes.c_void_p]
         lib.gdr_gate.restype = ctypes.c_int
+        lib.gdr_backward_workspace_size.argtypes = [ctypes.POINTER(Problem), ctypes.POINTER(ctypes.c_size_t)]
+        lib.gdr_backward_workspace_size.restype = ctypes.c_int
+        lib.gdr_backward.argtypes = [ctypes.POINTER(Problem), ctypes.POINTER(Tensors),
+                                     ctypes.POINTER(GradientPointers), ctypes.c_void_p, ctypes.c_size_t,
+                                     ctypes.c_void_p]
+        lib.gdr_backward.restype = ctypes.c_int
+        lib.gdr_gate_backward_workspace_size.argtypes = [ctypes.c_int64, ctypes.c_int32,
+                                                         ctypes.POINTER(ctypes.c_size_t)]
+        lib.gdr_gate_backward_workspace_size.restype = ctypes.c_int
+        lib.gdr_gate_backward.argtypes = ([ctypes.c_int64, ctypes.c_int32, ctypes.c_int32]
+                                          + [ctypes.c_void_p] * 11 + [ctypes.c_size_t, ctypes.c_void_p])
+        lib.gdr_gate_backward.restype = ctypes.c_int
         lib.gdr_slab_stream.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
                                         ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_void_p]
         lib.gdr_slab_stream.restype = ctypes.c_int
@@ -375,6 +396,144 @@ def gate(a, dt_bias, decay_scale, b=None, want_beta=False, out_decay=None, out_b
     check(lib.gdr_gate(a.numel(), heads, _dtype_code(a.dtype), _ptr(a), _ptr(dt_bias),
                        _ptr(decay_scale), _ptr(b), _ptr(decay), _ptr(beta), stream))
     return decay, beta
+
+
+class Gradients(NamedTuple):
+    """Results of ``backward``; None where the call has no such input (or, for
+    ``initial_state``, where it was not wanted)."""
+    q: torch.Tensor
+    k: torch.Tensor
+    v: torch.Tensor
+    gate: Optional[torch.Tensor]
+    beta: Optional[torch.Tensor]
+    initial_state: Optional[torch.Tensor]
+    a_log: Optional[torch.Tensor]
+    dt_bias: Optional[torch.Tensor]
+    gate_scale: Optional[torch.Tensor]
+
+
+def backward_workspace_size(problem: Problem) -> int:
+    n = ctypes.c_size_t(0)
+    check(load_library().gdr_backward_workspace_size(ctypes.byref(problem), ctypes.byref(n)))
+    return int(n.value)
+
+
+def backward(q, k, v, d_o, *, gate=None, beta=None, a_log=None, dt_bias=None, gate_scale=None, cu_seqlens=None,
+             seq_lens=None, initial_state=None, d_final_state=None, want_initial_state=None,
+             update_rule="gated_delta", gate_activation="none", beta_activation="none", qk_l2_norm=False,
+             scale=0.0, batch=None, out=None, workspace=None) -> Gradients:
+    """Gradients of ``forward``: the inputs of that call, ``d_o`` (o's shape
+    and dtype) and optionally ``d_final_state`` (B,HV,dv,dk) fp32, for the
+    rules 'linear', 'gated', 'delta' and 'gated_delta' with one log decay per
+    value head.  Nothing of the forward call has to be kept.
+
+    The gradients have their tensors' shapes and dtypes; beta and a raw gate
+    get theirs as given (through the sigmoid, the softplus and the L2 norm).
+    ``want_initial_state``: whether the initial states' gradient is returned
+    (default: when there is an initial state).  Rows of tokens that no request
+    covers are zero, or left as they are in a gradient passed in ``out`` (a
+    ``Gradients`` whose tensors are filled; None entries are allocated).
+    ``workspace``: a uint8 device tensor of ``backward_workspace_size`` bytes
+    (allocated here when not given)."""
+    lib = load_library()
+    dev = q.device
+    _need(q, "q", device=dev)
+    for name, t, dt in (("k", k, q.dtype), ("v", v, q.dtype), ("d_o", d_o, q.dtype), ("gate", gate, None),
+                        ("beta", beta, torch.float32), ("a_log", a_log, torch.float32),
+                        ("dt_bias", dt_bias, torch.float32), ("gate_scale", gate_scale, torch.float32),
+                        ("cu_seqlens", cu_seqlens, torch.int32), ("seq_lens", seq_lens, torch.int32),
+                        ("initial_state", initial_state, torch.float32),
+                        ("d_final_state", d_final_state, torch.float32)):
+        _need(t, name, dt, dev)
+    if k is None or v is None or d_o is None:
+        raise GDRError("GDR_E_INVALID", "k, v and d_o are required")
+    if batch is None and initial_state is None and d_final_state is not None:
+        batch = d_final_state.shape[0]
+    p = build_problem(q, k, v, gate=gate, beta=beta, a_log=a_log, dt_bias=dt_bias, cu_seqlens=cu_seqlens,
+                      initial_state=initial_state, update_rule=update_rule, gate_activation=gate_activation,
+                      beta_activation=beta_activation, qk_l2_norm=qk_l2_norm, scale=scale, batch=batch,
+                      gate_scale=gate_scale, seq_lens=seq_lens)
+    need = backward_workspace_size(p)
+    lead = tuple(q.shape[:-2])
+    states = (p.batch, p.num_heads_v, p.head_dim_v, p.head_dim_k)
+    check_shapes(p, lead, _shapes(q=q, k=k, v=v, out=d_o, gate=gate, beta=beta, a_log=a_log, dt_bias=dt_bias,
+                                  gate_scale=gate_scale, cu_seqlens=cu_seqlens, seq_lens=seq_lens,
+                                  initial_state=initial_state, final_state=d_final_state))
+    if want_initial_state is None:
+        want_initial_state = initial_state is not None
+    # rows of tokens outside every request are not written by the kernels
+    rows = torch.zeros if cu_seqlens is not None or seq_lens is not None or p.batch == 0 else torch.empty
+    grads = {}
+    for name, like, shape, new in (("q", q, None, rows), ("k", k, None, rows), ("v", v, None, rows),
+                                   ("gate", gate, None, rows), ("beta", beta, None, rows),
+                                   ("initial_state", None, states if want_initial_state else None, torch.empty),
+                                   ("a_log", a_log, None, torch.empty), ("dt_bias", dt_bias, None, torch.empty),
+                                   ("gate_scale", gate_scale, None, torch.empty)):
+        given = None if out is None else getattr(out, name)
+        if like is None and shape is None:
+            grads[name] = None
+            continue
+        shape = tuple(like.shape) if shape is None else shape
+        dtype = torch.float32 if like is None else like.dtype
+        if given is None:
+            given = new(shape, dtype=dtype, device=dev)
+        elif tuple(_need(given, "out." + name, dtype, dev).shape) != shape:
+            raise GDRError("GDR_E_INVALID", "out.%s has shape %s, expected %s" % (name, tuple(given.shape), shape))
+        grads[name] = given
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", device=dev)
+    t = Tensors(q=_ptr(q), k=_ptr(k), v=_ptr(v), gate=_ptr(gate), beta=_ptr(beta), a_log=_ptr(a_log),
+                dt_bias=_ptr(dt_bias), cu_seqlens=_ptr(cu_seqlens), initial_state=_ptr(initial_state),
+                gate_scale=_ptr(gate_scale), seq_lens=_ptr(seq_lens))
+    g = GradientPointers(d_o=_ptr(d_o), d_final_state=_ptr(d_final_state),
+                         **{"d_" + name: _ptr(x) for name, x in grads.items()})
+    with torch.cuda.device(dev):
+        stream = torch.cuda.current_stream(dev).cuda_stream
+        check(lib.gdr_backward(ctypes.byref(p), ctypes.byref(t), ctypes.byref(g), _ptr(workspace),
+                               workspace.numel() * workspace.element_size(), stream))
+    return Gradients(**grads)
+
+
+class GateGradients(NamedTuple):
+    """Results of ``gate_backward``; ``b`` is None without the update rate."""
+    a: torch.Tensor
+    b: Optional[torch.Tensor]
+    dt_bias: torch.Tensor
+    decay_scale: torch.Tensor
+
+
+def gate_backward(a, dt_bias, decay_scale, d_decay, b=None, d_beta=None, workspace=None) -> GateGradients:
+    """Gradients of ``gate``: ``d_decay`` (and ``d_beta``, with ``b``) have
+    a's shape and dtype; the gradients of dt_bias and decay_scale are sums
+    over every row, in fp32.  The last axis of ``a`` is the head axis."""
+    lib = load_library()
+    dev = a.device
+    _need(a, "a", device=dev)
+    heads = a.shape[-1] if a.dim() else 0
+    if (b is None) != (d_beta is None):
+        raise GDRError("GDR_E_INVALID", "b and d_beta must be given together")
+    for name, t in (("d_decay", d_decay), ("b", b), ("d_beta", d_beta)):
+        _need(t, name, a.dtype, dev)
+        if t is not None and t.shape != a.shape:
+            raise GDRError("GDR_E_INVALID", "%s must have a's shape" % name)
+    for name, t in (("dt_bias", dt_bias), ("decay_scale", decay_scale)):
+        if tuple(_need(t, name, torch.float32, dev).shape) != (heads,):
+            raise GDRError("GDR_E_INVALID", "%s must have shape (%d,)" % (name, heads))
+    n = ctypes.c_size_t(0)
+    check(lib.gdr_gate_backward_workspace_size(a.numel(), heads, ctypes.byref(n)))
+    if workspace is None:
+        workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", device=dev)
+    g = GateGradients(torch.empty_like(a), None if b is None else torch.empty_like(b),
+                      torch.empty_like(dt_bias), torch.empty_like(decay_scale))
+    with torch.cuda.device(dev):
+        stream = torch.cuda.current_stream(dev).cuda_stream
+        check(lib.gdr_gate_backward(a.numel(), heads, _dtype_code(a.dtype), _ptr(a), _ptr(dt_bias), _ptr(decay_scale),
+                                    _ptr(b), _ptr(d_decay), _ptr(d_beta), _ptr(g.a), _ptr(g.b), _ptr(g.dt_bias),
+                                    _ptr(g.decay_scale), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(), stream))
+    return g
 
 
 def slab_stream(slab, slot_ids, factor=1.0):

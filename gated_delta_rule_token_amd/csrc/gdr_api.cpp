@@ -11,6 +11,7 @@
 #include <mutex>
 #include <string>
 
+#include "gdr_backward_launch.hpp"
 #include "gdr_launch.hpp"
 
 // Workspace of gdr_forward_noalloc, one copy per GPU (see include/gdr.h).  In
@@ -106,7 +107,14 @@ gdr_status check_problem(const gdr_problem *p)
     return GDR_OK;
 }
 
-gdr_status check_tensors(const gdr_problem *p, const gdr_tensors *t)
+Range range_of(const char *name, const void *ptr, size_t bytes)
+{
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(ptr);
+    return Range{name, lo, ptr ? lo + bytes : lo};
+}
+
+// `backward`: the tensors of a backward pass, which reads neither o nor final_state.
+gdr_status check_tensors(const gdr_problem *p, const gdr_tensors *t, bool backward = false)
 {
     const int rule = p->update_rule;
     const bool decays = gdr::rule_decays(rule);
@@ -140,8 +148,9 @@ gdr_status check_tensors(const gdr_problem *p, const gdr_tensors *t)
         return fail(GDR_E_INVALID, "slot_ids must be given exactly when num_slots > 0");
     if (p->num_slots > 0 && t->initial_state)
         return fail(GDR_E_INVALID, "with a slot slab the state is read in place; initial_state must be NULL");
-    if (!t->final_state && state_rows(p) > 0) return fail(GDR_E_INVALID, "final_state (or the slab) is required");
-    if (T > 0 && (!t->q || !t->k || !t->v || !t->o)) return fail(GDR_E_INVALID, "q, k, v and o are required");
+    if (!backward && !t->final_state && state_rows(p) > 0) return fail(GDR_E_INVALID, "final_state (or the slab) is required");
+    if (T > 0 && (!t->q || !t->k || !t->v || (!backward && !t->o)))
+        return fail(GDR_E_INVALID, backward ? "q, k and v are required" : "q, k, v and o are required");
     if (p->batch > 0 && !t->cu_seqlens && p->seq_len == 0 && T != 0)
         return fail(GDR_E_INVALID, "seq_len must be set without cu_seqlens");
 
@@ -150,15 +159,13 @@ gdr_status check_tensors(const gdr_problem *p, const gdr_tensors *t)
                           t->seq_lens};
     for (const void *q : ptrs)
         if (q && !aligned16(q)) return fail(GDR_E_INVALID, "every tensor pointer must be 16-byte aligned");
+    if (backward) return GDR_OK;
 
     // aliasing: outputs must not overlap inputs or each other; final == initial is the in-place case
     const int64_t H = p->num_heads_qk, HV = p->num_heads_v, dk = p->head_dim_k, dv = p->head_dim_v;
     const size_t a = dsize(p->act_dtype);
     const size_t state_bytes = (size_t)state_rows(p) * HV * dv * dk * 4;
-    auto rng = [](const char *n, const void *ptr, size_t bytes) {
-        uintptr_t lo = reinterpret_cast<uintptr_t>(ptr);
-        return Range{n, lo, ptr ? lo + bytes : lo};
-    };
+    const auto rng = range_of;
     const Range out_o = rng("o", t->o, (size_t)T * HV * dv * a);
     const Range out_s = rng("final_state", t->final_state, state_bytes);
     const Range ins[] = {
@@ -311,9 +318,8 @@ gdr_status gdr_select_algo(const gdr_problem *problem, int32_t *algo)
 
 namespace {
 
-// Enqueue every kernel of a validated call on `stream`; `workspace` holds at
-// least gdr_workspace_size bytes.
-gdr_status launch_all(const gdr_problem *problem, const gdr_tensors *tensors, void *workspace, void *stream)
+// The kernels' argument block of a validated call.
+gdr::Params kernel_params(const gdr_problem *problem, const gdr_tensors *tensors)
 {
     const gdr_problem &p = *problem;
     const gdr_tensors &t = *tensors;
@@ -347,6 +353,108 @@ gdr_status launch_all(const gdr_problem *problem, const gdr_tensors *tensors, vo
     k.qk_l2_norm = p.qk_l2_norm != 0;
     k.beta_bcast = p.beta_per_token != 0;
     k.scale = p.scale != 0.f ? p.scale : 1.f / std::sqrt((float)p.head_dim_k);
+    return k;
+}
+
+// What the backward pass implements, and its launches' limits.
+gdr_status check_backward(const gdr_problem *p)
+{
+    if (p->update_rule == GDR_RULE_GATED_DELTA_V2 || p->decay_per_key)
+        return fail(GDR_E_UNSUPPORTED, "the backward pass takes one log decay per value head and no erase gate");
+    if (p->num_slots > 0) return fail(GDR_E_UNSUPPORTED, "the backward pass takes no state slab (use initial_state)");
+    const int64_t C = gdr::back_chunk(p->head_dim_k), chunks = (p->total_tokens + C - 1) / C + p->batch;
+    if (chunks * p->num_heads_v > INT32_MAX) return fail(GDR_E_INVALID, "total_tokens * num_heads_v too large");
+    return GDR_OK;
+}
+
+// Carve the workspace (256-byte aligned pieces) at `base` into `a`, with the
+// sizes the kernels need; returns the bytes (also when base is NULL).
+size_t back_layout(const gdr_problem *p, gdr::BackParams &a, void *base)
+{
+    const size_t C = gdr::back_chunk(p->head_dim_k), MB = C / 16, tri = MB * (MB + 1) / 2, KB = gdr::back_dk_tile(p->head_dim_k) / 16;
+    const size_t VB = (p->head_dim_v + 15) / 16, block = 256;  // floats of a 16x16 block
+    const size_t chunks = (p->total_tokens + C - 1) / C + p->batch, recs = chunks * p->num_heads_v;
+    const bool retr = gdr::rule_retrieves(p->update_rule);
+    a.chunks = (int32_t)chunks;
+    a.VB = (int32_t)VB;
+    size_t at = 0;
+    const auto take = [&](size_t n) {  // n 4-byte words
+        char *ptr = base ? static_cast<char *>(base) + at : nullptr;
+        at += (n * 4 + 255) / 256 * 256;
+        return static_cast<void *>(ptr);
+    };
+    const auto floats = [&](size_t n) { return static_cast<float *>(take(n)); };
+    a.off = static_cast<int32_t *>(take((size_t)p->batch + 1));
+    a.tok = static_cast<int32_t *>(take((size_t)p->batch * 2));
+    a.sc = floats(recs * gdr::BACK_SC * C);
+    a.gate_sums = p->gate_activation == GDR_GATE_QWEN ? floats(recs * 2) : nullptr;
+    a.d_beta = p->beta_per_token ? floats((size_t)p->total_tokens * p->num_heads_v) : nullptr;
+    a.pt = floats(recs * tri * block);
+    a.t1 = retr ? floats(recs * tri * block) : nullptr;
+    a.t2 = retr ? floats(recs * tri * block) : nullptr;
+    a.s = floats(recs * KB * VB * block);
+    a.ds = floats(recs * KB * VB * block);
+    a.e = floats(recs * MB * VB * block);
+    a.y = retr ? floats(recs * MB * VB * block) : nullptr;
+    return at;
+}
+
+gdr_status check_gradients(const gdr_problem *p, const gdr_tensors *t, const gdr_gradients *g, const void *workspace,
+                           size_t workspace_bytes)
+{
+    const int64_t T = p->total_tokens;
+    const bool decays = gdr::rule_decays(p->update_rule), has_beta = gdr::rule_has_beta(p->update_rule);
+    if (T > 0 && (!g->d_o || !g->d_q || !g->d_k || !g->d_v)) return fail(GDR_E_INVALID, "d_o, d_q, d_k and d_v are required");
+    if ((g->d_gate && !decays) || (T > 0 && decays && !g->d_gate))
+        return fail(GDR_E_INVALID, "d_gate must be given exactly when the update_rule decays");
+    if ((g->d_beta && !has_beta) || (T > 0 && has_beta && !g->d_beta))
+        return fail(GDR_E_INVALID, "d_beta must be given exactly when the update_rule has beta");
+    if ((g->d_a_log != nullptr) != (t->a_log != nullptr) || (g->d_dt_bias != nullptr) != (t->dt_bias != nullptr) ||
+        (g->d_gate_scale != nullptr) != (t->gate_scale != nullptr))
+        return fail(GDR_E_INVALID, "d_a_log, d_dt_bias and d_gate_scale must be given exactly when their tensors are");
+    const void *ptrs[] = {g->d_o, g->d_final_state, g->d_q, g->d_k, g->d_v, g->d_gate, g->d_beta, g->d_initial_state,
+                          g->d_a_log, g->d_dt_bias, g->d_gate_scale, workspace};
+    for (const void *q : ptrs)
+        if (q && !aligned16(q)) return fail(GDR_E_INVALID, "every tensor pointer must be 16-byte aligned");
+
+    const int64_t H = p->num_heads_qk, HV = p->num_heads_v, dk = p->head_dim_k, dv = p->head_dim_v;
+    const size_t act = dsize(p->act_dtype), qk = (size_t)T * H * dk * act, vo = (size_t)T * HV * dv * act;
+    const size_t gate = (size_t)T * HV * dsize(p->gate_dtype), beta = (size_t)T * (p->beta_per_token ? 1 : HV) * 4;
+    const size_t state = (size_t)p->batch * HV * dv * dk * 4, head = (size_t)HV * 4;
+    const Range outs[] = {
+        range_of("d_q", g->d_q, qk), range_of("d_k", g->d_k, qk), range_of("d_v", g->d_v, vo),
+        range_of("d_gate", g->d_gate, gate), range_of("d_beta", g->d_beta, beta),
+        range_of("d_initial_state", g->d_initial_state, state), range_of("d_a_log", g->d_a_log, head),
+        range_of("d_dt_bias", g->d_dt_bias, head), range_of("d_gate_scale", g->d_gate_scale, head),
+        range_of("workspace", workspace, workspace_bytes),
+    };
+    const Range ins[] = {
+        range_of("q", t->q, qk), range_of("k", t->k, qk), range_of("v", t->v, vo), range_of("d_o", g->d_o, vo),
+        range_of("gate", t->gate, gate), range_of("beta", t->beta, beta), range_of("a_log", t->a_log, head),
+        range_of("dt_bias", t->dt_bias, head), range_of("gate_scale", t->gate_scale, head),
+        range_of("cu_seqlens", t->cu_seqlens, (size_t)(p->batch + 1) * 4),
+        range_of("seq_lens", t->seq_lens, (size_t)p->batch * 4), range_of("initial_state", t->initial_state, state),
+        range_of("d_final_state", g->d_final_state, state),
+    };
+    const int n = sizeof outs / sizeof outs[0];
+    for (int i = 0; i < n; ++i) {
+        for (int j = i + 1; j < n; ++j)
+            if (overlaps(outs[i], outs[j])) return fail(GDR_E_ALIAS, "%s overlaps %s", outs[i].name, outs[j].name);
+        for (const Range &r : ins) {
+            // each workgroup reads its rows of d_final_state before it writes them
+            const bool in_place = g->d_initial_state == g->d_final_state && &r == &ins[12] && i == 5;
+            if (!in_place && overlaps(outs[i], r)) return fail(GDR_E_ALIAS, "%s overlaps %s", outs[i].name, r.name);
+        }
+    }
+    return GDR_OK;
+}
+
+// Enqueue every kernel of a validated call on `stream`; `workspace` holds at
+// least gdr_workspace_size bytes.
+gdr_status launch_all(const gdr_problem *problem, const gdr_tensors *tensors, void *workspace, void *stream)
+{
+    const gdr_problem &p = *problem;
+    const gdr::Params k = kernel_params(problem, tensors);
     if (p.batch == 0) return GDR_OK;
 
     const int act = p.act_dtype == GDR_F16 ? 1 : p.act_dtype == GDR_BF16 ? 2 : 0;
@@ -403,6 +511,64 @@ gdr_status gdr_forward_noalloc(const gdr_problem *problem, const gdr_tensors *te
     return launch_all(problem, tensors, ws, stream);
 }
 
+gdr_status gdr_backward_workspace_size(const gdr_problem *problem, size_t *bytes)
+{
+    g_last_error.clear();
+    if (!bytes) return fail(GDR_E_INVALID, "bytes is NULL");
+    gdr_status st = check_problem(problem);
+    if (st != GDR_OK) return st;
+    st = check_backward(problem);
+    if (st != GDR_OK) return st;
+    gdr::BackParams a{};
+    *bytes = back_layout(problem, a, nullptr);
+    return GDR_OK;
+}
+
+gdr_status gdr_backward(const gdr_problem *problem, const gdr_tensors *tensors, const gdr_gradients *gradients,
+                        void *workspace, size_t workspace_bytes, void *stream)
+{
+    g_last_error.clear();
+    if (!tensors || !gradients) return fail(GDR_E_INVALID, "%s is NULL", tensors ? "gradients" : "tensors");
+    gdr_status st = check_problem(problem);
+    if (st != GDR_OK) return st;
+    st = check_backward(problem);
+    if (st != GDR_OK) return st;
+    st = check_tensors(problem, tensors, true);
+    if (st != GDR_OK) return st;
+    gdr::BackParams a{};
+    const size_t need = back_layout(problem, a, nullptr);
+    if (!workspace || workspace_bytes < need) return fail(GDR_E_WORKSPACE, "workspace of %zu bytes required", need);
+    st = check_gradients(problem, tensors, gradients, workspace, need);
+    if (st != GDR_OK) return st;
+    back_layout(problem, a, workspace);
+
+    a.p = kernel_params(problem, tensors);
+    const bool retrieves = gdr::rule_retrieves(problem->update_rule);
+    a.decays = gdr::rule_decays(problem->update_rule);
+    a.d_o = gradients->d_o;
+    a.d_final = gradients->d_final_state;
+    a.dq = gradients->d_q;
+    a.dk = gradients->d_k;
+    a.dv = gradients->d_v;
+    a.d_gate = gradients->d_gate;
+    a.d_init = gradients->d_initial_state;
+    a.d_a_log = gradients->d_a_log;
+    a.d_dt_bias = gradients->d_dt_bias;
+    a.d_gate_scale = gradients->d_gate_scale;
+    if (problem->beta_per_token) a.d_rate = gradients->d_beta;  // a.d_beta: workspace, per head
+    else a.d_beta = gradients->d_beta;
+
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    hipError_t err = gdr::launch_back_table(a, s);
+    if (err == hipSuccess && problem->batch > 0)
+        err = problem->act_dtype == GDR_F16    ? gdr::launch_back_f16(a, retrieves, s)
+              : problem->act_dtype == GDR_BF16 ? gdr::launch_back_bf16(a, retrieves, s)
+                                               : gdr::launch_back_f32(a, retrieves, s);
+    if (err == hipSuccess) err = gdr::launch_back_sums(a, s);
+    if (err != hipSuccess) return fail(GDR_E_HIP, "kernel launch failed: %s", hipGetErrorString(err));
+    return GDR_OK;
+}
+
 gdr_status gdr_gate(int64_t count, int32_t heads, int32_t dtype, const void *a, const float *dt_bias,
                     const float *decay_scale, const void *b, void *decay, void *beta, void *stream)
 {
@@ -415,6 +581,67 @@ gdr_status gdr_gate(int64_t count, int32_t heads, int32_t dtype, const void *a, 
     if (beta && !b) return fail(GDR_E_INVALID, "beta requested without b");
     hipError_t err = gdr::launch_gate(count, heads, dtype == GDR_F16 ? 1 : dtype == GDR_BF16 ? 2 : 0, a, dt_bias, decay_scale, beta ? b : nullptr,
                                       decay, beta, static_cast<hipStream_t>(stream));
+    if (err != hipSuccess) return fail(GDR_E_HIP, "kernel launch failed: %s", hipGetErrorString(err));
+    return GDR_OK;
+}
+
+gdr_status gdr_gate_backward_workspace_size(int64_t count, int32_t heads, size_t *bytes)
+{
+    g_last_error.clear();
+    if (!bytes) return fail(GDR_E_INVALID, "bytes is NULL");
+    if (count < 0 || heads < 1) return fail(GDR_E_INVALID, "count must be >= 0 and heads >= 1");
+    *bytes = (size_t)gdr::gate_back_blocks(count / heads, heads) * 2 * heads * 4;
+    return GDR_OK;
+}
+
+gdr_status gdr_gate_backward(int64_t count, int32_t heads, int32_t dtype, const void *a, const float *dt_bias,
+                             const float *decay_scale, const void *b, const void *d_decay, const void *d_beta,
+                             void *d_a, void *d_b, float *d_dt_bias, float *d_decay_scale, void *workspace,
+                             size_t workspace_bytes, void *stream)
+{
+    size_t need = 0;
+    gdr_status st = gdr_gate_backward_workspace_size(count, heads, &need);
+    if (st != GDR_OK) return st;
+    if (count % heads != 0) return fail(GDR_E_INVALID, "count must be a multiple of heads (last axis)");
+    if (heads > 65535) return fail(GDR_E_INVALID, "heads must be at most 65535");
+    if (dtype != GDR_F32 && dtype != GDR_F16 && dtype != GDR_BF16)
+        return fail(GDR_E_INVALID, "dtype must be GDR_F32, GDR_F16 or GDR_BF16");
+    if (!dt_bias || !decay_scale || !d_dt_bias || !d_decay_scale || (count > 0 && (!a || !d_decay || !d_a)))
+        return fail(GDR_E_INVALID, "a, dt_bias, decay_scale, d_decay, d_a, d_dt_bias and d_decay_scale are required");
+    if (count > 0 && ((d_b != nullptr) != (b != nullptr) || (d_b != nullptr) != (d_beta != nullptr)))
+        return fail(GDR_E_INVALID, "b, d_beta and d_b must be given together");
+    const void *ptrs[] = {a, dt_bias, decay_scale, b, d_decay, d_beta, d_a, d_b, d_dt_bias, d_decay_scale, workspace};
+    for (const void *q : ptrs)
+        if (q && !aligned16(q)) return fail(GDR_E_INVALID, "every tensor pointer must be 16-byte aligned");
+    if (!workspace || workspace_bytes < need) return fail(GDR_E_WORKSPACE, "workspace of %zu bytes required", need);
+    const size_t n = (size_t)count * dsize(dtype), head = (size_t)heads * 4;
+    const Range outs[] = {range_of("d_a", d_a, n), range_of("d_b", d_b, n), range_of("d_dt_bias", d_dt_bias, head),
+                          range_of("d_decay_scale", d_decay_scale, head), range_of("workspace", workspace, need)};
+    const Range ins[] = {range_of("a", a, n), range_of("b", b, n), range_of("d_decay", d_decay, n),
+                         range_of("d_beta", d_beta, n), range_of("dt_bias", dt_bias, head),
+                         range_of("decay_scale", decay_scale, head)};
+    for (int i = 0; i < 5; ++i) {
+        for (int j = i + 1; j < 5; ++j)
+            if (overlaps(outs[i], outs[j])) return fail(GDR_E_ALIAS, "%s overlaps %s", outs[i].name, outs[j].name);
+        for (const Range &r : ins)
+            if (overlaps(outs[i], r)) return fail(GDR_E_ALIAS, "%s overlaps %s", outs[i].name, r.name);
+    }
+    gdr::GateBackParams g{};
+    g.rows = count / heads;
+    g.heads = heads;
+    g.dt = dtype == GDR_F16 ? 1 : dtype == GDR_BF16 ? 2 : 0;
+    g.a = a;
+    g.d_decay = d_decay;
+    g.b = b;
+    g.d_beta = d_beta;
+    g.dt_bias = dt_bias;
+    g.decay_scale = decay_scale;
+    g.d_a = d_a;
+    g.d_b = count > 0 ? d_b : nullptr;
+    g.d_dt_bias = d_dt_bias;
+    g.d_scale = d_decay_scale;
+    g.partial = static_cast<float *>(workspace);
+    hipError_t err = gdr::launch_gate_backward(g, static_cast<hipStream_t>(stream));
     if (err != hipSuccess) return fail(GDR_E_HIP, "kernel launch failed: %s", hipGetErrorString(err));
     return GDR_OK;
 }

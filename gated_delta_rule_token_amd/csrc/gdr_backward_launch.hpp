@@ -1,0 +1,63 @@
+// gdr_backward_launch.hpp -- the backward pass's argument block, workspace
+// layout and launchers (internal to libgdr).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "gdr_device.hpp"
+
+namespace gdr {
+
+// Tokens of a chunk: 64, or 32 where a chunk's q and k rows of up to 256
+// channels would not fit twice in LDS beside the chunk x chunk tiles.
+__host__ __device__ constexpr int back_chunk(int dk) { return dk > 128 ? 32 : 64; }
+__host__ __device__ constexpr int back_dk_tile(int dk) { return dk <= 64 ? 64 : dk <= 128 ? 128 : 256; }
+
+// Per (chunk, value head) scalars, a row of back_chunk floats each: e^G,
+// e^(Gamma - G), update rate, G as (hi, lo), and the factors of q (with the
+// scale) and k.
+enum BackScalar : int { SC_EG = 0, SC_KD, SC_B, SC_GH, SC_GL, SC_RQ, SC_RK, BACK_SC };
+
+struct BackParams {
+    Params p;                   // q, k, v, gate, beta, requests, initial state
+    const void *d_o;
+    const float *d_final;       // (B, HV, dv, dk) or nullptr (zeros)
+    void *dq, *dk, *dv, *d_gate;
+    float *d_beta;              // (T, HV): the output, or workspace when it is summed over the heads
+    float *d_rate;              // (T, 1) when d_beta is summed over the heads, or nullptr
+    float *gate_sums;           // raw-gate arm: per (chunk, value head) sums of d_a and of d_scale
+    float *d_a_log, *d_dt_bias, *d_gate_scale;
+    float *d_init;              // or nullptr
+    // workspace
+    int32_t *off;               // (B + 1) first chunk of each request; off[B] = chunks in use
+    int32_t *tok;               // (B, 2) first token and length of each request
+    float *sc, *t1, *t2, *pt, *s, *ds, *e, *y;
+    int32_t chunks;             // chunk budget: ceil(T / C) + B
+    int32_t VB;                 // 16-row blocks of dv
+    int32_t decays;
+};
+
+// Chunk table: request b covers [m_b, m_(b+1)) where m is the running maximum
+// of the clamped cu_seqlens (so ranges never overlap), or its part of a
+// uniform batch.
+hipError_t launch_back_table(const BackParams &a, hipStream_t s);
+hipError_t launch_back_f32(const BackParams &a, bool retrieves, hipStream_t s);
+hipError_t launch_back_f16(const BackParams &a, bool retrieves, hipStream_t s);
+hipError_t launch_back_bf16(const BackParams &a, bool retrieves, hipStream_t s);
+// After the gradients: parameters of the raw-gate arm and a rate shared by the heads.
+hipError_t launch_back_sums(const BackParams &a, hipStream_t s);
+
+// Gradients of the gate fusion (gdr_gate_backward); dt: 0 fp32, 1 fp16, 2 bf16.
+struct GateBackParams {
+    int64_t rows;
+    int32_t heads, dt;
+    const void *a, *d_decay, *b, *d_beta;
+    const float *dt_bias, *decay_scale;
+    void *d_a, *d_b;
+    float *d_dt_bias, *d_scale;
+    float *partial;             // gate_back_blocks x 2 x heads floats
+};
+int gate_back_blocks(int64_t rows, int heads);
+hipError_t launch_gate_backward(const GateBackParams &g, hipStream_t s);
+
+}  // namespace gdr

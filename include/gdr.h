@@ -243,6 +243,48 @@ gdr_status gdr_forward(const gdr_problem *problem, const gdr_tensors *tensors,
  * same call. */
 gdr_status gdr_forward_noalloc(const gdr_problem *problem, const gdr_tensors *tensors, void *stream);
 
+/* ---- Backward pass ---------------------------------------------------------
+ *
+ * Gradients of gdr_forward for the rules with one log decay per value head
+ * (LINEAR, GATED, DELTA, GATED_DELTA; not GATED_DELTA_V2 and not
+ * decay_per_key: GDR_E_UNSUPPORTED).  `problem` and `tensors` are the forward
+ * call's; nothing of that call has to be kept, the chain of states is formed
+ * again in the workspace.  tensors->o and tensors->final_state are not read
+ * and may be NULL.  States in a slab (num_slots > 0) have no backward pass
+ * (GDR_E_UNSUPPORTED): pass them as initial_state.  algo, chunk_size and
+ * scan_segments are the forward's choices and are not read.
+ *
+ * Requests must not overlap: with cu_seqlens, request b covers
+ * [m_b, m_(b+1)) where m_b is the largest of the entries up to b, clamped to
+ * [0, T] (for a non-decreasing cu_seqlens the forward's own range).  Gradient
+ * rows of tokens that no request covers are left as they were.
+ *
+ * All arithmetic and every sum is in fp32 (cumulative decays in fp64);
+ * gradients are rounded to nearest once, on store.  Sums over tokens and
+ * shared heads have a fixed order: equal calls give equal bits. */
+typedef struct {
+    const void *d_o;              /* (T, HV, dv) act dtype: gradient of o */
+    const float *d_final_state;   /* (B, HV, dv, dk): gradient of the final states, or NULL (zero) */
+    void *d_q, *d_k;              /* (T, H, dk) act dtype, summed over the value heads that share a head */
+    void *d_v;                    /* (T, HV, dv) act dtype */
+    void *d_gate;                 /* gate's shape and dtype; non-NULL iff the rule decays */
+    float *d_beta;                /* beta's shape, of beta as given (through the sigmoid); iff the rule has it */
+    float *d_initial_state;       /* (B, HV, dv, dk), or NULL when not wanted */
+    float *d_a_log, *d_dt_bias, *d_gate_scale; /* (HV): non-NULL iff the tensor itself is */
+} gdr_gradients;
+
+/* Bytes of device workspace gdr_backward needs for `problem`: per token and
+ * value head about 12 dv + 8 dv dk / 64 + 500 bytes (3.4 GB at 29,273 tokens,
+ * 32 heads, dk = dv = 128). */
+gdr_status gdr_backward_workspace_size(const gdr_problem *problem, size_t *bytes);
+
+/* Enqueue the backward pass on `stream`.  Arguments are checked on the host
+ * as in gdr_forward; no output may overlap an input, the workspace or another
+ * output (GDR_E_ALIAS; d_final_state and d_initial_state may be the same
+ * buffer). */
+gdr_status gdr_backward(const gdr_problem *problem, const gdr_tensors *tensors, const gdr_gradients *gradients,
+                        void *workspace, size_t workspace_bytes, void *stream);
+
 /* Standalone gate fusion ("com.microsoft.LinearAttentionGate", Description):
  *   decay[n] = decay_scale[h] * softplus(a[n] + dt_bias[h])
  *   beta[n]  = sigmoid(b[n])          (only when beta != NULL; needs b)
@@ -253,6 +295,21 @@ gdr_status gdr_forward_noalloc(const gdr_problem *problem, const gdr_tensors *te
 gdr_status gdr_gate(int64_t count, int32_t heads, int32_t dtype, const void *a,
                     const float *dt_bias, const float *decay_scale, const void *b,
                     void *decay, void *beta, void *stream);
+
+/* Gradients of gdr_gate:
+ *   d_a[n] = d_decay[n] * decay_scale[h] * sigmoid(a[n] + dt_bias[h])
+ *   d_b[n] = d_beta[n] * beta[n] * (1 - beta[n])     (with b, d_beta and d_b, all or none)
+ *   d_dt_bias[h] = sum of d_a,  d_decay_scale[h] = sum of d_decay * softplus(a + dt_bias)
+ * the sums over every row (n / heads), in fp32, in a fixed order.  a, b,
+ * d_decay, d_beta, d_a, d_b share `dtype` and are 16-byte aligned; d_dt_bias
+ * and d_decay_scale are fp32 (heads), written also when count is 0.
+ * `workspace`: gdr_gate_backward_workspace_size bytes of device memory.  No
+ * output may overlap an input, the workspace or another output. */
+gdr_status gdr_gate_backward_workspace_size(int64_t count, int32_t heads, size_t *bytes);
+gdr_status gdr_gate_backward(int64_t count, int32_t heads, int32_t dtype, const void *a, const float *dt_bias,
+                             const float *decay_scale, const void *b, const void *d_decay, const void *d_beta,
+                             void *d_a, void *d_b, float *d_dt_bias, float *d_decay_scale, void *workspace,
+                             size_t workspace_bytes, void *stream);
 
 /* Memory-traffic floor of a decode step over a state slab: a measurement
  * aid beside the operation, which computes nothing of it.  Multiplies in place
