@@ -9,11 +9,16 @@ never a fallback.
 """
 from .api import (  # noqa: F401
     GDRError,
+    backward,
     forward,
     gate,
+    gate_backward,
     library_path,
     load_library,
+    rms_norm,
+    rms_norm_backward,
     workspace_size,
 )
 
-__all__ = ["GDRError", "forward", "gate", "library_path", "load_library", "workspace_size"]
+__all__ = ["GDRError", "backward", "forward", "gate", "gate_backward", "library_path", "load_library", "rms_norm",
+           "rms_norm_backward", "workspace_size"]

@@ -23,7 +23,7 @@ _lib = None
 
 ABI_VERSION = 3  # GDR_ABI_VERSION of include/gdr.h the structs below mirror
 GDR_OK, GDR_E_INVALID, GDR_E_UNSUPPORTED, GDR_E_ALIAS, GDR_E_WORKSPACE, GDR_E_HIP = range(6)
-F32, F16, BF16 = 0, 1, 2
+F32, F16, BF16, E4M3 = 0, 1, 2, 3
 RULES = {"linear": 0, "gated": 1, "delta": 2, "gated_delta": 3, "gated_delta_v2": 4}
 GATES = {"none": 0, "qwen": 1}
 BETAS = {"none": 0, "sigmoid": 1}
@@ -80,7 +80,8 @@ class GradientPointers(ctypes.Structure):
 EXPORTS = ("gdr_abi_version", "gdr_status_str", "gdr_last_error", "gdr_validate",
            "gdr_workspace_size", "gdr_select_algo", "gdr_forward", "gdr_forward_noalloc",
            "gdr_backward_workspace_size", "gdr_backward", "gdr_gate", "gdr_gate_backward_workspace_size",
-           "gdr_gate_backward", "gdr_slab_stream")
+           "gdr_gate_backward", "gdr_rms_norm", "gdr_rms_norm_backward_workspace_size", "gdr_rms_norm_backward",
+           "gdr_slab_stream")
 NOALLOC_SCRATCH_BYTES = 256 << 20  # GDR_NOALLOC_SCRATCH_BYTES of include/gdr.h
 
 
@@ -131,6 +132,15 @@ def load_library():
         lib.gdr_gate_backward.argtypes = ([ctypes.c_int64, ctypes.c_int32, ctypes.c_int32]
                                           + [ctypes.c_void_p] * 11 + [ctypes.c_size_t, ctypes.c_void_p])
         lib.gdr_gate_backward.restype = ctypes.c_int
+        lib.gdr_rms_norm.argtypes = ([ctypes.c_int64] + [ctypes.c_int32] * 5 + [ctypes.c_float]
+                                     + [ctypes.c_void_p] * 8)
+        lib.gdr_rms_norm.restype = ctypes.c_int
+        lib.gdr_rms_norm_backward_workspace_size.argtypes = [ctypes.c_int64, ctypes.c_int32,
+                                                             ctypes.POINTER(ctypes.c_size_t)]
+        lib.gdr_rms_norm_backward_workspace_size.restype = ctypes.c_int
+        lib.gdr_rms_norm_backward.argtypes = ([ctypes.c_int64] + [ctypes.c_int32] * 3 + [ctypes.c_void_p] * 8
+                                              + [ctypes.c_size_t, ctypes.c_void_p])
+        lib.gdr_rms_norm_backward.restype = ctypes.c_int
         lib.gdr_slab_stream.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
                                         ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_void_p]
         lib.gdr_slab_stream.restype = ctypes.c_int
@@ -534,6 +544,110 @@ def gate_backward(a, dt_bias, decay_scale, d_decay, b=None, d_beta=None, workspa
                                     _ptr(g.decay_scale), _ptr(workspace),
                                     workspace.numel() * workspace.element_size(), stream))
     return g
+
+
+class NormOutput(NamedTuple):
+    """Results of ``rms_norm``: ``scale`` with an 8-bit output, ``residual``
+    with a residual, ``inv_rms`` when wanted; None otherwise."""
+    y: torch.Tensor
+    scale: Optional[torch.Tensor]
+    residual: Optional[torch.Tensor]
+    inv_rms: Optional[torch.Tensor]
+
+
+def _norm_rows(x, weight):
+    _need(x, "x", device=x.device)
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise GDRError("GDR_E_INVALID", "x needs a last axis of at least one column")
+    width = x.shape[-1]
+    if weight is not None:
+        _need(weight, "weight", device=x.device)
+        if tuple(weight.shape) != (width,):
+            raise GDRError("GDR_E_INVALID", "weight has shape %s, expected %s" % (tuple(weight.shape), (width,)))
+    return x.numel() // width, width
+
+
+def rms_norm(x, weight=None, *, residual=None, eps=1e-6, out_dtype=None, group=0, want_inv_rms=False,
+             residual_out=None) -> NormOutput:
+    """Root-mean-square norm over the last axis of ``x`` (fp32, fp16 or bf16):
+    y = r / sqrt(mean(r^2) + eps) * weight with r = x + residual, rounded to
+    x's dtype and returned as ``residual`` (written into ``residual_out`` when
+    given, which may be ``residual`` itself).  ``weight`` has x's dtype or
+    fp32.  ``out_dtype=torch.float8_e4m3fn`` gives y in 8 bits with
+    ``scale`` = max |y| / 448 over the row (shape (..., 1)), or over each
+    ``group`` columns (a power of two from 8 to 512).  ``want_inv_rms``: also
+    return 1 / sqrt(mean(r^2) + eps) per row, which ``rms_norm_backward`` takes."""
+    lib = load_library()
+    dev = x.device
+    rows, width = _norm_rows(x, weight)
+    _need(residual, "residual", x.dtype, dev)
+    if residual is not None and residual.shape != x.shape:
+        raise GDRError("GDR_E_INVALID", "residual must have x's shape")
+    if residual_out is not None:
+        if residual is None:
+            raise GDRError("GDR_E_INVALID", "residual_out given without residual")
+        if _need(residual_out, "residual_out", x.dtype, dev).shape != x.shape:
+            raise GDRError("GDR_E_INVALID", "residual_out must have x's shape")
+    elif residual is not None:
+        residual_out = torch.empty_like(x)
+    code = _dtype_code(x.dtype)
+    if out_dtype is None or out_dtype == x.dtype:
+        out_code, y, scale = code, torch.empty_like(x), None
+    elif out_dtype == torch.float8_e4m3fn:
+        groups = -(-width // group) if group > 0 else 1
+        out_code, y = E4M3, torch.empty(x.shape, dtype=out_dtype, device=dev)
+        scale = torch.empty(tuple(x.shape[:-1]) + (groups,), dtype=torch.float32, device=dev)
+    else:
+        raise GDRError("GDR_E_INVALID", "out_dtype must be x's dtype or torch.float8_e4m3fn, got %s" % out_dtype)
+    inv = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if want_inv_rms else None
+    with torch.cuda.device(dev):
+        stream = torch.cuda.current_stream(dev).cuda_stream
+        check(lib.gdr_rms_norm(rows, width, code, code if weight is None else _dtype_code(weight.dtype), out_code,
+                               int(group), float(eps), _ptr(x), _ptr(residual), _ptr(weight), _ptr(y), _ptr(scale),
+                               _ptr(residual_out), _ptr(inv), stream))
+    return NormOutput(y, scale, residual_out, inv)
+
+
+class NormGradients(NamedTuple):
+    """Results of ``rms_norm_backward``; ``weight`` (fp32) is None without one."""
+    x: torch.Tensor
+    weight: Optional[torch.Tensor]
+
+
+def rms_norm_backward(d_y, x, weight, inv_rms, *, d_residual=None, workspace=None) -> NormGradients:
+    """Gradients of ``rms_norm`` (with y in x's dtype).  ``x`` is what was
+    normalised: the forward call's ``residual`` result, or its x without one;
+    ``inv_rms`` is its result.  ``d_residual`` is the gradient of the
+    ``residual`` result, if any.  The returned gradient ``x`` is that of x and
+    of the residual alike; ``weight``'s is a sum over every row, in fp32."""
+    lib = load_library()
+    dev = x.device
+    rows, width = _norm_rows(x, weight)
+    for name, t in (("d_y", d_y), ("d_residual", d_residual)):
+        _need(t, name, x.dtype, dev)
+        if t is not None and t.shape != x.shape:
+            raise GDRError("GDR_E_INVALID", "%s must have x's shape" % name)
+    if d_y is None or inv_rms is None:
+        raise GDRError("GDR_E_INVALID", "d_y and inv_rms are required")
+    if _need(inv_rms, "inv_rms", torch.float32, dev).shape != x.shape[:-1]:
+        raise GDRError("GDR_E_INVALID", "inv_rms must have x's leading axes")
+    d_x = torch.empty_like(x)
+    d_weight = None
+    if weight is not None:
+        d_weight = torch.empty(width, dtype=torch.float32, device=dev)
+        if workspace is None:
+            n = ctypes.c_size_t(0)
+            check(lib.gdr_rms_norm_backward_workspace_size(rows, width, ctypes.byref(n)))
+            workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", device=dev)
+    code = _dtype_code(x.dtype)
+    with torch.cuda.device(dev):
+        stream = torch.cuda.current_stream(dev).cuda_stream
+        check(lib.gdr_rms_norm_backward(
+            rows, width, code, code if weight is None else _dtype_code(weight.dtype), _ptr(d_y), _ptr(x), _ptr(weight),
+            _ptr(inv_rms), _ptr(d_residual), _ptr(d_x), _ptr(d_weight), _ptr(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), stream))
+    return NormGradients(d_x, d_weight)
 
 
 def slab_stream(slab, slot_ids, factor=1.0):

@@ -13,6 +13,7 @@
 
 #include "gdr_backward_launch.hpp"
 #include "gdr_launch.hpp"
+#include "gdr_norm_launch.hpp"
 
 // Workspace of gdr_forward_noalloc, one copy per GPU (see include/gdr.h).  In
 // host code `scratch` is only a handle: its device address comes from
@@ -399,6 +400,21 @@ size_t back_layout(const gdr_problem *p, gdr::BackParams &a, void *base)
     return at;
 }
 
+// No output may overlap an input or another output, but for the pair (out,
+// in) of the same buffer.
+gdr_status check_overlap(const Range *outs, int n, const Range *ins, int m, int out = -1, int in = -1)
+{
+    for (int i = 0; i < n; ++i) {
+        for (int j = i + 1; j < n; ++j)
+            if (overlaps(outs[i], outs[j])) return fail(GDR_E_ALIAS, "%s overlaps %s", outs[i].name, outs[j].name);
+        for (int j = 0; j < m; ++j) {
+            if (i == out && j == in && outs[i].lo == ins[j].lo && outs[i].hi == ins[j].hi) continue;
+            if (overlaps(outs[i], ins[j])) return fail(GDR_E_ALIAS, "%s overlaps %s", outs[i].name, ins[j].name);
+        }
+    }
+    return GDR_OK;
+}
+
 gdr_status check_gradients(const gdr_problem *p, const gdr_tensors *t, const gdr_gradients *g, const void *workspace,
                            size_t workspace_bytes)
 {
@@ -436,16 +452,21 @@ gdr_status check_gradients(const gdr_problem *p, const gdr_tensors *t, const gdr
         range_of("seq_lens", t->seq_lens, (size_t)p->batch * 4), range_of("initial_state", t->initial_state, state),
         range_of("d_final_state", g->d_final_state, state),
     };
-    const int n = sizeof outs / sizeof outs[0];
-    for (int i = 0; i < n; ++i) {
-        for (int j = i + 1; j < n; ++j)
-            if (overlaps(outs[i], outs[j])) return fail(GDR_E_ALIAS, "%s overlaps %s", outs[i].name, outs[j].name);
-        for (const Range &r : ins) {
-            // each workgroup reads its rows of d_final_state before it writes them
-            const bool in_place = g->d_initial_state == g->d_final_state && &r == &ins[12] && i == 5;
-            if (!in_place && overlaps(outs[i], r)) return fail(GDR_E_ALIAS, "%s overlaps %s", outs[i].name, r.name);
-        }
-    }
+    // each workgroup reads its rows of d_final_state before it writes those of d_initial_state
+    return check_overlap(outs, 10, ins, 13, 5, 12);
+}
+
+int dtype_code(int32_t dtype) { return dtype == GDR_F16 ? 1 : dtype == GDR_BF16 ? 2 : 0; }
+
+gdr_status check_norm(int64_t rows, int32_t width, int32_t dtype, int32_t weight_dtype, bool weight)
+{
+    if (rows < 0 || width < 1) return fail(GDR_E_INVALID, "rows must be >= 0 and width >= 1");
+    if (rows > INT32_MAX) return fail(GDR_E_INVALID, "rows above 2^31-1");
+    if (width > gdr::NORM_MAX_WIDTH) return fail(GDR_E_UNSUPPORTED, "width above %lld", (long long)gdr::NORM_MAX_WIDTH);
+    if (dtype != GDR_F32 && dtype != GDR_F16 && dtype != GDR_BF16)
+        return fail(GDR_E_INVALID, "dtype must be GDR_F32, GDR_F16 or GDR_BF16");
+    if (weight && weight_dtype != dtype && weight_dtype != GDR_F32)
+        return fail(GDR_E_INVALID, "weight_dtype must be dtype or GDR_F32");
     return GDR_OK;
 }
 
@@ -620,12 +641,8 @@ gdr_status gdr_gate_backward(int64_t count, int32_t heads, int32_t dtype, const 
     const Range ins[] = {range_of("a", a, n), range_of("b", b, n), range_of("d_decay", d_decay, n),
                          range_of("d_beta", d_beta, n), range_of("dt_bias", dt_bias, head),
                          range_of("decay_scale", decay_scale, head)};
-    for (int i = 0; i < 5; ++i) {
-        for (int j = i + 1; j < 5; ++j)
-            if (overlaps(outs[i], outs[j])) return fail(GDR_E_ALIAS, "%s overlaps %s", outs[i].name, outs[j].name);
-        for (const Range &r : ins)
-            if (overlaps(outs[i], r)) return fail(GDR_E_ALIAS, "%s overlaps %s", outs[i].name, r.name);
-    }
+    st = check_overlap(outs, 5, ins, 6);
+    if (st != GDR_OK) return st;
     gdr::GateBackParams g{};
     g.rows = count / heads;
     g.heads = heads;
@@ -642,6 +659,108 @@ gdr_status gdr_gate_backward(int64_t count, int32_t heads, int32_t dtype, const 
     g.d_scale = d_decay_scale;
     g.partial = static_cast<float *>(workspace);
     hipError_t err = gdr::launch_gate_backward(g, static_cast<hipStream_t>(stream));
+    if (err != hipSuccess) return fail(GDR_E_HIP, "kernel launch failed: %s", hipGetErrorString(err));
+    return GDR_OK;
+}
+
+gdr_status gdr_rms_norm(int64_t rows, int32_t width, int32_t dtype, int32_t weight_dtype, int32_t out_dtype,
+                        int32_t group, float eps, const void *x, const void *residual, const void *weight,
+                        void *y, float *scale, void *residual_out, float *inv_rms, void *stream)
+{
+    g_last_error.clear();
+    gdr_status st = check_norm(rows, width, dtype, weight_dtype, weight != nullptr);
+    if (st != GDR_OK) return st;
+    const bool eight = out_dtype == GDR_E4M3;
+    if (!eight && out_dtype != dtype) return fail(GDR_E_INVALID, "out_dtype must be dtype or GDR_E4M3");
+    if (group != 0 && (group < 8 || group > 512 || (group & (group - 1)) != 0))
+        return fail(GDR_E_INVALID, "group must be 0 or a power of two from 8 to 512");
+    if (group != 0 && !eight) return fail(GDR_E_INVALID, "group needs an 8-bit output");
+    if (!std::isfinite(eps) || eps < 0.f) return fail(GDR_E_INVALID, "eps must be finite and >= 0");
+    if (rows > 0 && (!x || !y)) return fail(GDR_E_INVALID, "x and y are required");
+    if (rows > 0 && (scale != nullptr) != eight) return fail(GDR_E_INVALID, "scale must be given exactly with an 8-bit output");
+    if (rows > 0 && (residual != nullptr) != (residual_out != nullptr))
+        return fail(GDR_E_INVALID, "residual and residual_out must be given together");
+    const void *ptrs[] = {x, residual, weight, y, scale, residual_out, inv_rms};
+    for (const void *q : ptrs)
+        if (q && !aligned16(q)) return fail(GDR_E_INVALID, "every tensor pointer must be 16-byte aligned");
+    const size_t n = (size_t)rows * width, groups = group ? ((size_t)width + group - 1) / group : 1;
+    const Range outs[] = {range_of("residual_out", residual_out, n * dsize(dtype)),
+                          range_of("y", y, n * (eight ? 1 : dsize(dtype))),
+                          range_of("scale", scale, (size_t)rows * groups * 4),
+                          range_of("inv_rms", inv_rms, (size_t)rows * 4)};
+    const Range ins[] = {range_of("residual", residual, n * dsize(dtype)), range_of("x", x, n * dsize(dtype)),
+                         range_of("weight", weight, (size_t)width * dsize(weight_dtype))};
+    st = check_overlap(outs, 4, ins, 3, 0, 0);  // a row is read before it is written
+    if (st != GDR_OK) return st;
+    gdr::NormParams p{};
+    p.rows = rows;
+    p.width = width;
+    p.dt = dtype_code(dtype);
+    p.weight_dt = weight ? dtype_code(weight_dtype) : p.dt;
+    p.eight = eight;
+    p.group = group;
+    p.groups = (int32_t)groups;
+    p.eps = eps;
+    p.x = x;
+    p.residual = residual;
+    p.weight = weight;
+    p.y = y;
+    p.residual_out = residual_out;
+    p.scale = scale;
+    p.inv_rms = inv_rms;
+    hipError_t err = gdr::launch_norm(p, static_cast<hipStream_t>(stream));
+    if (err != hipSuccess) return fail(GDR_E_HIP, "kernel launch failed: %s", hipGetErrorString(err));
+    return GDR_OK;
+}
+
+gdr_status gdr_rms_norm_backward_workspace_size(int64_t rows, int32_t width, size_t *bytes)
+{
+    g_last_error.clear();
+    if (!bytes) return fail(GDR_E_INVALID, "bytes is NULL");
+    gdr_status st = check_norm(rows, width, GDR_F32, GDR_F32, false);
+    if (st != GDR_OK) return st;
+    *bytes = (size_t)gdr::norm_back_blocks(rows, width) * width * 4;
+    return GDR_OK;
+}
+
+gdr_status gdr_rms_norm_backward(int64_t rows, int32_t width, int32_t dtype, int32_t weight_dtype, const void *d_y,
+                                 const void *x, const void *weight, const float *inv_rms, const void *d_residual,
+                                 void *d_x, float *d_weight, void *workspace, size_t workspace_bytes, void *stream)
+{
+    g_last_error.clear();
+    gdr_status st = check_norm(rows, width, dtype, weight_dtype, weight != nullptr);
+    if (st != GDR_OK) return st;
+    if (rows > 0 && (!d_y || !x || !inv_rms || !d_x)) return fail(GDR_E_INVALID, "d_y, x, inv_rms and d_x are required");
+    if ((weight != nullptr) != (d_weight != nullptr)) return fail(GDR_E_INVALID, "d_weight must be given exactly when weight is");
+    const void *ptrs[] = {d_y, x, weight, inv_rms, d_residual, d_x, d_weight, workspace};
+    for (const void *q : ptrs)
+        if (q && !aligned16(q)) return fail(GDR_E_INVALID, "every tensor pointer must be 16-byte aligned");
+    size_t need = 0;
+    if (d_weight) {
+        gdr_rms_norm_backward_workspace_size(rows, width, &need);
+        if (!workspace || workspace_bytes < need) return fail(GDR_E_WORKSPACE, "workspace of %zu bytes required", need);
+    }
+    const size_t n = (size_t)rows * width * dsize(dtype), w = (size_t)width * 4;
+    const Range outs[] = {range_of("d_x", d_x, n), range_of("d_weight", d_weight, w), range_of("workspace", workspace, need)};
+    const Range ins[] = {range_of("d_y", d_y, n), range_of("x", x, n), range_of("d_residual", d_residual, n),
+                         range_of("weight", weight, (size_t)width * dsize(weight_dtype)),
+                         range_of("inv_rms", inv_rms, (size_t)rows * 4)};
+    st = check_overlap(outs, 3, ins, 5);
+    if (st != GDR_OK) return st;
+    gdr::NormBackParams p{};
+    p.rows = rows;
+    p.width = width;
+    p.dt = dtype_code(dtype);
+    p.weight_dt = weight ? dtype_code(weight_dtype) : p.dt;
+    p.d_y = d_y;
+    p.x = x;
+    p.weight = weight;
+    p.d_residual = d_residual;
+    p.inv_rms = inv_rms;
+    p.d_x = d_x;
+    p.d_weight = d_weight;
+    p.partial = d_weight ? static_cast<float *>(workspace) : nullptr;
+    hipError_t err = gdr::launch_norm_backward(p, static_cast<hipStream_t>(stream));
     if (err != hipSuccess) return fail(GDR_E_HIP, "kernel launch failed: %s", hipGetErrorString(err));
     return GDR_OK;
 }

@@ -103,7 +103,10 @@ typedef enum {
  * value fp16 cannot represent exactly, outside magnitudes 2^-17 to 65504,
  * is computed by the recurrent kernel instead) and widen it to fp32 in the
  * per-key form. */
-typedef enum { GDR_F32 = 0, GDR_F16 = 1, GDR_BF16 = 2 } gdr_dtype;
+typedef enum {
+    GDR_F32 = 0, GDR_F16 = 1, GDR_BF16 = 2,
+    GDR_E4M3 = 3  /* 8 bits (4 exponent, 3 mantissa, largest 448, no infinities): gdr_rms_norm's output only */
+} gdr_dtype;
 
 typedef enum {
     GDR_RULE_LINEAR = 0,
@@ -310,6 +313,38 @@ gdr_status gdr_gate_backward(int64_t count, int32_t heads, int32_t dtype, const 
                              const float *decay_scale, const void *b, const void *d_decay, const void *d_beta,
                              void *d_a, void *d_b, float *d_dt_bias, float *d_decay_scale, void *workspace,
                              size_t workspace_bytes, void *stream);
+
+/* Root-mean-square norm of `rows` rows of `width` columns (1 to 32,768), with
+ * the residual's addition: in front of the projections that feed the
+ * recurrence, or over every head of its output (rows = T * HV, width = dv).
+ *   r = x + residual, rounded to `dtype` (r = x when residual is NULL)
+ *   y = r * inv * weight,  inv = 1 / sqrt(mean(r^2) + eps)
+ * x, residual, residual_out (receives r; given exactly when residual is, and
+ * may be the same buffer) have `dtype` (F32, F16 or BF16); weight (width, or
+ * NULL for ones) has weight_dtype, which is dtype or F32; inv_rms (rows, fp32,
+ * or NULL) receives inv, which the backward pass takes.  y has out_dtype:
+ * dtype, or GDR_E4M3 with scales.  Then scale (rows, ceil(width / group)),
+ * or (rows, 1) with group = 0, receives max |y| / 448 over each `group`
+ * columns of a row (1 where that is 0), and y holds y / scale, rounded to
+ * nearest even; group is 0 or a power of two from 8 to 512.  Arithmetic and
+ * sums in fp32.  A row that holds NaN or an infinity gives what the formulas
+ * give. */
+gdr_status gdr_rms_norm(int64_t rows, int32_t width, int32_t dtype, int32_t weight_dtype, int32_t out_dtype,
+                        int32_t group, float eps, const void *x, const void *residual, const void *weight,
+                        void *y, float *scale, void *residual_out, float *inv_rms, void *stream);
+
+/* Gradients of gdr_rms_norm (with y in `dtype`): x is the r that the forward
+ * pass normalised (its residual_out, or its x), inv_rms what it wrote.
+ *   d_x = inv * (t - h * mean(t * h)) + d_residual,  h = x * inv, t = weight * d_y
+ *   d_weight = sum over rows of d_y * h   (fp32; non-NULL iff weight is)
+ * d_residual, the gradient that reaches r besides through y, may be NULL; d_x
+ * is the gradient of x and of the residual alike.  The sum over rows has a
+ * fixed order.  `workspace`: gdr_rms_norm_backward_workspace_size bytes (not
+ * needed without a weight). */
+gdr_status gdr_rms_norm_backward_workspace_size(int64_t rows, int32_t width, size_t *bytes);
+gdr_status gdr_rms_norm_backward(int64_t rows, int32_t width, int32_t dtype, int32_t weight_dtype, const void *d_y,
+                                 const void *x, const void *weight, const float *inv_rms, const void *d_residual,
+                                 void *d_x, float *d_weight, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Memory-traffic floor of a decode step over a state slab: a measurement
  * aid beside the operation, which computes nothing of it.  Multiplies in place
