@@ -78,13 +78,17 @@ __device__ __forceinline__ f4 mfma4(f4 a, f4 b, f4 c)
     return c;
 }
 
-// e^(hi + lo) for a small correction lo
-__device__ __forceinline__ float exp_split(float hi, float lo) { return expf(hi) * (1.f + lo); }
+// e^(hi + lo), |lo| below |hi| or so: the sum's rounding error enters as a factor
+__device__ __forceinline__ float exp_split(float hi, float lo)
+{
+    const float s = hi + lo;
+    return expf(s) * (1.f + ((hi - s) + lo));
+}
 
 __device__ __forceinline__ float exp_of(double x)
 {
     const float hi = (float)x;
-    return exp_split(hi, (float)(x - (double)hi));
+    return expf(hi) * (1.f + (float)(x - (double)hi));
 }
 
 // 4x4 transpose within each quad of lanes: element p of lane q <- element q of lane p
