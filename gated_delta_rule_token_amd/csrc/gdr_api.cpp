@@ -5,6 +5,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -365,6 +366,9 @@ gdr_status check_backward(const gdr_problem *p)
     if (p->num_slots > 0) return fail(GDR_E_UNSUPPORTED, "the backward pass takes no state slab (use initial_state)");
     const int64_t C = gdr::back_chunk(p->head_dim_k), chunks = (p->total_tokens + C - 1) / C + p->batch;
     if (chunks * p->num_heads_v > INT32_MAX) return fail(GDR_E_INVALID, "total_tokens * num_heads_v too large");
+    // the kernels address a chunk's rows, and a head's state, by 31-bit byte offsets
+    const int64_t row = std::max((int64_t)p->num_heads_qk * p->head_dim_k, (int64_t)p->num_heads_v * p->head_dim_v);
+    if (row * C * 4 > INT32_MAX) return fail(GDR_E_INVALID, "heads * head dim too large");
     return GDR_OK;
 }
 
@@ -372,8 +376,9 @@ gdr_status check_backward(const gdr_problem *p)
 // sizes the kernels need; returns the bytes (also when base is NULL).
 size_t back_layout(const gdr_problem *p, gdr::BackParams &a, void *base)
 {
-    const size_t C = gdr::back_chunk(p->head_dim_k), MB = C / 16, tri = MB * (MB + 1) / 2, KB = gdr::back_dk_tile(p->head_dim_k) / 16;
-    const size_t VB = (p->head_dim_v + 15) / 16, block = 256;  // floats of a 16x16 block
+    const size_t C = gdr::back_chunk(p->head_dim_k), MB = C / 16, KB = gdr::back_dk_tile(p->head_dim_k) / 16;
+    const size_t VB = (p->head_dim_v + 63) / 64 * 4, block = 256;  // words of a fragment block
+    const size_t tri = 3 * gdr::back_tri_blocks((int)C), planes = p->act_dtype == GDR_F32 ? 3 : p->act_dtype == GDR_F16 ? 2 : 1;
     const size_t chunks = (p->total_tokens + C - 1) / C + p->batch, recs = chunks * p->num_heads_v;
     const bool retr = gdr::rule_retrieves(p->update_rule);
     a.chunks = (int32_t)chunks;
@@ -388,11 +393,12 @@ size_t back_layout(const gdr_problem *p, gdr::BackParams &a, void *base)
     a.off = static_cast<int32_t *>(take((size_t)p->batch + 1));
     a.tok = static_cast<int32_t *>(take((size_t)p->batch * 2));
     a.sc = floats(recs * gdr::BACK_SC * C);
+    a.gx = floats(recs * gdr::GX * C);
     a.gate_sums = p->gate_activation == GDR_GATE_QWEN ? floats(recs * 2) : nullptr;
     a.d_beta = p->beta_per_token ? floats((size_t)p->total_tokens * p->num_heads_v) : nullptr;
-    a.pt = floats(recs * tri * block);
-    a.t1 = retr ? floats(recs * tri * block) : nullptr;
-    a.t2 = retr ? floats(recs * tri * block) : nullptr;
+    const auto halves = [&](size_t n) { return static_cast<uint16_t *>(take(n)); };
+    a.act = halves(chunks * p->num_heads_qk * 2 * planes * (MB * KB / 2) * block);
+    a.tri = halves(recs * (retr ? 3 : 1) * tri * block);
     a.s = floats(recs * KB * VB * block);
     a.ds = floats(recs * KB * VB * block);
     a.e = floats(recs * MB * VB * block);

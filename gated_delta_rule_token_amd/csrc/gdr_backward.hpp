@@ -31,18 +31,29 @@
 //   k_back_prep    per chunk and q/k head: the two triangular inverses, P, decay factors
 //   k_back_states  per request, head and 64 state rows: forward chain, keeps S0 and E of every chunk
 //   k_back_chain   the same backwards: dS1, Y, dV
-//   k_back_grad    per chunk and q/k head: dQ, dK (summed over the value heads that share them), dg, db
-// Every product runs on v_mfma_f32_16x16x4_f32: fp32 operands, so that fp32
-// gradients keep fp32's precision at any scale of the incoming gradient.
+//   k_back_grad    per chunk and q/k head: dQ, dK (summed over the value heads that share them)
+//   k_back_gate    per chunk and value head: dg, db
 //
-// Fragments.  The 16x16 fp32 accumulator of that instruction (lane l = 16 j +
-// c, element i: row 4 j + i, column c) is, element by element, also its B
-// operand with k = 4 j + i: a wave that holds S^T (dk x 16 state rows) feeds
-// it to K S^T, and the result to (I + ..)^-1, and that result to the state
-// update, with no move between lanes.  The A operand then takes k = 4 j + i
-// too, four consecutive elements of a row.  What one kernel leaves for the
-// next is stored as such blocks ("fragment blocks"): 256 floats, lane l's
-// four at 4 l, holding row c, columns 4 j + i.
+// Planes.  The products run on v_mfma_f32_16x16x32_bf16 at fp32's precision
+// and range: an fp32 operand is cut into three bf16 planes of 8 significant
+// bits each, whose sum is the operand exactly, and of the nine products of
+// two such operands the six of up to 2^-16 relative size are formed (the
+// others are below 2^-24 of the product).  A bf16 activation is one plane, an
+// fp16 one two, so that a product with q, k or d_o takes three or five.  The
+// rate of the instruction is 16 times the fp32 matrix instruction's, so six
+// products are 2.7 times as fast as the fp32 one and three 5.3 times; unlike
+// a split into fp16 pairs it needs no scaling, whatever the size of the
+// incoming gradient.
+//
+// Fragments.  Of a 16x16 fp32 accumulator lane l = 16 j + c holds rows 4 j + i
+// (i = 0..3) of column c.  Two accumulators over rows 32 x + 0..15 and + 16..31
+// are, element by element, the B operand over those 32 rows if operand slot e
+// of lane group j stands for row 32 x + 16 (e / 4) + 4 j + e % 4, the order
+// used for every operand here: a wave that holds S^T (dk x 16 state rows)
+// feeds it to K S^T, that result to (I + ..)^-1, and that one to the state
+// update, with no move between lanes.  What a kernel leaves for the next one
+// lies as such fragments: 512 bf16 a block and plane (lane l's eight at 8 l),
+// or fp32 blocks of 16x16 (lane l's four at 4 l, holding row c, columns 4 j + i).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -54,15 +65,34 @@ namespace gdr {
 namespace {
 
 typedef float f4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u2 __attribute__((ext_vector_type(2)));
+typedef unsigned int u4 __attribute__((ext_vector_type(4)));
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 
-constexpr int FRAG = 256;  // floats of a fragment block
+constexpr int FRAG = 256;    // floats of an fp32 fragment block
+constexpr int BLOCK = 512;   // bf16 of a plane's fragment block
+
+template <typename TA> constexpr int planes_of = sizeof(TA) == 4 ? 3 : 1;
+template <> constexpr int planes_of<half_t> = 2;
 
 template <int DK> struct Geo {
     static constexpr int C = back_chunk(DK);
-    static constexpr int MB = C / 16, KB = DK / 16, TRI = MB * (MB + 1) / 2;
-    static constexpr int LD = DK + 4;   // floats of a staged q/k row
-    static constexpr int LC = C + 4;    // floats of a staged chunk x chunk row
+    static constexpr int MB = C / 16, KB = DK / 16, MX = MB / 2, KX = KB / 2, TRI = MB * (MB + 1) / 2;
+    static constexpr int LC = C + 4;           // floats of a chunk x chunk row in LDS
+    static constexpr int ACT = MB * KX;        // blocks of a plane of a chunk's q or k
+    static constexpr int NT = back_tri_blocks(C);
 };
+
+// Blocks of a triangular chunk x chunk operand, 32 columns each.  Lower: row
+// block m, columns of block pair y <= m / 2.  Upper: row block m, y >= m / 2.
+template <int MB> __device__ __forceinline__ constexpr int lower_block(int m, int y) { return m < 2 ? m : 2 * m - 2 + y; }
+template <int MB> __device__ __forceinline__ constexpr int upper_block(int m, int y)
+{
+    return MB == 2 ? m : m < 2 ? 2 * m + y : m + 2;
+}
+
+// A value that every lane of the wave has alike, in a scalar register.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
 __device__ __forceinline__ constexpr int tri(int m, int k) { return m * (m + 1) / 2 + k; }
 
@@ -76,6 +106,83 @@ __device__ __forceinline__ f4 mfma4(f4 a, f4 b, f4 c)
 #pragma unroll
     for (int i = 0; i < 4; ++i) c = mfma1(a[i], b[i], c);
     return c;
+}
+
+__device__ __forceinline__ f4 mfma(b8 a, b8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+
+// a b over the products of planes i + j <= 2, smallest first
+template <int NA, int NB>
+__device__ __forceinline__ f4 mm(const b8 (&a)[NA], const b8 (&b)[NB], f4 c)
+{
+#pragma unroll
+    for (int s = 2; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i <= s; ++i)
+            if (i < NA && s - i < NB) c = mfma(a[i], b[s - i], c);
+    return c;
+}
+
+// The top 16 bits of two words.
+__device__ __forceinline__ unsigned int top_halves(unsigned int lo, unsigned int hi)
+{
+    return __builtin_amdgcn_perm(hi, lo, 0x07060302);
+}
+
+// Two floats as N bf16 planes, one word each: each plane is the top 8
+// significant bits of what the planes before it leave.
+template <int N>
+__device__ __forceinline__ void split_pair(float x, float y, unsigned int (&w)[N])
+{
+#pragma unroll
+    for (int p = 0; p < N; ++p) {
+        const unsigned int a = __builtin_bit_cast(unsigned int, x), b = __builtin_bit_cast(unsigned int, y);
+        w[p] = top_halves(a, b);
+        if (p + 1 < N) {
+            x -= __builtin_bit_cast(float, a & 0xffff0000u);
+            y -= __builtin_bit_cast(float, b & 0xffff0000u);
+        }
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void split4(f4 v, u2 (&w)[N])
+{
+    unsigned int lo[N], hi[N];
+    split_pair<N>(v[0], v[1], lo);
+    split_pair<N>(v[2], v[3], hi);
+#pragma unroll
+    for (int p = 0; p < N; ++p) w[p] = u2{lo[p], hi[p]};
+}
+
+// Two accumulators (rows 0..15 and 16..31 of a 32-row step) as an operand.
+template <int N>
+__device__ __forceinline__ void split8(f4 a, f4 b, b8 (&out)[N])
+{
+    u2 lo[N], hi[N];
+    split4<N>(a, lo);
+    split4<N>(b, hi);
+#pragma unroll
+    for (int p = 0; p < N; ++p) out[p] = __builtin_bit_cast(b8, u4{lo[p][0], lo[p][1], hi[p][0], hi[p][1]});
+}
+
+__device__ __forceinline__ b8 get_block(const uint16_t *blk)
+{
+    return __builtin_bit_cast(b8, *reinterpret_cast<const u4 *>(blk + (threadIdx.x & 63) * 8));
+}
+
+__device__ __forceinline__ void put_block(uint16_t *blk, b8 v)
+{
+    *reinterpret_cast<u4 *>(blk + (threadIdx.x & 63) * 8) = __builtin_bit_cast(u4, v);
+}
+
+// Half (of 16 columns) `half` of a block of each of three planes, `stride`
+// apart: lane `at`'s four.
+__device__ __forceinline__ void put_half(uint16_t *blk, size_t stride, int at, int half, f4 v)
+{
+    u2 w[3];
+    split4<3>(v, w);
+#pragma unroll
+    for (int p = 0; p < 3; ++p) *reinterpret_cast<u2 *>(blk + p * stride + at * 8 + half * 4) = w[p];
 }
 
 // e^(hi + lo), |lo| below |hi| or so: the sum's rounding error enters as a factor
@@ -94,64 +201,110 @@ __device__ __forceinline__ float exp_of(double x)
 // 4x4 transpose within each quad of lanes: element p of lane q <- element q of lane p
 __device__ __forceinline__ f4 quad_transpose(f4 v)
 {
-    const int lane = threadIdx.x;
-    const bool odd = lane & 1, up = lane & 2;
-    float g = dpp_mov<0xB1>(odd ? v[0] : v[1]);  // lane ^ 1
-    v = odd ? f4{g, v[1], v[2], v[3]} : f4{v[0], g, v[2], v[3]};
-    g = dpp_mov<0xB1>(odd ? v[2] : v[3]);
-    v = odd ? f4{v[0], v[1], g, v[3]} : f4{v[0], v[1], v[2], g};
-    g = dpp_mov<0x4E>(up ? v[0] : v[2]);         // lane ^ 2
-    v = up ? f4{g, v[1], v[2], v[3]} : f4{v[0], v[1], g, v[3]};
-    g = dpp_mov<0x4E>(up ? v[1] : v[3]);
-    v = up ? f4{v[0], g, v[2], v[3]} : f4{v[0], v[1], v[2], g};
-    return v;
+    const bool odd = threadIdx.x & 1, up = threadIdx.x & 2;
+    f4 g;  // the other lane's, moved by every lane before any choice
+#pragma unroll
+    for (int i = 0; i < 4; ++i) g[i] = dpp_mov<0xB1>(v[i ^ 1]);  // lane ^ 1
+    v = f4{odd ? g[0] : v[0], odd ? v[1] : g[1], odd ? g[2] : v[2], odd ? v[3] : g[3]};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) g[i] = dpp_mov<0x4E>(v[i ^ 2]);  // lane ^ 2
+    return f4{up ? g[0] : v[0], up ? g[1] : v[1], up ? v[2] : g[2], up ? v[3] : g[3]};
 }
 
-// Accumulator tile -> fragment block whose rows are the tile's columns.
-__device__ __forceinline__ void put_frag_cols(float *blk, f4 v)
+// Where a lane's four lie in a fragment whose rows are an accumulator tile's rows, after quad_transpose.
+__device__ __forceinline__ int quad_lane()
 {
-    *reinterpret_cast<f4 *>(blk + (threadIdx.x & 63) * 4) = v;
+    const int lane = threadIdx.x & 63, c = lane & 15, j = lane >> 4;
+    return (4 * j + (c & 3)) + 16 * (c >> 2);
 }
 
 // Accumulator tile -> fragment block whose rows are the tile's rows.
 __device__ __forceinline__ void put_frag_rows(float *blk, f4 v)
 {
-    const int lane = threadIdx.x & 63, c = lane & 15, j = lane >> 4;
-    *reinterpret_cast<f4 *>(blk + ((4 * j + (c & 3)) + 16 * (c >> 2)) * 4) = quad_transpose(v);
+    *reinterpret_cast<f4 *>(blk + quad_lane() * 4) = quad_transpose(v);
 }
 
 __device__ __forceinline__ f4 get_frag(const float *blk) { return *reinterpret_cast<const f4 *>(blk + (threadIdx.x & 63) * 4); }
 
-// Four consecutive elements of a row of `width` (from column c), as they lie
-// in memory; columns past the width are zero.  Rows start 16-byte aligned
-// arrays whose width is a multiple of 4 when vec.
+// ---- rows of a chunk in memory
+// A chunk's `cnt` valid rows of `width` elements, `step` elements apart, as a
+// buffer: a load past the last valid row gives zero and a store there does
+// nothing, by the bounds check of the buffer instructions, so that a lane's
+// offset is the same for every chunk and no load stands under a condition
+// (one would be waited for where it is issued).  Lanes whose column lies past
+// the width use offset NOWHERE.  VEC: both widths are multiples of 4 (four
+// elements from a column that is one lie all within the row or all past it);
+// without it elements go one by one.
 template <typename TA> struct Raw4 { TA x[4]; };
 
-template <typename TA>
-__device__ __forceinline__ Raw4<TA> load_raw4(const TA *row, int c, int width, bool vec)
-{
-    Raw4<TA> r;
-    if (vec) {
-        if (c < width) {
-            if constexpr (sizeof(TA) == 4) *reinterpret_cast<uint4 *>(&r) = *reinterpret_cast<const uint4 *>(row + c);
-            else *reinterpret_cast<uint2 *>(&r) = *reinterpret_cast<const uint2 *>(row + c);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) r.x[i] = from_f32<TA>(0.f);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r.x[i] = c + i < width ? row[c + i] : from_f32<TA>(0.f);
+constexpr unsigned NOWHERE = 0x80000000u;
+
+struct ChunkRows {
+    __amdgpu_buffer_rsrc_t buf;
+    template <typename TA>
+    __device__ __forceinline__ ChunkRows(const TA *first, int cnt, int step, int width)
+    {
+        const unsigned bytes = ((unsigned)(cnt - 1) * (unsigned)step + (unsigned)width) * (unsigned)sizeof(TA);  // < 2^31
+        buf = __builtin_amdgcn_make_buffer_rsrc(const_cast<TA *>(first), 0, (int)bytes, 0x00027000);
     }
-    return r;
+};
+
+// byte offsets of elements c .. c + 3 of row `row`
+template <bool VEC, typename TA> struct At4 {
+    unsigned x[VEC ? 1 : 4];
+    __device__ __forceinline__ At4(int row, int step, int c, int width)
+    {
+#pragma unroll
+        for (int i = 0; i < (VEC ? 1 : 4); ++i)
+            x[i] = c + i < width ? ((unsigned)row * (unsigned)step + (unsigned)(c + i)) * (unsigned)sizeof(TA) : NOWHERE;
+    }
+    // `rows` rows of `step` elements further (NOWHERE stays past every buffer)
+    __device__ __forceinline__ At4 down(int rows, int step) const
+    {
+        // formed anew at each use (one addition): kept over a chain's steps the
+        // offsets would take registers that its operands need
+        asm volatile("" : "+s"(step));
+        At4 a = *this;
+#pragma unroll
+        for (int i = 0; i < (VEC ? 1 : 4); ++i) a.x[i] += (unsigned)rows * (unsigned)step * (unsigned)sizeof(TA);
+        return a;
+    }
+};
+
+template <bool VEC, typename TA>
+__device__ __forceinline__ Raw4<TA> load_raw4(const ChunkRows &rows, const At4<VEC, TA> &at)
+{
+    if constexpr (VEC && sizeof(TA) == 4)
+        return __builtin_bit_cast(Raw4<TA>, __builtin_amdgcn_raw_buffer_load_b128(rows.buf, at.x[0], 0, 0));
+    else if constexpr (VEC)
+        return __builtin_bit_cast(Raw4<TA>, __builtin_amdgcn_raw_buffer_load_b64(rows.buf, at.x[0], 0, 0));
+    else {
+        Raw4<TA> r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(TA) == 4) r.x[i] = __builtin_bit_cast(TA, __builtin_amdgcn_raw_buffer_load_b32(rows.buf, at.x[i], 0, 0));
+            else r.x[i] = __builtin_bit_cast(TA, __builtin_amdgcn_raw_buffer_load_b16(rows.buf, at.x[i], 0, 0));
+        }
+        return r;
+    }
 }
 
-template <typename TA> __device__ __forceinline__ Raw4<TA> zero_raw4()
+template <bool VEC, typename TA>
+__device__ __forceinline__ void store4(const ChunkRows &rows, const At4<VEC, TA> &at, f4 v)
 {
     Raw4<TA> r;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r.x[i] = from_f32<TA>(0.f);
-    return r;
+    for (int i = 0; i < 4; ++i) r.x[i] = from_f32<TA>(v[i]);
+    if constexpr (VEC && sizeof(TA) == 4)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, r), rows.buf, at.x[0], 0, 0);
+    else if constexpr (VEC)
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u2, r), rows.buf, at.x[0], 0, 0);
+    else
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(TA) == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned int, r.x[i]), rows.buf, at.x[i], 0, 0);
+            else __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, r.x[i]), rows.buf, at.x[i], 0, 0);
+        }
 }
 
 template <typename TA> __device__ __forceinline__ f4 widen(const Raw4<TA> &r)
@@ -159,21 +312,16 @@ template <typename TA> __device__ __forceinline__ f4 widen(const Raw4<TA> &r)
     return f4{to_f32(r.x[0]), to_f32(r.x[1]), to_f32(r.x[2]), to_f32(r.x[3])};
 }
 
-template <typename TA>
-__device__ __forceinline__ void store4(TA *row, int c, int width, bool vec, f4 v)
+// Values loaded a step ahead, taken up here: without this the compiler moves
+// their conversion up to the load, and the wait for memory with it.
+template <typename T> __device__ __forceinline__ void arrive(T &v)
 {
-    if (vec) {
-        if (c >= width) return;
-        Raw4<TA> r;
+    static_assert(sizeof(T) % 4 == 0, "whole registers");
+    unsigned int w[sizeof(T) / 4];
+    __builtin_memcpy(w, &v, sizeof(T));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) r.x[i] = from_f32<TA>(v[i]);
-        if constexpr (sizeof(TA) == 4) *reinterpret_cast<uint4 *>(row + c) = *reinterpret_cast<const uint4 *>(&r);
-        else *reinterpret_cast<uint2 *>(row + c) = *reinterpret_cast<const uint2 *>(&r);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (c + i < width) row[c + i] = from_f32<TA>(v[i]);
-    }
+    for (unsigned n = 0; n < sizeof(T) / 4; ++n) asm volatile("" : "+v"(w[n]));
+    __builtin_memcpy(&v, w, sizeof(T));
 }
 
 __device__ __forceinline__ float dot4(f4 a, f4 b) { return a[0] * b[0] + a[1] * b[1] + a[2] * b[2] + a[3] * b[3]; }
@@ -195,26 +343,96 @@ __device__ __forceinline__ void chunk_tokens(const BackParams &a, int ci, int C,
         if (a.off[mid] <= ci) lo = mid;
         else hi = mid - 1;
     }
-    const int64_t skip = (int64_t)(ci - a.off[lo]) * C;
-    t0 = (int64_t)a.tok[2 * lo] + skip;
-    const int64_t left = (int64_t)a.tok[2 * lo + 1] - skip;
-    cnt = left < C ? (int)left : C;
+    const int skip = uniform(ci - a.off[lo]) * C;
+    t0 = (int64_t)uniform(a.tok[2 * lo]) + skip;
+    cnt = min(uniform(a.tok[2 * lo + 1]) - skip, C);
 }
+
+// Rows of q or k in LDS as planes: C rows of LD bf16, plane after plane.  The
+// pad of 16 makes consecutive rows start 8 banks apart, so that the 8-byte
+// reads of 16 rows (row_operand) and the transposing reads of 4 rows (col_operand)
+// go over all banks evenly.
+template <int DK> struct Rows {
+    using G = Geo<DK>;
+    static constexpr int LD = DK + 16, PLANE = G::C * LD;
+    // channels 32 x + .. of row `row`
+    template <int NP> static __device__ __forceinline__ void row_operand(const uint16_t *rows, int row, int x, b8 (&out)[NP])
+    {
+        const int j = (threadIdx.x & 63) >> 4;
+#pragma unroll
+        for (int q = 0; q < NP; ++q) {
+            const uint16_t *at = rows + q * PLANE + row * LD + 32 * x + 4 * j;
+            const u2 lo = *reinterpret_cast<const u2 *>(at), hi = *reinterpret_cast<const u2 *>(at + 16);
+            out[q] = __builtin_bit_cast(b8, u4{lo[0], lo[1], hi[0], hi[1]});
+        }
+    }
+    // tokens 32 y + .. of channel 16 kb + c: the transposing read hands lane c
+    // of a group of 16 column c of the 4 rows by 16 columns that the group addresses
+    template <int NP> static __device__ __forceinline__ void col_operand(const uint16_t *rows, int kb, int y, b8 (&out)[NP])
+    {
+        const int lane = threadIdx.x & 63, c = lane & 15, j = lane >> 4;
+#pragma unroll
+        for (int q = 0; q < NP; ++q) {
+            const uint16_t *at = rows + q * PLANE + (32 * y + 4 * j + (c >> 2)) * LD + 16 * kb + (c & 3) * 4;
+            typedef short s4 __attribute__((ext_vector_type(4)));
+            typedef __attribute__((address_space(3))) s4 lds_s4;
+            const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)at);
+            const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(at + 16 * LD));
+            const u2 l = __builtin_bit_cast(u2, lo), h = __builtin_bit_cast(u2, hi);
+            out[q] = __builtin_bit_cast(b8, u4{l[0], l[1], h[0], h[1]});
+        }
+    }
+};
+
+// A chunk's rows of q or k on their way from memory to LDS planes, four
+// elements at a time, in the registers of NT threads.
+template <int DK, typename TA, int NT, bool VEC> struct StageRows {
+    using G = Geo<DK>;
+    static constexpr int LPR = DK / 4, N = G::C * LPR / NT, NP = planes_of<TA>;
+    Raw4<TA> x[N];
+    // the thread's place in the first NT / LPR rows
+    static __device__ __forceinline__ At4<VEC, TA> place(int step, int dk)
+    {
+        return At4<VEC, TA>(threadIdx.x / LPR, step, threadIdx.x % LPR * 4, dk);
+    }
+    __device__ __forceinline__ void load(const TA *first, int cnt, int step, int dk, const At4<VEC, TA> &at)
+    {
+        const ChunkRows rows(first, cnt, step, dk);
+#pragma unroll
+        for (int n = 0; n < N; ++n) x[n] = load_raw4(rows, at.down(n * (NT / LPR), step));
+    }
+    __device__ __forceinline__ void store(uint16_t *rows) const
+    {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int g = threadIdx.x + NT * n;
+            u2 w[NP];
+            if constexpr (NP == 1) w[0] = __builtin_bit_cast(u2, x[n]);
+            else split4<NP>(widen(x[n]), w);
+#pragma unroll
+            for (int q = 0; q < NP; ++q)
+                *reinterpret_cast<u2 *>(rows + q * Rows<DK>::PLANE + g / LPR * Rows<DK>::LD + g % LPR * 4) = w[q];
+        }
+    }
+};
 
 // ---------------------------------------------------------------- prologue
 // One workgroup per (chunk, q/k head); the value heads that share the head in
-// turn.  The products K K^T and Q K^T are formed once for them.  Each unit
-// lower triangular inverse goes by 16x16 blocks: the diagonal ones by forward
+// turn.  It leaves k and q of the chunk as operand fragments with channels as
+// rows (KT, QT) for k_back_grad.  The products K K^T and Q K^T are formed once
+// for the value heads.  Each unit lower triangular inverse goes by 16x16
+// blocks on the fp32 matrix instruction: the diagonal ones by forward
 // substitution, a thread a column; then wave j takes block column j down,
 // T_ij = -T_ii sum_k N_ik T_kj, its T_kj staying in the accumulators' layout.
-template <int DK, typename TA, bool RETR>
+template <int DK, typename TA, bool RETR, bool VEC>
 __global__ __launch_bounds__(256) void k_back_prep(const BackParams a)
 {
     using G = Geo<DK>;
-    constexpr int C = G::C, MB = G::MB, KB = G::KB, LD = G::LD, LC = G::LC, TRI = G::TRI;
-    constexpr int SLOTS = (TRI + 3) / 4, INV = 16 * 20;
-    constexpr int STAGE = 2 * C * LD, SOLVE = C * LC + 2 * MB * INV;
-    __shared__ __align__(16) float mem[STAGE > SOLVE ? STAGE : SOLVE];
+    using RW = Rows<DK>;
+    constexpr int C = G::C, MB = G::MB, MX = G::MX, KX = G::KX, LC = G::LC, TRI = G::TRI, ACT = G::ACT, NT = G::NT;
+    constexpr int NP = planes_of<TA>, SLOTS = (TRI + 3) / 4, INV = 16 * 20;
+    constexpr int STAGE = 2 * NP * RW::PLANE * 2, SOLVE = (C * LC + 2 * MB * INV) * 4;
+    __shared__ __align__(16) char mem[STAGE > SOLVE ? STAGE : SOLVE];
     __shared__ double s_G[C];
     __shared__ __align__(16) float s_b[C];
     __shared__ float s_rq[C], s_rk[C];
@@ -226,41 +444,50 @@ __global__ __launch_bounds__(256) void k_back_prep(const BackParams a)
     int cnt;
     chunk_tokens(a, ci, C, t0, cnt);
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, j = lane >> 4;
-    float *Kh = mem, *Qh = mem + C * LD;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), c = lane & 15, j = lane >> 4;
+    uint16_t *Kr = reinterpret_cast<uint16_t *>(mem), *Qr = Kr + NP * RW::PLANE;
 
-    // rows of q and k, normalised
-    constexpr int LPR = DK / 4;  // lanes of a row
-    const bool vec = p.dk % 4 == 0;
+    // rows of q and k, and the reciprocals of their norms
+    {
+        StageRows<DK, TA, 256, VEC> k, q;
+        constexpr int LPR = DK / 4;  // lanes of a row
+        const size_t first = ((size_t)t0 * p.H + hq) * p.dk;
+        const auto at = k.place(p.H * p.dk, p.dk);
+        k.load(static_cast<const TA *>(p.k) + first, cnt, p.H * p.dk, p.dk, at);
+        q.load(static_cast<const TA *>(p.q) + first, cnt, p.H * p.dk, p.dk, at);
 #pragma unroll
-    for (int n = 0; n < C * LPR / 256; ++n) {
-        const int g = tid + 256 * n, t = g / LPR, col = g % LPR * 4;
-        f4 q = {0.f, 0.f, 0.f, 0.f}, k = q;
-        if (t < cnt) {
-            const size_t row = ((size_t)(t0 + t) * p.H + hq) * p.dk;
-            q = widen(load_raw4(static_cast<const TA *>(p.q) + row, col, p.dk, vec));
-            k = widen(load_raw4(static_cast<const TA *>(p.k) + row, col, p.dk, vec));
-        }
-        float rq = 1.f, rk = 1.f;
-        if (p.qk_l2_norm) {
-            float sq = dot4(q, q), sk = dot4(k, k);
+        for (int n = 0; n < k.N; ++n) {
+            const int g = tid + 256 * n;
+            float rq = 1.f, rk = 1.f;
+            if (p.qk_l2_norm) {
+                const f4 qv = widen(q.x[n]), kv = widen(k.x[n]);
+                float sq = dot4(qv, qv), sk = dot4(kv, kv);
 #pragma unroll
-            for (int o = 1; o < LPR; o <<= 1) {
-                sq += __shfl_xor(sq, o);
-                sk += __shfl_xor(sk, o);
+                for (int o = 1; o < LPR; o <<= 1) {
+                    sq += __shfl_xor(sq, o);
+                    sk += __shfl_xor(sk, o);
+                }
+                rq = 1.f / sqrtf(sq + 1e-12f);
+                rk = 1.f / sqrtf(sk + 1e-12f);
             }
-            rq = 1.f / sqrtf(sq + 1e-12f);
-            rk = 1.f / sqrtf(sk + 1e-12f);
+            if (g % LPR == 0) {
+                s_rq[g / LPR] = rq * p.scale;
+                s_rk[g / LPR] = rk;
+            }
         }
-        rq *= p.scale;
-        *reinterpret_cast<f4 *>(Kh + t * LD + col) = k * rk;
-        *reinterpret_cast<f4 *>(Qh + t * LD + col) = q * rq;
-        if (col == 0) {
-            s_rq[t] = rq;
-            s_rk[t] = rk;
-        }
+        k.store(Kr);
+        q.store(Qr);
     }
     __syncthreads();
+
+    uint16_t *act = a.act + (size_t)blockIdx.x * 2 * NP * ACT * BLOCK;
+    for (int n = wave; n < 2 * ACT; n += 4) {
+        const int kind = n / ACT, blk = n % ACT;
+        b8 v[NP];
+        RW::col_operand(kind == 0 ? Kr : Qr, blk / MX, blk % MX, v);
+#pragma unroll
+        for (int q = 0; q < NP; ++q) put_block(act + (size_t)((kind * NP + q) * ACT + blk) * BLOCK, v[q]);
+    }
 
     // lower triangle of Q K^T and K K^T, tile (m, kb): rows t of block m, columns s of block kb
     f4 qk[SLOTS], kk[SLOTS];
@@ -274,23 +501,36 @@ __global__ __launch_bounds__(256) void k_back_prep(const BackParams a)
         tk[n] = id - tri(m, 0);
         qk[n] = kk[n] = f4{0.f, 0.f, 0.f, 0.f};
         if (id < TRI) {
-            const float *qr = Qh + (16 * tm[n] + c) * LD + 4 * j, *kr = Kh + (16 * tm[n] + c) * LD + 4 * j,
-                        *sr = Kh + (16 * tk[n] + c) * LD + 4 * j;
-#pragma unroll 4
-            for (int x = 0; x < KB; ++x) {
-                const f4 s = *reinterpret_cast<const f4 *>(sr + 16 * x);
-                qk[n] = mfma4(*reinterpret_cast<const f4 *>(qr + 16 * x), s, qk[n]);
-                if (RETR) kk[n] = mfma4(*reinterpret_cast<const f4 *>(kr + 16 * x), s, kk[n]);
+#pragma unroll
+            for (int x = 0; x < KX; ++x) {
+                b8 s[NP], q[NP], k[NP];
+                RW::row_operand(Kr, 16 * tk[n] + c, x, s);
+                RW::row_operand(Qr, 16 * tm[n] + c, x, q);
+                qk[n] = mm(q, s, qk[n]);
+                if (RETR) {
+                    RW::row_operand(Kr, 16 * tm[n] + c, x, k);
+                    kk[n] = mm(k, s, kk[n]);
+                }
+            }
+            const float rs = s_rk[16 * tk[n] + c];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = 16 * tm[n] + 4 * j + i;
+                qk[n][i] *= rs * s_rq[t];
+                kk[n][i] *= rs * s_rk[t];
             }
         }
     }
     __syncthreads();  // the staged rows give way to L and the diagonal inverses
 
-    float *Lm = mem, *inv = mem + C * LC;
+    float *Lm = reinterpret_cast<float *>(mem), *inv = Lm + C * LC;
     const int R = p.HV / p.H;
+    const f4 zero = {0.f, 0.f, 0.f, 0.f};
     for (int r = 0; r < R; ++r) {
         const int h = hq * R + r;
         const size_t rec = (size_t)ci * p.HV + h;
+        constexpr size_t STRIDE = (size_t)NT * BLOCK;
+        uint16_t *pt = a.tri + rec * 3 * (RETR ? 3 : 1) * STRIDE;  // P^T; (I + diag(b) L)^-T; (I + L diag(b))^-1
         if (wave == 0) {
             double g = 0.0;
             float b = 0.f;
@@ -326,21 +566,25 @@ __global__ __launch_bounds__(256) void k_back_prep(const BackParams a)
         __syncthreads();
 #pragma unroll
         for (int n = 0; n < SLOTS; ++n) {
-            if (tm[n] >= 0) {
-                const int s = 16 * tk[n] + c;
+            const int m = tm[n], kb = tk[n];
+            if (m >= 0) {
+                const int s = 16 * kb + c;
                 const double gs = s_G[s];
                 f4 P;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int t = 16 * tm[n] + 4 * j + i;
+                    const int t = 16 * m + 4 * j + i;
                     const float e = s <= t ? exp_of(s_G[t] - gs) : 0.f;
                     P[i] = e * qk[n][i];
                     if (RETR) Lm[t * LC + s] = s < t ? e * kk[n][i] : 0.f;
                 }
-                put_frag_cols(a.pt + (rec * TRI + tri(tm[n], tk[n])) * FRAG, P);
+                uint16_t *blk = pt + upper_block<MB>(kb, m / 2) * BLOCK;
+                put_half(blk, STRIDE, lane, m & 1, P);
+                if (m == kb && (m & 1)) put_half(blk, STRIDE, lane, 0, zero);
             }
         }
         if constexpr (RETR) {
+            uint16_t *t2 = pt + 3 * STRIDE, *t1 = t2 + 3 * STRIDE;
             __syncthreads();
             // z = 0: I + L diag(b);  z = 1: I + diag(b) L
             if (tid < 2 * MB * 16) {
@@ -363,14 +607,14 @@ __global__ __launch_bounds__(256) void k_back_prep(const BackParams a)
                 for (int z = 0; z < 2; ++z) {
                     f4 T[MB];
 #pragma unroll
-                    for (int i = 0; i < MB; ++i) T[i] = f4{0.f, 0.f, 0.f, 0.f};
+                    for (int i = 0; i < MB; ++i) T[i] = zero;
 #pragma unroll
                     for (int i = 0; i < MB; ++i) {
                         if (i == wave) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e) T[i][e] = inv[(z * MB + i) * INV + (4 * j + e) * 20 + c];
                         } else if (i > wave) {
-                            f4 acc = {0.f, 0.f, 0.f, 0.f};
+                            f4 acc = zero;
                             const float bt = s_b[16 * i + c];
 #pragma unroll
                             for (int k = 0; k < i; ++k) {
@@ -380,11 +624,18 @@ __global__ __launch_bounds__(256) void k_back_prep(const BackParams a)
                                 acc = mfma4(N, T[k], acc);
                             }
                             const f4 Ti = *reinterpret_cast<const f4 *>(inv + (z * MB + i) * INV + c * 20 + 4 * j);
-                            T[i] = -mfma4(Ti, acc, f4{0.f, 0.f, 0.f, 0.f});
+                            T[i] = -mfma4(Ti, acc, zero);
                         }
-                        if (i >= wave) {
-                            if (z == 0) put_frag_rows(a.t1 + (rec * TRI + tri(i, wave)) * FRAG, T[i]);
-                            else put_frag_cols(a.t2 + (rec * TRI + tri(i, wave)) * FRAG, T[i]);
+                        if (i >= wave) {  // tile: rows t of block i, columns s of block `wave`
+                            if (z == 0) {
+                                uint16_t *blk = t1 + lower_block<MB>(i, wave / 2) * BLOCK;
+                                put_half(blk, STRIDE, quad_lane(), wave & 1, quad_transpose(T[i]));
+                                if (i == wave && !(i & 1)) put_half(blk, STRIDE, lane, 1, zero);
+                            } else {
+                                uint16_t *blk = t2 + upper_block<MB>(wave, i / 2) * BLOCK;
+                                put_half(blk, STRIDE, lane, i & 1, T[i]);
+                                if (i == wave && (i & 1)) put_half(blk, STRIDE, lane, 0, zero);
+                            }
                         }
                     }
                 }
@@ -394,143 +645,211 @@ __global__ __launch_bounds__(256) void k_back_prep(const BackParams a)
     }
 }
 
-// ---------------------------------------------------------------- staging of a chunk's q or k rows
-// Each of NT threads holds C * DK / 4 / NT groups of four elements between
-// the global load (stage_load) and the LDS store (stage_store).
-template <int DK, typename TA, int NT> struct Stage {
-    using G = Geo<DK>;
-    static constexpr int LPR = DK / 4, N = G::C * LPR / NT;
-    Raw4<TA> x[N];
-    float r[N];
-
-    __device__ __forceinline__ void load(const TA *src, const float *scale, int64_t t0, int cnt, int heads, int head,
-                                         int dk, bool vec)
+// ---------------------------------------------------------------- pieces of the chains
+// BLOCKS consecutive fragment blocks on their way from memory to LDS, in the
+// registers of 256 threads.
+template <int BLOCKS> struct Copy {
+    static constexpr int WORDS = BLOCKS * 64, N = (WORDS + 255) / 256;
+    u4 x[N];
+    __device__ __forceinline__ void load(const uint16_t *src)
     {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            const int g = threadIdx.x + NT * n, t = g / LPR, col = g % LPR * 4;
-            x[n] = t < cnt ? load_raw4(src + ((size_t)(t0 + t) * heads + head) * dk, col, dk, vec) : zero_raw4<TA>();
-            r[n] = scale[t];
+            const int at = threadIdx.x + 256 * n;
+            x[n] = reinterpret_cast<const u4 *>(src)[at < WORDS ? at : 0];
         }
     }
-    __device__ __forceinline__ void store(float *dst) const
+    __device__ __forceinline__ void store(uint16_t *dst) const
     {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            const int g = threadIdx.x + NT * n, t = g / LPR, col = g % LPR * 4;
-            *reinterpret_cast<f4 *>(dst + t * G::LD + col) = widen(x[n]) * r[n];
+            const int at = threadIdx.x + 256 * n;
+            if (at < WORDS) reinterpret_cast<u4 *>(dst)[at] = x[n];
         }
     }
 };
 
-// Column `col` (of `width`) of the chunk's rows in the accumulators' layout.
-template <int MB, typename TA>
-__device__ __forceinline__ void load_cols(f4 (&out)[MB], const TA *src, int64_t t0, int cnt, int heads, int head, int width,
-                                          int col, int j)
-{
+// Columns 16 vb .. + 15 (of `width`) of the chunk's rows: a lane loads four
+// columns of row 16 m + 4 j + c % 4, and a transpose within quads of lanes
+// gives the accumulators' layout.
+template <int MB, typename TA, bool VEC> struct Cols {
+    Raw4<TA> x[MB];
+    static __device__ __forceinline__ At4<VEC, TA> place(int vb, int step, int width)
+    {
+        const int lane = threadIdx.x & 63, c = lane & 15, j = lane >> 4;
+        return At4<VEC, TA>(4 * j + (c & 3), step, 16 * vb + 4 * (c >> 2), width);
+    }
+    __device__ __forceinline__ void load(const TA *first, int cnt, int step, int width, const At4<VEC, TA> &at)
+    {
+        const ChunkRows rows(first, cnt, step, width);
 #pragma unroll
-    for (int m = 0; m < MB; ++m)
+        for (int m = 0; m < MB; ++m) x[m] = load_raw4(rows, at.down(16 * m, step));
+    }
+    __device__ __forceinline__ void get(f4 (&out)[MB]) const
+    {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int t = 16 * m + 4 * j + i;
-            out[m][i] = t < cnt && col < width ? to_f32(src[((size_t)(t0 + t) * heads + head) * width + col]) : 0.f;
-        }
-}
+        for (int m = 0; m < MB; ++m) out[m] = quad_transpose(widen(x[m]));
+    }
+};
 
-// One (request, head)'s state rows `col` as S^T tiles: dk = 16 kb + 4 j + i.
-template <int KB>
-__device__ __forceinline__ void load_state(f4 (&S)[KB], const float *row, int dk, bool ok, int j)
+// Row `row` of a (request, head)'s dv state rows as S^T tiles: dk = 16 kb + 4 j + i.
+template <bool VEC, int KB>
+__device__ __forceinline__ void load_state(f4 (&S)[KB], const float *head, int row, int dv, int dk, int j)
 {
-    const bool vec = dk % 4 == 0;
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
-        S[kb] = ok ? widen(load_raw4(row, 16 * kb + 4 * j, dk, vec)) : f4{0.f, 0.f, 0.f, 0.f};
-}
-
-// rows (token) x dk times the state: acc[m] += K[16 m ..][:] S^T
-template <int DK>
-__device__ __forceinline__ void rows_times_state(f4 (&acc)[Geo<DK>::MB], const float *rows, const f4 (&S)[Geo<DK>::KB], int c, int j)
-{
-    using G = Geo<DK>;
-#pragma unroll
-    for (int kb = 0; kb < G::KB; ++kb) {
-        f4 x[G::MB];
-#pragma unroll
-        for (int m = 0; m < G::MB; ++m) x[m] = *reinterpret_cast<const f4 *>(rows + (16 * m + c) * G::LD + 16 * kb + 4 * j);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int m = 0; m < G::MB; ++m) acc[m] = mfma1(x[m][i], S[kb][i], acc[m]);
+    for (int kb = 0; kb < KB; ++kb) {
+        S[kb] = f4{0.f, 0.f, 0.f, 0.f};
+        if (head) S[kb] = widen(load_raw4(ChunkRows(head, dv, dk, dk), At4<VEC, float>(row, dk, 16 * kb + 4 * j, dk)));
     }
 }
 
-// state update: S[kb] += rows^T X
-template <int DK>
-__device__ __forceinline__ void state_update(f4 (&S)[Geo<DK>::KB], const float *rows, const f4 (&X)[Geo<DK>::MB], int c, int j)
+// acc[m] += K S^T, K's planes in LDS
+template <int DK, int NP>
+__device__ __forceinline__ void rows_times_state(f4 (&acc)[Geo<DK>::MB], const uint16_t *rows, const f4 (&S)[Geo<DK>::KB], int c)
 {
     using G = Geo<DK>;
 #pragma unroll
-    for (int m = 0; m < G::MB; ++m)
+    for (int x = 0; x < G::KX; ++x) {
+        __builtin_amdgcn_sched_barrier(0);  // one step's operands in registers at a time
+        b8 s[3];
+        split8<3>(S[2 * x], S[2 * x + 1], s);
+        b8 k[G::MB][NP];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float *row = rows + (16 * m + 4 * j + i) * G::LD + c;
+        for (int m = 0; m < G::MB; ++m) Rows<DK>::row_operand(rows, 16 * m + c, x, k[m]);
 #pragma unroll
-            for (int kb = 0; kb < G::KB; ++kb) S[kb] = mfma1(row[16 * kb], X[m][i], S[kb]);
-        }
+        for (int n = 2; n >= 0; --n)
+#pragma unroll
+            for (int i = 0; i <= n; ++i)
+                if (i < NP)
+#pragma unroll
+                    for (int m = 0; m < G::MB; ++m) acc[m] = mfma(k[m][i], s[n - i], acc[m]);
+    }
 }
+
+// S[kb] += rows^T X, the rows' (k's or q's) planes in LDS, X by token blocks
+template <int DK, int NP>
+__device__ __forceinline__ void state_update(f4 (&S)[Geo<DK>::KB], const uint16_t *rows, const f4 (&X)[Geo<DK>::MB])
+{
+    using G = Geo<DK>;
+#pragma unroll
+    for (int y = 0; y < G::MX; ++y) {
+        b8 x[3];
+        split8<3>(X[2 * y], X[2 * y + 1], x);
+#pragma unroll
+        for (int k0 = 0; k0 < G::KB; k0 += 4) {
+            __builtin_amdgcn_sched_barrier(0);
+            b8 k[4][NP];
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb) Rows<DK>::col_operand(rows, k0 + kb, y, k[kb]);
+#pragma unroll
+            for (int n = 2; n >= 0; --n)
+#pragma unroll
+                for (int i = 0; i <= n; ++i)
+                    if (i < NP)
+#pragma unroll
+                        for (int kb = 0; kb < 4; ++kb) S[k0 + kb] = mfma(k[kb][i], x[n - i], S[k0 + kb]);
+        }
+    }
+}
+
+// acc[m] += T X over token blocks 2 y and 2 y + 1 for a triangular operand's planes in LDS
+template <int MB, bool UPPER, int NB>
+__device__ __forceinline__ void tri_times(f4 (&acc)[MB], const uint16_t *T, int y, const b8 (&x)[NB])
+{
+    constexpr int NT = back_tri_blocks(16 * MB);
+#pragma unroll
+    for (int i = 2; i >= 0; --i) {  // planes of T, smallest first
+        b8 t[MB];
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+            if (UPPER ? 2 * y + 1 >= m : 2 * y <= m)
+                t[m] = get_block(T + (i * NT + (UPPER ? upper_block<MB>(m, y) : lower_block<MB>(m, y))) * BLOCK);
+#pragma unroll
+        for (int n = 2 - i; n >= 0; --n)
+            if (n < NB)
+#pragma unroll
+                for (int m = 0; m < MB; ++m)
+                    if (UPPER ? 2 * y + 1 >= m : 2 * y <= m) acc[m] = mfma(t[m], x[n], acc[m]);
+    }
+}
+
+// Scalars of a chunk on their way to LDS: thread t < C holds token t's.
+struct ChunkScalars {
+    float eg, kd, b, rq, rk;
+    __device__ __forceinline__ void load(const float *sc, int C, int t)
+    {
+        t = t < C ? t : C - 1;
+        eg = sc[SC_EG * C + t];
+        kd = sc[SC_KD * C + t];
+        b = sc[SC_B * C + t];
+        rq = sc[SC_RQ * C + t];
+        rk = sc[SC_RK * C + t];
+    }
+};
 
 // ---------------------------------------------------------------- forward chain
 // One workgroup per (request, value head, 64 state rows); wave w keeps S^T of
-// 16 rows in its accumulators over the whole chain.
-template <int DK, typename TA, bool RETR>
-__global__ __launch_bounds__(256, 2) void k_back_states(const BackParams a)
+// 16 rows in its accumulators over the whole chain.  Everything that a step
+// reads from memory is loaded one step ahead: within the step there are only
+// LDS reads, and stores that nothing waits for.
+template <int DK, typename TA, bool RETR, bool VEC>
+__global__ __launch_bounds__(256, back_chain_waves<TA>(DK)) void k_back_states(const BackParams a)
 {
     using G = Geo<DK>;
-    constexpr int C = G::C, MB = G::MB, KB = G::KB, TRI = G::TRI;
-    __shared__ __align__(16) float Kh[C * G::LD];
+    constexpr int C = G::C, MB = G::MB, MX = G::MX, KB = G::KB, NT = G::NT, NP = planes_of<TA>;
+    constexpr int TRIS = RETR ? 3 : 1;  // triangular operands of a record
+    __shared__ __align__(16) uint16_t Kr[NP * Rows<DK>::PLANE];
+    __shared__ __align__(16) uint16_t T[RETR ? 3 * NT * BLOCK : 8];
     __shared__ __align__(16) float s_eg[C], s_x[C];
+    __shared__ float s_gamma;
     const Params &p = a.p;
-    const int tiles = (a.VB + 3) / 4;
+    const int tiles = a.VB / 4;
     const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles, h = bh % p.HV, b = bh / p.HV;
-    const int first = a.off[b], count = a.off[b + 1] - first;
+    const int first = uniform(a.off[b]), count = uniform(a.off[b + 1]) - first;
     if (count == 0) return;
     const int hq = h / (p.HV / p.H);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, j = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), c = lane & 15, j = lane >> 4;
     const int vb = tile * 4 + wave, col = vb * 16 + c;
-    const bool on = vb < a.VB, vec = p.dk % 4 == 0;
-    const int64_t start = a.tok[2 * b];
-    const int64_t len = a.tok[2 * b + 1];
+    const int64_t start = uniform(a.tok[2 * b]);
+    const int len = uniform(a.tok[2 * b + 1]);
 
-    f4 S[KB];
-    load_state(S, p.init ? p.init + (((size_t)b * p.HV + h) * p.dv + col) * p.dk : nullptr, p.dk,
-               p.init != nullptr && col < p.dv, j);
-    Stage<DK, TA, 256> k;
-    {
-        const float *sc = a.sc + ((size_t)first * p.HV + h) * (BACK_SC * C);
-        k.load(static_cast<const TA *>(p.k), sc + SC_RK * C, start, len < C ? (int)len : C, p.H, hq, p.dk, vec);
-    }
+    f4 S[KB], E[MB];
+    load_state<VEC>(S, p.init ? p.init + (size_t)bh * p.dv * p.dk : nullptr, col, p.dv, p.dk, j);
+    StageRows<DK, TA, 256, VEC> k;
+    Copy<RETR ? 3 * NT : 0> tri_next;
+    ChunkScalars x;
+    Cols<MB, TA, VEC> v;
+    const int kstep = p.H * p.dk, vstep = p.HV * p.dv;
+    const auto kat = k.place(kstep, p.dk);
+    const auto vat = v.place(vb, vstep, p.dv);
+    auto fetch = [&](int n) {
+        const int cnt = min(len - n * C, C);
+        const size_t t0 = (size_t)start + (size_t)n * C, rec = (size_t)(first + n) * p.HV + h;
+        k.load(static_cast<const TA *>(p.k) + t0 * kstep + hq * p.dk, cnt, kstep, p.dk, kat);
+        tri_next.load(a.tri + (rec * TRIS + TRIS - 1) * 3 * NT * BLOCK);
+        x.load(a.sc + rec * (BACK_SC * C), C, tid);
+        v.load(static_cast<const TA *>(p.v) + t0 * vstep + h * p.dv, cnt, vstep, p.dv, vat);
+    };
+    auto stage = [&](int n) {  // chunk n's operands into LDS, the next chunk's on their way
+        lds_barrier();  // the previous step's reads
+        arrive(k.x);
+        arrive(x);
+        arrive(v.x);
+        k.store(Kr);
+        tri_next.store(T);
+        if (tid < C) {
+            s_eg[tid] = x.eg * x.rk;
+            s_x[tid] = x.kd * x.b * x.rk;
+            if (tid == C - 1) s_gamma = x.eg;
+        }
+        v.get(E);
+        fetch(min(n + 1, count - 1));
+        lds_barrier();
+    };
+    fetch(0);
     for (int n = 0; n < count; ++n) {
         const size_t rec = (size_t)(first + n) * p.HV + h;
-        const int64_t t0 = start + (int64_t)n * C;
-        const int64_t left = len - (int64_t)n * C;
-        const int cnt = left < C ? (int)left : C;
-        const float *sc = a.sc + rec * (BACK_SC * C);
-        lds_barrier();  // the previous step's reads of Kh, s_*
-        k.store(Kh);
-        if (tid < C) {
-            s_eg[tid] = sc[SC_EG * C + tid];
-            s_x[tid] = sc[SC_KD * C + tid] * sc[SC_B * C + tid];
-        }
-        const float gamma = sc[SC_EG * C + C - 1];
-        if (n + 1 < count) {
-            const int64_t rest = left - C;
-            k.load(static_cast<const TA *>(p.k), sc + (size_t)p.HV * (BACK_SC * C) + SC_RK * C, t0 + C,
-                   rest < C ? (int)rest : C, p.H, hq, p.dk, vec);
-        }
-        lds_barrier();
-        if (!on) continue;
-        f4 E[MB];
-        load_cols<MB>(E, static_cast<const TA *>(p.v), t0, cnt, p.HV, h, p.dv, col, j);
+        stage(n);
         float *Sw = a.s + (rec * KB * a.VB + vb) * FRAG;
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) put_frag_rows(Sw + (size_t)kb * a.VB * FRAG, S[kb]);
@@ -538,18 +857,18 @@ __global__ __launch_bounds__(256, 2) void k_back_states(const BackParams a)
             f4 Y[MB];
 #pragma unroll
             for (int m = 0; m < MB; ++m) Y[m] = f4{0.f, 0.f, 0.f, 0.f};
-            rows_times_state<DK>(Y, Kh, S, c, j);
-            f4 Z[MB];
+            rows_times_state<DK, NP>(Y, Kr, S, c);
 #pragma unroll
             for (int m = 0; m < MB; ++m) {
-                Z[m] = E[m] - *reinterpret_cast<const f4 *>(s_eg + 16 * m + 4 * j) * Y[m];
+                Y[m] = E[m] - *reinterpret_cast<const f4 *>(s_eg + 16 * m + 4 * j) * Y[m];
                 E[m] = f4{0.f, 0.f, 0.f, 0.f};
             }
-            const float *T = a.t1 + rec * TRI * FRAG;
 #pragma unroll
-            for (int kb = 0; kb < MB; ++kb)
-#pragma unroll
-                for (int m = kb; m < MB; ++m) E[m] = mfma4(get_frag(T + tri(m, kb) * FRAG), Z[kb], E[m]);
+            for (int y = 0; y < MX; ++y) {
+                b8 z[3];
+                split8<3>(Y[2 * y], Y[2 * y + 1], z);
+                tri_times<MB, false>(E, T, y, z);
+            }
         }
         float *Ew = a.e + (rec * MB * a.VB + vb) * FRAG;
 #pragma unroll
@@ -557,87 +876,103 @@ __global__ __launch_bounds__(256, 2) void k_back_states(const BackParams a)
             put_frag_rows(Ew + (size_t)m * a.VB * FRAG, E[m]);
             E[m] *= *reinterpret_cast<const f4 *>(s_x + 16 * m + 4 * j);
         }
+        const float gamma = s_gamma;
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) S[kb] *= gamma;
-        state_update<DK>(S, Kh, E, c, j);
+        state_update<DK, NP>(S, Kr, E);
     }
 }
 
 // ---------------------------------------------------------------- backward chain
-template <int DK, typename TA, bool RETR>
-__global__ __launch_bounds__(256, 2) void k_back_chain(const BackParams a)
+template <int DK, typename TA, bool RETR, bool VEC>
+__global__ __launch_bounds__(256, back_chain_waves<TA>(DK)) void k_back_chain(const BackParams a)
 {
     using G = Geo<DK>;
-    constexpr int C = G::C, MB = G::MB, KB = G::KB, TRI = G::TRI;
-    __shared__ __align__(16) float Kh[C * G::LD], Qh[C * G::LD];
-    __shared__ __align__(16) float s_eg[C], s_kd[C], s_b[C];
+    constexpr int C = G::C, MB = G::MB, MX = G::MX, KB = G::KB, NT = G::NT, NP = planes_of<TA>;
+    constexpr int TRIS = RETR ? 3 : 1;
+    __shared__ __align__(16) uint16_t Kr[NP * Rows<DK>::PLANE], Qr[NP * Rows<DK>::PLANE];
+    __shared__ __align__(16) uint16_t T[(RETR ? 6 : 3) * NT * BLOCK];  // P^T, then (I + diag(b) L)^-T
+    __shared__ __align__(16) float s_kd[C], s_b[C], s_q[C], s_k[C];
+    __shared__ float s_gamma;
     const Params &p = a.p;
-    const int tiles = (a.VB + 3) / 4;
+    const int tiles = a.VB / 4;
     const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles, h = bh % p.HV, b = bh / p.HV;
-    const int first = a.off[b], count = a.off[b + 1] - first;
+    const int first = uniform(a.off[b]), count = uniform(a.off[b + 1]) - first;
     const int hq = h / (p.HV / p.H);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, j = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), c = lane & 15, j = lane >> 4;
     const int vb = tile * 4 + wave, col = vb * 16 + c;
-    const bool on = vb < a.VB, vec = p.dk % 4 == 0;
-    const int64_t start = a.tok[2 * b];
-    const int64_t len = a.tok[2 * b + 1];
-    const TA *kp = static_cast<const TA *>(p.k), *qp = static_cast<const TA *>(p.q);
+    const int64_t start = uniform(a.tok[2 * b]);
+    const int len = uniform(a.tok[2 * b + 1]);
 
     f4 dS[KB];
-    const size_t srow = (((size_t)b * p.HV + h) * p.dv + col) * p.dk;
-    load_state(dS, a.d_final ? a.d_final + srow : nullptr, p.dk, a.d_final != nullptr && col < p.dv, j);
-    Stage<DK, TA, 256> k, q;
+    load_state<VEC>(dS, a.d_final ? a.d_final + (size_t)bh * p.dv * p.dk : nullptr, col, p.dv, p.dk, j);
+    StageRows<DK, TA, 256, VEC> k, q;
+    Copy<(RETR ? 6 : 3) * NT> tri_next;
+    ChunkScalars x;
+    Cols<MB, TA, VEC> o;
+    const int kstep = p.H * p.dk, vstep = p.HV * p.dv;
+    const auto kat = k.place(kstep, p.dk);
+    const auto vat = o.place(vb, vstep, p.dv);
     auto fetch = [&](int n) {
-        const float *sc = a.sc + ((size_t)(first + n) * p.HV + h) * (BACK_SC * C);
-        const int64_t left = len - (int64_t)n * C;
-        const int cnt = left < C ? (int)left : C;
-        k.load(kp, sc + SC_RK * C, start + (int64_t)n * C, cnt, p.H, hq, p.dk, vec);
-        q.load(qp, sc + SC_RQ * C, start + (int64_t)n * C, cnt, p.H, hq, p.dk, vec);
+        const int cnt = min(len - n * C, C);
+        const size_t t0 = (size_t)start + (size_t)n * C, rec = (size_t)(first + n) * p.HV + h;
+        k.load(static_cast<const TA *>(p.k) + t0 * kstep + hq * p.dk, cnt, kstep, p.dk, kat);
+        q.load(static_cast<const TA *>(p.q) + t0 * kstep + hq * p.dk, cnt, kstep, p.dk, kat);
+        tri_next.load(a.tri + rec * TRIS * 3 * NT * BLOCK);
+        x.load(a.sc + rec * (BACK_SC * C), C, tid);
+        o.load(static_cast<const TA *>(a.d_o) + t0 * vstep + h * p.dv, cnt, vstep, p.dv, vat);
+    };
+    f4 dO[MB];
+    auto stage = [&](int n) {
+        lds_barrier();
+        arrive(k.x);
+        arrive(q.x);
+        arrive(x);
+        arrive(o.x);
+        k.store(Kr);
+        q.store(Qr);
+        tri_next.store(T);
+        if (tid < C) {
+            s_kd[tid] = x.kd * x.rk;
+            s_b[tid] = x.b;
+            s_q[tid] = x.eg * x.rq;
+            s_k[tid] = -x.eg * x.rk;
+            if (tid == C - 1) s_gamma = x.eg;
+        }
+        o.get(dO);
+        fetch(max(n - 1, 0));
+        lds_barrier();
     };
     if (count > 0) fetch(count - 1);
     for (int n = count - 1; n >= 0; --n) {
         const size_t rec = (size_t)(first + n) * p.HV + h;
-        const int64_t t0 = start + (int64_t)n * C;
-        const int64_t left = len - (int64_t)n * C;
-        const int cnt = left < C ? (int)left : C;
-        const float *sc = a.sc + rec * (BACK_SC * C);
-        lds_barrier();
-        k.store(Kh);
-        q.store(Qh);
-        if (tid < C) {
-            s_eg[tid] = sc[SC_EG * C + tid];
-            s_kd[tid] = sc[SC_KD * C + tid];
-            s_b[tid] = sc[SC_B * C + tid];
-        }
-        const float gamma = sc[SC_EG * C + C - 1];
-        if (n > 0) fetch(n - 1);
-        lds_barrier();
-        if (!on) continue;
-        f4 dO[MB];
-        load_cols<MB>(dO, static_cast<const TA *>(a.d_o), t0, cnt, p.HV, h, p.dv, col, j);
+        const int cnt = min(len - n * C, C);
+        stage(n);
         float *Sw = a.ds + (rec * KB * a.VB + vb) * FRAG;
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) put_frag_rows(Sw + (size_t)kb * a.VB * FRAG, dS[kb]);
         f4 D[MB];
 #pragma unroll
         for (int m = 0; m < MB; ++m) D[m] = f4{0.f, 0.f, 0.f, 0.f};
-        rows_times_state<DK>(D, Kh, dS, c, j);
+        rows_times_state<DK, NP>(D, Kr, dS, c);
 #pragma unroll
         for (int m = 0; m < MB; ++m) D[m] *= *reinterpret_cast<const f4 *>(s_kd + 16 * m + 4 * j);
-        const float *P = a.pt + rec * TRI * FRAG;
 #pragma unroll
-        for (int kb = 0; kb < MB; ++kb)
-#pragma unroll
-            for (int m = 0; m <= kb; ++m) D[m] = mfma4(get_frag(P + tri(kb, m) * FRAG), dO[kb], D[m]);
+        for (int y = 0; y < MX; ++y) {
+            b8 g[NP];
+            split8<NP>(dO[2 * y], dO[2 * y + 1], g);
+            tri_times<MB, true>(D, T, y, g);
+        }
         if constexpr (RETR) {
             f4 Y[MB];
 #pragma unroll
             for (int m = 0; m < MB; ++m) Y[m] = f4{0.f, 0.f, 0.f, 0.f};
-            const float *T = a.t2 + rec * TRI * FRAG;
 #pragma unroll
-            for (int kb = 0; kb < MB; ++kb)
-#pragma unroll
-                for (int m = 0; m <= kb; ++m) Y[m] = mfma4(get_frag(T + tri(kb, m) * FRAG), D[kb], Y[m]);
+            for (int y = 0; y < MX; ++y) {
+                b8 d[3];
+                split8<3>(D[2 * y], D[2 * y + 1], d);
+                tri_times<MB, true>(Y, T + 3 * NT * BLOCK, y, d);
+            }
             float *Yw = a.y + (rec * MB * a.VB + vb) * FRAG;
 #pragma unroll
             for (int m = 0; m < MB; ++m) {
@@ -645,43 +980,53 @@ __global__ __launch_bounds__(256, 2) void k_back_chain(const BackParams a)
                 D[m] = Y[m] * *reinterpret_cast<const f4 *>(s_b + 16 * m + 4 * j);
             }
         }
+        const ChunkRows dvrows(static_cast<const TA *>(a.dv) + ((size_t)start + (size_t)n * C) * vstep + h * p.dv, cnt, vstep, p.dv);
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
-            const f4 eg = *reinterpret_cast<const f4 *>(s_eg + 16 * m + 4 * j);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = 16 * m + 4 * j + i;
-                if (t < cnt && col < p.dv)
-                    static_cast<TA *>(a.dv)[((size_t)(t0 + t) * p.HV + h) * p.dv + col] = from_f32<TA>(D[m][i]);
-            }
-            dO[m] *= eg;
-            D[m] *= -eg;
+            store4(dvrows, vat.down(16 * m, vstep), quad_transpose(D[m]));
+            dO[m] *= *reinterpret_cast<const f4 *>(s_q + 16 * m + 4 * j);
+            D[m] *= *reinterpret_cast<const f4 *>(s_k + 16 * m + 4 * j);
         }
+        const float gamma = s_gamma;
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) dS[kb] *= gamma;
-        state_update<DK>(dS, Qh, dO, c, j);
-        if constexpr (RETR) state_update<DK>(dS, Kh, D, c, j);
+        state_update<DK, NP>(dS, Qr, dO);
+        if constexpr (RETR) state_update<DK, NP>(dS, Kr, D);
     }
-    if (a.d_init && on && col < p.dv) {
+    if (a.d_init) {
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) store4(a.d_init + srow, 16 * kb + 4 * j, p.dk, vec, dS[kb]);
+        for (int kb = 0; kb < KB; ++kb)
+            store4(ChunkRows(a.d_init + (size_t)bh * p.dv * p.dk, p.dv, p.dk, p.dk), At4<VEC, float>(col, p.dk, 16 * kb + 4 * j, p.dk), dS[kb]);
     }
 }
 
 // ---------------------------------------------------------------- gradients of a chunk
 // One workgroup (8 waves) per (chunk, q/k head), the value heads that share it
-// in turn, dQ and dK summed over them in the accumulators.  Wave (tb, part)
-// owns the 16 tokens of block tb as accumulator columns and 1/PARTS of the key
-// channels as rows; of the chunk x chunk products it forms SBW column blocks.
-template <int DK, typename TA, bool RETR>
+// in turn, dQ and dK summed over them in the accumulators.  A wave owns KW
+// blocks of 16 key channels (accumulator rows) of TW blocks of 16 tokens
+// (columns): the states' operands, which it alone uses, go from memory to its
+// registers, those over tokens (d_o, Y, E) through LDS, cut into planes once
+// for all waves, 32 state rows a step, double buffered.  Of the chunk x chunk
+// products wave (ft, part) forms column blocks part * SBW .. of row block ft.
+template <int DK, typename TA, bool RETR, bool VEC>
 __global__ __launch_bounds__(512, 2) void k_back_grad(const BackParams a)
 {
     using G = Geo<DK>;
-    constexpr int C = G::C, MB = G::MB, KB = G::KB, LD = G::LD, LC = G::LC;
-    constexpr int PARTS = 8 / MB, KBW = KB / PARTS, SBW = (MB + PARTS - 1) / PARTS;
-    __shared__ __align__(16) float Kh[C * LD], Qh[C * LD], Fe[C * LC], Wm[C * LC];
-    __shared__ __align__(16) float s_sc[5 * C];
-    __shared__ float s_u[PARTS][C], s_w[PARTS][C], s_db[C], s_row[C][MB], s_col[MB][C], s_dot[8];
+    constexpr int C = G::C, MB = G::MB, MX = G::MX, KB = G::KB, KX = G::KX, ACT = G::ACT, NT = G::NT, NP = planes_of<TA>;
+    constexpr int KW = DK == 256 ? 2 : 1, TW = KB * MB / 8 / KW, SPAN = MB / TW, KWAVES = 8 / SPAN;
+    constexpr int PARTS = 8 / MB, SBW = (MB + PARTS - 1) / PARTS;
+    constexpr int NB = NP + 3 + (RETR ? 3 : 0);  // planes of a token block: d_o, E, Y
+    constexpr int SETS = RETR ? 4 : 2;           // chunk x chunk operands: F by rows and columns, W likewise
+    constexpr int IN = NB * MB * BLOCK, TRI_SET = 3 * NT * BLOCK;
+    // the token blocks' planes, two steps of them, and then the chunk x chunk operands
+    __shared__ __align__(16) uint16_t s_mem[2 * IN > SETS * TRI_SET ? 2 * IN : SETS * TRI_SET];
+    __shared__ __align__(16) float s_sc[BACK_SC * C];
+    __shared__ float s_u[KWAVES][C], s_w[KWAVES][C], s_db[C], s_row[C][MB], s_col[MB][C], s_dot[KWAVES];
+    // each thread's q and k elements: in registers they would push the accumulators
+    // into scratch memory; fp32 rows do not fit beside the rest
+    constexpr bool PARK = sizeof(TA) == 2;
+    __shared__ Raw4<TA> s_qk[PARK ? 2 * KW * TW : 1][PARK ? 512 : 1];
+    __shared__ f4 s_gram[RETR ? 2 : 1][SBW][512];  // each thread's elements of its tiles of K Q^T and K K^T
 
     const Params &p = a.p;
     const int ci = blockIdx.x / p.H, hq = blockIdx.x % p.H;
@@ -689,149 +1034,293 @@ __global__ __launch_bounds__(512, 2) void k_back_grad(const BackParams a)
     int64_t t0;
     int cnt;
     chunk_tokens(a, ci, C, t0, cnt);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, j = lane >> 4;
-    const int tb = wave / PARTS, part = wave % PARTS, kb0 = part * KBW;
-    const int t = 16 * tb + c;
-    const bool live = t < cnt, veck = p.dk % 4 == 0, vecv = p.dv % 4 == 0;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), c = lane & 15, j = lane >> 4;
+    const int kw = wave / SPAN, kb0 = kw * KW, tb0 = wave % SPAN * TW;
+    const int ft = wave / PARTS, part = wave % PARTS;
     const int R = p.HV / p.H;
-    {
-        const float *sc = a.sc + ((size_t)ci * p.HV + (size_t)hq * R) * (BACK_SC * C);
-        Stage<DK, TA, 512> k, q;
-        k.load(static_cast<const TA *>(p.k), sc + SC_RK * C, t0, cnt, p.H, hq, p.dk, veck);
-        q.load(static_cast<const TA *>(p.q), sc + SC_RQ * C, t0, cnt, p.H, hq, p.dk, veck);
-        k.store(Kh);
-        q.store(Qh);
-    }
-    __syncthreads();
     const f4 zero = {0.f, 0.f, 0.f, 0.f};
-    // tiles of (K Q^T, K K^T): rows s of block sb, columns t
-    f4 qk[SBW], kk[SBW];
-    bool use[SBW];
+    const uint16_t *act = a.act + (size_t)blockIdx.x * 2 * NP * ACT * BLOCK;
+
+    const size_t first = ((size_t)t0 * p.H + hq) * p.dk;  // the chunk's first element of q and k
+    // q and k of the wave's channels and tokens
+    Raw4<TA> qr[PARK ? 1 : KW][PARK ? 1 : TW], kr[PARK ? 1 : KW][PARK ? 1 : TW];
+    const int kstep = p.H * p.dk, vstep = p.HV * p.dv;
+    const ChunkRows qrows(static_cast<const TA *>(p.q) + first, cnt, kstep, p.dk), krows(static_cast<const TA *>(p.k) + first, cnt, kstep, p.dk);
 #pragma unroll
-    for (int x = 0; x < SBW; ++x) {
-        const int sb = part * SBW + x;
-        use[x] = sb <= tb;
-        qk[x] = kk[x] = zero;
-        if (use[x]) {
-#pragma unroll 4
-            for (int kb = 0; kb < KB; ++kb) {
-                const f4 s = *reinterpret_cast<const f4 *>(Kh + (16 * sb + c) * LD + 16 * kb + 4 * j);
-                qk[x] = mfma4(s, *reinterpret_cast<const f4 *>(Qh + t * LD + 16 * kb + 4 * j), qk[x]);
-                if (RETR) kk[x] = mfma4(s, *reinterpret_cast<const f4 *>(Kh + t * LD + 16 * kb + 4 * j), kk[x]);
+    for (int x = 0; x < KW; ++x) {
+#pragma unroll
+        for (int w = 0; w < TW; ++w) {
+            const At4<VEC, TA> at(16 * (tb0 + w) + c, kstep, 16 * (kb0 + x) + 4 * j, p.dk);
+            if constexpr (PARK) {
+                s_qk[x * TW + w][tid] = load_raw4(qrows, at);
+                s_qk[(KW + x) * TW + w][tid] = load_raw4(krows, at);
+            } else {
+                qr[x][w] = load_raw4(qrows, at);
+                kr[x][w] = load_raw4(krows, at);
             }
         }
     }
-    f4 dq[KBW], dk[KBW];
+    auto q_of = [&](int x, int w) {
+        if constexpr (PARK) return widen(s_qk[x * TW + w][tid]);
+        else return widen(qr[x][w]);
+    };
+    auto k_of = [&](int x, int w) {
+        if constexpr (PARK) return widen(s_qk[(KW + x) * TW + w][tid]);
+        else return widen(kr[x][w]);
+    };
+    // tiles of (K Q^T, K K^T), rows s of block sb, columns t of block ft, of the normalised rows
+    bool use[SBW];
+    {
+        const float *sc = a.sc + ((size_t)ci * p.HV + (size_t)hq * R) * (BACK_SC * C);
+        const int t = 16 * ft + c;
+        auto operand = [&](const ChunkRows &rows, int block, int y, b8 (&out)[NP]) {
+            const int lo = 32 * y + 4 * j;
+            split8<NP>(widen(load_raw4(rows, At4<VEC, TA>(16 * block + c, kstep, lo, p.dk))),
+                       widen(load_raw4(rows, At4<VEC, TA>(16 * block + c, kstep, lo + 16, p.dk))), out);
+        };
 #pragma unroll
-    for (int kb = 0; kb < KBW; ++kb) dq[kb] = dk[kb] = zero;
+        for (int x = 0; x < SBW; ++x) {
+            const int sb = part * SBW + x;
+            use[x] = sb <= ft;
+            if (use[x]) {
+                f4 qk = zero, kk = zero;
+                for (int y = 0; y < KX; ++y) {
+                    b8 s[NP], q[NP], k[NP];
+                    operand(krows, sb, y, s);
+                    operand(qrows, ft, y, q);
+                    qk = mm(s, q, qk);
+                    if (RETR) {
+                        operand(krows, ft, y, k);
+                        kk = mm(s, k, kk);
+                    }
+                }
+                const float rq = sc[SC_RQ * C + t], rk = sc[SC_RK * C + t];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float rs = sc[SC_RK * C + 16 * sb + 4 * j + i];
+                    qk[i] *= rs * rq;
+                    kk[i] *= rs * rk;
+                }
+                s_gram[0][x][tid] = qk;
+                if (RETR) s_gram[1][x][tid] = kk;
+            }
+        }
+    }
+    f4 dq[KW][TW], dk[KW][TW];
+#pragma unroll
+    for (int x = 0; x < KW; ++x)
+#pragma unroll
+        for (int w = 0; w < TW; ++w) dq[x][w] = dk[x][w] = zero;
 
+    // What a step over 32 state rows takes from memory, loaded two steps ahead:
+    // the wave's blocks of S0 and dS1, and the token block that it cuts into
+    // planes for all waves (E: waves 0 .., Y: waves 4 .., d_o: waves o_blk).
+    const int VX = a.VB / 2;
+    const int y_blk = wave - 4, o_blk = MB == 4 ? wave : wave - 2;
+    const bool is_e = wave < MB, is_y = RETR && y_blk >= 0 && y_blk < MB, is_o = o_blk >= 0 && o_blk < MB;
+    const int z_blk = is_e ? wave : is_y ? y_blk : 0;
+    struct In {
+        f4 z[2], s[KW][2], d[KW][2];
+        Raw4<TA> o[2];
+    } ahead[2];
+    auto fetch = [&](In &f, int r, int vx) {
+        const int h = hq * R + r;
+        const size_t rec = (size_t)ci * p.HV + h;
+        const float *Sp = a.s + (rec * KB + kb0) * a.VB * FRAG, *Dp = a.ds + (rec * KB + kb0) * a.VB * FRAG;
+        const float *Zp = (is_y ? a.y : a.e) + (rec * MB + z_blk) * a.VB * FRAG;
+        const ChunkRows orows(static_cast<const TA *>(a.d_o) + ((size_t)t0 * p.HV + h) * p.dv, cnt, vstep, p.dv);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int vb = 2 * vx + n;
+            f.z[n] = get_frag(Zp + (size_t)vb * FRAG);
+            f.o[n] = load_raw4(orows, At4<VEC, TA>(16 * (is_o ? o_blk : 0) + c, vstep, 16 * vb + 4 * j, p.dv));
+#pragma unroll
+            for (int x = 0; x < KW; ++x) {
+                f.s[x][n] = get_frag(Sp + ((size_t)x * a.VB + vb) * FRAG);
+                f.d[x][n] = get_frag(Dp + ((size_t)x * a.VB + vb) * FRAG);
+            }
+        }
+    };
+    // block m's planes: d_o at [0, NP), E at [NP, NP + 3), Y after
+    auto stage = [&](const In &f, uint16_t *dst) {
+        if (is_e || is_y) {
+            b8 v[3];
+            uint16_t *at = dst + (size_t)(z_blk * NB + NP + (is_y ? 3 : 0)) * BLOCK;
+            split8<3>(f.z[0], f.z[1], v);
+#pragma unroll
+            for (int n = 0; n < 3; ++n) put_block(at + n * BLOCK, v[n]);
+        }
+        if (is_o) {
+            b8 v[NP];
+            split8<NP>(widen(f.o[0]), widen(f.o[1]), v);
+#pragma unroll
+            for (int n = 0; n < NP; ++n) put_block(dst + (size_t)(o_blk * NB + n) * BLOCK, v[n]);
+        }
+    };
+    // The loads stand under no condition: past the last step of the last head
+    // the last step is loaded again (a load that may not have been issued
+    // would make the wait for the one before it a wait for all).
+    float sc_next;  // a thread's word of the chunk's scalars, a head ahead
+    auto fetch_scalars = [&](int r) {
+        const int n = tid < BACK_SC * C ? tid : 0;
+        sc_next = a.sc[((size_t)ci * p.HV + (size_t)hq * R + r) * (BACK_SC * C) + n];
+    };
+    fetch_scalars(0);
+    fetch(ahead[0], 0, 0);
+    fetch(ahead[1], 0, 1);
     for (int r = 0; r < R; ++r) {
         const int h = hq * R + r;
         const size_t rec = (size_t)ci * p.HV + h;
-        for (int n = tid; n < 5 * C; n += 512) s_sc[n] = a.sc[rec * (BACK_SC * C) + n];
-        __syncthreads();
-        const float *s_b = s_sc + SC_B * C, *s_gh = s_sc + SC_GH * C, *s_gl = s_sc + SC_GL * C;
-        const float eg = s_sc[SC_EG * C + t], kd = s_sc[SC_KD * C + t], bt = s_b[t];
+        static_assert(BACK_SC * C <= 512, "a word a thread");
+        arrive(sc_next);
+        if (tid < BACK_SC * C) s_sc[tid] = sc_next;
+        fetch_scalars(min(r + 1, R - 1));
+        const float *s_eg = s_sc + SC_EG * C, *s_kd = s_sc + SC_KD * C, *s_b = s_sc + SC_B * C, *s_gh = s_sc + SC_GH * C,
+                    *s_gl = s_sc + SC_GL * C, *s_rq = s_sc + SC_RQ * C, *s_rk = s_sc + SC_RK * C;
 
-        // products over the state rows
-        f4 A1[KBW], A2[KBW], A3[KBW], F[SBW], X[SBW];
+        // ---- products over the state rows
+        f4 A1[KW][TW], A2[KW][TW], A3[KW][TW], F[SBW], X[SBW];
 #pragma unroll
-        for (int kb = 0; kb < KBW; ++kb) A1[kb] = A2[kb] = A3[kb] = zero;
+        for (int x = 0; x < KW; ++x)
+#pragma unroll
+            for (int w = 0; w < TW; ++w) A1[x][w] = A2[x][w] = A3[x][w] = zero;
 #pragma unroll
         for (int x = 0; x < SBW; ++x) F[x] = X[x] = zero;
-        float db = 0.f, dot = 0.f;
-        const TA *orow = static_cast<const TA *>(a.d_o) + ((size_t)(t0 + t) * p.HV + h) * p.dv;
-        const float *Sp = a.s + rec * KB * a.VB * FRAG, *Dp = a.ds + rec * KB * a.VB * FRAG;
-        const float *Ep = a.e + rec * MB * a.VB * FRAG, *Yp = RETR ? a.y + rec * MB * a.VB * FRAG : nullptr;
-        for (int vb = 0; vb < a.VB; ++vb) {
-            const f4 o = live ? widen(load_raw4(orow, 16 * vb + 4 * j, p.dv, vecv)) : zero;
-            const f4 e = get_frag(Ep + ((size_t)tb * a.VB + vb) * FRAG);
-            const f4 y = RETR ? get_frag(Yp + ((size_t)tb * a.VB + vb) * FRAG) : zero;
-            f4 s[KBW], d[KBW];
+        float dot = 0.f;
+        auto step = [&](In &f, int vx) {
+            uint16_t *in = s_mem + (vx & 1) * IN;
+            arrive(f);
+            stage(f, in);
+            b8 sp[KW][3], dp[KW][3];
 #pragma unroll
-            for (int kb = 0; kb < KBW; ++kb) {
-                s[kb] = get_frag(Sp + ((size_t)(kb0 + kb) * a.VB + vb) * FRAG);
-                d[kb] = get_frag(Dp + ((size_t)(kb0 + kb) * a.VB + vb) * FRAG);
+            for (int x = 0; x < KW; ++x) {
+                if (tb0 == 0) dot += dot4(f.s[x][0], f.d[x][0]) + dot4(f.s[x][1], f.d[x][1]);
+                split8<3>(f.s[x][0], f.s[x][1], sp[x]);
+                split8<3>(f.d[x][0], f.d[x][1], dp[x]);
+            }
+            const bool wrap = vx + 2 >= VX;
+            fetch(f, wrap ? min(r + 1, R - 1) : r, wrap ? vx + 2 - VX : vx + 2);
+            lds_barrier();  // one a step: the other buffer's readers have passed the last one
+#pragma unroll
+            for (int w = 0; w < TW; ++w) {
+                __builtin_amdgcn_sched_barrier(0);  // one block's operands in registers at a time
+                const uint16_t *at = in + (size_t)(tb0 + w) * NB * BLOCK;
+                b8 ob[NP], eb[3], yb[3];
+#pragma unroll
+                for (int n = 0; n < NP; ++n) ob[n] = get_block(at + n * BLOCK);
+#pragma unroll
+                for (int n = 0; n < 3; ++n) {
+                    eb[n] = get_block(at + (NP + n) * BLOCK);
+                    if (RETR) yb[n] = get_block(at + (NP + 3 + n) * BLOCK);
+                }
+#pragma unroll
+                for (int x = 0; x < KW; ++x) {
+#pragma unroll
+                    for (int n = 2; n >= 0; --n)
+#pragma unroll
+                        for (int i = 0; i <= n; ++i) {  // three accumulators side by side
+                            if (n - i < NP) A1[x][w] = mfma(sp[x][i], ob[n - i], A1[x][w]);
+                            A3[x][w] = mfma(dp[x][i], eb[n - i], A3[x][w]);
+                            if (RETR) A2[x][w] = mfma(sp[x][i], yb[n - i], A2[x][w]);
+                        }
+                }
             }
 #pragma unroll
             for (int x = 0; x < SBW; ++x)
                 if (use[x]) {
-                    const f4 es = get_frag(Ep + ((size_t)(part * SBW + x) * a.VB + vb) * FRAG);
-                    F[x] = mfma4(es, o, F[x]);
-                    if (RETR) X[x] = mfma4(es, y, X[x]);
+                    const uint16_t *rs = in + (size_t)((part * SBW + x) * NB + NP) * BLOCK, *ct = in + (size_t)ft * NB * BLOCK;
+                    b8 es[3], ob[NP], yb[3];
+#pragma unroll
+                    for (int n = 0; n < 3; ++n) es[n] = get_block(rs + n * BLOCK);
+#pragma unroll
+                    for (int n = 0; n < NP; ++n) ob[n] = get_block(ct + n * BLOCK);
+                    F[x] = mm(es, ob, F[x]);
+                    if (RETR) {
+#pragma unroll
+                        for (int n = 0; n < 3; ++n) yb[n] = get_block(ct + (NP + 3 + n) * BLOCK);
+                        X[x] = mm(es, yb, X[x]);
+                    }
                 }
-            if (RETR) db += dot4(y, e);
-            const f4 bd = RETR ? e * bt : e;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int kb = 0; kb < KBW; ++kb) {
-                    A1[kb] = mfma1(s[kb][i], o[i], A1[kb]);
-                    A3[kb] = mfma1(d[kb][i], bd[i], A3[kb]);
-                    if (RETR) A2[kb] = mfma1(s[kb][i], y[i], A2[kb]);
-                }
-            if (tb == 0)
-#pragma unroll
-                for (int kb = 0; kb < KBW; ++kb) dot += dot4(s[kb], d[kb]);
+        };
+        for (int vx = 0; vx < VX; vx += 2) {
+            step(ahead[0], vx);
+            step(ahead[1], vx + 1);
         }
 
-        // per token: what crosses the token from the state
-        float u = 0.f, w = 0.f;
+        // ---- per token: what crosses the token from the state
 #pragma unroll
-        for (int kb = 0; kb < KBW; ++kb) {
-            const f4 qh = *reinterpret_cast<const f4 *>(Qh + t * LD + 16 * (kb0 + kb) + 4 * j);
-            const f4 kh = *reinterpret_cast<const f4 *>(Kh + t * LD + 16 * (kb0 + kb) + 4 * j);
-            A1[kb] *= eg;
-            A3[kb] *= kd;
-            w += dot4(qh, A1[kb]);
-            u += dot4(kh, A3[kb]);
-            dq[kb] += A1[kb];
-            dk[kb] += A3[kb];
-            if (RETR) {
-                A2[kb] *= -bt * eg;
-                w += dot4(kh, A2[kb]);
-                dk[kb] += A2[kb];
+        for (int w = 0; w < TW; ++w) {
+            const int t = 16 * (tb0 + w) + c;
+            const float eg = s_eg[t], kd = s_kd[t] * s_b[t], be = -s_b[t] * eg;
+            float u = 0.f, v = 0.f;
+#pragma unroll
+            for (int x = 0; x < KW; ++x) {
+                const f4 qh = q_of(x, w) * s_rq[t], kh = k_of(x, w) * s_rk[t];
+                A1[x][w] *= eg;
+                A3[x][w] *= kd;
+                v += dot4(qh, A1[x][w]);
+                u += dot4(kh, A3[x][w]);
+                dq[x][w] += A1[x][w];
+                dk[x][w] += A3[x][w];
+                if (RETR) {
+                    A2[x][w] *= be;
+                    v += dot4(kh, A2[x][w]);
+                    dk[x][w] += A2[x][w];
+                }
+            }
+            u = sum_j(u);
+            v = sum_j(v);
+            if (j == 0) {
+                s_u[kw][t] = u;
+                s_w[kw][t] = v;
             }
         }
-        u = sum_j(u);
-        w = sum_j(w);
-        db = sum_j(db);
-        if (j == 0) {
-            s_u[part][t] = u;
-            s_w[part][t] = w;
-            if (part == 0) s_db[t] = db;
-        }
-        if (tb == 0) {
+        if (tb0 == 0) {
 #pragma unroll
-            for (int o = 1; o < 64; o <<= 1) dot += __shfl_xor(dot, o);
-            if (lane == 0) s_dot[part] = dot;
+            for (int n = 1; n < 64; n <<= 1) dot += __shfl_xor(dot, n);
+            if (lane == 0) s_dot[kw] = dot;
         }
 
-        // the chunk x chunk tiles: factors, and M's part of dg
+        lds_barrier();  // the last step's operands give way to the tiles'
+        // ---- the chunk x chunk tiles: factors, M's part of dg, operands by rows and by columns
 #pragma unroll
         for (int x = 0; x < SBW; ++x)
             if (use[x]) {
-                const int s0 = 16 * (part * SBW + x) + 4 * j;
-                const float gh = s_gh[t], gl = s_gl[t];
+                const int sb = part * SBW + x, s0 = 16 * sb + 4 * j, t = 16 * ft + c;
+                const float gh = s_gh[t], gl = s_gl[t], bt = s_b[t];
+                const f4 rks = *reinterpret_cast<const f4 *>(s_rk + s0);
+                const f4 qk = s_gram[0][x][tid], kk = RETR ? s_gram[1][x][tid] : zero;
                 f4 f, wv = zero, M;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int s = s0 + i;
-                    const float e = s <= t ? exp_split(gh - s_gh[s], gl - s_gl[s]) * (RETR ? s_b[s] : 1.f) : 0.f;
-                    f[i] = F[x][i] * e;
-                    M[i] = s < t ? f[i] * qk[x][i] : 0.f;
+                    const int n = s0 + i;
+                    const float ex = n <= t ? exp_split(gh - s_gh[n], gl - s_gl[n]) * s_b[n] : 0.f;
+                    f[i] = F[x][i] * ex;
+                    M[i] = n < t ? f[i] * qk[i] : 0.f;
                     if (RETR) {
-                        wv[i] = s < t ? bt * e * X[x][i] : 0.f;
-                        M[i] -= wv[i] * kk[x][i];
+                        wv[i] = n < t ? -bt * ex * X[x][i] : 0.f;
+                        M[i] += wv[i] * kk[i];
+                        if (n == t) s_db[t] = X[x][i];  // Y_t . E_t
                     }
                 }
-                *reinterpret_cast<f4 *>(Fe + t * LC + s0) = f;
-                if (RETR) *reinterpret_cast<f4 *>(Wm + t * LC + s0) = wv;
+                constexpr size_t STRIDE = (size_t)NT * BLOCK;
+                const int lo = lower_block<MB>(ft, sb / 2) * BLOCK, up = upper_block<MB>(sb, ft / 2) * BLOCK;
+                put_half(s_mem + lo, STRIDE, lane, sb & 1, f * rks);
+                put_half(s_mem + TRI_SET + up, STRIDE, quad_lane(), ft & 1, quad_transpose(f * s_rq[t]));
+                if (RETR) {
+                    put_half(s_mem + (SETS - 2) * TRI_SET + lo, STRIDE, lane, sb & 1, wv * rks);
+                    put_half(s_mem + (SETS - 1) * TRI_SET + up, STRIDE, quad_lane(), ft & 1, quad_transpose(wv * s_rk[t]));
+                }
+                if (sb == ft) {  // the half of a diagonal block pair that lies outside the triangle
+#pragma unroll
+                    for (int n = 0; n < SETS; ++n)
+                        if ((n & 1) == (sb & 1)) put_half(s_mem + n * TRI_SET + (n & 1 ? up : lo), STRIDE, lane, n & 1 ? 0 : 1, zero);
+                }
                 // sums over the columns before each one, within the tile's row t ...
                 const float four = (M[0] + M[1]) + (M[2] + M[3]);
                 const float a1 = __shfl_up(four, 16), a2 = __shfl_up(four, 32), a3 = __shfl_up(four, 48);
                 float pre = (j > 0 ? a1 : 0.f) + (j > 1 ? a2 : 0.f) + (j > 2 ? a3 : 0.f);
-                if (j == 3) s_row[t][part * SBW + x] = pre + four;
+                if (j == 3) s_row[t][sb] = pre + four;
                 // ... then over the rows t >= s
                 f4 sum;
 #pragma unroll
@@ -841,177 +1330,228 @@ __global__ __launch_bounds__(512, 2) void k_back_grad(const BackParams a)
                 }
                 if (c == 0)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) s_col[tb][s0 + i] = sum[i];
+                    for (int i = 0; i < 4; ++i) s_col[ft][s0 + i] = sum[i];
             }
         __syncthreads();
 
-        // products over the chunk's tokens
+        // ---- products over the chunk's tokens
 #pragma unroll
-        for (int sb = 0; sb < MB; ++sb) {
-            if (sb <= tb) {  // row t: columns s <= t
-                const f4 f = *reinterpret_cast<const f4 *>(Fe + t * LC + 16 * sb + 4 * j);
-                const f4 wv = RETR ? *reinterpret_cast<const f4 *>(Wm + t * LC + 16 * sb + 4 * j) : zero;
+        for (int yy = 0; yy < MX; ++yy) {
+            b8 kt[KW][NP], qt[KW][NP];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+            for (int x = 0; x < KW; ++x)
 #pragma unroll
-                    for (int kb = 0; kb < KBW; ++kb) {
-                        const float x = Kh[(16 * sb + 4 * j + i) * LD + 16 * (kb0 + kb) + c];
-                        dq[kb] = mfma1(x, f[i], dq[kb]);
-                        if (RETR) dk[kb] = mfma1(x, -wv[i], dk[kb]);
+                for (int n = 0; n < NP; ++n) {
+                    kt[x][n] = get_block(act + (size_t)(n * ACT + (kb0 + x) * MX + yy) * BLOCK);
+                    qt[x][n] = get_block(act + (size_t)((NP + n) * ACT + (kb0 + x) * MX + yy) * BLOCK);
+                }
+#pragma unroll
+            for (int w = 0; w < TW; ++w) {
+                const int tb = tb0 + w;
+                b8 v[3];
+                auto get = [&](int set, int blk) {
+#pragma unroll
+                    for (int n = 0; n < 3; ++n) v[n] = get_block(s_mem + set * TRI_SET + (n * NT + blk) * BLOCK);
+                };
+                if (2 * yy <= tb) {  // row t: columns s <= t
+                    const int blk = lower_block<MB>(tb, yy);
+                    get(0, blk);
+#pragma unroll
+                    for (int x = 0; x < KW; ++x) dq[x][w] = mm(kt[x], v, dq[x][w]);
+                    if (RETR) {
+                        get(SETS - 2, blk);
+#pragma unroll
+                        for (int x = 0; x < KW; ++x) dk[x][w] = mm(kt[x], v, dk[x][w]);
                     }
-            }
-            if (sb >= tb) {  // column t: rows >= t
+                }
+                if (2 * yy + 1 >= tb) {  // column t: rows >= t
+                    const int blk = upper_block<MB>(tb, yy);
+                    get(1, blk);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = 16 * sb + 4 * j + i;
-                    const float f = Fe[row * LC + t], wv = RETR ? -Wm[row * LC + t] : 0.f;
+                    for (int x = 0; x < KW; ++x) dk[x][w] = mm(qt[x], v, dk[x][w]);
+                    if (RETR) {
+                        get(SETS - 1, blk);
 #pragma unroll
-                    for (int kb = 0; kb < KBW; ++kb) {
-                        dk[kb] = mfma1(Qh[row * LD + 16 * (kb0 + kb) + c], f, dk[kb]);
-                        if (RETR) dk[kb] = mfma1(Kh[row * LD + 16 * (kb0 + kb) + c], wv, dk[kb]);
+                        for (int x = 0; x < KW; ++x) dk[x][w] = mm(kt[x], v, dk[x][w]);
                     }
                 }
             }
         }
 
-        // wave 0, a lane a token: dg and db
-        if (wave == 0) {
-            const int s = lane < C ? lane : C - 1;
-            const bool mine = lane < C;
-            float us = 0.f, ws = 0.f;
+        // ---- what k_back_gate joins to dg and db, a row of the record a wave
+        if (lane < C) {
+            float x = 0.f;
+            if (wave == GX_U || wave == GX_W) {
 #pragma unroll
-            for (int n = 0; n < PARTS; ++n) {
-                us += s_u[n][s];
-                ws += s_w[n][s];
+                for (int n = 0; n < KWAVES; ++n) x += wave == GX_U ? s_u[n][lane] : s_w[n][lane];
+            } else if (wave == GX_DB) {
+                x = RETR ? s_db[lane] : 0.f;
+            } else if (wave == GX_COL) {
+#pragma unroll
+                for (int m = 0; m < MB; ++m) x += m >= lane / 16 ? s_col[m][lane] : 0.f;
+            } else if (wave == GX_STATE) {
+#pragma unroll
+                for (int n = 0; n < KWAVES; ++n) x += s_dot[n];
+                x *= s_eg[C - 1];
+            } else {  // columns of the blocks before block wave - GX_ROW + 1
+#pragma unroll
+                for (int m = 0; m < MB - 1; ++m) x += m <= wave - GX_ROW && m <= lane / 16 ? s_row[lane][m] : 0.f;
             }
-            us = mine ? us : 0.f;
-            ws = mine ? ws : 0.f;
-            float rows[MB];  // rows[m]: suffix sums over t of the sums over columns of blocks before m
-            rows[0] = 0.f;
-#pragma unroll
-            for (int m = 1; m < MB; ++m) rows[m] = rows[m - 1] + (mine && m - 1 <= lane / 16 ? s_row[s][m - 1] : 0.f);
-            float pre = us, suf = ws;
-#pragma unroll
-            for (int o = 1; o < 64; o <<= 1) {
-                const float x = __shfl_up(pre, o), y = __shfl_down(suf, o);
-                if (lane >= o) pre += x;
-                if (lane + o < 64) suf += y;
-#pragma unroll
-                for (int m = 1; m < MB; ++m) {
-                    const float z = __shfl_down(rows[m], o);
-                    if (lane + o < 64) rows[m] += z;
-                }
-            }
-            pre = __shfl_up(pre, 1);
-            float g = lane > 0 ? pre : 0.f;
-            g += suf;
-            const int blk = s / 16;
-#pragma unroll
-            for (int m = 0; m < MB; ++m) {
-                if (m == blk) g += rows[m];
-                if (m >= blk) g += s_col[m][s];
-            }
-            float d = 0.f;
-#pragma unroll
-            for (int n = 0; n < PARTS; ++n) d += s_dot[n];
-            g += s_sc[SC_EG * C + C - 1] * d;
-            float da = 0.f, ds = 0.f;  // raw-gate arm: d of the projection (and of the bias), d of the scale
-            if (lane < cnt) {
-                const size_t th = (size_t)(t0 + lane) * p.HV + h;
-                if (a.decays) {
-                    if (p.gate_qwen) {
-                        const float x = load_gate(p, th) + p.dt_bias[h];
-                        da = g * gate_scale(p, h) * sigmoid_f32(x);
-                        ds = g * softplus_f32(x);
-                        g = da;
-                    }
-                    if (p.gate_dt == 1) static_cast<half_t *>(a.d_gate)[th] = from_f32<half_t>(g);
-                    else if (p.gate_dt == 2) static_cast<bf16_t *>(a.d_gate)[th] = from_f32<bf16_t>(g);
-                    else static_cast<float *>(a.d_gate)[th] = g;
-                }
-                if (RETR) {
-                    const float rate = s_b[lane];
-                    a.d_beta[th] = p.beta_sigmoid ? s_db[lane] * rate * (1.f - rate) : s_db[lane];
-                }
-            }
-            if (p.gate_qwen) {
-#pragma unroll
-                for (int o = 1; o < 64; o <<= 1) {
-                    da += __shfl_xor(da, o);
-                    ds += __shfl_xor(ds, o);
-                }
-                if (lane == 0) {
-                    a.gate_sums[2 * rec] = da;
-                    a.gate_sums[2 * rec + 1] = ds;
-                }
-            }
+            a.gx[(rec * GX + wave) * C + lane] = x;
         }
         __syncthreads();
     }
 
     // through the L2 norm: d x = r (d x^ - x^ (x^ . d x^)), x^ = r x
-    float nq = 0.f, nk = 0.f;
-    const float *sc = a.sc + ((size_t)ci * p.HV + (size_t)hq * R) * (BACK_SC * C);
-    const float rq = sc[SC_RQ * C + t], rk = sc[SC_RK * C + t], inv = 1.f / p.scale;
+    const float *s_rq = s_sc + SC_RQ * C, *s_rk = s_sc + SC_RK * C;
+    const float inv = 1.f / p.scale;
     if (p.qk_l2_norm) {
 #pragma unroll
-        for (int kb = 0; kb < KBW; ++kb) {
-            nq += dot4(*reinterpret_cast<const f4 *>(Qh + t * LD + 16 * (kb0 + kb) + 4 * j), dq[kb]);
-            nk += dot4(*reinterpret_cast<const f4 *>(Kh + t * LD + 16 * (kb0 + kb) + 4 * j), dk[kb]);
-        }
-        nq = sum_j(nq);
-        nk = sum_j(nk);
-        if (j == 0) {
-            s_u[part][t] = nq;
-            s_w[part][t] = nk;
+        for (int w = 0; w < TW; ++w) {
+            float nq = 0.f, nk = 0.f;
+#pragma unroll
+            for (int x = 0; x < KW; ++x) {
+                nq += dot4(q_of(x, w), dq[x][w]);
+                nk += dot4(k_of(x, w), dk[x][w]);
+            }
+            nq = sum_j(nq);
+            nk = sum_j(nk);
+            if (j == 0) {
+                s_u[kw][16 * (tb0 + w) + c] = nq;
+                s_w[kw][16 * (tb0 + w) + c] = nk;
+            }
         }
         __syncthreads();
-        nq = nk = 0.f;
-#pragma unroll
-        for (int n = 0; n < PARTS; ++n) {
-            nq += s_u[n][t];
-            nk += s_w[n][t];
-        }
-        nq *= inv * inv;
     }
-    if (live) {
-        const size_t row = ((size_t)(t0 + t) * p.H + hq) * p.dk;
 #pragma unroll
-        for (int kb = 0; kb < KBW; ++kb) {
-            const int col = 16 * (kb0 + kb) + 4 * j;
-            f4 gq = dq[kb], gk = dk[kb];
-            if (p.qk_l2_norm) {
-                gq -= *reinterpret_cast<const f4 *>(Qh + t * LD + col) * nq;
-                gk -= *reinterpret_cast<const f4 *>(Kh + t * LD + col) * nk;
+    for (int w = 0; w < TW; ++w) {
+        const int t = 16 * (tb0 + w) + c;
+        const float rq = s_rq[t], rk = s_rk[t];
+        float nq = 0.f, nk = 0.f;
+        if (p.qk_l2_norm) {
+#pragma unroll
+            for (int n = 0; n < KWAVES; ++n) {
+                nq += s_u[n][t];
+                nk += s_w[n][t];
             }
-            store4(static_cast<TA *>(a.dq) + row, col, p.dk, veck, gq * rq);
-            store4(static_cast<TA *>(a.dk) + row, col, p.dk, veck, gk * rk);
+            nq *= rq * inv * rq * inv;  // rq holds the scale too
+            nk *= rk * rk;
+        }
+#pragma unroll
+        for (int x = 0; x < KW; ++x) {
+            const At4<VEC, TA> at(t, kstep, 16 * (kb0 + x) + 4 * j, p.dk);
+            f4 gq = dq[x][w], gk = dk[x][w];
+            if (p.qk_l2_norm) {
+                gq -= q_of(x, w) * nq;
+                gk -= k_of(x, w) * nk;
+            }
+            store4(ChunkRows(static_cast<const TA *>(a.dq) + first, cnt, kstep, p.dk), at, gq * rq);
+            store4(ChunkRows(static_cast<const TA *>(a.dk) + first, cnt, kstep, p.dk), at, gk * rk);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- dg and db
+// A wave per (chunk, value head), a lane a token:
+//   dg_s = e^Gamma <dS1, S0> + sum_{t<s} u_t + sum_{t>=s} w_t + sum_{t>=s>r} M_tr
+// the last from the sums over r of whole blocks before s's own (rows) and
+// within it (col); then the raw gate's and the rate's activation.
+template <int C, bool RETR>
+__global__ __launch_bounds__(256) void k_back_gate(const BackParams a)
+{
+    constexpr int MB = C / 16;
+    const Params &p = a.p;
+    const int64_t rec = (int64_t)blockIdx.x * 4 + uniform(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    const int ci = (int)(rec / p.HV), h = (int)(rec % p.HV);
+    if (ci >= a.off[p.B]) return;
+    int64_t t0;
+    int cnt;
+    chunk_tokens(a, ci, C, t0, cnt);
+    const float *x = a.gx + (size_t)rec * GX * C;
+    const int n0 = lane < C ? lane : C - 1;
+    const bool mine = lane < C;
+    const size_t th = (size_t)(t0 + (lane < cnt ? lane : cnt - 1)) * p.HV + h;
+    const float raw = a.decays && p.gate_qwen ? load_gate(p, th) + p.dt_bias[h] : 0.f;
+    const float rate = RETR ? a.sc[(size_t)rec * (BACK_SC * C) + SC_B * C + n0] : 0.f;
+    const float col = x[GX_COL * C + n0], state = x[GX_STATE * C], db = x[GX_DB * C + n0];
+    float pre = mine ? x[GX_U * C + n0] : 0.f, suf = mine ? x[GX_W * C + n0] : 0.f;
+    float rows[MB];
+    rows[0] = 0.f;
+#pragma unroll
+    for (int m = 1; m < MB; ++m) rows[m] = mine ? x[(GX_ROW + m - 1) * C + n0] : 0.f;
+#pragma unroll
+    for (int n = 1; n < 64; n <<= 1) {
+        const float v = __shfl_up(pre, n), w = __shfl_down(suf, n);
+        if (lane >= n) pre += v;
+        if (lane + n < 64) suf += w;
+#pragma unroll
+        for (int m = 1; m < MB; ++m) {
+            const float z = __shfl_down(rows[m], n);
+            if (lane + n < 64) rows[m] += z;
+        }
+    }
+    pre = __shfl_up(pre, 1);
+    float g = (lane > 0 ? pre : 0.f) + suf + col + state;
+#pragma unroll
+    for (int m = 1; m < MB; ++m) g += m == n0 / 16 ? rows[m] : 0.f;
+    float da = 0.f, ds = 0.f;  // raw-gate arm: d of the projection (and of the bias), d of the scale
+    if (lane < cnt) {
+        if (a.decays) {
+            if (p.gate_qwen) {
+                da = g * gate_scale(p, h) * sigmoid_f32(raw);
+                ds = g * softplus_f32(raw);
+                g = da;
+            }
+            if (p.gate_dt == 1) static_cast<half_t *>(a.d_gate)[th] = from_f32<half_t>(g);
+            else if (p.gate_dt == 2) static_cast<bf16_t *>(a.d_gate)[th] = from_f32<bf16_t>(g);
+            else static_cast<float *>(a.d_gate)[th] = g;
+        }
+        if (RETR) a.d_beta[th] = p.beta_sigmoid ? db * rate * (1.f - rate) : db;
+    }
+    if (a.decays && p.gate_qwen) {
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            da += __shfl_xor(da, o);
+            ds += __shfl_xor(ds, o);
+        }
+        if (lane == 0) {
+            a.gate_sums[2 * rec] = da;
+            a.gate_sums[2 * rec + 1] = ds;
         }
     }
 }
 
 // ---------------------------------------------------------------- launches
-template <int DK, typename TA, bool RETR>
+template <int DK, typename TA, bool RETR, bool VEC>
 hipError_t launch_back_typed(const BackParams &a, hipStream_t s)
 {
     const Params &p = a.p;
-    const unsigned per_chunk = (unsigned)a.chunks * p.H, chains = (unsigned)p.B * p.HV * ((a.VB + 3) / 4);
-    if (a.chunks > 0) {
-        hipLaunchKernelGGL((k_back_prep<DK, TA, RETR>), dim3(per_chunk), dim3(256), 0, s, a);
-        hipLaunchKernelGGL((k_back_states<DK, TA, RETR>), dim3(chains), dim3(256), 0, s, a);
-    }
-    hipLaunchKernelGGL((k_back_chain<DK, TA, RETR>), dim3(chains), dim3(256), 0, s, a);
-    if (a.chunks > 0) hipLaunchKernelGGL((k_back_grad<DK, TA, RETR>), dim3(per_chunk), dim3(512), 0, s, a);
+    const unsigned per_chunk = (unsigned)a.chunks * p.H, chains = (unsigned)p.B * p.HV * (a.VB / 4);
+    hipLaunchKernelGGL((k_back_prep<DK, TA, RETR, VEC>), dim3(per_chunk), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_back_states<DK, TA, RETR, VEC>), dim3(chains), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_back_chain<DK, TA, RETR, VEC>), dim3(chains), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_back_grad<DK, TA, RETR, VEC>), dim3(per_chunk), dim3(512), 0, s, a);
+    if (RETR || a.decays)
+        hipLaunchKernelGGL((k_back_gate<Geo<DK>::C, RETR>), dim3(((unsigned)a.chunks * p.HV + 3) / 4), dim3(256), 0, s, a);
     return hipGetLastError();
+}
+
+template <int DK, typename TA>
+hipError_t launch_back_dk(const BackParams &a, bool retrieves, hipStream_t s)
+{
+    const bool vec = a.p.dk % 4 == 0 && a.p.dv % 4 == 0;
+    if (retrieves) return vec ? launch_back_typed<DK, TA, true, true>(a, s) : launch_back_typed<DK, TA, true, false>(a, s);
+    return vec ? launch_back_typed<DK, TA, false, true>(a, s) : launch_back_typed<DK, TA, false, false>(a, s);
 }
 
 template <typename TA>
 hipError_t launch_back_act(const BackParams &a, bool retrieves, hipStream_t s)
 {
     const int dk = a.p.dk;
-    if (dk <= 64) return retrieves ? launch_back_typed<64, TA, true>(a, s) : launch_back_typed<64, TA, false>(a, s);
-    if (dk <= 128) return retrieves ? launch_back_typed<128, TA, true>(a, s) : launch_back_typed<128, TA, false>(a, s);
-    return retrieves ? launch_back_typed<256, TA, true>(a, s) : launch_back_typed<256, TA, false>(a, s);
+    return dk <= 64 ? launch_back_dk<64, TA>(a, retrieves, s)
+           : dk <= 128 ? launch_back_dk<128, TA>(a, retrieves, s)
+                       : launch_back_dk<256, TA>(a, retrieves, s);
 }
 
 }  // namespace

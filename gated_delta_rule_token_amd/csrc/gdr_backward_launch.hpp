@@ -13,10 +13,22 @@ namespace gdr {
 __host__ __device__ constexpr int back_chunk(int dk) { return dk > 128 ? 32 : 64; }
 __host__ __device__ constexpr int back_dk_tile(int dk) { return dk <= 64 ? 64 : dk <= 128 ? 128 : 256; }
 
+// 16 x 32 blocks of a triangular chunk x chunk operand
+__host__ __device__ constexpr int back_tri_blocks(int C) { return C == 64 ? 6 : 2; }
+
+// Waves a SIMD of the chains: two workgroups a CU where a chunk's rows leave
+// room for them in LDS, one (and twice the registers) where they do not.
+template <typename TA> constexpr int back_chain_waves(int dk) { return sizeof(TA) == 2 && dk <= 128 ? 2 : 1; }
+
 // Per (chunk, value head) scalars, a row of back_chunk floats each: e^G,
 // e^(Gamma - G), update rate, G as (hi, lo), and the factors of q (with the
 // scale) and k.
 enum BackScalar : int { SC_EG = 0, SC_KD, SC_B, SC_GH, SC_GL, SC_RQ, SC_RK, BACK_SC };
+
+// Rows (of back_chunk floats) of what k_back_grad leaves for dg and db, per
+// (chunk, value head): u, w, Y . E, M's sums within the column's own block,
+// the state's part, and M's sums over the column blocks before each block.
+enum BackGateRow : int { GX_U = 0, GX_W, GX_DB, GX_COL, GX_STATE, GX_ROW, GX = GX_ROW + 3 };
 
 struct BackParams {
     Params p;                   // q, k, v, gate, beta, requests, initial state
@@ -31,9 +43,12 @@ struct BackParams {
     // workspace
     int32_t *off;               // (B + 1) first chunk of each request; off[B] = chunks in use
     int32_t *tok;               // (B, 2) first token and length of each request
-    float *sc, *t1, *t2, *pt, *s, *ds, *e, *y;
+    uint16_t *act;              // per (chunk, q/k head): operand fragments of k^T, q^T
+    uint16_t *tri;              // per (chunk, value head): P^T, and with retrieval (I + diag(b) L)^-T, (I + L diag(b))^-1
+    float *sc, *s, *ds, *e, *y; // scalars; S0, dS1, E, Y as fp32 fragments
+    float *gx;                  // see BackGateRow
     int32_t chunks;             // chunk budget: ceil(T / C) + B
-    int32_t VB;                 // 16-row blocks of dv
+    int32_t VB;                 // 16-row blocks of dv, a multiple of 4
     int32_t decays;
 };
 
