@@ -378,7 +378,7 @@ size_t back_layout(const gdr_problem *p, gdr::BackParams &a, void *base)
 {
     const size_t C = gdr::back_chunk(p->head_dim_k), MB = C / 16, KB = gdr::back_dk_tile(p->head_dim_k) / 16;
     const size_t VB = (p->head_dim_v + 63) / 64 * 4, block = 256;  // words of a fragment block
-    const size_t tri = 3 * gdr::back_tri_blocks((int)C), planes = p->act_dtype == GDR_F32 ? 3 : p->act_dtype == GDR_F16 ? 2 : 1;
+    const size_t tri = 3 * gdr::back_tri_blocks((int)C);
     const size_t chunks = (p->total_tokens + C - 1) / C + p->batch, recs = chunks * p->num_heads_v;
     const bool retr = gdr::rule_retrieves(p->update_rule);
     a.chunks = (int32_t)chunks;
@@ -397,7 +397,8 @@ size_t back_layout(const gdr_problem *p, gdr::BackParams &a, void *base)
     a.gate_sums = p->gate_activation == GDR_GATE_QWEN ? floats(recs * 2) : nullptr;
     a.d_beta = p->beta_per_token ? floats((size_t)p->total_tokens * p->num_heads_v) : nullptr;
     const auto halves = [&](size_t n) { return static_cast<uint16_t *>(take(n)); };
-    a.act = halves(chunks * p->num_heads_qk * 2 * planes * (MB * KB / 2) * block);
+    a.where = static_cast<int32_t *>(take(chunks * 2));
+    a.act = p->act_dtype == GDR_F32 ? halves(chunks * p->num_heads_qk * 2 * 3 * (MB * KB / 2) * block) : nullptr;
     a.tri = halves(recs * (retr ? 3 : 1) * tri * block);
     a.s = floats(recs * KB * VB * block);
     a.ds = floats(recs * KB * VB * block);

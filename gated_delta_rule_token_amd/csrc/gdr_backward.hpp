@@ -94,6 +94,13 @@ template <int MB> __device__ __forceinline__ constexpr int upper_block(int m, in
 // A value that every lane of the wave has alike, in a scalar register.
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
+// A value that the compiler knows nothing of.
+__device__ __forceinline__ int opaque(int x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 __device__ __forceinline__ constexpr int tri(int m, int k) { return m * (m + 1) / 2 + k; }
 
 __device__ __forceinline__ f4 mfma1(float a, float b, f4 c)
@@ -334,7 +341,8 @@ __device__ __forceinline__ float sum_j(float x)
     return x;
 }
 
-// The request of chunk `ci`, its first token and how many of C tokens it has.
+// Chunk `ci`'s first token and how many of C tokens it has, by its request
+// (k_back_prep, which leaves them in a.where for the kernels after it).
 __device__ __forceinline__ void chunk_tokens(const BackParams &a, int ci, int C, int64_t &t0, int &cnt)
 {
     int lo = 0, hi = a.p.B - 1;  // largest b with off[b] <= ci (ci < off[B])
@@ -384,6 +392,32 @@ template <int DK> struct Rows {
     }
 };
 
+// The same rows as the 16-bit activations themselves, cut into planes as they are read.
+template <int DK, typename TA> struct RawRows {
+    static __device__ __forceinline__ void planes(const b8 (&raw)[1], b8 (&out)[planes_of<TA>])
+    {
+        if constexpr (planes_of<TA> == 1) {
+            out[0] = raw[0];
+        } else {
+            const u4 w = __builtin_bit_cast(u4, raw[0]);
+            split8<planes_of<TA>>(widen(__builtin_bit_cast(Raw4<TA>, u2{w[0], w[1]})),
+                                  widen(__builtin_bit_cast(Raw4<TA>, u2{w[2], w[3]})), out);
+        }
+    }
+    static __device__ __forceinline__ void row_operand(const uint16_t *rows, int row, int x, b8 (&out)[planes_of<TA>])
+    {
+        b8 raw[1];
+        Rows<DK>::row_operand(rows, row, x, raw);
+        planes(raw, out);
+    }
+    static __device__ __forceinline__ void col_operand(const uint16_t *rows, int kb, int y, b8 (&out)[planes_of<TA>])
+    {
+        b8 raw[1];
+        Rows<DK>::col_operand(rows, kb, y, raw);
+        planes(raw, out);
+    }
+};
+
 // A chunk's rows of q or k on their way from memory to LDS planes, four
 // elements at a time, in the registers of NT threads.
 template <int DK, typename TA, int NT, bool VEC> struct StageRows {
@@ -400,6 +434,15 @@ template <int DK, typename TA, int NT, bool VEC> struct StageRows {
         const ChunkRows rows(first, cnt, step, dk);
 #pragma unroll
         for (int n = 0; n < N; ++n) x[n] = load_raw4(rows, at.down(n * (NT / LPR), step));
+    }
+    // as they are (16-bit activations)
+    __device__ __forceinline__ void store_raw(uint16_t *rows) const
+    {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int g = threadIdx.x + NT * n;
+            *reinterpret_cast<u2 *>(rows + g / LPR * Rows<DK>::LD + g % LPR * 4) = __builtin_bit_cast(u2, x[n]);
+        }
     }
     __device__ __forceinline__ void store(uint16_t *rows) const
     {
@@ -418,8 +461,8 @@ template <int DK, typename TA, int NT, bool VEC> struct StageRows {
 
 // ---------------------------------------------------------------- prologue
 // One workgroup per (chunk, q/k head); the value heads that share the head in
-// turn.  It leaves k and q of the chunk as operand fragments with channels as
-// rows (KT, QT) for k_back_grad.  The products K K^T and Q K^T are formed once
+// turn.  Of fp32 rows it leaves k and q as operand fragments with channels as
+// rows (KT, QT) for k_back_grad, whose LDS has no room for them.  The products K K^T and Q K^T are formed once
 // for the value heads.  Each unit lower triangular inverse goes by 16x16
 // blocks on the fp32 matrix instruction: the diagonal ones by forward
 // substitution, a thread a column; then wave j takes block column j down,
@@ -445,6 +488,10 @@ __global__ __launch_bounds__(256) void k_back_prep(const BackParams a)
     chunk_tokens(a, ci, C, t0, cnt);
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), c = lane & 15, j = lane >> 4;
+    if (hq == 0 && tid == 0) {
+        a.where[2 * ci] = (int32_t)t0;
+        a.where[2 * ci + 1] = cnt;
+    }
     uint16_t *Kr = reinterpret_cast<uint16_t *>(mem), *Qr = Kr + NP * RW::PLANE;
 
     // rows of q and k, and the reciprocals of their norms
@@ -480,13 +527,15 @@ __global__ __launch_bounds__(256) void k_back_prep(const BackParams a)
     }
     __syncthreads();
 
-    uint16_t *act = a.act + (size_t)blockIdx.x * 2 * NP * ACT * BLOCK;
-    for (int n = wave; n < 2 * ACT; n += 4) {
-        const int kind = n / ACT, blk = n % ACT;
-        b8 v[NP];
-        RW::col_operand(kind == 0 ? Kr : Qr, blk / MX, blk % MX, v);
+    if constexpr (NP == 3) {
+        uint16_t *act = a.act + (size_t)blockIdx.x * 2 * NP * ACT * BLOCK;
+        for (int n = wave; n < 2 * ACT; n += 4) {
+            const int kind = n / ACT, blk = n % ACT;
+            b8 v[NP];
+            RW::col_operand(kind == 0 ? Kr : Qr, blk / MX, blk % MX, v);
 #pragma unroll
-        for (int q = 0; q < NP; ++q) put_block(act + (size_t)((kind * NP + q) * ACT + blk) * BLOCK, v[q]);
+            for (int q = 0; q < NP; ++q) put_block(act + (size_t)((kind * NP + q) * ACT + blk) * BLOCK, v[q]);
+        }
     }
 
     // lower triangle of Q K^T and K K^T, tile (m, kb): rows t of block m, columns s of block kb
@@ -1022,18 +1071,16 @@ __global__ __launch_bounds__(512, 2) void k_back_grad(const BackParams a)
     __shared__ __align__(16) uint16_t s_mem[2 * IN > SETS * TRI_SET ? 2 * IN : SETS * TRI_SET];
     __shared__ __align__(16) float s_sc[BACK_SC * C];
     __shared__ float s_u[KWAVES][C], s_w[KWAVES][C], s_db[C], s_row[C][MB], s_col[MB][C], s_dot[KWAVES];
-    // each thread's q and k elements: in registers they would push the accumulators
-    // into scratch memory; fp32 rows do not fit beside the rest
+    // the chunk's rows of k and q; fp32 rows do not fit beside the rest
     constexpr bool PARK = sizeof(TA) == 2;
-    __shared__ Raw4<TA> s_qk[PARK ? 2 * KW * TW : 1][PARK ? 512 : 1];
+    __shared__ __align__(16) uint16_t s_k[PARK ? Rows<DK>::PLANE : 8], s_q[PARK ? Rows<DK>::PLANE : 8];
     __shared__ f4 s_gram[RETR ? 2 : 1][SBW][512];  // each thread's elements of its tiles of K Q^T and K K^T
 
     const Params &p = a.p;
     const int ci = blockIdx.x / p.H, hq = blockIdx.x % p.H;
     if (ci >= a.off[p.B]) return;
-    int64_t t0;
-    int cnt;
-    chunk_tokens(a, ci, C, t0, cnt);
+    const int64_t t0 = uniform(a.where[2 * ci]);
+    const int cnt = uniform(a.where[2 * ci + 1]);
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), c = lane & 15, j = lane >> 4;
     const int kw = wave / SPAN, kb0 = kw * KW, tb0 = wave % SPAN * TW;
     const int ft = wave / PARTS, part = wave % PARTS;
@@ -1042,30 +1089,38 @@ __global__ __launch_bounds__(512, 2) void k_back_grad(const BackParams a)
     const uint16_t *act = a.act + (size_t)blockIdx.x * 2 * NP * ACT * BLOCK;
 
     const size_t first = ((size_t)t0 * p.H + hq) * p.dk;  // the chunk's first element of q and k
-    // q and k of the wave's channels and tokens
-    Raw4<TA> qr[PARK ? 1 : KW][PARK ? 1 : TW], kr[PARK ? 1 : KW][PARK ? 1 : TW];
     const int kstep = p.H * p.dk, vstep = p.HV * p.dv;
     const ChunkRows qrows(static_cast<const TA *>(p.q) + first, cnt, kstep, p.dk), krows(static_cast<const TA *>(p.k) + first, cnt, kstep, p.dk);
+    // q and k of the wave's channels and tokens
+    Raw4<TA> qr[PARK ? 1 : KW][PARK ? 1 : TW], kr[PARK ? 1 : KW][PARK ? 1 : TW];
+    if constexpr (PARK) {
+        StageRows<DK, TA, 512, VEC> k, q;
+        const auto at = k.place(kstep, p.dk);
+        k.load(static_cast<const TA *>(p.k) + first, cnt, kstep, p.dk, at);
+        q.load(static_cast<const TA *>(p.q) + first, cnt, kstep, p.dk, at);
+        k.store_raw(s_k);
+        q.store_raw(s_q);
+        __syncthreads();
+    } else {
 #pragma unroll
-    for (int x = 0; x < KW; ++x) {
+        for (int x = 0; x < KW; ++x)
 #pragma unroll
-        for (int w = 0; w < TW; ++w) {
-            const At4<VEC, TA> at(16 * (tb0 + w) + c, kstep, 16 * (kb0 + x) + 4 * j, p.dk);
-            if constexpr (PARK) {
-                s_qk[x * TW + w][tid] = load_raw4(qrows, at);
-                s_qk[(KW + x) * TW + w][tid] = load_raw4(krows, at);
-            } else {
+            for (int w = 0; w < TW; ++w) {
+                const At4<VEC, TA> at(16 * (tb0 + w) + c, kstep, 16 * (kb0 + x) + 4 * j, p.dk);
                 qr[x][w] = load_raw4(qrows, at);
                 kr[x][w] = load_raw4(krows, at);
             }
-        }
     }
+    auto row_of = [&](const uint16_t *rows, int x, int w) {
+        return widen(*reinterpret_cast<const Raw4<TA> *>(rows + (16 * (tb0 + w) + (opaque(threadIdx.x) & 15)) * Rows<DK>::LD +
+                                                         16 * (kb0 + x) + 4 * ((threadIdx.x & 63) >> 4)));
+    };
     auto q_of = [&](int x, int w) {
-        if constexpr (PARK) return widen(s_qk[x * TW + w][tid]);
+        if constexpr (PARK) return row_of(s_q, x, w);
         else return widen(qr[x][w]);
     };
     auto k_of = [&](int x, int w) {
-        if constexpr (PARK) return widen(s_qk[(KW + x) * TW + w][tid]);
+        if constexpr (PARK) return row_of(s_k, x, w);
         else return widen(kr[x][w]);
     };
     // tiles of (K Q^T, K K^T), rows s of block sb, columns t of block ft, of the normalised rows
@@ -1073,7 +1128,11 @@ __global__ __launch_bounds__(512, 2) void k_back_grad(const BackParams a)
     {
         const float *sc = a.sc + ((size_t)ci * p.HV + (size_t)hq * R) * (BACK_SC * C);
         const int t = 16 * ft + c;
-        auto operand = [&](const ChunkRows &rows, int block, int y, b8 (&out)[NP]) {
+        auto operand = [&](const ChunkRows &rows, const uint16_t *lds, int block, int y, b8 (&out)[NP]) {
+            if constexpr (PARK) {
+                RawRows<DK, TA>::row_operand(lds, 16 * block + c, y, out);
+                return;
+            }
             const int lo = 32 * y + 4 * j;
             split8<NP>(widen(load_raw4(rows, At4<VEC, TA>(16 * block + c, kstep, lo, p.dk))),
                        widen(load_raw4(rows, At4<VEC, TA>(16 * block + c, kstep, lo + 16, p.dk))), out);
@@ -1084,13 +1143,14 @@ __global__ __launch_bounds__(512, 2) void k_back_grad(const BackParams a)
             use[x] = sb <= ft;
             if (use[x]) {
                 f4 qk = zero, kk = zero;
+#pragma unroll 2
                 for (int y = 0; y < KX; ++y) {
                     b8 s[NP], q[NP], k[NP];
-                    operand(krows, sb, y, s);
-                    operand(qrows, ft, y, q);
+                    operand(krows, s_k, sb, y, s);
+                    operand(qrows, s_q, ft, y, q);
                     qk = mm(s, q, qk);
                     if (RETR) {
-                        operand(krows, ft, y, k);
+                        operand(krows, s_k, ft, y, k);
                         kk = mm(s, k, kk);
                     }
                 }
@@ -1172,6 +1232,9 @@ __global__ __launch_bounds__(512, 2) void k_back_grad(const BackParams a)
         const int h = hq * R + r;
         const size_t rec = (size_t)ci * p.HV + h;
         static_assert(BACK_SC * C <= 512, "a word a thread");
+        // the lane's numbers anew for each head: what is derived from them would
+        // else be formed once, ahead of the loop, and kept in scratch memory
+        const int tid = opaque(threadIdx.x), lane = tid & 63, c = lane & 15, j = lane >> 4;
         arrive(sc_next);
         if (tid < BACK_SC * C) s_sc[tid] = sc_next;
         fetch_scalars(min(r + 1, R - 1));
@@ -1339,12 +1402,18 @@ __global__ __launch_bounds__(512, 2) void k_back_grad(const BackParams a)
         for (int yy = 0; yy < MX; ++yy) {
             b8 kt[KW][NP], qt[KW][NP];
 #pragma unroll
-            for (int x = 0; x < KW; ++x)
+            for (int x = 0; x < KW; ++x) {
+                if constexpr (PARK) {
+                    RawRows<DK, TA>::col_operand(s_k, kb0 + x, yy, kt[x]);
+                    RawRows<DK, TA>::col_operand(s_q, kb0 + x, yy, qt[x]);
+                } else {
 #pragma unroll
-                for (int n = 0; n < NP; ++n) {
-                    kt[x][n] = get_block(act + (size_t)(n * ACT + (kb0 + x) * MX + yy) * BLOCK);
-                    qt[x][n] = get_block(act + (size_t)((NP + n) * ACT + (kb0 + x) * MX + yy) * BLOCK);
+                    for (int n = 0; n < NP; ++n) {
+                        kt[x][n] = get_block(act + (size_t)(n * ACT + (kb0 + x) * MX + yy) * BLOCK);
+                        qt[x][n] = get_block(act + (size_t)((NP + n) * ACT + (kb0 + x) * MX + yy) * BLOCK);
+                    }
                 }
+            }
 #pragma unroll
             for (int w = 0; w < TW; ++w) {
                 const int tb = tb0 + w;
@@ -1465,9 +1534,8 @@ __global__ __launch_bounds__(256) void k_back_gate(const BackParams a)
     const int lane = threadIdx.x & 63;
     const int ci = (int)(rec / p.HV), h = (int)(rec % p.HV);
     if (ci >= a.off[p.B]) return;
-    int64_t t0;
-    int cnt;
-    chunk_tokens(a, ci, C, t0, cnt);
+    const int64_t t0 = uniform(a.where[2 * ci]);
+    const int cnt = uniform(a.where[2 * ci + 1]);
     const float *x = a.gx + (size_t)rec * GX * C;
     const int n0 = lane < C ? lane : C - 1;
     const bool mine = lane < C;

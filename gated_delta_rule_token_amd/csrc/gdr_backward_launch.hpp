@@ -43,7 +43,8 @@ struct BackParams {
     // workspace
     int32_t *off;               // (B + 1) first chunk of each request; off[B] = chunks in use
     int32_t *tok;               // (B, 2) first token and length of each request
-    uint16_t *act;              // per (chunk, q/k head): operand fragments of k^T, q^T
+    int32_t *where;             // (chunks, 2) first token and length of each chunk
+    uint16_t *act;              // fp32 activations, per (chunk, q/k head): operand fragments of k^T, q^T
     uint16_t *tri;              // per (chunk, value head): P^T, and with retrieval (I + diag(b) L)^-T, (I + L diag(b))^-1
     float *sc, *s, *ds, *e, *y; // scalars; S0, dS1, E, Y as fp32 fragments
     float *gx;                  // see BackGateRow
