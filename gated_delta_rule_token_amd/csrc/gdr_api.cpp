@@ -372,6 +372,17 @@ gdr_status check_backward(const gdr_problem *p)
     return GDR_OK;
 }
 
+// Segments of the backward pass's chains, `chains` workgroups of them.
+int32_t back_segments(const gdr_problem *p, int64_t chains)
+{
+    if (chains < 1) return 1;
+    const int64_t per_req = (p->total_tokens + p->batch - 1) / p->batch / gdr::back_chunk(p->head_dim_k);
+    int64_t n = 256 / chains;
+    if (n > per_req / 4) n = per_req / 4;
+    if (n > 16) n = 16;
+    return n >= 3 ? (int32_t)n : 1;
+}
+
 // Carve the workspace (256-byte aligned pieces) at `base` into `a`, with the
 // sizes the kernels need; returns the bytes (also when base is NULL).
 size_t back_layout(const gdr_problem *p, gdr::BackParams &a, void *base)
@@ -404,6 +415,14 @@ size_t back_layout(const gdr_problem *p, gdr::BackParams &a, void *base)
     a.ds = floats(recs * KB * VB * block);
     a.e = floats(recs * MB * VB * block);
     a.y = retr ? floats(recs * MB * VB * block) : nullptr;
+    const size_t pairs = (size_t)p->batch * p->num_heads_v;
+    a.nseg = back_segments(p, (int64_t)(pairs * (VB / 4)));
+    if (a.nseg > 1) {
+        a.seg_m = floats(pairs * a.nseg * KB * KB * block);
+        a.seg_mt = floats(pairs * a.nseg * KB * KB * block);
+        a.seg_carry = floats(pairs * a.nseg * VB * KB * block);
+        a.seg_state = floats(pairs * a.nseg * VB * KB * block);
+    }
     return at;
 }
 

@@ -231,6 +231,12 @@ __device__ __forceinline__ void put_frag_rows(float *blk, f4 v)
     *reinterpret_cast<f4 *>(blk + quad_lane() * 4) = quad_transpose(v);
 }
 
+// Accumulator tile -> fragment block whose rows are the tile's columns: as it lies.
+__device__ __forceinline__ void put_frag_cols(float *blk, f4 v)
+{
+    *reinterpret_cast<f4 *>(blk + (threadIdx.x & 63) * 4) = v;
+}
+
 __device__ __forceinline__ f4 get_frag(const float *blk) { return *reinterpret_cast<const f4 *>(blk + (threadIdx.x & 63) * 4); }
 
 // ---- rows of a chunk in memory
@@ -759,7 +765,6 @@ __device__ __forceinline__ void rows_times_state(f4 (&acc)[Geo<DK>::MB], const u
     using G = Geo<DK>;
 #pragma unroll
     for (int x = 0; x < G::KX; ++x) {
-        __builtin_amdgcn_sched_barrier(0);  // one step's operands in registers at a time
         b8 s[3];
         split8<3>(S[2 * x], S[2 * x + 1], s);
         b8 k[G::MB][NP];
@@ -786,7 +791,6 @@ __device__ __forceinline__ void state_update(f4 (&S)[Geo<DK>::KB], const uint16_
         split8<3>(X[2 * y], X[2 * y + 1], x);
 #pragma unroll
         for (int k0 = 0; k0 < G::KB; k0 += 4) {
-            __builtin_amdgcn_sched_barrier(0);
             b8 k[4][NP];
 #pragma unroll
             for (int kb = 0; kb < 4; ++kb) Rows<DK>::col_operand(rows, k0 + kb, y, k[kb]);
@@ -836,13 +840,89 @@ struct ChunkScalars {
     }
 };
 
+// ---------------------------------------------------------------- segments
+// A chain step maps every state row s affinely and alike, s <- s M_c + c_c.
+// With few (request, head) pairs a chain is cut into segments: a first pass
+// (CARRY) gives each segment's M (rows of the identity as start, values left
+// out) and its c (zero start, nothing kept), k_back_join hands the true states
+// from segment to segment, and the pass that keeps its results runs all
+// segments side by side.  Backwards a row of dS takes M^T, so M is formed once.
+// States between kernels are accumulators as they lie: [pair][segment][row
+// block][kb][lane] float4.
+struct Segment {
+    int first, count, len;  // chunks; tokens
+    int64_t start;
+    // segment `seg` of a.nseg of request b
+    template <int C> static __device__ __forceinline__ Segment of(const BackParams &a, int b, int seg)
+    {
+        const int f0 = uniform(a.off[b]), n0 = uniform(a.off[b + 1]) - f0;
+        const int lo = (int)((int64_t)n0 * seg / a.nseg), hi = (int)((int64_t)n0 * (seg + 1) / a.nseg);
+        return Segment{f0 + lo, hi - lo, min(uniform(a.tok[2 * b + 1]) - lo * C, (hi - lo) * C), (int64_t)uniform(a.tok[2 * b]) + lo * C};
+    }
+};
+
+__device__ __forceinline__ size_t seg_at(const BackParams &a, int bh, int seg, int blocks, int block, int KB)
+{
+    return ((((size_t)bh * a.nseg + seg) * blocks + block) * KB) * FRAG;
+}
+
+template <int KB> __device__ __forceinline__ void put_state(float *at, const f4 (&S)[KB])
+{
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) put_frag_cols(at + kb * FRAG, S[kb]);
+}
+
+template <int KB> __device__ __forceinline__ void get_state(f4 (&S)[KB], const float *at)
+{
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) S[kb] = get_frag(at + kb * FRAG);
+}
+
+// One workgroup per (request, value head, 64 state rows): the states at the
+// segments' starts (backwards: at their ends), one after the other.
+template <int DK, bool REVERSE, bool VEC>
+__global__ __launch_bounds__(256) void k_back_join(const BackParams a)
+{
+    using G = Geo<DK>;
+    constexpr int KB = G::KB, KX = G::KX;
+    const Params &p = a.p;
+    const int tiles = a.VB / 4, tile = blockIdx.x % tiles, bh = blockIdx.x / tiles;
+    const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane & 15, j = lane >> 4;
+    const int vb = tile * 4 + wave, col = 16 * vb + c;
+    const float *init = REVERSE ? a.d_final : p.init;
+    f4 S[KB];
+    load_state<VEC>(S, init ? init + (size_t)bh * p.dv * p.dk : nullptr, col, p.dv, p.dk, j);
+    for (int n = 0; n < a.nseg; ++n) {
+        const int seg = REVERSE ? a.nseg - 1 - n : n;
+        put_state<KB>(a.seg_state + seg_at(a, bh, seg, a.VB, vb, KB), S);
+        if (n + 1 == a.nseg) break;
+        f4 next[KB];
+        get_state<KB>(next, a.seg_carry + seg_at(a, bh, seg, a.VB, vb, KB));
+        b8 x[KX][3];
+#pragma unroll
+        for (int y = 0; y < KX; ++y) split8<3>(S[2 * y], S[2 * y + 1], x[y]);
+        const float *M = (REVERSE ? a.seg_m : a.seg_mt) + seg_at(a, bh, seg, KB, 0, KB);
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {  // rows kb of the result, fragment blocks (kb, 2 y) and (kb, 2 y + 1)
+#pragma unroll
+            for (int y = 0; y < KX; ++y) {
+                b8 m[3];
+                split8<3>(get_frag(M + (kb * KB + 2 * y) * FRAG), get_frag(M + (kb * KB + 2 * y + 1) * FRAG), m);
+                next[kb] = mm(m, x[y], next[kb]);
+            }
+        }
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) S[kb] = next[kb];
+    }
+}
+
 // ---------------------------------------------------------------- forward chain
-// One workgroup per (request, value head, 64 state rows); wave w keeps S^T of
+// One workgroup per (segment, request, value head, 64 state rows); wave w keeps S^T of
 // 16 rows in its accumulators over the whole chain.  Everything that a step
 // reads from memory is loaded one step ahead: within the step there are only
 // LDS reads, and stores that nothing waits for.
-template <int DK, typename TA, bool RETR, bool VEC>
-__global__ __launch_bounds__(256, back_chain_waves<TA>(DK)) void k_back_states(const BackParams a)
+template <int DK, typename TA, bool RETR, bool VEC, bool CARRY>
+__global__ __launch_bounds__(256, planes_of<TA> <= 2 && DK <= 128 ? 2 : 1) void k_back_states(const BackParams a)
 {
     using G = Geo<DK>;
     constexpr int C = G::C, MB = G::MB, MX = G::MX, KB = G::KB, NT = G::NT, NP = planes_of<TA>;
@@ -852,18 +932,29 @@ __global__ __launch_bounds__(256, back_chain_waves<TA>(DK)) void k_back_states(c
     __shared__ __align__(16) float s_eg[C], s_x[C];
     __shared__ float s_gamma;
     const Params &p = a.p;
-    const int tiles = a.VB / 4;
-    const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles, h = bh % p.HV, b = bh / p.HV;
-    const int first = uniform(a.off[b]), count = uniform(a.off[b + 1]) - first;
-    if (count == 0) return;
+    const int tiles = a.VB / 4 + (CARRY ? KB / 4 : 0);
+    const int tile = blockIdx.x % tiles, pair = blockIdx.x / tiles, bh = pair % (p.B * p.HV), seg = pair / (p.B * p.HV);
+    const int h = bh % p.HV, b = bh / p.HV;
+    const Segment sg = Segment::of<C>(a, b, seg);
+    const int first = sg.first, count = sg.count, len = sg.len;
+    const int64_t start = sg.start;
+    if (!CARRY && count == 0) return;
     const int hq = h / (p.HV / p.H);
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), c = lane & 15, j = lane >> 4;
-    const int vb = tile * 4 + wave, col = vb * 16 + c;
-    const int64_t start = uniform(a.tok[2 * b]);
-    const int len = uniform(a.tok[2 * b + 1]);
+    const bool map = CARRY && tile >= a.VB / 4;  // rows of M
+    const int vb = tile * 4 + wave - (map ? a.VB : 0), col = vb * 16 + c;
 
     f4 S[KB], E[MB];
-    load_state<VEC>(S, p.init ? p.init + (size_t)bh * p.dv * p.dk : nullptr, col, p.dv, p.dk, j);
+    if constexpr (CARRY) {
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) S[kb][i] = map && 16 * kb + 4 * j + i == col ? 1.f : 0.f;
+    } else if (a.nseg > 1) {
+        get_state<KB>(S, a.seg_state + seg_at(a, bh, seg, a.VB, vb, KB));
+    } else {
+        load_state<VEC>(S, p.init ? p.init + (size_t)bh * p.dv * p.dk : nullptr, col, p.dv, p.dk, j);
+    }
     StageRows<DK, TA, 256, VEC> k;
     Copy<RETR ? 3 * NT : 0> tri_next;
     ChunkScalars x;
@@ -895,13 +986,19 @@ __global__ __launch_bounds__(256, back_chain_waves<TA>(DK)) void k_back_states(c
         fetch(min(n + 1, count - 1));
         lds_barrier();
     };
-    fetch(0);
+    if (count > 0) fetch(0);
     for (int n = 0; n < count; ++n) {
         const size_t rec = (size_t)(first + n) * p.HV + h;
         stage(n);
-        float *Sw = a.s + (rec * KB * a.VB + vb) * FRAG;
+        if constexpr (CARRY) {
+            if (map)
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) put_frag_rows(Sw + (size_t)kb * a.VB * FRAG, S[kb]);
+                for (int m = 0; m < MB; ++m) E[m] = f4{0.f, 0.f, 0.f, 0.f};
+        } else {
+            float *Sw = a.s + (rec * KB * a.VB + vb) * FRAG;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) put_frag_rows(Sw + (size_t)kb * a.VB * FRAG, S[kb]);
+        }
         if constexpr (RETR) {
             f4 Y[MB];
 #pragma unroll
@@ -922,7 +1019,7 @@ __global__ __launch_bounds__(256, back_chain_waves<TA>(DK)) void k_back_states(c
         float *Ew = a.e + (rec * MB * a.VB + vb) * FRAG;
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
-            put_frag_rows(Ew + (size_t)m * a.VB * FRAG, E[m]);
+            if (!CARRY) put_frag_rows(Ew + (size_t)m * a.VB * FRAG, E[m]);
             E[m] *= *reinterpret_cast<const f4 *>(s_x + 16 * m + 4 * j);
         }
         const float gamma = s_gamma;
@@ -930,11 +1027,22 @@ __global__ __launch_bounds__(256, back_chain_waves<TA>(DK)) void k_back_states(c
         for (int kb = 0; kb < KB; ++kb) S[kb] *= gamma;
         state_update<DK, NP>(S, Kr, E);
     }
+    if constexpr (CARRY) {
+        if (map) {  // M as fragment blocks of its rows (for M) and of its columns (for M^T)
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                put_frag_cols(a.seg_m + seg_at(a, bh, seg, KB, vb, KB) + kb * FRAG, S[kb]);
+                put_frag_rows(a.seg_mt + seg_at(a, bh, seg, KB, kb, KB) + vb * FRAG, S[kb]);
+            }
+        } else {
+            put_state<KB>(a.seg_carry + seg_at(a, bh, seg, a.VB, vb, KB), S);
+        }
+    }
 }
 
 // ---------------------------------------------------------------- backward chain
-template <int DK, typename TA, bool RETR, bool VEC>
-__global__ __launch_bounds__(256, back_chain_waves<TA>(DK)) void k_back_chain(const BackParams a)
+template <int DK, typename TA, bool RETR, bool VEC, bool CARRY>
+__global__ __launch_bounds__(256, planes_of<TA> == 1 && DK <= 128 ? 2 : 1) void k_back_chain(const BackParams a)
 {
     using G = Geo<DK>;
     constexpr int C = G::C, MB = G::MB, MX = G::MX, KB = G::KB, NT = G::NT, NP = planes_of<TA>;
@@ -945,16 +1053,24 @@ __global__ __launch_bounds__(256, back_chain_waves<TA>(DK)) void k_back_chain(co
     __shared__ float s_gamma;
     const Params &p = a.p;
     const int tiles = a.VB / 4;
-    const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles, h = bh % p.HV, b = bh / p.HV;
-    const int first = uniform(a.off[b]), count = uniform(a.off[b + 1]) - first;
+    const int tile = blockIdx.x % tiles, pair = blockIdx.x / tiles, bh = pair % (p.B * p.HV), seg = pair / (p.B * p.HV);
+    const int h = bh % p.HV, b = bh / p.HV;
+    const Segment sg = Segment::of<C>(a, b, seg);
+    const int first = sg.first, count = sg.count, len = sg.len;
+    const int64_t start = sg.start;
     const int hq = h / (p.HV / p.H);
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), c = lane & 15, j = lane >> 4;
     const int vb = tile * 4 + wave, col = vb * 16 + c;
-    const int64_t start = uniform(a.tok[2 * b]);
-    const int len = uniform(a.tok[2 * b + 1]);
 
     f4 dS[KB];
-    load_state<VEC>(dS, a.d_final ? a.d_final + (size_t)bh * p.dv * p.dk : nullptr, col, p.dv, p.dk, j);
+    if constexpr (CARRY) {
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) dS[kb] = f4{0.f, 0.f, 0.f, 0.f};
+    } else if (a.nseg > 1) {
+        get_state<KB>(dS, a.seg_state + seg_at(a, bh, seg, a.VB, vb, KB));
+    } else {
+        load_state<VEC>(dS, a.d_final ? a.d_final + (size_t)bh * p.dv * p.dk : nullptr, col, p.dv, p.dk, j);
+    }
     StageRows<DK, TA, 256, VEC> k, q;
     Copy<(RETR ? 6 : 3) * NT> tri_next;
     ChunkScalars x;
@@ -997,9 +1113,11 @@ __global__ __launch_bounds__(256, back_chain_waves<TA>(DK)) void k_back_chain(co
         const size_t rec = (size_t)(first + n) * p.HV + h;
         const int cnt = min(len - n * C, C);
         stage(n);
-        float *Sw = a.ds + (rec * KB * a.VB + vb) * FRAG;
+        if constexpr (!CARRY) {
+            float *Sw = a.ds + (rec * KB * a.VB + vb) * FRAG;
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) put_frag_rows(Sw + (size_t)kb * a.VB * FRAG, dS[kb]);
+            for (int kb = 0; kb < KB; ++kb) put_frag_rows(Sw + (size_t)kb * a.VB * FRAG, dS[kb]);
+        }
         f4 D[MB];
 #pragma unroll
         for (int m = 0; m < MB; ++m) D[m] = f4{0.f, 0.f, 0.f, 0.f};
@@ -1025,14 +1143,14 @@ __global__ __launch_bounds__(256, back_chain_waves<TA>(DK)) void k_back_chain(co
             float *Yw = a.y + (rec * MB * a.VB + vb) * FRAG;
 #pragma unroll
             for (int m = 0; m < MB; ++m) {
-                put_frag_rows(Yw + (size_t)m * a.VB * FRAG, Y[m]);
+                if (!CARRY) put_frag_rows(Yw + (size_t)m * a.VB * FRAG, Y[m]);
                 D[m] = Y[m] * *reinterpret_cast<const f4 *>(s_b + 16 * m + 4 * j);
             }
         }
         const ChunkRows dvrows(static_cast<const TA *>(a.dv) + ((size_t)start + (size_t)n * C) * vstep + h * p.dv, cnt, vstep, p.dv);
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
-            store4(dvrows, vat.down(16 * m, vstep), quad_transpose(D[m]));
+            if (!CARRY) store4(dvrows, vat.down(16 * m, vstep), quad_transpose(D[m]));
             dO[m] *= *reinterpret_cast<const f4 *>(s_q + 16 * m + 4 * j);
             D[m] *= *reinterpret_cast<const f4 *>(s_k + 16 * m + 4 * j);
         }
@@ -1042,7 +1160,9 @@ __global__ __launch_bounds__(256, back_chain_waves<TA>(DK)) void k_back_chain(co
         state_update<DK, NP>(dS, Qr, dO);
         if constexpr (RETR) state_update<DK, NP>(dS, Kr, D);
     }
-    if (a.d_init) {
+    if constexpr (CARRY) {
+        put_state<KB>(a.seg_carry + seg_at(a, bh, seg, a.VB, vb, KB), dS);
+    } else if (a.d_init && seg == 0) {
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
             store4(ChunkRows(a.d_init + (size_t)bh * p.dv * p.dk, p.dv, p.dk, p.dk), At4<VEC, float>(col, p.dk, 16 * kb + 4 * j, p.dk), dS[kb]);
@@ -1595,10 +1715,19 @@ template <int DK, typename TA, bool RETR, bool VEC>
 hipError_t launch_back_typed(const BackParams &a, hipStream_t s)
 {
     const Params &p = a.p;
-    const unsigned per_chunk = (unsigned)a.chunks * p.H, chains = (unsigned)p.B * p.HV * (a.VB / 4);
-    hipLaunchKernelGGL((k_back_prep<DK, TA, RETR, VEC>), dim3(per_chunk), dim3(256), 0, s, a);
-    hipLaunchKernelGGL((k_back_states<DK, TA, RETR, VEC>), dim3(chains), dim3(256), 0, s, a);
-    hipLaunchKernelGGL((k_back_chain<DK, TA, RETR, VEC>), dim3(chains), dim3(256), 0, s, a);
+    const unsigned per_chunk = (unsigned)a.chunks * p.H, pairs = (unsigned)p.B * p.HV, tiles = a.VB / 4;
+    const dim3 chains(pairs * a.nseg * tiles), block(256);
+    hipLaunchKernelGGL((k_back_prep<DK, TA, RETR, VEC>), dim3(per_chunk), block, 0, s, a);
+    if (a.nseg > 1) {
+        hipLaunchKernelGGL((k_back_states<DK, TA, RETR, VEC, true>), dim3(pairs * a.nseg * (tiles + Geo<DK>::KB / 4)), block, 0, s, a);
+        hipLaunchKernelGGL((k_back_join<DK, false, VEC>), dim3(pairs * tiles), block, 0, s, a);
+    }
+    hipLaunchKernelGGL((k_back_states<DK, TA, RETR, VEC, false>), chains, block, 0, s, a);
+    if (a.nseg > 1) {
+        hipLaunchKernelGGL((k_back_chain<DK, TA, RETR, VEC, true>), chains, block, 0, s, a);
+        hipLaunchKernelGGL((k_back_join<DK, true, VEC>), dim3(pairs * tiles), block, 0, s, a);
+    }
+    hipLaunchKernelGGL((k_back_chain<DK, TA, RETR, VEC, false>), chains, block, 0, s, a);
     hipLaunchKernelGGL((k_back_grad<DK, TA, RETR, VEC>), dim3(per_chunk), dim3(512), 0, s, a);
     if (RETR || a.decays)
         hipLaunchKernelGGL((k_back_gate<Geo<DK>::C, RETR>), dim3(((unsigned)a.chunks * p.HV + 3) / 4), dim3(256), 0, s, a);

@@ -16,10 +16,6 @@ __host__ __device__ constexpr int back_dk_tile(int dk) { return dk <= 64 ? 64 : 
 // 16 x 32 blocks of a triangular chunk x chunk operand
 __host__ __device__ constexpr int back_tri_blocks(int C) { return C == 64 ? 6 : 2; }
 
-// Waves a SIMD of the chains: two workgroups a CU where a chunk's rows leave
-// room for them in LDS, one (and twice the registers) where they do not.
-template <typename TA> constexpr int back_chain_waves(int dk) { return sizeof(TA) == 2 && dk <= 128 ? 2 : 1; }
-
 // Per (chunk, value head) scalars, a row of back_chunk floats each: e^G,
 // e^(Gamma - G), update rate, G as (hi, lo), and the factors of q (with the
 // scale) and k.
@@ -48,6 +44,9 @@ struct BackParams {
     uint16_t *tri;              // per (chunk, value head): P^T, and with retrieval (I + diag(b) L)^-T, (I + L diag(b))^-1
     float *sc, *s, *ds, *e, *y; // scalars; S0, dS1, E, Y as fp32 fragments
     float *gx;                  // see BackGateRow
+    // between the segments of a chain (nseg > 1): M by rows and by columns, carries, states at their starts
+    float *seg_m, *seg_mt, *seg_carry, *seg_state;
+    int32_t nseg;
     int32_t chunks;             // chunk budget: ceil(T / C) + B
     int32_t VB;                 // 16-row blocks of dv, a multiple of 4
     int32_t decays;

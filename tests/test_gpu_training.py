@@ -108,6 +108,17 @@ def test_backward_shapes(shape, rule):
     check(workloads.random_case(21, update_rule=rule, qk_l2_norm=int(rule == "gated"), **SHAPES[shape]), what=shape)
 
 
+@pytest.mark.parametrize("rule", ["linear", "gated", "delta", "gated_delta"])
+@pytest.mark.parametrize("lens,H,HV,DK,DV", [([1000], 1, 1, 32, 32), ([1700, 3, 0, 900], 1, 2, 128, 80), ([450], 1, 1, 200, 30),
+                                             ([2100], 1, 1, 12, 9)])
+def test_backward_of_long_chains(lens, H, HV, DK, DV, rule):
+    """Few heads and long requests: the chains run in segments."""
+    case = workloads.random_case(40, lengths=lens, H=H, HV=HV, DK=DK, DV=DV, update_rule=rule, qk_l2_norm=1)
+    if case["gate"] is not None:
+        case["gate"] *= 0.02  # states that reach over several segments
+    check(case, what="long")
+
+
 @pytest.mark.parametrize("dtype", [np.float32, np.float16, "bf16"], ids=["f32", "f16", "bf16"])
 @pytest.mark.parametrize("shape", ["odd", "d128", "wide_keys"])
 def test_backward_raw_gate_types(shape, dtype):
