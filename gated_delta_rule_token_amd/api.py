@@ -158,6 +158,16 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _enqueue(fn, dev, *args):
+    """Call a library function on torch's current stream of ``dev``, with that
+    device current (a launch needs its stream's device to be)."""
+    if dev.index == torch.cuda.current_device():
+        check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+
+
 def _dtype_code(dt):
     if dt == torch.float32:
         return F32
@@ -498,10 +508,8 @@ def backward(q, k, v, d_o, *, gate=None, beta=None, a_log=None, dt_bias=None, ga
                 gate_scale=_ptr(gate_scale), seq_lens=_ptr(seq_lens))
     g = GradientPointers(d_o=_ptr(d_o), d_final_state=_ptr(d_final_state),
                          **{"d_" + name: _ptr(x) for name, x in grads.items()})
-    with torch.cuda.device(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
-        check(lib.gdr_backward(ctypes.byref(p), ctypes.byref(t), ctypes.byref(g), _ptr(workspace),
-                               workspace.numel() * workspace.element_size(), stream))
+    _enqueue(lib.gdr_backward, dev, ctypes.byref(p), ctypes.byref(t), ctypes.byref(g), _ptr(workspace),
+             workspace.numel() * workspace.element_size())
     return Gradients(**grads)
 
 
@@ -537,12 +545,9 @@ def gate_backward(a, dt_bias, decay_scale, d_decay, b=None, d_beta=None, workspa
     _need(workspace, "workspace", device=dev)
     g = GateGradients(torch.empty_like(a), None if b is None else torch.empty_like(b),
                       torch.empty_like(dt_bias), torch.empty_like(decay_scale))
-    with torch.cuda.device(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
-        check(lib.gdr_gate_backward(a.numel(), heads, _dtype_code(a.dtype), _ptr(a), _ptr(dt_bias), _ptr(decay_scale),
-                                    _ptr(b), _ptr(d_decay), _ptr(d_beta), _ptr(g.a), _ptr(g.b), _ptr(g.dt_bias),
-                                    _ptr(g.decay_scale), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), stream))
+    _enqueue(lib.gdr_gate_backward, dev, a.numel(), heads, _dtype_code(a.dtype), _ptr(a), _ptr(dt_bias),
+             _ptr(decay_scale), _ptr(b), _ptr(d_decay), _ptr(d_beta), _ptr(g.a), _ptr(g.b), _ptr(g.dt_bias),
+             _ptr(g.decay_scale), _ptr(workspace), workspace.numel() * workspace.element_size())
     return g
 
 
@@ -600,11 +605,9 @@ def rms_norm(x, weight=None, *, residual=None, eps=1e-6, out_dtype=None, group=0
     else:
         raise GDRError("GDR_E_INVALID", "out_dtype must be x's dtype or torch.float8_e4m3fn, got %s" % out_dtype)
     inv = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if want_inv_rms else None
-    with torch.cuda.device(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
-        check(lib.gdr_rms_norm(rows, width, code, code if weight is None else _dtype_code(weight.dtype), out_code,
-                               int(group), float(eps), _ptr(x), _ptr(residual), _ptr(weight), _ptr(y), _ptr(scale),
-                               _ptr(residual_out), _ptr(inv), stream))
+    _enqueue(lib.gdr_rms_norm, dev, rows, width, code, code if weight is None else _dtype_code(weight.dtype), out_code,
+             int(group), float(eps), _ptr(x), _ptr(residual), _ptr(weight), _ptr(y), _ptr(scale), _ptr(residual_out),
+             _ptr(inv))
     return NormOutput(y, scale, residual_out, inv)
 
 
@@ -641,12 +644,9 @@ def rms_norm_backward(d_y, x, weight, inv_rms, *, d_residual=None, workspace=Non
             workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
     _need(workspace, "workspace", device=dev)
     code = _dtype_code(x.dtype)
-    with torch.cuda.device(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
-        check(lib.gdr_rms_norm_backward(
-            rows, width, code, code if weight is None else _dtype_code(weight.dtype), _ptr(d_y), _ptr(x), _ptr(weight),
-            _ptr(inv_rms), _ptr(d_residual), _ptr(d_x), _ptr(d_weight), _ptr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), stream))
+    _enqueue(lib.gdr_rms_norm_backward, dev, rows, width, code, code if weight is None else _dtype_code(weight.dtype),
+             _ptr(d_y), _ptr(x), _ptr(weight), _ptr(inv_rms), _ptr(d_residual), _ptr(d_x), _ptr(d_weight),
+             _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
     return NormGradients(d_x, d_weight)
 
 

@@ -780,28 +780,45 @@ __device__ __forceinline__ void rows_times_state(f4 (&acc)[Geo<DK>::MB], const u
     }
 }
 
-// S[kb] += rows^T X, the rows' (k's or q's) planes in LDS, X by token blocks
-template <int DK, int NP>
-__device__ __forceinline__ void state_update(f4 (&S)[Geo<DK>::KB], const uint16_t *rows, const f4 (&X)[Geo<DK>::MB])
+// S = gamma S + rows^T X (+ rows2^T X2), the rows' (k's or q's) planes in LDS, X
+// by token blocks.  The products are summed by themselves and reach S in one
+// rounding: added to it plane by plane they would round it six times a chunk,
+// and over a long chain without decay that error adds up.
+template <int DK, int NP, bool TWO>
+__device__ __forceinline__ void state_update(f4 (&S)[Geo<DK>::KB], float gamma, const uint16_t *rows, const f4 (&X)[Geo<DK>::MB],
+                                             const uint16_t *rows2, const f4 (&X2)[Geo<DK>::MB])
 {
     using G = Geo<DK>;
+    b8 x[TWO ? 2 : 1][G::MX][3];
 #pragma unroll
     for (int y = 0; y < G::MX; ++y) {
-        b8 x[3];
-        split8<3>(X[2 * y], X[2 * y + 1], x);
+        split8<3>(X[2 * y], X[2 * y + 1], x[0][y]);
+        if (TWO) split8<3>(X2[2 * y], X2[2 * y + 1], x[TWO ? 1 : 0][y]);
+    }
 #pragma unroll
-        for (int k0 = 0; k0 < G::KB; k0 += 4) {
-            b8 k[4][NP];
+    for (int k0 = 0; k0 < G::KB; k0 += 4) {
+        f4 sum[4];
 #pragma unroll
-            for (int kb = 0; kb < 4; ++kb) Rows<DK>::col_operand(rows, k0 + kb, y, k[kb]);
+        for (int kb = 0; kb < 4; ++kb) sum[kb] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int n = 2; n >= 0; --n)
+        for (int y = 0; y < G::MX; ++y)
 #pragma unroll
-                for (int i = 0; i <= n; ++i)
-                    if (i < NP)
+            for (int two = 0; two < (TWO ? 2 : 1); ++two) {
+                b8 k[4][NP];
 #pragma unroll
-                        for (int kb = 0; kb < 4; ++kb) S[k0 + kb] = mfma(k[kb][i], x[n - i], S[k0 + kb]);
-        }
+                for (int kb = 0; kb < 4; ++kb) Rows<DK>::col_operand(two ? rows2 : rows, k0 + kb, y, k[kb]);
+#pragma unroll
+                for (int n = 2; n >= 0; --n)
+#pragma unroll
+                    for (int i = 0; i <= n; ++i)
+                        if (i < NP)
+#pragma unroll
+                            for (int kb = 0; kb < 4; ++kb) sum[kb] = mfma(k[kb][i], x[two][y][n - i], sum[kb]);
+            }
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) S[k0 + kb][i] = fmaf(gamma, S[k0 + kb][i], sum[kb][i]);
     }
 }
 
@@ -1022,10 +1039,7 @@ __global__ __launch_bounds__(256, planes_of<TA> <= 2 && DK <= 128 ? 2 : 1) void 
             if (!CARRY) put_frag_rows(Ew + (size_t)m * a.VB * FRAG, E[m]);
             E[m] *= *reinterpret_cast<const f4 *>(s_x + 16 * m + 4 * j);
         }
-        const float gamma = s_gamma;
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) S[kb] *= gamma;
-        state_update<DK, NP>(S, Kr, E);
+        state_update<DK, NP, false>(S, s_gamma, Kr, E, Kr, E);
     }
     if constexpr (CARRY) {
         if (map) {  // M as fragment blocks of its rows (for M) and of its columns (for M^T)
@@ -1154,11 +1168,7 @@ __global__ __launch_bounds__(256, planes_of<TA> == 1 && DK <= 128 ? 2 : 1) void 
             dO[m] *= *reinterpret_cast<const f4 *>(s_q + 16 * m + 4 * j);
             D[m] *= *reinterpret_cast<const f4 *>(s_k + 16 * m + 4 * j);
         }
-        const float gamma = s_gamma;
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) dS[kb] *= gamma;
-        state_update<DK, NP>(dS, Qr, dO);
-        if constexpr (RETR) state_update<DK, NP>(dS, Kr, D);
+        state_update<DK, NP, RETR>(dS, s_gamma, Qr, dO, Kr, D);
     }
     if constexpr (CARRY) {
         put_state<KB>(a.seg_carry + seg_at(a, bh, seg, a.VB, vb, KB), dS);

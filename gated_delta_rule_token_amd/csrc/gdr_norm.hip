@@ -11,46 +11,99 @@
 //
 // Bound by memory: one pass over the data.  A row lies in the registers of
 // TPR threads, NV vectors of 8 elements each, between its load and its store;
-// the sums and the maxima go over lanes (and, past one wave, over LDS).
+// the sums and the maxima go over lanes (and, past one wave, over LDS).  The
+// next row is on its way, as it lies in memory, while one is worked on.
 // Vectors are loaded whatever the row's alignment (16-bit rows of odd width
-// start at any even byte); only the vector that holds the row's end is loaded
-// by element.
+// start at any even byte), the last one of a row from 8 elements before its
+// end, so that no load stands under a condition.
 #include "gdr_norm_launch.hpp"
 
 namespace gdr {
 namespace {
 
 constexpr float E4M3_MAX = 448.f;
+constexpr int64_t NORM_BLOCKS = 256 * 8;  // workgroups of the forward pass: eight a CU
 
-template <typename T> struct __attribute__((packed, aligned(sizeof(T)))) Vec8 { T x[8]; };
+// 16 bytes from any even address.
+typedef uint32_t v4 __attribute__((ext_vector_type(4), aligned(2)));
 
-template <typename T>
-__device__ __forceinline__ void load8(const T *row, int col, int width, float (&out)[8])
-{
-    if (col + 8 <= width) {
-        const Vec8<T> v = *reinterpret_cast<const Vec8<T> *>(row + col);
+// Eight elements as they lie in memory: whole registers (as elements, 16-bit
+// ones would take a register each).
+template <typename T> struct Raw8 {
+    static constexpr int WORDS = 2 * sizeof(T);
+    uint32_t w[WORDS];
+    __device__ __forceinline__ void load(const T *src)
+    {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) out[i] = to_f32(v.x[i]);
-    } else {
+        for (int n = 0; n < WORDS / 4; ++n) {
+            const v4 x = reinterpret_cast<const v4 *>(src)[n];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) out[i] = col + i < width ? to_f32(row[col + i]) : 0.f;
+            for (int i = 0; i < 4; ++i) w[4 * n + i] = x[i];
+        }
     }
-}
-
-template <typename T>
-__device__ __forceinline__ void store8(T *row, int col, int width, const float (&v)[8])
-{
-    if (col + 8 <= width) {
-        Vec8<T> o;
+    // What was widened before is forgotten: else it would be kept in fp32.
+    __device__ __forceinline__ void again()
+    {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o.x[i] = from_f32<T>(v[i]);
-        *reinterpret_cast<Vec8<T> *>(row + col) = o;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (col + i < width) row[col + i] = from_f32<T>(v[i]);
+        for (int i = 0; i < WORDS; ++i) asm volatile("" : "+v"(w[i]));
     }
-}
+    __device__ __forceinline__ float get(int i) const
+    {
+        if constexpr (sizeof(T) == 4) return __builtin_bit_cast(float, w[i]);
+        else return to_f32(__builtin_bit_cast(T, (uint16_t)(w[i / 2] >> (16 * (i % 2)))));
+    }
+    __device__ __forceinline__ void set(int i, T x)
+    {
+        if constexpr (sizeof(T) == 4) w[i] = __builtin_bit_cast(uint32_t, x);
+        else if (i % 2 == 0) w[i / 2] = __builtin_bit_cast(uint16_t, x);
+        else w[i / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, x) << 16;
+    }
+};
+
+// A thread's vector of a row: columns col .. col + 7, of which [lo, hi) are
+// its own, loaded from column `base` on.  EXACT: the width is a multiple of 8.
+template <bool EXACT> struct Place {
+    int col, base, lo, hi;
+    __device__ __forceinline__ Place(int vector, int width)
+    {
+        col = vector * 8;
+        base = col + 8 <= width ? col : width < 8 ? 0 : width - 8;
+        lo = col < width ? col - base : 8;
+        hi = width < 8 ? width : 8;
+    }
+    __device__ __forceinline__ bool on() const { return lo < 8; }
+    __device__ __forceinline__ bool own(int i) const { return EXACT ? on() : i >= lo && i < hi; }
+    __device__ __forceinline__ bool full() const { return EXACT ? on() : lo == 0 && hi == 8; }
+    template <typename T> __device__ __forceinline__ void load(Raw8<T> &r, const T *row) const
+    {
+        if (EXACT || hi == 8) {
+            r.load(row + base);
+        } else {  // a row narrower than a vector
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r.set(i, row[i < hi ? i : 0]);
+        }
+    }
+    template <typename T> __device__ __forceinline__ void widen(const Raw8<T> &r, float (&out)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) out[i] = own(i) ? r.get(i) : 0.f;
+    }
+    template <typename T> __device__ __forceinline__ void store(T *row, const float (&v)[8]) const
+    {
+        if (full()) {
+            Raw8<T> o;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o.set(i, from_f32<T>(v[i]));
+    #pragma unroll
+            for (int n = 0; n < Raw8<T>::WORDS / 4; ++n)
+                reinterpret_cast<v4 *>(row + base)[n] = v4{o.w[4 * n], o.w[4 * n + 1], o.w[4 * n + 2], o.w[4 * n + 3]};
+        } else if (!EXACT && on()) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (own(i)) row[base + i] = from_f32<T>(v[i]);
+        }
+    }
+};
 
 // Eight values as e4m3, rounded to nearest even; |v| <= 448 but for NaN,
 // which stays NaN.
@@ -91,98 +144,108 @@ __device__ __forceinline__ float row_reduce(float x, Op op, float *s)
 
 constexpr int threads_of(int tpr) { return tpr < 256 ? 256 : tpr; }
 
-template <typename T, typename TW, int TPR, int NV>
+// A workgroup takes rows blockIdx.x * ROWS + group, + gridDim.x * ROWS, ...
+template <typename T, typename TW, int TPR, int NV, bool EXACT>
 __global__ __launch_bounds__(threads_of(TPR)) void k_norm(const NormParams p)
 {
     __shared__ float s_red[16];
     constexpr int ROWS = threads_of(TPR) / TPR;
-    const int lane = threadIdx.x % TPR;
-    const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
+    constexpr bool AHEAD = TPR < 1024;  // the widest rows leave no registers for the next one
+    const int lane = threadIdx.x % TPR, width = p.width;
+    const int64_t stride = (int64_t)gridDim.x * ROWS;
+    int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
     if (ROWS > 1 && row >= p.rows) return;  // whole groups of TPR lanes; no barrier below when ROWS > 1
-    const size_t base = (size_t)row * p.width;
-    const T *x = static_cast<const T *>(p.x) + base;
-    const T *res = p.residual ? static_cast<const T *>(p.residual) + base : nullptr;
-    float r[NV][8], w[NV][8], sum = 0.f;
+    Raw8<TW> w[NV];
+    Raw8<T> x[NV], a[NV];
+    auto fetch = [&](int64_t row) {
+        const size_t at = (size_t)row * width;
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-        const int col = (lane + TPR * n) * 8;
+        for (int n = 0; n < NV; ++n) {
+            const Place<EXACT> v(lane + TPR * n, width);
+            v.load(x[n], static_cast<const T *>(p.x) + at);
+            if (p.residual) v.load(a[n], static_cast<const T *>(p.residual) + at);
+        }
+    };
+    if (AHEAD) fetch(row);
+    if (p.weight)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r[n][i] = 0.f;
-        if (col < p.width) {
-            load8(x, col, p.width, r[n]);
-            if (res) {
+        for (int n = 0; n < NV; ++n) Place<EXACT>(lane + TPR * n, width).load(w[n], static_cast<const TW *>(p.weight));
+    for (; row < p.rows; row += stride) {
+        if (!AHEAD) fetch(row);
+        const size_t at = (size_t)row * width;
+        float r[NV][8], sum = 0.f;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const Place<EXACT> v(lane + TPR * n, width);
+            v.widen(x[n], r[n]);
+            if (p.residual) {
                 float y[8];
-                load8(res, col, p.width, y);
+                v.widen(a[n], y);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) r[n][i] = to_f32(from_f32<T>(r[n][i] + y[i]));
             }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += r[n][i] * r[n][i];
         }
-    }
+        if (AHEAD) fetch(row + stride < p.rows ? row + stride : row);
+        sum = row_reduce<TPR>(sum, Add(), s_red);
+        // every load of the row has come back: residual_out may be the residual itself
+        if (p.residual_out)
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-        const int col = (lane + TPR * n) * 8;
+            for (int n = 0; n < NV; ++n) Place<EXACT>(lane + TPR * n, width).store(static_cast<T *>(p.residual_out) + at, r[n]);
+        const float inv = 1.f / sqrtf(sum / (float)width + p.eps);
+        if (p.inv_rms && lane == 0) p.inv_rms[row] = inv;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[n][i] = 1.f;
-        if (col < p.width) {
-            if (p.weight) load8(static_cast<const TW *>(p.weight), col, p.width, w[n]);
-            if (p.residual_out) store8(static_cast<T *>(p.residual_out) + base, col, p.width, r[n]);
-        }
+        for (int n = 0; n < NV; ++n)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += r[n][i] * r[n][i];
-    }
-    sum = row_reduce<TPR>(sum, Add(), s_red);
-    const float inv = 1.f / sqrtf(sum / (float)p.width + p.eps);
-    if (p.inv_rms && lane == 0) p.inv_rms[row] = inv;
-#pragma unroll
-    for (int n = 0; n < NV; ++n)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r[n][i] = r[n][i] * inv * w[n][i];
+            for (int i = 0; i < 8; ++i) r[n][i] = p.weight ? r[n][i] * inv * w[n].get(i) : r[n][i] * inv;
 
-    if (!p.eight) {
+        if (!p.eight) {
+#pragma unroll
+            for (int n = 0; n < NV; ++n) Place<EXACT>(lane + TPR * n, width).store(static_cast<T *>(p.y) + at, r[n]);
+            continue;
+        }
+        float top[NV], all = 0.f;
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            const int col = (lane + TPR * n) * 8;
-            if (col < p.width) store8(static_cast<T *>(p.y) + base, col, p.width, r[n]);
-        }
-        return;
-    }
-    float top[NV], all = 0.f;
+            const Place<EXACT> v(lane + TPR * n, width);
+            top[n] = 0.f;
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-        top[n] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if ((lane + TPR * n) * 8 + i < p.width) top[n] = Max()(fabsf(r[n][i]), top[n]);
-        all = Max()(top[n], all);
-    }
-    const int lanes = p.group / 8;  // lanes of a group, a power of two
-    const bool whole = p.group == 0 || p.group >= p.width;
-    if (whole) all = row_reduce<TPR>(all, Max(), s_red);
-#pragma unroll
-    for (int n = 0; n < NV; ++n) {
-        float m = all;
-        if (!whole) {
-            m = top[n];
-            for (int o = 1; o < lanes; o <<= 1) m = Max()(m, __shfl_xor(m, o));
-        }
-        float scale = m / E4M3_MAX;
-        if (scale == 0.f) scale = 1.f;
-        const int v = lane + TPR * n, col = v * 8;
-        if (col >= p.width) continue;
-        if (whole ? v == 0 : v % lanes == 0) p.scale[(size_t)row * p.groups + (whole ? 0 : v / lanes)] = scale;
-        float q[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float t = r[n][i] / scale;
-            // a rounding of the quotient may pass the largest value by an ulp
-            q[i] = t > E4M3_MAX ? E4M3_MAX : t < -E4M3_MAX ? -E4M3_MAX : t;
-        }
-        const Bytes8 b = to_e4m3(q);
-        uint8_t *out = static_cast<uint8_t *>(p.y) + base;
-        if (col + 8 <= p.width) *reinterpret_cast<Bytes8 *>(out + col) = b;
-        else
             for (int i = 0; i < 8; ++i)
-                if (col + i < p.width) out[col + i] = (uint8_t)(b.x[i / 4] >> (8 * (i % 4)));
+                if (v.own(i)) top[n] = Max()(fabsf(r[n][i]), top[n]);
+            all = Max()(top[n], all);
+        }
+        const int lanes = p.group / 8;  // lanes of a group, a power of two
+        const bool whole = p.group == 0 || p.group >= width;
+        if (whole) all = row_reduce<TPR>(all, Max(), s_red);
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            float m = all;
+            if (!whole) {
+                m = top[n];
+                for (int o = 1; o < lanes; o <<= 1) m = Max()(m, __shfl_xor(m, o));
+            }
+            float scale = m / E4M3_MAX;
+            if (scale == 0.f) scale = 1.f;
+            const int vec = lane + TPR * n;
+            const Place<EXACT> v(vec, width);
+            if (v.on() && (whole ? vec == 0 : vec % lanes == 0))
+                p.scale[(size_t)row * p.groups + (whole ? 0 : vec / lanes)] = scale;
+            const float inv_scale = 1.f / scale;
+            float q[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float t = r[n][i] * inv_scale;
+                // two roundings may pass the largest value by an ulp or two
+                q[i] = t > E4M3_MAX ? E4M3_MAX : t < -E4M3_MAX ? -E4M3_MAX : t;
+            }
+            const Bytes8 b = to_e4m3(q);
+            uint8_t *out = static_cast<uint8_t *>(p.y) + at + v.base;
+            if (v.full()) *reinterpret_cast<Bytes8 *>(out) = b;
+            else if (!EXACT)
+                for (int i = 0; i < 8; ++i)
+                    if (v.own(i)) out[i] = (uint8_t)(b.x[i / 4] >> (8 * (i % 4)));
+        }
     }
 }
 
@@ -192,66 +255,80 @@ __global__ __launch_bounds__(threads_of(TPR)) void k_norm(const NormParams p)
 // gradient stays in its registers until the end.  Its sums over the
 // workgroup's row groups and then (second kernel) over the workgroups have a
 // fixed order.
-template <typename T, typename TW, int TPR, int NV>
+template <typename T, typename TW, int TPR, int NV, bool EXACT>
 __global__ __launch_bounds__(threads_of(TPR)) void k_norm_back(const NormBackParams p)
 {
     __shared__ float s_red[16];
     __shared__ float s_dw[TPR < 256 ? 256 * 8 : 1];
     constexpr int ROWS = threads_of(TPR) / TPR;
-    const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
-    float w[NV][8], dw[NV][8];
+    constexpr bool AHEAD = TPR < 1024;
+    const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR, width = p.width;
+    const int64_t stride = (int64_t)gridDim.x * ROWS;
+    int64_t row = (int64_t)blockIdx.x * ROWS + group;
+    float dw[NV][8];
+    Raw8<TW> w[NV];
+    Raw8<T> x[NV], y[NV], a[NV];
+    float inv_next = 0.f;
+    auto fetch = [&](int64_t row) {
+        const size_t at = (size_t)row * width;
+        inv_next = p.inv_rms[row];
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const Place<EXACT> v(lane + TPR * n, width);
+            v.load(x[n], static_cast<const T *>(p.x) + at);
+            v.load(y[n], static_cast<const T *>(p.d_y) + at);
+            if (p.d_residual) v.load(a[n], static_cast<const T *>(p.d_residual) + at);
+        }
+    };
+    if (AHEAD && row < p.rows) fetch(row);
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
-        const int col = (lane + TPR * n) * 8;
+        if (p.weight) Place<EXACT>(lane + TPR * n, width).load(w[n], static_cast<const TW *>(p.weight));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            w[n][i] = 1.f;
-            dw[n][i] = 0.f;
-        }
-        if (p.weight && col < p.width) load8(static_cast<const TW *>(p.weight), col, p.width, w[n]);
+        for (int i = 0; i < 8; ++i) dw[n][i] = 0.f;
     }
-    for (int64_t row = (int64_t)blockIdx.x * ROWS + group; row < p.rows; row += (int64_t)gridDim.x * ROWS) {
-        const size_t base = (size_t)row * p.width;
-        const float inv = p.inv_rms[row];
-        float h[NV][8], t[NV][8], sum = 0.f;
+    for (; row < p.rows; row += stride) {
+        if (!AHEAD) fetch(row);
+        const size_t at = (size_t)row * width;
+        const float inv = inv_next;
+        float sum = 0.f;
+        Raw8<T> xr[NV], yr[NV], ar[NV];  // widened again where they are used: a row in fp32 would take twice the registers
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            const int col = (lane + TPR * n) * 8;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) h[n][i] = t[n][i] = 0.f;
-            if (col < p.width) {
-                load8(static_cast<const T *>(p.x) + base, col, p.width, h[n]);
-                load8(static_cast<const T *>(p.d_y) + base, col, p.width, t[n]);
-            }
-        }
-#pragma unroll
-        for (int n = 0; n < NV; ++n)
+            const Place<EXACT> v(lane + TPR * n, width);
+            xr[n] = x[n];
+            yr[n] = y[n];
+            ar[n] = a[n];
+            float h[8], t[8];
+            v.widen(xr[n], h);
+            v.widen(yr[n], t);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                h[n][i] *= inv;
-                dw[n][i] += t[n][i] * h[n][i];
-                t[n][i] *= w[n][i];
-                sum += t[n][i] * h[n][i];
+                h[i] *= inv;
+                dw[n][i] += t[i] * h[i];
+                sum += (p.weight ? t[i] * w[n].get(i) : t[i]) * h[i];
             }
-        sum = row_reduce<TPR>(sum, Add(), s_red) / (float)p.width;
+        }
+        if (AHEAD) fetch(row + stride < p.rows ? row + stride : row);
+        sum = row_reduce<TPR>(sum, Add(), s_red) / (float)width;
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            const int col = (lane + TPR * n) * 8;
-            if (col >= p.width) continue;
+            xr[n].again();
+            yr[n].again();
             float d[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) d[i] = 0.f;
-            if (p.d_residual) load8(static_cast<const T *>(p.d_residual) + base, col, p.width, d);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) d[i] += inv * (t[n][i] - h[n][i] * sum);
-            store8(static_cast<T *>(p.d_x) + base, col, p.width, d);
+            for (int i = 0; i < 8; ++i) {
+                const float t = p.weight ? yr[n].get(i) * w[n].get(i) : yr[n].get(i);
+                d[i] = inv * (t - xr[n].get(i) * inv * sum);
+                if (p.d_residual) d[i] += ar[n].get(i);
+            }
+            Place<EXACT>(lane + TPR * n, width).store(static_cast<T *>(p.d_x) + at, d);
         }
     }
     if (!p.partial) return;
-    float *out = p.partial + (size_t)blockIdx.x * p.width;
+    float *out = p.partial + (size_t)blockIdx.x * width;
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
-        const int col = (lane + TPR * n) * 8;
         if constexpr (ROWS > 1) {
             __syncthreads();
 #pragma unroll
@@ -262,47 +339,60 @@ __global__ __launch_bounds__(threads_of(TPR)) void k_norm_back(const NormBackPar
 #pragma unroll
                     for (int i = 0; i < 8; ++i) dw[n][i] += s_dw[(g * TPR + lane) * 8 + i];
         }
-        if (group == 0 && col < p.width) store8(out, col, p.width, dw[n]);
+        if (group == 0) Place<EXACT>(lane + TPR * n, width).store(out, dw[n]);
     }
 }
 
-// Workgroup: 64 columns, four threads a column, each every fourth partial row.
+// Workgroup: 16 columns, 16 threads a column, each every 16th partial row.
 __global__ __launch_bounds__(256) void k_norm_back_sums(const NormBackParams p, int blocks)
 {
-    __shared__ float s[256];
-    const int64_t col = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
+    __shared__ float s[16][17];
+    const int c = threadIdx.x & 15, r = threadIdx.x >> 4, col = blockIdx.x * 16 + c;
     float sum = 0.f;
-    if (col < p.width)
-        for (int b = threadIdx.x >> 6; b < blocks; b += 4) sum += p.partial[(size_t)b * p.width + col];
-    s[threadIdx.x] = sum;
+    if (col < p.width) {
+#pragma unroll 8
+        for (int b = r; b < blocks; b += 16) sum += p.partial[(size_t)b * p.width + col];
+    }
+    s[r][c] = sum;
     __syncthreads();
-    if (threadIdx.x < 64 && col < p.width)
-        p.d_weight[col] = (s[threadIdx.x] + s[threadIdx.x + 64]) + (s[threadIdx.x + 128] + s[threadIdx.x + 192]);
+    if (r == 0 && col < p.width) {
+        for (int n = 1; n < 16; ++n) sum += s[n][c];
+        p.d_weight[col] = sum;
+    }
 }
 
-// Threads and vectors of a row.  Up to 64 vectors of 8 a row takes the power
-// of two of lanes that covers it; up to 4,096 columns one wave; past that a
-// workgroup.
-template <typename F>
+// Threads and vectors of a row: up to 64 vectors the power of two of lanes
+// that covers it, then one wave up to WAVE vectors a lane, which spares the
+// barriers; past that a workgroup.  At 29,273 rows of 2,048 in bf16 the forward
+// pass takes 92 us with a row a wave (four vectors a lane); the backward pass
+// 100 us so and 88 us with a row a workgroup, as its lanes then hold a quarter
+// of the three rows and the weight's gradient.
+template <int WAVE, typename F>
 hipError_t by_width(int64_t width, F &&f)
 {
+    using std::integral_constant;
     const int64_t v = (width + 7) / 8;
-    if (v <= 16) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 1>());
-    if (v <= 32) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 1>());
-    if (v <= 64) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 1>());
-    if (v <= 128) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 2>());
-    if (v <= 256) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 1>());
-    if (v <= 512) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 2>());
-    if (v <= 1024) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 4>());
-    return f(std::integral_constant<int, 1024>(), std::integral_constant<int, 4>());
+    if (v <= 16) return f(integral_constant<int, 16>(), integral_constant<int, 1>());
+    if (v <= 32) return f(integral_constant<int, 32>(), integral_constant<int, 1>());
+    if (v <= 64) return f(integral_constant<int, 64>(), integral_constant<int, 1>());
+    if (v <= 128) return f(integral_constant<int, 64>(), integral_constant<int, 2>());
+    if constexpr (WAVE >= 4)
+        if (v <= 256) return f(integral_constant<int, 64>(), integral_constant<int, 4>());
+    if (v <= 256) return f(integral_constant<int, 256>(), integral_constant<int, 1>());
+    if (v <= 512) return f(integral_constant<int, 256>(), integral_constant<int, 2>());
+    if (v <= 1024) return f(integral_constant<int, 256>(), integral_constant<int, 4>());
+    return f(integral_constant<int, 1024>(), integral_constant<int, 4>());
 }
 
 template <typename T, typename TW>
 hipError_t norm_typed(const NormParams &p, hipStream_t s)
 {
-    return by_width(p.width, [&](auto tpr, auto nv) {
+    return by_width<4>(p.width, [&](auto tpr, auto nv) {
         constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value, ROWS = threads_of(TPR) / TPR;
-        hipLaunchKernelGGL((k_norm<T, TW, TPR, NV>), dim3((unsigned)((p.rows + ROWS - 1) / ROWS)), dim3(threads_of(TPR)), 0, s, p);
+        const int64_t need = (p.rows + ROWS - 1) / ROWS;
+        const dim3 blocks((unsigned)(need < NORM_BLOCKS ? need : NORM_BLOCKS)), threads(threads_of(TPR));
+        if (p.width % 8 == 0) hipLaunchKernelGGL((k_norm<T, TW, TPR, NV, true>), blocks, threads, 0, s, p);
+        else hipLaunchKernelGGL((k_norm<T, TW, TPR, NV, false>), blocks, threads, 0, s, p);
         return hipGetLastError();
     });
 }
@@ -310,12 +400,15 @@ hipError_t norm_typed(const NormParams &p, hipStream_t s)
 template <typename T, typename TW>
 hipError_t norm_back_typed(const NormBackParams &p, hipStream_t s)
 {
-    return by_width(p.width, [&](auto tpr, auto nv) {
+    return by_width<2>(p.width, [&](auto tpr, auto nv) {
         constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
         const int blocks = norm_back_blocks(p.rows, p.width);
-        hipLaunchKernelGGL((k_norm_back<T, TW, TPR, NV>), dim3((unsigned)blocks), dim3(threads_of(TPR)), 0, s, p);
+        if (p.width % 8 == 0)
+            hipLaunchKernelGGL((k_norm_back<T, TW, TPR, NV, true>), dim3((unsigned)blocks), dim3(threads_of(TPR)), 0, s, p);
+        else
+            hipLaunchKernelGGL((k_norm_back<T, TW, TPR, NV, false>), dim3((unsigned)blocks), dim3(threads_of(TPR)), 0, s, p);
         if (p.partial)
-            hipLaunchKernelGGL(k_norm_back_sums, dim3((unsigned)((p.width + 63) / 64)), dim3(256), 0, s, p, blocks);
+            hipLaunchKernelGGL(k_norm_back_sums, dim3((unsigned)((p.width + 15) / 16)), dim3(256), 0, s, p, blocks);
         return hipGetLastError();
     });
 }
@@ -332,8 +425,10 @@ hipError_t by_types(const P &p, F &&f)
 
 int norm_back_blocks(int64_t rows, int64_t width)
 {
-    const int64_t n = rows * width / 16384;  // elements a workgroup, up to four workgroups per CU
-    return n < 1 ? 1 : n > 1024 ? 1024 : (int)n;
+    // 16,384 elements a workgroup, up to two workgroups a CU (29,273 rows of
+    // 2,048 in bf16: 88 us; with four, whose partial rows are twice as many, 97 us)
+    const int64_t n = rows * width / 16384;
+    return n < 1 ? 1 : n > 512 ? 512 : (int)n;
 }
 
 hipError_t launch_norm(const NormParams &p, hipStream_t s)
