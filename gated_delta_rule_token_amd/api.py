@@ -74,7 +74,7 @@ class GradientPointers(ctypes.Structure):
     """gdr_gradients"""
     _fields_ = [(name, ctypes.c_void_p) for name in (
         "d_o", "d_final_state", "d_q", "d_k", "d_v", "d_gate", "d_beta", "d_initial_state", "d_a_log",
-        "d_dt_bias", "d_gate_scale")]
+        "d_dt_bias", "d_gate_scale")] + [("zero_rest", ctypes.c_int32)]
 
 
 EXPORTS = ("gdr_abi_version", "gdr_status_str", "gdr_last_error", "gdr_validate",
@@ -432,6 +432,9 @@ class Gradients(NamedTuple):
     gate_scale: Optional[torch.Tensor]
 
 
+_TOKEN_ROWS = ("q", "k", "v", "gate", "beta")
+
+
 def backward_workspace_size(problem: Problem) -> int:
     n = ctypes.c_size_t(0)
     check(load_library().gdr_backward_workspace_size(ctypes.byref(problem), ctypes.byref(n)))
@@ -481,22 +484,17 @@ def backward(q, k, v, d_o, *, gate=None, beta=None, a_log=None, dt_bias=None, ga
                                   initial_state=initial_state, final_state=d_final_state))
     if want_initial_state is None:
         want_initial_state = initial_state is not None
-    # rows of tokens outside every request are not written by the kernels
-    rows = torch.zeros if cu_seqlens is not None or seq_lens is not None or p.batch == 0 else torch.empty
-    grads = {}
-    for name, like, shape, new in (("q", q, None, rows), ("k", k, None, rows), ("v", v, None, rows),
-                                   ("gate", gate, None, rows), ("beta", beta, None, rows),
-                                   ("initial_state", None, states if want_initial_state else None, torch.empty),
-                                   ("a_log", a_log, None, torch.empty), ("dt_bias", dt_bias, None, torch.empty),
-                                   ("gate_scale", gate_scale, None, torch.empty)):
-        given = None if out is None else getattr(out, name)
-        if like is None and shape is None:
+    grads, zero_rest = {}, out is None
+    for name, like in (("q", q), ("k", k), ("v", v), ("gate", gate), ("beta", beta), ("initial_state", None),
+                       ("a_log", a_log), ("dt_bias", dt_bias), ("gate_scale", gate_scale)):
+        if like is None and not (name == "initial_state" and want_initial_state):
             grads[name] = None
             continue
-        shape = tuple(like.shape) if shape is None else shape
-        dtype = torch.float32 if like is None else like.dtype
+        shape, dtype = (states, torch.float32) if like is None else (tuple(like.shape), like.dtype)
+        given = None if out is None else getattr(out, name)
         if given is None:
-            given = new(shape, dtype=dtype, device=dev)
+            # beside gradients of the caller's, whose other rows stay, zeros go into the new ones here
+            given = (torch.empty if zero_rest or name not in _TOKEN_ROWS else torch.zeros)(shape, dtype=dtype, device=dev)
         elif tuple(_need(given, "out." + name, dtype, dev).shape) != shape:
             raise GDRError("GDR_E_INVALID", "out.%s has shape %s, expected %s" % (name, tuple(given.shape), shape))
         grads[name] = given
@@ -506,7 +504,7 @@ def backward(q, k, v, d_o, *, gate=None, beta=None, a_log=None, dt_bias=None, ga
     t = Tensors(q=_ptr(q), k=_ptr(k), v=_ptr(v), gate=_ptr(gate), beta=_ptr(beta), a_log=_ptr(a_log),
                 dt_bias=_ptr(dt_bias), cu_seqlens=_ptr(cu_seqlens), initial_state=_ptr(initial_state),
                 gate_scale=_ptr(gate_scale), seq_lens=_ptr(seq_lens))
-    g = GradientPointers(d_o=_ptr(d_o), d_final_state=_ptr(d_final_state),
+    g = GradientPointers(d_o=_ptr(d_o), d_final_state=_ptr(d_final_state), zero_rest=int(zero_rest),
                          **{"d_" + name: _ptr(x) for name, x in grads.items()})
     _enqueue(lib.gdr_backward, dev, ctypes.byref(p), ctypes.byref(t), ctypes.byref(g), _ptr(workspace),
              workspace.numel() * workspace.element_size())

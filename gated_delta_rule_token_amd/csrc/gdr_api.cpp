@@ -446,6 +446,7 @@ gdr_status check_gradients(const gdr_problem *p, const gdr_tensors *t, const gdr
 {
     const int64_t T = p->total_tokens;
     const bool decays = gdr::rule_decays(p->update_rule), has_beta = gdr::rule_has_beta(p->update_rule);
+    if (g->zero_rest != 0 && g->zero_rest != 1) return fail(GDR_E_INVALID, "zero_rest must be 0 or 1");
     if (T > 0 && (!g->d_o || !g->d_q || !g->d_k || !g->d_v)) return fail(GDR_E_INVALID, "d_o, d_q, d_k and d_v are required");
     if ((g->d_gate && !decays) || (T > 0 && decays && !g->d_gate))
         return fail(GDR_E_INVALID, "d_gate must be given exactly when the update_rule decays");
@@ -607,6 +608,8 @@ gdr_status gdr_backward(const gdr_problem *problem, const gdr_tensors *tensors, 
 
     hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t err = gdr::launch_back_table(a, s);
+    const bool all = !tensors->cu_seqlens && !tensors->seq_lens && problem->batch > 0;  // no token without a request
+    if (err == hipSuccess && gradients->zero_rest && !all) err = gdr::launch_back_zero(a, (int)dsize(problem->act_dtype), s);
     if (err == hipSuccess && problem->batch > 0)
         err = problem->act_dtype == GDR_F16    ? gdr::launch_back_f16(a, retrieves, s)
               : problem->act_dtype == GDR_BF16 ? gdr::launch_back_bf16(a, retrieves, s)

@@ -466,13 +466,16 @@ template <int DK, typename TA, int NT, bool VEC> struct StageRows {
 };
 
 // ---------------------------------------------------------------- prologue
-// One workgroup per (chunk, q/k head); the value heads that share the head in
-// turn.  Of fp32 rows it leaves k and q as operand fragments with channels as
-// rows (KT, QT) for k_back_grad, whose LDS has no room for them.  The products K K^T and Q K^T are formed once
-// for the value heads.  Each unit lower triangular inverse goes by 16x16
-// blocks on the fp32 matrix instruction: the diagonal ones by forward
-// substitution, a thread a column; then wave j takes block column j down,
-// T_ij = -T_ii sum_k N_ik T_kj, its T_kj staying in the accumulators' layout.
+// One workgroup per (chunk, value head).  Value heads that share a q/k head
+// each form its K K^T and Q K^T: one workgroup for all of them, the heads in
+// turn, took 28 us of the smallest call against 19 us, and gained 5 % of the
+// kernel on a long batch of two heads a group (372 and 392 us).  Of fp32 rows it
+// leaves k and q as operand fragments with channels as rows (KT, QT) for
+// k_back_grad, whose LDS has no room for them.  Each unit lower triangular
+// inverse goes by 16x16 blocks on the fp32 matrix instruction: the diagonal
+// ones by forward substitution, a thread a column; then wave j takes block
+// column j down, T_ij = -T_ii sum_k N_ik T_kj, its T_kj staying in the
+// accumulators' layout.
 template <int DK, typename TA, bool RETR, bool VEC>
 __global__ __launch_bounds__(256) void k_back_prep(const BackParams a)
 {
@@ -487,19 +490,50 @@ __global__ __launch_bounds__(256) void k_back_prep(const BackParams a)
     __shared__ float s_rq[C], s_rk[C];
 
     const Params &p = a.p;
-    const int ci = blockIdx.x / p.H, hq = blockIdx.x % p.H;
+    const int ci = blockIdx.x / p.HV, h = blockIdx.x % p.HV, R = p.HV / p.H, hq = h / R;
     if (ci >= a.off[p.B]) return;
     int64_t t0;
     int cnt;
     chunk_tokens(a, ci, C, t0, cnt);
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), c = lane & 15, j = lane >> 4;
-    if (hq == 0 && tid == 0) {
+    if (h == 0 && tid == 0) {
         a.where[2 * ci] = (int32_t)t0;
         a.where[2 * ci + 1] = cnt;
     }
     uint16_t *Kr = reinterpret_cast<uint16_t *>(mem), *Qr = Kr + NP * RW::PLANE;
 
+    // decays and rates, a lane a token
+    if (wave == 0) {
+        double g = 0.0;
+        float b = 0.f;
+        if (lane < cnt) {
+            const size_t th = (size_t)(t0 + lane) * p.HV + h;
+            if (a.decays) {
+                // a decay of -inf (a reset) would make differences of G undefined; e^-1e5 is 0 too
+                const float x = log_decay(p, th, h);
+                g = x < -1e5f ? -1e5 : (double)x;
+            }
+            b = RETR ? update_rate(p, th) : 1.f;
+        }
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const double x = __shfl_up(g, o);
+            if (lane >= o) g += x;
+        }
+        const double end = __shfl(g, C - 1);
+        if (lane < C) {
+            s_G[lane] = g;
+            s_b[lane] = b;
+            float *sc = a.sc + (size_t)blockIdx.x * (BACK_SC * C);
+            const float hi = (float)g;
+            sc[SC_EG * C + lane] = exp_of(g);
+            sc[SC_KD * C + lane] = exp_of(end - g);
+            sc[SC_B * C + lane] = b;
+            sc[SC_GH * C + lane] = hi;
+            sc[SC_GL * C + lane] = (float)(g - (double)hi);
+        }
+    }
     // rows of q and k, and the reciprocals of their norms
     {
         StageRows<DK, TA, 256, VEC> k, q;
@@ -534,8 +568,8 @@ __global__ __launch_bounds__(256) void k_back_prep(const BackParams a)
     __syncthreads();
 
     if constexpr (NP == 3) {
-        uint16_t *act = a.act + (size_t)blockIdx.x * 2 * NP * ACT * BLOCK;
-        for (int n = wave; n < 2 * ACT; n += 4) {
+        uint16_t *act = a.act + ((size_t)ci * p.H + hq) * 2 * NP * ACT * BLOCK;
+        for (int n = h % R == 0 ? wave : 2 * ACT; n < 2 * ACT; n += 4) {
             const int kind = n / ACT, blk = n % ACT;
             b8 v[NP];
             RW::col_operand(kind == 0 ? Kr : Qr, blk / MX, blk % MX, v);
@@ -579,46 +613,16 @@ __global__ __launch_bounds__(256) void k_back_prep(const BackParams a)
     __syncthreads();  // the staged rows give way to L and the diagonal inverses
 
     float *Lm = reinterpret_cast<float *>(mem), *inv = Lm + C * LC;
-    const int R = p.HV / p.H;
     const f4 zero = {0.f, 0.f, 0.f, 0.f};
-    for (int r = 0; r < R; ++r) {
-        const int h = hq * R + r;
-        const size_t rec = (size_t)ci * p.HV + h;
+    {
+        const size_t rec = blockIdx.x;
         constexpr size_t STRIDE = (size_t)NT * BLOCK;
         uint16_t *pt = a.tri + rec * 3 * (RETR ? 3 : 1) * STRIDE;  // P^T; (I + diag(b) L)^-T; (I + L diag(b))^-1
-        if (wave == 0) {
-            double g = 0.0;
-            float b = 0.f;
-            if (lane < cnt) {
-                const size_t th = (size_t)(t0 + lane) * p.HV + h;
-                if (a.decays) {
-                    // a decay of -inf (a reset) would make differences of G undefined; e^-1e5 is 0 too
-                    const float x = log_decay(p, th, h);
-                    g = x < -1e5f ? -1e5 : (double)x;
-                }
-                b = RETR ? update_rate(p, th) : 1.f;
-            }
-#pragma unroll
-            for (int o = 1; o < 64; o <<= 1) {
-                const double x = __shfl_up(g, o);
-                if (lane >= o) g += x;
-            }
-            const double end = __shfl(g, C - 1);
-            if (lane < C) {
-                s_G[lane] = g;
-                s_b[lane] = b;
-                float *sc = a.sc + rec * (BACK_SC * C);
-                const float hi = (float)g;
-                sc[SC_EG * C + lane] = exp_of(g);
-                sc[SC_KD * C + lane] = exp_of(end - g);
-                sc[SC_B * C + lane] = b;
-                sc[SC_GH * C + lane] = hi;
-                sc[SC_GL * C + lane] = (float)(g - (double)hi);
-                sc[SC_RQ * C + lane] = s_rq[lane];
-                sc[SC_RK * C + lane] = s_rk[lane];
-            }
+        if (tid < C) {
+            float *sc = a.sc + rec * (BACK_SC * C);
+            sc[SC_RQ * C + tid] = s_rq[tid];
+            sc[SC_RK * C + tid] = s_rk[tid];
         }
-        __syncthreads();
 #pragma unroll
         for (int n = 0; n < SLOTS; ++n) {
             const int m = tm[n], kb = tk[n];
@@ -696,7 +700,6 @@ __global__ __launch_bounds__(256) void k_back_prep(const BackParams a)
                 }
             }
         }
-        __syncthreads();  // before the next head overwrites s_G, s_b, L
     }
 }
 
@@ -1727,7 +1730,7 @@ hipError_t launch_back_typed(const BackParams &a, hipStream_t s)
     const Params &p = a.p;
     const unsigned per_chunk = (unsigned)a.chunks * p.H, pairs = (unsigned)p.B * p.HV, tiles = a.VB / 4;
     const dim3 chains(pairs * a.nseg * tiles), block(256);
-    hipLaunchKernelGGL((k_back_prep<DK, TA, RETR, VEC>), dim3(per_chunk), block, 0, s, a);
+    hipLaunchKernelGGL((k_back_prep<DK, TA, RETR, VEC>), dim3((unsigned)a.chunks * p.HV), block, 0, s, a);
     if (a.nseg > 1) {
         hipLaunchKernelGGL((k_back_states<DK, TA, RETR, VEC, true>), dim3(pairs * a.nseg * (tiles + Geo<DK>::KB / 4)), block, 0, s, a);
         hipLaunchKernelGGL((k_back_join<DK, false, VEC>), dim3(pairs * tiles), block, 0, s, a);

@@ -59,6 +59,8 @@ hipError_t launch_back_table(const BackParams &a, hipStream_t s);
 hipError_t launch_back_f32(const BackParams &a, bool retrieves, hipStream_t s);
 hipError_t launch_back_f16(const BackParams &a, bool retrieves, hipStream_t s);
 hipError_t launch_back_bf16(const BackParams &a, bool retrieves, hipStream_t s);
+// Zero in the gradient rows of tokens that no request covers (after the table).
+hipError_t launch_back_zero(const BackParams &a, int act_bytes, hipStream_t s);
 // After the gradients: parameters of the raw-gate arm and a rate shared by the heads.
 hipError_t launch_back_sums(const BackParams &a, hipStream_t s);
 

@@ -260,7 +260,8 @@ gdr_status gdr_forward_noalloc(const gdr_problem *problem, const gdr_tensors *te
  * Requests must not overlap: with cu_seqlens, request b covers
  * [m_b, m_(b+1)) where m_b is the largest of the entries up to b, clamped to
  * [0, T] (for a non-decreasing cu_seqlens the forward's own range).  Gradient
- * rows of tokens that no request covers are left as they were.
+ * rows of tokens that no request covers are left as they were, or set to zero
+ * with zero_rest.
  *
  * All arithmetic and every sum is in fp32 (cumulative decays in fp64);
  * gradients are rounded to nearest once, on store.  Sums over tokens and
@@ -274,6 +275,7 @@ typedef struct {
     float *d_beta;                /* beta's shape, of beta as given (through the sigmoid); iff the rule has it */
     float *d_initial_state;       /* (B, HV, dv, dk), or NULL when not wanted */
     float *d_a_log, *d_dt_bias, *d_gate_scale; /* (HV): non-NULL iff the tensor itself is */
+    int32_t zero_rest;            /* 1: zero in the rows (of d_q .. d_beta) of tokens that no request covers */
 } gdr_gradients;
 
 /* Bytes of device workspace gdr_backward needs for `problem`: per token and
