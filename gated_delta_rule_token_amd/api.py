@@ -470,7 +470,7 @@ def backward(q, k, v, d_o, *, gate=None, beta=None, a_log=None, dt_bias=None, ga
         _need(t, name, dt, dev)
     if k is None or v is None or d_o is None:
         raise GDRError("GDR_E_INVALID", "k, v and d_o are required")
-    if batch is None and initial_state is None and d_final_state is not None:
+    if batch is None and initial_state is None and d_final_state is not None and d_final_state.dim() == 4:
         batch = d_final_state.shape[0]
     p = build_problem(q, k, v, gate=gate, beta=beta, a_log=a_log, dt_bias=dt_bias, cu_seqlens=cu_seqlens,
                       initial_state=initial_state, update_rule=update_rule, gate_activation=gate_activation,

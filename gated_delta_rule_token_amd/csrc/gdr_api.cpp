@@ -372,15 +372,25 @@ gdr_status check_backward(const gdr_problem *p)
     return GDR_OK;
 }
 
-// Segments of the backward pass's chains, `chains` workgroups of them.
+// Segments of the backward pass's chains, `chains` workgroups of them.  With n
+// segments the two chains of N steps take about 2 N / n steps each (a segment's
+// map first, then its results) and n hand-overs from segment to segment, worth
+// one step together with the later launches' latency; workgroups past one per
+// CU only slow each other, but for bf16's (two a CU) in long chains.  Measured,
+// bf16, dk = dv = 128, one request, 1 segment against the rule's choice: 4,096
+// tokens x 8 heads 697 / 246 us (n = 16; n = 32: 291), 512 x 4 heads 140 / 127
+// (5), 16,384 x 64 heads 4618 / 4214 (4), 65,536 x 16 heads 15.7 / 4.74 ms (16;
+// n = 8: 5.0); and where it stays at 1: 512 x 32 heads 162 / 175 with 4, four
+// requests of 2,048 x 16 heads 684 / 701 with 4, 8,192 x 128 heads 3160 / 4113
+// with 4.
 int32_t back_segments(const gdr_problem *p, int64_t chains)
 {
     if (chains < 1) return 1;
-    const int64_t per_req = (p->total_tokens + p->batch - 1) / p->batch / gdr::back_chunk(p->head_dim_k);
-    int64_t n = 256 / chains;
-    if (n > per_req / 4) n = per_req / 4;
-    if (n > 16) n = 16;
-    return n >= 3 ? (int32_t)n : 1;
+    const int64_t N = (p->total_tokens + p->batch - 1) / p->batch / gdr::back_chunk(p->head_dim_k);
+    const bool two = N >= 128 && p->act_dtype == GDR_BF16 && p->head_dim_k <= 128;
+    int64_t n = (two ? 512 : 256) / chains;
+    n = std::min(std::min(n, (int64_t)(2.0 * std::sqrt((double)N))), (int64_t)64);
+    return n >= 3 && n * N >= 40 ? (int32_t)n : 1;
 }
 
 // Carve the workspace (256-byte aligned pieces) at `base` into `a`, with the
@@ -479,7 +489,8 @@ gdr_status check_gradients(const gdr_problem *p, const gdr_tensors *t, const gdr
         range_of("seq_lens", t->seq_lens, (size_t)p->batch * 4), range_of("initial_state", t->initial_state, state),
         range_of("d_final_state", g->d_final_state, state),
     };
-    // each workgroup reads its rows of d_final_state before it writes those of d_initial_state
+    // a workgroup reads its rows of d_final_state before it writes those of
+    // d_initial_state; in segments k_back_join reads them, a launch earlier
     return check_overlap(outs, 10, ins, 13, 5, 12);
 }
 

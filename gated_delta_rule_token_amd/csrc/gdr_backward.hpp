@@ -898,41 +898,77 @@ template <int KB> __device__ __forceinline__ void get_state(f4 (&S)[KB], const f
     for (int kb = 0; kb < KB; ++kb) S[kb] = get_frag(at + kb * FRAG);
 }
 
-// One workgroup per (request, value head, 64 state rows): the states at the
-// segments' starts (backwards: at their ends), one after the other.
+// One workgroup per (request, value head, 16 state rows): the states at the
+// segments' starts (backwards: at their ends), one after the other.  A wave
+// forms two 16-channel blocks of each state from all of the one before, which
+// goes round the waves through LDS as planes; its rows of M and its carry are
+// loaded a segment ahead.
 template <int DK, bool REVERSE, bool VEC>
-__global__ __launch_bounds__(256) void k_back_join(const BackParams a)
+__global__ __launch_bounds__(DK * 2) void k_back_join(const BackParams a)
 {
     using G = Geo<DK>;
     constexpr int KB = G::KB, KX = G::KX;
+    __shared__ __align__(16) uint16_t s_x[2][3 * KX * BLOCK];
     const Params &p = a.p;
-    const int tiles = a.VB / 4, tile = blockIdx.x % tiles, bh = blockIdx.x / tiles;
+    const int vb = blockIdx.x % a.VB, bh = blockIdx.x / a.VB;
     const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane & 15, j = lane >> 4;
-    const int vb = tile * 4 + wave, col = 16 * vb + c;
     const float *init = REVERSE ? a.d_final : p.init;
-    f4 S[KB];
-    load_state<VEC>(S, init ? init + (size_t)bh * p.dv * p.dk : nullptr, col, p.dv, p.dk, j);
+    f4 m[2][KB], carry[2];
+    auto rows = [&](int seg) { return (REVERSE ? a.seg_m : a.seg_mt) + seg_at(a, bh, seg, KB, 2 * wave, KB); };
+    auto add = [&](int seg) { return a.seg_carry + seg_at(a, bh, seg, a.VB, vb, KB) + 2 * wave * FRAG; };
+    auto fetch = [&](const float *M, int kb) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) m[h][kb] = get_frag(M + (h * KB + kb) * FRAG);
+    };
+    {
+        const int seg = REVERSE ? a.nseg - 1 : 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) carry[h] = get_frag(add(seg) + h * FRAG);
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) fetch(rows(seg), kb);
+    }
+    f4 S[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        S[x] = f4{0.f, 0.f, 0.f, 0.f};
+        if (init)
+            S[x] = widen(load_raw4(ChunkRows(init + (size_t)bh * p.dv * p.dk, p.dv, p.dk, p.dk),
+                                   At4<VEC, float>(16 * vb + c, p.dk, 16 * (2 * wave + x) + 4 * j, p.dk)));
+    }
     for (int n = 0; n < a.nseg; ++n) {
         const int seg = REVERSE ? a.nseg - 1 - n : n;
-        put_state<KB>(a.seg_state + seg_at(a, bh, seg, a.VB, vb, KB), S);
+        float *out = a.seg_state + seg_at(a, bh, seg, a.VB, vb, KB) + 2 * wave * FRAG;
+        uint16_t *x = s_x[n & 1];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            put_frag_cols(out + h * FRAG, S[h]);
+            put_half(x + wave * BLOCK, KX * BLOCK, lane, h, S[h]);
+        }
         if (n + 1 == a.nseg) break;
-        f4 next[KB];
-        get_state<KB>(next, a.seg_carry + seg_at(a, bh, seg, a.VB, vb, KB));
-        b8 x[KX][3];
+        lds_barrier();  // one a segment: the other buffer's readers have passed the last one
+        const int ahead = min(n + 1, a.nseg - 2), to = REVERSE ? a.nseg - 1 - ahead : ahead;
+        arrive(carry);
 #pragma unroll
-        for (int y = 0; y < KX; ++y) split8<3>(S[2 * y], S[2 * y + 1], x[y]);
-        const float *M = (REVERSE ? a.seg_m : a.seg_mt) + seg_at(a, bh, seg, KB, 0, KB);
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {  // rows kb of the result, fragment blocks (kb, 2 y) and (kb, 2 y + 1)
-#pragma unroll
-            for (int y = 0; y < KX; ++y) {
-                b8 m[3];
-                split8<3>(get_frag(M + (kb * KB + 2 * y) * FRAG), get_frag(M + (kb * KB + 2 * y + 1) * FRAG), m);
-                next[kb] = mm(m, x[y], next[kb]);
-            }
+        for (int h = 0; h < 2; ++h) {
+            S[h] = carry[h];
+            carry[h] = get_frag(add(to) + h * FRAG);
         }
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) S[kb] = next[kb];
+        for (int y = 0; y < KX; ++y) {
+            b8 r[2][3], v[3];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                arrive(m[h][2 * y]);
+                arrive(m[h][2 * y + 1]);
+                split8<3>(m[h][2 * y], m[h][2 * y + 1], r[h]);
+            }
+            fetch(rows(to), 2 * y);
+            fetch(rows(to), 2 * y + 1);
+#pragma unroll
+            for (int q = 0; q < 3; ++q) v[q] = get_block(x + (q * KX + y) * BLOCK);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) S[h] = mm(r[h], v, S[h]);
+        }
     }
 }
 
@@ -1733,12 +1769,12 @@ hipError_t launch_back_typed(const BackParams &a, hipStream_t s)
     hipLaunchKernelGGL((k_back_prep<DK, TA, RETR, VEC>), dim3((unsigned)a.chunks * p.HV), block, 0, s, a);
     if (a.nseg > 1) {
         hipLaunchKernelGGL((k_back_states<DK, TA, RETR, VEC, true>), dim3(pairs * a.nseg * (tiles + Geo<DK>::KB / 4)), block, 0, s, a);
-        hipLaunchKernelGGL((k_back_join<DK, false, VEC>), dim3(pairs * tiles), block, 0, s, a);
+        hipLaunchKernelGGL((k_back_join<DK, false, VEC>), dim3(pairs * a.VB), dim3(DK * 2), 0, s, a);
     }
     hipLaunchKernelGGL((k_back_states<DK, TA, RETR, VEC, false>), chains, block, 0, s, a);
     if (a.nseg > 1) {
         hipLaunchKernelGGL((k_back_chain<DK, TA, RETR, VEC, true>), chains, block, 0, s, a);
-        hipLaunchKernelGGL((k_back_join<DK, true, VEC>), dim3(pairs * tiles), block, 0, s, a);
+        hipLaunchKernelGGL((k_back_join<DK, true, VEC>), dim3(pairs * a.VB), dim3(DK * 2), 0, s, a);
     }
     hipLaunchKernelGGL((k_back_chain<DK, TA, RETR, VEC, false>), chains, block, 0, s, a);
     hipLaunchKernelGGL((k_back_grad<DK, TA, RETR, VEC>), dim3(per_chunk), dim3(512), 0, s, a);
