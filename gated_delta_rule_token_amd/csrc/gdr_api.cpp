@@ -614,14 +614,13 @@ gdr_status gdr_backward(const gdr_problem *problem, const gdr_tensors *tensors, 
     a.d_a_log = gradients->d_a_log;
     a.d_dt_bias = gradients->d_dt_bias;
     a.d_gate_scale = gradients->d_gate_scale;
+    a.zero_rest = gradients->zero_rest && (tensors->cu_seqlens || tensors->seq_lens || problem->batch == 0);
     if (problem->beta_per_token) a.d_rate = gradients->d_beta;  // a.d_beta: workspace, per head
     else a.d_beta = gradients->d_beta;
 
     hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t err = gdr::launch_back_table(a, s);
-    const bool all = !tensors->cu_seqlens && !tensors->seq_lens && problem->batch > 0;  // no token without a request
-    if (err == hipSuccess && gradients->zero_rest && !all) err = gdr::launch_back_zero(a, (int)dsize(problem->act_dtype), s);
-    if (err == hipSuccess && problem->batch > 0)
+    if (err == hipSuccess && (problem->batch > 0 || (a.zero_rest && problem->total_tokens > 0)))
         err = problem->act_dtype == GDR_F16    ? gdr::launch_back_f16(a, retrieves, s)
               : problem->act_dtype == GDR_BF16 ? gdr::launch_back_bf16(a, retrieves, s)
                                                : gdr::launch_back_f32(a, retrieves, s);

@@ -71,46 +71,6 @@ hipError_t launch_back_table(const BackParams &a, hipStream_t s)
     return hipGetLastError();
 }
 
-// ---------------------------------------------------------------- rows of no request
-// Zero in the gradient rows of tokens that no request covers: those before the
-// first and after the last one of cu_seqlens, and those past seq_lens[b].
-__global__ __launch_bounds__(256) void k_back_zero(const BackParams a, int act)
-{
-    const Params &p = a.p;
-    const int64_t first = p.B > 0 ? a.tok[0] : 0;
-    const int64_t last = p.B > 0 ? (int64_t)a.tok[2 * p.B - 2] + a.tok[2 * p.B - 1] : 0;
-    const int gate = p.gate_dt ? 2 : 4;
-    auto clear = [&](void *base, size_t row, size_t bytes) {  // an even number of bytes a row
-        if (!base) return;
-        uint16_t *at = reinterpret_cast<uint16_t *>(static_cast<char *>(base) + row * bytes);
-        for (size_t n = threadIdx.x; n < bytes / 2; n += 256) at[n] = 0;
-    };
-    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
-        if (p.cu_seqlens) {
-            if (t >= first && t < last) {  // on to the first token of this workgroup after them
-                const int64_t skip = (last - t + gridDim.x - 1) / gridDim.x;
-                t += (skip - 1) * gridDim.x;
-                continue;
-            }
-        } else if (p.L > 0 && t % p.L < a.tok[2 * (t / p.L) + 1]) {
-            continue;
-        }
-        clear(a.dq, t, (size_t)p.H * p.dk * act);
-        clear(a.dk, t, (size_t)p.H * p.dk * act);
-        clear(a.dv, t, (size_t)p.HV * p.dv * act);
-        if (a.decays) clear(a.d_gate, t, (size_t)p.HV * gate);
-        if (a.d_rate) clear(a.d_rate, t, 4);
-        else if (p.beta) clear(a.d_beta, t, (size_t)p.HV * 4);
-    }
-}
-
-hipError_t launch_back_zero(const BackParams &a, int act_bytes, hipStream_t s)
-{
-    if (a.p.T == 0) return hipSuccess;
-    hipLaunchKernelGGL(k_back_zero, dim3((unsigned)(a.p.T < 1024 ? a.p.T : 1024)), dim3(256), 0, s, a, act_bytes);
-    return hipGetLastError();
-}
-
 // ---------------------------------------------------------------- sums over chunks and heads
 // Block (256) sum in a fixed order.
 __device__ __forceinline__ float block_sum(float x, float *s)
@@ -173,8 +133,8 @@ hipError_t launch_back_sums(const BackParams &a, hipStream_t s)
 //   d_dt_bias = sum over rows of d_a,  d_scale = sum over rows of d_decay softplus(x)
 // Memory-bound and elementwise but for the sums.  A thread keeps V columns
 // (heads) and walks down the rows of its workgroup's slice, so that the sums
-// stay in registers; the slices' sums are joined in a fixed order by a second
-// kernel.  V = 8 where a row is a whole number of 16-byte vectors.
+// stay in registers; the sums of several slices are joined in a fixed order by
+// a second kernel.  V = 8 where a row is a whole number of 16-byte vectors.
 // The elementwise functions are the hardware's 2^x and 1/x (an ulp each) with
 // short series of their own, good to a few ulps: with expf, log1pf and IEEE
 // divisions the kernel was bound by its 200 VALU instructions an element
@@ -283,7 +243,8 @@ __global__ __launch_bounds__(GATE_THREADS) void k_gate_back(const GateBackParams
             if ((int)threadIdx.x < outs)
                 for (int q = 1; q < parts; ++q) sum += s_sum[q * outs + threadIdx.x];
         }
-        if (n < outs && part == 0 && at < g.heads) g.partial[((size_t)blockIdx.x * 2 + which) * g.heads + at] = sum;
+        if (n < outs && part == 0 && at < g.heads)
+            (gridDim.x > 1 ? g.partial + ((size_t)blockIdx.x * 2 + which) * g.heads : which ? g.d_scale : g.d_dt_bias)[at] = sum;
     }
 }
 
@@ -298,9 +259,12 @@ __global__ __launch_bounds__(256) void k_gate_back_sums(const GateBackParams g, 
     if (threadIdx.x == 0) (which ? g.d_scale : g.d_dt_bias)[h] = sum;
 }
 
+// Slices of 4096 elements, up to two workgroups per CU.  Up to 8192 elements
+// of whole vectors are one slice, whose sums need no second launch (256 x 32 in
+// fp16: GATE1 us against GATE2 in two slices).
 int gate_back_blocks(int64_t rows, int heads)
 {
-    const int64_t n = rows * heads / 4096;  // elements of a slice, up to two workgroups per CU
+    const int64_t n = rows * heads <= 8192 && heads % 8 == 0 ? 1 : rows * heads / 4096;
     return n < 1 ? 1 : n > 512 ? 512 : (int)n;
 }
 
@@ -320,7 +284,7 @@ hipError_t launch_gate_backward(const GateBackParams &g, hipStream_t s)
     if (g.dt == 1) launch_gate_typed<half_t>(g, slices, s);
     else if (g.dt == 2) launch_gate_typed<bf16_t>(g, slices, s);
     else launch_gate_typed<float>(g, slices, s);
-    hipLaunchKernelGGL(k_gate_back_sums, dim3(g.heads, 2), dim3(256), 0, s, g, slices);
+    if (slices > 1) hipLaunchKernelGGL(k_gate_back_sums, dim3(g.heads, 2), dim3(256), 0, s, g, slices);
     return hipGetLastError();
 }
 

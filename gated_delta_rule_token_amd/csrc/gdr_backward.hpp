@@ -465,6 +465,42 @@ template <int DK, typename TA, int NT, bool VEC> struct StageRows {
     }
 };
 
+// Zero in the gradient rows of tokens that no request covers: those before the
+// first and after the last one of cu_seqlens, and those past seq_lens[b].  Run
+// by the workgroups `n` of `of` that have no chunk, of which there is always
+// one (a request leaves part of its last chunk or the budget's spare one), and
+// the more the fewer tokens are covered.
+__device__ __forceinline__ void zero_rest(const BackParams &a, int64_t n, int64_t of, int act)
+{
+    const Params &p = a.p;
+    const int64_t first = p.B > 0 ? a.tok[0] : 0;
+    const int64_t last = p.B > 0 ? (int64_t)a.tok[2 * p.B - 2] + a.tok[2 * p.B - 1] : 0;
+    auto clear = [&](void *base, size_t row, size_t bytes) {  // an even number of bytes a row
+        char *at = static_cast<char *>(base) + row * bytes;
+        if (bytes % 16 == 0)
+            for (size_t i = threadIdx.x; i < bytes / 16; i += 256) reinterpret_cast<u4 *>(at)[i] = u4{0, 0, 0, 0};
+        else
+            for (size_t i = threadIdx.x; i < bytes / 2; i += 256) reinterpret_cast<uint16_t *>(at)[i] = 0;
+    };
+    for (int64_t t = n; t < p.T; t += of) {
+        int64_t from = first, end = last;  // of the covered tokens that t may be one of
+        if (!p.cu_seqlens && p.B > 0) {
+            from = t / p.L * p.L;
+            end = from + a.tok[2 * (t / p.L) + 1];
+        }
+        if (t >= from && t < end) {  // on to this workgroup's last token before their end
+            t += (end - 1 - t) / of * of;
+            continue;
+        }
+        clear(a.dq, t, (size_t)p.H * p.dk * act);
+        clear(a.dk, t, (size_t)p.H * p.dk * act);
+        clear(a.dv, t, (size_t)p.HV * p.dv * act);
+        if (a.decays) clear(a.d_gate, t, (size_t)p.HV * (p.gate_dt ? 2 : 4));
+        if (a.d_rate) clear(a.d_rate, t, 4);
+        else if (a.d_beta) clear(a.d_beta, t, (size_t)p.HV * 4);
+    }
+}
+
 // ---------------------------------------------------------------- prologue
 // One workgroup per (chunk, value head).  Value heads that share a q/k head
 // each form its K K^T and Q K^T: one workgroup for all of them, the heads in
@@ -490,8 +526,11 @@ __global__ __launch_bounds__(256) void k_back_prep(const BackParams a)
     __shared__ float s_rq[C], s_rk[C];
 
     const Params &p = a.p;
-    const int ci = blockIdx.x / p.HV, h = blockIdx.x % p.HV, R = p.HV / p.H, hq = h / R;
-    if (ci >= a.off[p.B]) return;
+    const int ci = blockIdx.x / p.HV, h = blockIdx.x % p.HV, R = p.HV / p.H, hq = h / R, used = a.off[p.B];
+    if (ci >= used) {
+        if (a.zero_rest) zero_rest(a, blockIdx.x - used * p.HV, (a.chunks - used) * p.HV, sizeof(TA));
+        return;
+    }
     int64_t t0;
     int cnt;
     chunk_tokens(a, ci, C, t0, cnt);
@@ -1767,6 +1806,7 @@ hipError_t launch_back_typed(const BackParams &a, hipStream_t s)
     const unsigned per_chunk = (unsigned)a.chunks * p.H, pairs = (unsigned)p.B * p.HV, tiles = a.VB / 4;
     const dim3 chains(pairs * a.nseg * tiles), block(256);
     hipLaunchKernelGGL((k_back_prep<DK, TA, RETR, VEC>), dim3((unsigned)a.chunks * p.HV), block, 0, s, a);
+    if (p.B == 0) return hipGetLastError();
     if (a.nseg > 1) {
         hipLaunchKernelGGL((k_back_states<DK, TA, RETR, VEC, true>), dim3(pairs * a.nseg * (tiles + Geo<DK>::KB / 4)), block, 0, s, a);
         hipLaunchKernelGGL((k_back_join<DK, false, VEC>), dim3(pairs * a.VB), dim3(DK * 2), 0, s, a);

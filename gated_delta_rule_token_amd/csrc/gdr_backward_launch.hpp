@@ -50,6 +50,7 @@ struct BackParams {
     int32_t chunks;             // chunk budget: ceil(T / C) + B
     int32_t VB;                 // 16-row blocks of dv, a multiple of 4
     int32_t decays;
+    int32_t zero_rest;          // zero in the gradient rows of tokens that no request covers
 };
 
 // Chunk table: request b covers [m_b, m_(b+1)) where m is the running maximum
@@ -59,8 +60,6 @@ hipError_t launch_back_table(const BackParams &a, hipStream_t s);
 hipError_t launch_back_f32(const BackParams &a, bool retrieves, hipStream_t s);
 hipError_t launch_back_f16(const BackParams &a, bool retrieves, hipStream_t s);
 hipError_t launch_back_bf16(const BackParams &a, bool retrieves, hipStream_t s);
-// Zero in the gradient rows of tokens that no request covers (after the table).
-hipError_t launch_back_zero(const BackParams &a, int act_bytes, hipStream_t s);
 // After the gradients: parameters of the raw-gate arm and a rate shared by the heads.
 hipError_t launch_back_sums(const BackParams &a, hipStream_t s);
 

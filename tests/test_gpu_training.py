@@ -305,6 +305,91 @@ def test_backward_updates_the_state_gradient_in_place():
     assert got.initial_state is buf and torch.equal(buf, want.initial_state)
 
 
+@pytest.fixture
+def poisoned(monkeypatch):
+    """Every tensor that the binding allocates starts as NaN (workspaces, too)."""
+    real = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: (lambda t: (t.view(-1).view(torch.uint8).fill_(255), t)[1]
+                                                          if t.is_cuda and t.numel() else t)(real(*a, **kw)))
+
+
+@pytest.mark.parametrize("rule,dtype,DK,DV", [("gated_delta", "bf16", 16, 16), ("gated_delta", np.float32, 12, 9),
+                                              ("delta", np.float16, 5, 3), ("linear", np.float32, 130, 8)])
+@pytest.mark.parametrize("cu", [[0, 90], [30, 10, 60, 70], [90, 90], [0, 0], [0], [95], [0, 1]])
+def test_backward_zeroes_rows_of_no_request(poisoned, rule, dtype, DK, DV, cu):
+    case = workloads.random_case(37, lengths=[90], H=1, HV=3, DK=DK, DV=DV, dtype=dtype, update_rule=rule, with_initial=False)
+    case["cu_seqlens"] = np.int32(cu)
+    if rule == "delta":
+        case["beta"] = np.ascontiguousarray(case["beta"][:, :1])
+    m = np.maximum.accumulate(np.clip(cu, 0, 90))
+    d_o, _ = draw_gradients(dict(case, cu_seqlens=np.int32([0, 90])), False)
+    d_o[:m[0]] = np.nan
+    d_o[m[-1]:] = np.nan
+    got = gpu_backward(case, d_o, None)
+    want = oracle_backward(case, d_o, None) if len(cu) > 1 else None
+    for name in ("q", "k", "v", "gate", "beta"):
+        t = getattr(got, name)
+        if t is not None:
+            assert torch.all(t[:m[0]] == 0) and torch.all(t[m[-1]:] == 0), name
+            if m[-1] > m[0]:
+                assert_close(host(t)[m[0]:m[-1]], want[name][m[0]:m[-1]], tol(t), "rest d_%s" % name)
+
+
+@pytest.mark.parametrize("seq_lens", [[70, 70, 70], [0, 0, 0], [1, 70, 33], [80, -3, 69]])
+def test_backward_zeroes_the_padding(poisoned, seq_lens):
+    case = workloads.random_case(38, rank4_batch=(3, 70), seq_lens=[70, 70, 70], H=1, HV=2, DK=16, DV=24, update_rule="gated_delta")
+    case["seq_lens"] = np.int32(seq_lens)
+    d_o, d_st = draw_gradients(dict(case, seq_lens=np.clip(seq_lens, 0, 70).astype(np.int32)), True)
+    got = gpu_backward(case, d_o, d_st)
+    case["seq_lens"] = np.clip(seq_lens, 0, 70).astype(np.int32)
+    want = oracle_backward(case, d_o, d_st)
+    for name in ("q", "k", "v", "gate", "beta"):
+        t = getattr(got, name)
+        assert_close(host(t), want[name], FP32, "padded d_%s" % name)
+        for b, n in enumerate(case["seq_lens"]):
+            assert torch.all(t[b, n:] == 0), name
+
+
+def test_backward_in_segments_in_place_twice_at_once_and_replayed(poisoned):
+    """A chain cut into segments: d_final_state's buffer taken for
+    d_initial_state, two calls at once on two streams, and a captured call."""
+    from gated_delta_rule_token_amd import api
+    case = workloads.random_case(39, lengths=[3000, 0, 700], H=1, HV=2, DK=64, DV=64, dtype="bf16", update_rule="gated_delta", **RAW)
+    d_o, d_st = draw_gradients(case, True)
+    d = to_dev(case)
+    kw = {name: d[name] for name in NAMES}
+    kw.update({name: case[name] for name in FLAGS})
+    d_o, d_st = torch.from_numpy(d_o).cuda().bfloat16(), torch.from_numpy(d_st).cuda()
+    call = lambda **over: api.backward(d["q"], d["k"], d["v"], d_o, **{**dict(kw, d_final_state=d_st), **over})  # noqa: E731
+    want = call()
+    torch.cuda.synchronize()
+    same = lambda got: all(torch.equal(getattr(got, n), getattr(want, n)) for n in INPUTS  # noqa: E731
+                           if getattr(want, n) is not None)
+    buf = d_st.clone()
+    none = dict.fromkeys(("q", "k", "v", "gate", "beta", "a_log", "dt_bias", "gate_scale"))
+    assert same(call(d_final_state=buf, out=api.Gradients(initial_state=buf, **none)))
+    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+    results = []
+    for s in side:
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            results += [call(), call()]
+    for s in side:
+        s.synchronize()
+    assert all(map(same, results))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = call()
+    for replay in range(3):
+        for name in INPUTS:
+            if getattr(captured, name) is not None:
+                getattr(captured, name).zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(captured), replay
+        assert same(call()), replay
+
+
 def test_backward_refuses_wrong_tensors():
     from gated_delta_rule_token_amd import api
     case = workloads.random_case(36, lengths=[8], H=1, HV=2, DK=16, DV=16, update_rule="gated_delta")
@@ -504,6 +589,35 @@ def test_norm_replays_in_a_graph_and_gives_equal_bits():
             for s, t in zip(a, b):
                 if s is not None:
                     assert torch.equal(s.view(torch.uint8), t.view(torch.uint8)), replay
+
+
+@pytest.mark.parametrize("rows,heads", [(256, 32), (1024, 8), (1025, 8), (1, 4096), (7, 1176)])
+def test_gate_backward_in_one_slice_and_in_several(rows, heads):
+    """Up to 8192 elements the sums need no second launch: the same results on
+    both sides of that size, into memory that starts as NaN, on replays too."""
+    from gated_delta_rule_token_amd import api
+    rng = np.random.Generator(np.random.PCG64(rows + heads))
+    draw = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).cuda()  # noqa: E731
+    a, d, bias, scale = draw(rows, heads), draw(rows, heads), draw(heads), draw(heads)
+    ws = torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")
+    got = api.gate_backward(a, bias, scale, d, workspace=ws)
+    x = a.double() + bias.double()
+    d_a = d.double() * scale.double() * torch.sigmoid(x)
+    sums = d_a.sum(0), (d.double() * torch.nn.functional.softplus(x)).sum(0)
+    terms = d_a.abs().sum(0), (d.double() * torch.nn.functional.softplus(x)).abs().sum(0)
+    for g, want, size in zip((got.dt_bias, got.decay_scale), sums, terms):
+        # each term is good to 16 half steps (sigmoid, softplus and two products), and
+        # a term is added at most 40 times on its way through a thread, a workgroup and the slices
+        assert torch.all((g.double() - want).abs() <= 56 * 2.0 ** -24 * size)
+    assert torch.all((got.a.double() - d_a).abs() <= 16 * 2.0 ** -24 * d_a.abs())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = api.gate_backward(a, bias, scale, d, workspace=ws)
+    for _ in range(3):
+        ws.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(s, t) for s, t in zip(captured, got) if s is not None)
 
 
 # ------------------------------------------------------------------ as they are used together

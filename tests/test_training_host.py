@@ -64,6 +64,8 @@ BAD = [
     ("d_v_over_d_o", (), (), dict(d_v=_fake(20)), api.GDR_E_ALIAS),
     ("d_initial_over_initial", (), (), dict(d_initial_state=_fake(9)), api.GDR_E_ALIAS),
     ("d_initial_partly_over_d_final", (), (), dict(d_initial_state=_fake(21) + 256), api.GDR_E_ALIAS),
+    ("zero_rest_of_2", (), (), dict(zero_rest=2), api.GDR_E_INVALID),
+    ("rows_too_wide", dict(num_heads_qk=140000, num_heads_v=140000, head_dim_k=64, head_dim_v=64), (), (), api.GDR_E_INVALID),
     ("workspace_over_q", (), dict(q=_fake(40) + 4096), (), api.GDR_E_ALIAS),
 ]
 
