@@ -205,16 +205,23 @@ __device__ __forceinline__ float exp_of(double x)
     return expf(hi) * (1.f + (float)(x - (double)hi));
 }
 
+// x of another lane of the quad (every lane is written: no value to keep, and
+// no move to set one)
+template <int CTRL> __device__ __forceinline__ float quad_move(float x)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xF, 0xF, true));
+}
+
 // 4x4 transpose within each quad of lanes: element p of lane q <- element q of lane p
 __device__ __forceinline__ f4 quad_transpose(f4 v)
 {
     const bool odd = threadIdx.x & 1, up = threadIdx.x & 2;
     f4 g;  // the other lane's, moved by every lane before any choice
 #pragma unroll
-    for (int i = 0; i < 4; ++i) g[i] = dpp_mov<0xB1>(v[i ^ 1]);  // lane ^ 1
+    for (int i = 0; i < 4; ++i) g[i] = quad_move<0xB1>(v[i ^ 1]);  // lane ^ 1
     v = f4{odd ? g[0] : v[0], odd ? v[1] : g[1], odd ? g[2] : v[2], odd ? v[3] : g[3]};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) g[i] = dpp_mov<0x4E>(v[i ^ 2]);  // lane ^ 2
+    for (int i = 0; i < 4; ++i) g[i] = quad_move<0x4E>(v[i ^ 2]);  // lane ^ 2
     return f4{up ? g[0] : v[0], up ? g[1] : v[1], up ? v[2] : g[2], up ? v[3] : g[3]};
 }
 
