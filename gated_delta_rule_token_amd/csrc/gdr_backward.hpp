@@ -262,10 +262,23 @@ constexpr unsigned NOWHERE = 0x80000000u;
 struct ChunkRows {
     __amdgpu_buffer_rsrc_t buf;
     template <typename TA>
-    __device__ __forceinline__ ChunkRows(const TA *first, int cnt, int step, int width)
+    __device__ __forceinline__ ChunkRows(const TA *first, int cnt, int step, int width, bool live = true)
     {
-        const unsigned bytes = ((unsigned)(cnt - 1) * (unsigned)step + (unsigned)width) * (unsigned)sizeof(TA);  // < 2^31
+        const unsigned bytes = live ? ((unsigned)(cnt - 1) * (unsigned)step + (unsigned)width) * (unsigned)sizeof(TA) : 0;  // < 2^31
         buf = __builtin_amdgcn_make_buffer_rsrc(const_cast<TA *>(first), 0, (int)bytes, 0x00027000);
+    }
+};
+
+// fp32 fragment blocks as a buffer, `blocks` of them (none: every load gives zero)
+struct Frags {
+    __amdgpu_buffer_rsrc_t buf;
+    __device__ __forceinline__ Frags(const float *first, int blocks)
+    {
+        buf = __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(first), 0, blocks * FRAG * 4, 0x00027000);
+    }
+    __device__ __forceinline__ f4 get(int block) const
+    {
+        return __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(buf, (threadIdx.x & 63) * 16, block * FRAG * 4, 0));
     }
 };
 
@@ -1399,20 +1412,21 @@ __global__ __launch_bounds__(512, 2) void k_back_grad(const BackParams a)
         Raw4<TA> o[2];
     } ahead[2];
     auto fetch = [&](In &f, int r, int vx) {
-        const int h = hq * R + r;
+        const bool live = r < R;
+        const int h = hq * R + min(r, R - 1);
         const size_t rec = (size_t)ci * p.HV + h;
-        const float *Sp = a.s + (rec * KB + kb0) * a.VB * FRAG, *Dp = a.ds + (rec * KB + kb0) * a.VB * FRAG;
-        const float *Zp = (is_y ? a.y : a.e) + (rec * MB + z_blk) * a.VB * FRAG;
-        const ChunkRows orows(static_cast<const TA *>(a.d_o) + ((size_t)t0 * p.HV + h) * p.dv, cnt, vstep, p.dv);
+        const Frags S(a.s + (rec * KB + kb0) * a.VB * FRAG, live ? KW * a.VB : 0), D(a.ds + (rec * KB + kb0) * a.VB * FRAG, live ? KW * a.VB : 0);
+        const Frags Z((is_y ? a.y : a.e) + (rec * MB + z_blk) * a.VB * FRAG, live ? a.VB : 0);
+        const ChunkRows orows(static_cast<const TA *>(a.d_o) + ((size_t)t0 * p.HV + h) * p.dv, cnt, vstep, p.dv, live);
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
             const int vb = 2 * vx + n;
-            f.z[n] = get_frag(Zp + (size_t)vb * FRAG);
+            f.z[n] = Z.get(vb);
             f.o[n] = load_raw4(orows, At4<VEC, TA>(16 * (is_o ? o_blk : 0) + c, vstep, 16 * vb + 4 * j, p.dv));
 #pragma unroll
             for (int x = 0; x < KW; ++x) {
-                f.s[x][n] = get_frag(Sp + ((size_t)x * a.VB + vb) * FRAG);
-                f.d[x][n] = get_frag(Dp + ((size_t)x * a.VB + vb) * FRAG);
+                f.s[x][n] = S.get(x * a.VB + vb);
+                f.d[x][n] = D.get(x * a.VB + vb);
             }
         }
     };
@@ -1433,8 +1447,8 @@ __global__ __launch_bounds__(512, 2) void k_back_grad(const BackParams a)
         }
     };
     // The loads stand under no condition: past the last step of the last head
-    // the last step is loaded again (a load that may not have been issued
-    // would make the wait for the one before it a wait for all).
+    // they are of buffers with nothing in them (a load that may not have been
+    // issued would make the wait for the one before it a wait for all).
     float sc_next;  // a thread's word of the chunk's scalars, a head ahead
     auto fetch_scalars = [&](int r) {
         const int n = tid < BACK_SC * C ? tid : 0;
@@ -1477,7 +1491,7 @@ __global__ __launch_bounds__(512, 2) void k_back_grad(const BackParams a)
                 split8<3>(f.d[x][0], f.d[x][1], dp[x]);
             }
             const bool wrap = vx + 2 >= VX;
-            fetch(f, wrap ? min(r + 1, R - 1) : r, wrap ? vx + 2 - VX : vx + 2);
+            fetch(f, wrap ? r + 1 : r, wrap ? vx + 2 - VX : vx + 2);
             lds_barrier();  // one a step: the other buffer's readers have passed the last one
 #pragma unroll
             for (int w = 0; w < TW; ++w) {
