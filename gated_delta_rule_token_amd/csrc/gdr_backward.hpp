@@ -28,11 +28,20 @@
 //
 // Kernels, in order:
 //   k_back_table   chunk table (one workgroup)
-//   k_back_prep    per chunk and q/k head: the two triangular inverses, P, decay factors
+//   k_back_prep    per chunk and value head: the two triangular inverses, P, decay factors
 //   k_back_states  per request, head and 64 state rows: forward chain, keeps S0 and E of every chunk
 //   k_back_chain   the same backwards: dS1, Y, dV
+//   k_back_join    between the segments of a chain, where it is cut (see there)
 //   k_back_grad    per chunk and q/k head: dQ, dK (summed over the value heads that share them)
 //   k_back_gate    per chunk and value head: dg, db
+// and the sums over chunks or heads (k_back_gate_sums, k_back_rate_sums).
+//
+// Figures at the kernels are of a ragged batch of 8 requests, 29,273 tokens, 16
+// q/k and 32 value heads, dk = dv = 128, bf16: 3.2 ms, of which 0.23 ms are the
+// floor of its inputs and outputs at the copy rate (5.2 TB/s) and 1.0 ms that of
+// its products, in planes, at the rate of a large bf16 product (1234 TFLOP/s).
+// What the kernels hand on (S0 and dS1 64 KB each, E and Y 32 KB each, the
+// triangular operands 54 KB a chunk and head) is 3.6 GB, written and read once.
 //
 // Planes.  The products run on v_mfma_f32_16x16x32_bf16 at fp32's precision
 // and range: an fp32 operand is cut into three bf16 planes of 8 significant
@@ -526,12 +535,13 @@ __device__ __forceinline__ void zero_rest(const BackParams &a, int64_t n, int64_
 // each form its K K^T and Q K^T: one workgroup for all of them, the heads in
 // turn, took 28 us of the smallest call against 19 us, and gained 5 % of the
 // kernel on a long batch of two heads a group (372 and 392 us).  Of fp32 rows it
-// leaves k and q as operand fragments with channels as rows (KT, QT) for
-// k_back_grad, whose LDS has no room for them.  Each unit lower triangular
+// leaves k and q as operand fragments with channels as rows (once a q/k head)
+// for k_back_grad, whose LDS has no room for them.  Each unit lower triangular
 // inverse goes by 16x16 blocks on the fp32 matrix instruction: the diagonal
 // ones by forward substitution, a thread a column; then wave j takes block
 // column j down, T_ij = -T_ii sum_k N_ik T_kj, its T_kj staying in the
-// accumulators' layout.
+// accumulators' layout.  390 us: 0.83 GB written and 0.5 GB read, 3.4 TB/s; bound
+// by the solves' dependent steps, hidden behind other workgroups' (4 a CU).
 template <int DK, typename TA, bool RETR, bool VEC>
 __global__ __launch_bounds__(256) void k_back_prep(const BackParams a)
 {
@@ -921,7 +931,8 @@ struct ChunkScalars {
 
 // ---------------------------------------------------------------- segments
 // A chain step maps every state row s affinely and alike, s <- s M_c + c_c.
-// With few (request, head) pairs a chain is cut into segments: a first pass
+// With few (request, head) pairs a chain is cut into a.nseg segments (the rule is
+// at back_segments): a first pass
 // (CARRY) gives each segment's M (rows of the identity as start, values left
 // out) and its c (zero start, nothing kept), k_back_join hands the true states
 // from segment to segment, and the pass that keeps its results runs all
@@ -961,7 +972,8 @@ template <int KB> __device__ __forceinline__ void get_state(f4 (&S)[KB], const f
 // segments' starts (backwards: at their ends), one after the other.  A wave
 // forms two 16-channel blocks of each state from all of the one before, which
 // goes round the waves through LDS as planes; its rows of M and its carry are
-// loaded a segment ahead.
+// loaded a segment ahead.  65,536 tokens x 16 heads: 14 us for 8 segments; with
+// 64 state rows a workgroup, each wave all channels of 16 of them, 65 us.
 template <int DK, bool REVERSE, bool VEC>
 __global__ __launch_bounds__(DK * 2) void k_back_join(const BackParams a)
 {
@@ -1035,7 +1047,10 @@ __global__ __launch_bounds__(DK * 2) void k_back_join(const BackParams a)
 // One workgroup per (segment, request, value head, 64 state rows); wave w keeps S^T of
 // 16 rows in its accumulators over the whole chain.  Everything that a step
 // reads from memory is loaded one step ahead: within the step there are only
-// LDS reads, and stores that nothing waits for.
+// LDS reads, and stores that nothing waits for.  Two workgroups a CU where
+// registers allow.  656 us: 1.45 GB written and 1.3 GB read, 4.2 TB/s over all,
+// but the longest request's 109 steps, 6 us each, are what it waits for: while
+// all 512 chains run it is bound by memory and VALU, at the end by latency.
 template <int DK, typename TA, bool RETR, bool VEC, bool CARRY>
 __global__ __launch_bounds__(256, planes_of<TA> <= 2 && DK <= 128 ? 2 : 1) void k_back_states(const BackParams a)
 {
@@ -1153,6 +1168,13 @@ __global__ __launch_bounds__(256, planes_of<TA> <= 2 && DK <= 128 ? 2 : 1) void 
 }
 
 // ---------------------------------------------------------------- backward chain
+// As the forward chain; a step has two triangular products and the update of
+// dS by q and by k.  1.03 ms: 1.7 GB written and 2.4 GB read, 3.9 TB/s; 109 steps
+// of 9.4 us, of which a wave's 198 matrix instructions take 1.3 us and its 1100
+// VALU instructions (planes, transposes) 2 us: 56 % of the waves' time is waiting
+// for LDS and the step before.  Transposes across banks instead of quads spared
+// 300 of the latter and were no faster; nor was one XCD for the workgroups that
+// share operands (1041 us against 1047).
 template <int DK, typename TA, bool RETR, bool VEC, bool CARRY>
 __global__ __launch_bounds__(256, planes_of<TA> == 1 && DK <= 128 ? 2 : 1) void k_back_chain(const BackParams a)
 {
@@ -1285,6 +1307,10 @@ __global__ __launch_bounds__(256, planes_of<TA> == 1 && DK <= 128 ? 2 : 1) void 
 // registers, those over tokens (d_o, Y, E) through LDS, cut into planes once
 // for all waves, 32 state rows a step, double buffered.  Of the chunk x chunk
 // products wave (ft, part) forms column blocks part * SBW .. of row block ft.
+// 1.34 ms: 3.9 GB read and 0.33 GB written, 3.2 TB/s, one workgroup a CU (151 KB of
+// LDS, 256 VGPRs); matrix and VALU instructions fill two thirds of the SIMDs'
+// cycles, the rest is waiting between a head's phases.  Keeping the rows of q
+// and k in LDS spared 0.4 ms against reading them again for each head.
 template <int DK, typename TA, bool RETR, bool VEC>
 __global__ __launch_bounds__(512, 2) void k_back_grad(const BackParams a)
 {
@@ -1750,7 +1776,7 @@ __global__ __launch_bounds__(512, 2) void k_back_grad(const BackParams a)
 }
 
 // ---------------------------------------------------------------- dg and db
-// A wave per (chunk, value head), a lane a token:
+// A wave per (chunk, value head), a lane a token (24 us):
 //   dg_s = e^Gamma <dS1, S0> + sum_{t<s} u_t + sum_{t>=s} w_t + sum_{t>=s>r} M_tr
 // the last from the sums over r of whole blocks before s's own (rows) and
 // within it (col); then the raw gate's and the rate's activation.

@@ -231,11 +231,12 @@ __global__ __launch_bounds__(threads_of(TPR)) void k_norm(const NormParams p)
             const Place<EXACT> v(vec, width);
             if (v.on() && (whole ? vec == 0 : vec % lanes == 0))
                 p.scale[(size_t)row * p.groups + (whole ? 0 : vec / lanes)] = scale;
-            const float inv_scale = 1.f / scale;
+            const float up = scale < 0x1p-100f ? 0x1p64f : 1.f;  // the reciprocal of a denormal scale may be infinite
+            const float inv_scale = 1.f / (scale * up);
             float q[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float t = r[n][i] * inv_scale;
+                const float t = r[n][i] * up * inv_scale;
                 // two roundings may pass the largest value by an ulp or two
                 q[i] = t > E4M3_MAX ? E4M3_MAX : t < -E4M3_MAX ? -E4M3_MAX : t;
             }
@@ -366,7 +367,9 @@ __global__ __launch_bounds__(256) void k_norm_back_sums(const NormBackParams p, 
 // barriers; past that a workgroup.  At 29,273 rows of 2,048 in bf16 the forward
 // pass takes 92 us with a row a wave (four vectors a lane); the backward pass
 // 100 us so and 88 us with a row a workgroup, as its lanes then hold a quarter
-// of the three rows and the weight's gradient.
+// of the three rows and the weight's gradient.  The widest rows (above 16,384)
+// do not fit a workgroup's registers backwards: 3,000 rows of 32,768 in bf16
+// take 641 us, 4 times the copy rate's 152 (forward 159 us).
 template <int WAVE, typename F>
 hipError_t by_width(int64_t width, F &&f)
 {
@@ -381,6 +384,7 @@ hipError_t by_width(int64_t width, F &&f)
     if (v <= 256) return f(integral_constant<int, 256>(), integral_constant<int, 1>());
     if (v <= 512) return f(integral_constant<int, 256>(), integral_constant<int, 2>());
     if (v <= 1024) return f(integral_constant<int, 256>(), integral_constant<int, 4>());
+    if (v <= 2048) return f(integral_constant<int, 1024>(), integral_constant<int, 2>());
     return f(integral_constant<int, 1024>(), integral_constant<int, 4>());
 }
 

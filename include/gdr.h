@@ -278,9 +278,11 @@ typedef struct {
     int32_t zero_rest;            /* 1: zero in the rows (of d_q .. d_beta) of tokens that no request covers */
 } gdr_gradients;
 
-/* Bytes of device workspace gdr_backward needs for `problem`: per token and
- * value head about 12 dv + 8 dv dk / 64 + 500 bytes (3.4 GB at 29,273 tokens,
- * 32 heads, dk = dv = 128). */
+/* Bytes of device workspace gdr_backward needs for `problem`: about 256 KB per
+ * 64 tokens of a request and value head at dk = dv = 128 (3.8 GB at 29,273
+ * tokens in 8 requests, 32 heads), more for fp32 activations, and less without
+ * retrieval.  Calls that overlap in time need workspaces of their own; nothing
+ * in it has to start at zero or be kept between calls. */
 gdr_status gdr_backward_workspace_size(const gdr_problem *problem, size_t *bytes);
 
 /* Enqueue the backward pass on `stream`.  Arguments are checked on the host
@@ -330,7 +332,7 @@ gdr_status gdr_gate_backward(int64_t count, int32_t heads, int32_t dtype, const 
  * columns of a row (1 where that is 0), and y holds y / scale, rounded to
  * nearest even; group is 0 or a power of two from 8 to 512.  Arithmetic and
  * sums in fp32.  A row that holds NaN or an infinity gives what the formulas
- * give. */
+ * give, and so does one whose squares pass fp32's range (inv = 0). */
 gdr_status gdr_rms_norm(int64_t rows, int32_t width, int32_t dtype, int32_t weight_dtype, int32_t out_dtype,
                         int32_t group, float eps, const void *x, const void *residual, const void *weight,
                         void *y, float *scale, void *residual_out, float *inv_rms, void *stream);

@@ -543,6 +543,30 @@ def test_norm_of_infinities_nan_and_extremes():
     assert torch.isfinite(eight.y[2:].float()).all() and torch.isfinite(eight.scale[2:]).all()
 
 
+@pytest.mark.parametrize("size", [1e-30, 1e-37, 1e-38, 1e-41, 1e-45])
+@pytest.mark.parametrize("group", [0, 32])
+def test_norm_in_8_bits_of_tiny_rows(size, group):
+    """Scales down to denormal ones, whose reciprocal is infinite: zeros stay
+    zero, and y8 is e4m3(y / scale) of the fp32 y and scale."""
+    from gated_delta_rule_token_amd import api
+    rng = np.random.Generator(np.random.PCG64(7))
+    x = torch.from_numpy((rng.standard_normal((5, 200)) * size).astype(np.float32)).cuda()
+    x[:, ::7] = 0.0
+    y = api.rms_norm(x, eps=1.0).y  # inv = 1: y = x
+    got = api.rms_norm(x, eps=1.0, out_dtype=torch.float8_e4m3fn, group=group)
+    assert torch.equal(y, x)
+    for c in range(0, 200, group or 200):
+        part = slice(c, c + (group or 200))
+        top = y[:, part].double().abs().amax(1, keepdim=True)
+        scale = got.scale[:, c // (group or 200)][:, None].double()
+        # m / 448 in fp32, by half a step of a normal or a denormal value, and 1 where that is 0
+        assert torch.all(((scale - top / 448).abs() <= 2.0 ** -23 * top / 448 + 2.0 ** -149) | (scale == 1))
+        q, want = got.y[:, part].double(), (y[:, part].double() / scale).clamp(-448, 448)
+        assert torch.all(q[want == 0] == 0)
+        # half a step of e4m3 (2^-4 of the value, 2^-10 below its normal range), and the product's roundings
+        assert torch.all((q - want).abs() <= (2.0 ** -4 + 2.0 ** -20) * want.abs() + 2.0 ** -10 + 2.0 ** -30)
+
+
 def test_norm_in_place_residual_empty_rows_and_refusals():
     from gated_delta_rule_token_amd import api
     x, res, w, _, _ = _norm_inputs(33, 200, torch.float16)
