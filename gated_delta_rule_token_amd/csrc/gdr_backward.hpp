@@ -536,12 +536,15 @@ __device__ __forceinline__ void zero_rest(const BackParams &a, int64_t n, int64_
 // turn, took 28 us of the smallest call against 19 us, and gained 5 % of the
 // kernel on a long batch of two heads a group (372 and 392 us).  Of fp32 rows it
 // leaves k and q as operand fragments with channels as rows (once a q/k head)
-// for k_back_grad, whose LDS has no room for them.  Each unit lower triangular
-// inverse goes by 16x16 blocks on the fp32 matrix instruction: the diagonal
-// ones by forward substitution, a thread a column; then wave j takes block
-// column j down, T_ij = -T_ii sum_k N_ik T_kj, its T_kj staying in the
-// accumulators' layout.  390 us: 0.83 GB written and 0.5 GB read, 3.4 TB/s; bound
-// by the solves' dependent steps, hidden behind other workgroups' (4 a CU).
+// for k_back_grad, whose LDS has no room for them.  Both inverses come from
+// one solve: with U = -(I + L diag(b))^-1 L,
+//   (I + L diag(b))^-1 = I + U diag(b),   (I + diag(b) L)^-1 = I + diag(b) U
+// (two solves: 390 us).  It goes by 16x16 blocks on the fp32 matrix instruction:
+// the diagonal ones by forward substitution, a thread a column; then wave j
+// takes block column j down, U_ij = -(I + U_ii diag(b)) (L_ij + sum_k L_ik diag(b) U_kj)
+// over j <= k < i, its U_kj staying in the accumulators' layout.  360 us: 0.85 GB
+// written and 0.5 GB read, 3.8 TB/s; bound by the solve's dependent steps, hidden
+// behind other workgroups' (4 a CU).
 template <int DK, typename TA, bool RETR, bool VEC>
 __global__ __launch_bounds__(256) void k_back_prep(const BackParams a)
 {
@@ -549,7 +552,7 @@ __global__ __launch_bounds__(256) void k_back_prep(const BackParams a)
     using RW = Rows<DK>;
     constexpr int C = G::C, MB = G::MB, MX = G::MX, KX = G::KX, LC = G::LC, TRI = G::TRI, ACT = G::ACT, NT = G::NT;
     constexpr int NP = planes_of<TA>, SLOTS = (TRI + 3) / 4, INV = 16 * 20;
-    constexpr int STAGE = 2 * NP * RW::PLANE * 2, SOLVE = (C * LC + 2 * MB * INV) * 4;
+    constexpr int STAGE = 2 * NP * RW::PLANE * 2, SOLVE = (C * LC + MB * INV) * 4;
     __shared__ __align__(16) char mem[STAGE > SOLVE ? STAGE : SOLVE];
     __shared__ double s_G[C];
     __shared__ __align__(16) float s_b[C];
@@ -714,57 +717,54 @@ __global__ __launch_bounds__(256) void k_back_prep(const BackParams a)
         if constexpr (RETR) {
             uint16_t *t2 = pt + 3 * STRIDE, *t1 = t2 + 3 * STRIDE;
             __syncthreads();
-            // z = 0: I + L diag(b);  z = 1: I + diag(b) L
-            if (tid < 2 * MB * 16) {
-                const int z = tid / (MB * 16), d = tid / 16 % MB, col = tid & 15;
+            if (tid < MB * 16) {
+                const int d = tid / 16, col = tid & 15;
                 float x[16];
 #pragma unroll
                 for (int row = 0; row < 16; ++row) {
-                    const float bt = s_b[16 * d + row];
-                    float acc = row == col ? 1.f : 0.f;
+                    float acc = -Lm[(16 * d + row) * LC + 16 * d + col];
 #pragma unroll
-                    for (int s = 0; s < row; ++s)
-                        acc -= Lm[(16 * d + row) * LC + 16 * d + s] * (z ? bt : s_b[16 * d + s]) * x[s];
+                    for (int s = 0; s < row; ++s) acc -= Lm[(16 * d + row) * LC + 16 * d + s] * s_b[16 * d + s] * x[s];
                     x[row] = acc;
-                    inv[(z * MB + d) * INV + row * 20 + col] = acc;
+                    inv[d * INV + row * 20 + col] = acc;
                 }
             }
             __syncthreads();
             if (wave < MB) {
+                const float b = s_b[16 * wave + c];
+                f4 U[MB];
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    f4 T[MB];
+                for (int i = 0; i < MB; ++i) U[i] = zero;
 #pragma unroll
-                    for (int i = 0; i < MB; ++i) T[i] = zero;
+                for (int i = 0; i < MB; ++i) {
+                    if (i == wave) {
 #pragma unroll
-                    for (int i = 0; i < MB; ++i) {
-                        if (i == wave) {
+                        for (int e = 0; e < 4; ++e) U[i][e] = inv[i * INV + (4 * j + e) * 20 + c];
+                    } else if (i > wave) {
+                        f4 acc;
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) T[i][e] = inv[(z * MB + i) * INV + (4 * j + e) * 20 + c];
-                        } else if (i > wave) {
-                            f4 acc = zero;
-                            const float bt = s_b[16 * i + c];
+                        for (int e = 0; e < 4; ++e) acc[e] = Lm[(16 * i + 4 * j + e) * LC + 16 * wave + c];
 #pragma unroll
-                            for (int k = 0; k < i; ++k) {
-                                if (k < wave) continue;
-                                f4 N = *reinterpret_cast<const f4 *>(Lm + (16 * i + c) * LC + 16 * k + 4 * j);
-                                N *= z ? f4{bt, bt, bt, bt} : *reinterpret_cast<const f4 *>(s_b + 16 * k + 4 * j);
-                                acc = mfma4(N, T[k], acc);
-                            }
-                            const f4 Ti = *reinterpret_cast<const f4 *>(inv + (z * MB + i) * INV + c * 20 + 4 * j);
-                            T[i] = -mfma4(Ti, acc, zero);
+                        for (int k = 0; k < i; ++k) {
+                            if (k < wave) continue;
+                            acc = mfma4(*reinterpret_cast<const f4 *>(Lm + (16 * i + c) * LC + 16 * k + 4 * j) *
+                                            *reinterpret_cast<const f4 *>(s_b + 16 * k + 4 * j), U[k], acc);
                         }
-                        if (i >= wave) {  // tile: rows t of block i, columns s of block `wave`
-                            if (z == 0) {
-                                uint16_t *blk = t1 + lower_block<MB>(i, wave / 2) * BLOCK;
-                                put_half(blk, STRIDE, quad_lane(), wave & 1, quad_transpose(T[i]));
-                                if (i == wave && !(i & 1)) put_half(blk, STRIDE, lane, 1, zero);
-                            } else {
-                                uint16_t *blk = t2 + upper_block<MB>(wave, i / 2) * BLOCK;
-                                put_half(blk, STRIDE, lane, i & 1, T[i]);
-                                if (i == wave && (i & 1)) put_half(blk, STRIDE, lane, 0, zero);
-                            }
-                        }
+                        f4 T = *reinterpret_cast<const f4 *>(inv + i * INV + c * 20 + 4 * j) * *reinterpret_cast<const f4 *>(s_b + 16 * i + 4 * j);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) T[e] += c == 4 * j + e ? 1.f : 0.f;
+                        U[i] = -mfma4(T, acc, zero);
+                    }
+                    if (i >= wave) {  // tile: rows t of block i, columns s of block `wave`
+                        f4 one = zero;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) one[e] = i == wave && c == 4 * j + e ? 1.f : 0.f;
+                        uint16_t *blk = t1 + lower_block<MB>(i, wave / 2) * BLOCK;
+                        put_half(blk, STRIDE, quad_lane(), wave & 1, quad_transpose(U[i] * b + one));
+                        if (i == wave && !(i & 1)) put_half(blk, STRIDE, lane, 1, zero);
+                        blk = t2 + upper_block<MB>(wave, i / 2) * BLOCK;
+                        put_half(blk, STRIDE, lane, i & 1, *reinterpret_cast<const f4 *>(s_b + 16 * i + 4 * j) * U[i] + one);
+                        if (i == wave && (i & 1)) put_half(blk, STRIDE, lane, 0, zero);
                     }
                 }
             }
