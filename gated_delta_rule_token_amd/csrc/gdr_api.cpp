@@ -413,6 +413,7 @@ size_t back_layout(const gdr_problem *p, gdr::BackParams &a, void *base)
     const auto floats = [&](size_t n) { return static_cast<float *>(take(n)); };
     a.off = static_cast<int32_t *>(take((size_t)p->batch + 1));
     a.tok = static_cast<int32_t *>(take((size_t)p->batch * 2));
+    a.order = static_cast<int32_t *>(take((size_t)p->batch));
     a.sc = floats(recs * gdr::BACK_SC * C);
     a.gx = floats(recs * gdr::GX * C);
     a.gate_sums = p->gate_activation == GDR_GATE_QWEN ? floats(recs * 2) : nullptr;
@@ -432,6 +433,8 @@ size_t back_layout(const gdr_problem *p, gdr::BackParams &a, void *base)
         a.seg_mt = floats(pairs * a.nseg * KB * KB * block);
         a.seg_carry = floats(pairs * a.nseg * VB * KB * block);
         a.seg_state = floats(pairs * a.nseg * VB * KB * block);
+        a.seg_dcarry = floats(pairs * a.nseg * VB * KB * block);
+        a.seg_dstate = floats(pairs * a.nseg * VB * KB * block);
     }
     return at;
 }

@@ -9,11 +9,16 @@ namespace gdr {
 // clamped cu_seqlens entries up to b: for a non-decreasing cu_seqlens its own
 // range, and in any case ranges that do not overlap, so two requests never
 // write one gradient row and the chunk counts sum to at most
-// ceil(T / C) + B.  off[] is the exclusive prefix sum of the chunk counts.
+// ceil(T / C) + B.  off[] is the exclusive prefix sum of the chunk counts, and
+// order[] the requests from the longest to the shortest, up to RANKED of them:
+// the chains start in that order.
+constexpr int RANKED = 1024;
+
 __global__ __launch_bounds__(256) void k_back_table(const BackParams a, int C)
 {
     __shared__ int64_t s_m[256], s_n[256];
     __shared__ int64_t carry_m, carry_n;
+    __shared__ int32_t s_len[RANKED];
     const Params &p = a.p;
     const int tid = threadIdx.x;
     if (tid == 0) {
@@ -54,6 +59,8 @@ __global__ __launch_bounds__(256) void k_back_table(const BackParams a, int C)
             a.off[b] = (int32_t)(carry_n + s_n[tid] - n);
             a.tok[2 * b] = (int32_t)start;
             a.tok[2 * b + 1] = (int32_t)(end - start);
+            if (p.B <= RANKED) s_len[b] = (int32_t)n;
+            else a.order[b] = b;
         }
         __syncthreads();
         if (tid == 255) {
@@ -63,6 +70,13 @@ __global__ __launch_bounds__(256) void k_back_table(const BackParams a, int C)
         __syncthreads();
     }
     if (tid == 0) a.off[p.B] = (int32_t)carry_n;
+    if (p.B <= RANKED)
+        for (int b = tid; b < p.B; b += 256) {
+            const int32_t n = s_len[b];
+            int rank = 0;
+            for (int i = 0; i < p.B; ++i) rank += s_len[i] > n || (s_len[i] == n && i < b);
+            a.order[rank] = b;
+        }
 }
 
 hipError_t launch_back_table(const BackParams &a, hipStream_t s)

@@ -975,18 +975,18 @@ template <int KB> __device__ __forceinline__ void get_state(f4 (&S)[KB], const f
 // loaded a segment ahead.  65,536 tokens x 16 heads: 14 us for 8 segments; with
 // 64 state rows a workgroup, each wave all channels of 16 of them, 65 us.
 template <int DK, bool REVERSE, bool VEC>
-__global__ __launch_bounds__(DK * 2) void k_back_join(const BackParams a)
+__device__ __forceinline__ void join_segments(const BackParams &a, int block, uint16_t (&s_x)[2][3 * Geo<DK>::KX * BLOCK])
 {
     using G = Geo<DK>;
     constexpr int KB = G::KB, KX = G::KX;
-    __shared__ __align__(16) uint16_t s_x[2][3 * KX * BLOCK];
     const Params &p = a.p;
-    const int vb = blockIdx.x % a.VB, bh = blockIdx.x / a.VB;
+    const int vb = block % a.VB, bh = block / a.VB;
+    float *seg_carry = REVERSE ? a.seg_dcarry : a.seg_carry, *seg_state = REVERSE ? a.seg_dstate : a.seg_state;
     const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane & 15, j = lane >> 4;
     const float *init = REVERSE ? a.d_final : p.init;
     f4 m[2][KB], carry[2];
     auto rows = [&](int seg) { return (REVERSE ? a.seg_m : a.seg_mt) + seg_at(a, bh, seg, KB, 2 * wave, KB); };
-    auto add = [&](int seg) { return a.seg_carry + seg_at(a, bh, seg, a.VB, vb, KB) + 2 * wave * FRAG; };
+    auto add = [&](int seg) { return seg_carry + seg_at(a, bh, seg, a.VB, vb, KB) + 2 * wave * FRAG; };
     auto fetch = [&](const float *M, int kb) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) m[h][kb] = get_frag(M + (h * KB + kb) * FRAG);
@@ -1008,7 +1008,7 @@ __global__ __launch_bounds__(DK * 2) void k_back_join(const BackParams a)
     }
     for (int n = 0; n < a.nseg; ++n) {
         const int seg = REVERSE ? a.nseg - 1 - n : n;
-        float *out = a.seg_state + seg_at(a, bh, seg, a.VB, vb, KB) + 2 * wave * FRAG;
+        float *out = seg_state + seg_at(a, bh, seg, a.VB, vb, KB) + 2 * wave * FRAG;
         uint16_t *x = s_x[n & 1];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -1043,6 +1043,15 @@ __global__ __launch_bounds__(DK * 2) void k_back_join(const BackParams a)
     }
 }
 
+template <int DK, bool VEC>
+__global__ __launch_bounds__(DK * 2) void k_back_join(const BackParams a)
+{
+    __shared__ __align__(16) uint16_t s_x[2][3 * Geo<DK>::KX * BLOCK];
+    const int n = gridDim.x / 2;
+    if ((int)blockIdx.x < n) join_segments<DK, false, VEC>(a, blockIdx.x, s_x);
+    else join_segments<DK, true, VEC>(a, blockIdx.x - n, s_x);
+}
+
 // ---------------------------------------------------------------- forward chain
 // One workgroup per (segment, request, value head, 64 state rows); wave w keeps S^T of
 // 16 rows in its accumulators over the whole chain.  Everything that a step
@@ -1051,20 +1060,25 @@ __global__ __launch_bounds__(DK * 2) void k_back_join(const BackParams a)
 // registers allow.  656 us: 1.45 GB written and 1.3 GB read, 4.2 TB/s over all,
 // but the longest request's 109 steps, 6 us each, are what it waits for: while
 // all 512 chains run it is bound by memory and VALU, at the end by latency.
+template <int DK, typename TA, bool RETR> struct StatesLds {
+    __align__(16) uint16_t Kr[planes_of<TA> * Rows<DK>::PLANE];
+    __align__(16) uint16_t T[RETR ? 3 * Geo<DK>::NT * BLOCK : 8];
+    __align__(16) float s_eg[Geo<DK>::C], s_x[Geo<DK>::C];
+    float s_gamma;
+};
+
 template <int DK, typename TA, bool RETR, bool VEC, bool CARRY>
-__global__ __launch_bounds__(256, planes_of<TA> <= 2 && DK <= 128 ? 2 : 1) void k_back_states(const BackParams a)
+__device__ __forceinline__ void states_chain(const BackParams &a, int block, StatesLds<DK, TA, RETR> &lds)
 {
     using G = Geo<DK>;
     constexpr int C = G::C, MB = G::MB, MX = G::MX, KB = G::KB, NT = G::NT, NP = planes_of<TA>;
     constexpr int TRIS = RETR ? 3 : 1;  // triangular operands of a record
-    __shared__ __align__(16) uint16_t Kr[NP * Rows<DK>::PLANE];
-    __shared__ __align__(16) uint16_t T[RETR ? 3 * NT * BLOCK : 8];
-    __shared__ __align__(16) float s_eg[C], s_x[C];
-    __shared__ float s_gamma;
+    uint16_t *Kr = lds.Kr, *T = lds.T;
+    float *s_eg = lds.s_eg, *s_x = lds.s_x, &s_gamma = lds.s_gamma;
     const Params &p = a.p;
     const int tiles = a.VB / 4 + (CARRY ? KB / 4 : 0);
-    const int tile = blockIdx.x % tiles, pair = blockIdx.x / tiles, bh = pair % (p.B * p.HV), seg = pair / (p.B * p.HV);
-    const int h = bh % p.HV, b = bh / p.HV;
+    const int tile = block % tiles, pair = block / tiles, seg = pair / (p.B * p.HV);
+    const int h = pair % p.HV, b = uniform(a.order[pair / p.HV % p.B]), bh = b * p.HV + h;
     const Segment sg = Segment::of<C>(a, b, seg);
     const int first = sg.first, count = sg.count, len = sg.len;
     const int64_t start = sg.start;
@@ -1175,20 +1189,25 @@ __global__ __launch_bounds__(256, planes_of<TA> <= 2 && DK <= 128 ? 2 : 1) void 
 // for LDS and the step before.  Transposes across banks instead of quads spared
 // 300 of the latter and were no faster; nor was one XCD for the workgroups that
 // share operands (1041 us against 1047).
+template <int DK, typename TA, bool RETR> struct ChainLds {
+    __align__(16) uint16_t Kr[planes_of<TA> * Rows<DK>::PLANE], Qr[planes_of<TA> * Rows<DK>::PLANE];
+    __align__(16) uint16_t T[(RETR ? 6 : 3) * Geo<DK>::NT * BLOCK];  // P^T, then (I + diag(b) L)^-T
+    __align__(16) float s_kd[Geo<DK>::C], s_b[Geo<DK>::C], s_q[Geo<DK>::C], s_k[Geo<DK>::C];
+    float s_gamma;
+};
+
 template <int DK, typename TA, bool RETR, bool VEC, bool CARRY>
-__global__ __launch_bounds__(256, planes_of<TA> == 1 && DK <= 128 ? 2 : 1) void k_back_chain(const BackParams a)
+__device__ __forceinline__ void gradient_chain(const BackParams &a, int block, ChainLds<DK, TA, RETR> &lds)
 {
     using G = Geo<DK>;
     constexpr int C = G::C, MB = G::MB, MX = G::MX, KB = G::KB, NT = G::NT, NP = planes_of<TA>;
     constexpr int TRIS = RETR ? 3 : 1;
-    __shared__ __align__(16) uint16_t Kr[NP * Rows<DK>::PLANE], Qr[NP * Rows<DK>::PLANE];
-    __shared__ __align__(16) uint16_t T[(RETR ? 6 : 3) * NT * BLOCK];  // P^T, then (I + diag(b) L)^-T
-    __shared__ __align__(16) float s_kd[C], s_b[C], s_q[C], s_k[C];
-    __shared__ float s_gamma;
+    uint16_t *Kr = lds.Kr, *Qr = lds.Qr, *T = lds.T;
+    float *s_kd = lds.s_kd, *s_b = lds.s_b, *s_q = lds.s_q, *s_k = lds.s_k, &s_gamma = lds.s_gamma;
     const Params &p = a.p;
     const int tiles = a.VB / 4;
-    const int tile = blockIdx.x % tiles, pair = blockIdx.x / tiles, bh = pair % (p.B * p.HV), seg = pair / (p.B * p.HV);
-    const int h = bh % p.HV, b = bh / p.HV;
+    const int tile = block % tiles, pair = block / tiles, seg = pair / (p.B * p.HV);
+    const int h = pair % p.HV, b = uniform(a.order[pair / p.HV % p.B]), bh = b * p.HV + h;
     const Segment sg = Segment::of<C>(a, b, seg);
     const int first = sg.first, count = sg.count, len = sg.len;
     const int64_t start = sg.start;
@@ -1201,7 +1220,7 @@ __global__ __launch_bounds__(256, planes_of<TA> == 1 && DK <= 128 ? 2 : 1) void 
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) dS[kb] = f4{0.f, 0.f, 0.f, 0.f};
     } else if (a.nseg > 1) {
-        get_state<KB>(dS, a.seg_state + seg_at(a, bh, seg, a.VB, vb, KB));
+        get_state<KB>(dS, a.seg_dstate + seg_at(a, bh, seg, a.VB, vb, KB));
     } else {
         load_state<VEC>(dS, a.d_final ? a.d_final + (size_t)bh * p.dv * p.dk : nullptr, col, p.dv, p.dk, j);
     }
@@ -1291,12 +1310,42 @@ __global__ __launch_bounds__(256, planes_of<TA> == 1 && DK <= 128 ? 2 : 1) void 
         state_update<DK, NP, RETR>(dS, s_gamma, Qr, dO, Kr, D);
     }
     if constexpr (CARRY) {
-        put_state<KB>(a.seg_carry + seg_at(a, bh, seg, a.VB, vb, KB), dS);
+        put_state<KB>(a.seg_dcarry + seg_at(a, bh, seg, a.VB, vb, KB), dS);
     } else if (a.d_init && seg == 0) {
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
             store4(ChunkRows(a.d_init + (size_t)bh * p.dv * p.dk, p.dv, p.dk, p.dk), At4<VEC, float>(col, p.dk, 16 * kb + 4 * j, p.dk), dS[kb]);
     }
+}
+
+// ---------------------------------------------------------------- the chains' kernels
+// Neither chain reads what the other writes, so one launch may hold both.
+template <int DK, typename TA, bool RETR, bool VEC, bool CARRY>
+__global__ __launch_bounds__(256, planes_of<TA> <= 2 && DK <= 128 ? 2 : 1) void k_back_states(const BackParams a)
+{
+    __shared__ StatesLds<DK, TA, RETR> lds;
+    states_chain<DK, TA, RETR, VEC, CARRY>(a, blockIdx.x, lds);
+}
+
+template <int DK, typename TA, bool RETR, bool VEC, bool CARRY>
+__global__ __launch_bounds__(256, planes_of<TA> == 1 && DK <= 128 ? 2 : 1) void k_back_chain(const BackParams a)
+{
+    __shared__ ChainLds<DK, TA, RETR> lds;
+    gradient_chain<DK, TA, RETR, VEC, CARRY>(a, blockIdx.x, lds);
+}
+
+// Workgroup 2 n: the nth of the backward chain, 2 n + 1: of the forward one,
+// which with CARRY has more.
+template <int DK, typename TA, bool RETR, bool VEC, bool CARRY>
+__global__ __launch_bounds__(256, planes_of<TA> == 1 && DK <= 128 ? 2 : 1) void k_back_chains(const BackParams a, int chains)
+{
+    __shared__ union {
+        StatesLds<DK, TA, RETR> states;
+        ChainLds<DK, TA, RETR> chain;
+    } lds;
+    const int n = blockIdx.x;
+    if (n < 2 * chains && n % 2 == 0) gradient_chain<DK, TA, RETR, VEC, CARRY>(a, n / 2, lds.chain);
+    else states_chain<DK, TA, RETR, VEC, CARRY>(a, n < 2 * chains ? n / 2 : n - chains, lds.states);
 }
 
 // ---------------------------------------------------------------- gradients of a chunk
@@ -1851,19 +1900,26 @@ hipError_t launch_back_typed(const BackParams &a, hipStream_t s)
 {
     const Params &p = a.p;
     const unsigned per_chunk = (unsigned)a.chunks * p.H, pairs = (unsigned)p.B * p.HV, tiles = a.VB / 4;
-    const dim3 chains(pairs * a.nseg * tiles), block(256);
+    const unsigned chains = pairs * a.nseg * tiles, carry = pairs * a.nseg * (tiles + Geo<DK>::KB / 4);
+    const dim3 block(256);
     hipLaunchKernelGGL((k_back_prep<DK, TA, RETR, VEC>), dim3((unsigned)a.chunks * p.HV), block, 0, s, a);
     if (p.B == 0) return hipGetLastError();
+    const bool both = planes_of<TA> == 1 || 2 * chains <= 256;
     if (a.nseg > 1) {
-        hipLaunchKernelGGL((k_back_states<DK, TA, RETR, VEC, true>), dim3(pairs * a.nseg * (tiles + Geo<DK>::KB / 4)), block, 0, s, a);
-        hipLaunchKernelGGL((k_back_join<DK, false, VEC>), dim3(pairs * a.VB), dim3(DK * 2), 0, s, a);
+        if (both) {
+            hipLaunchKernelGGL((k_back_chains<DK, TA, RETR, VEC, true>), dim3(chains + carry), block, 0, s, a, (int)chains);
+        } else {
+            hipLaunchKernelGGL((k_back_states<DK, TA, RETR, VEC, true>), dim3(carry), block, 0, s, a);
+            hipLaunchKernelGGL((k_back_chain<DK, TA, RETR, VEC, true>), dim3(chains), block, 0, s, a);
+        }
+        hipLaunchKernelGGL((k_back_join<DK, VEC>), dim3(2 * pairs * a.VB), dim3(DK * 2), 0, s, a);
     }
-    hipLaunchKernelGGL((k_back_states<DK, TA, RETR, VEC, false>), chains, block, 0, s, a);
-    if (a.nseg > 1) {
-        hipLaunchKernelGGL((k_back_chain<DK, TA, RETR, VEC, true>), chains, block, 0, s, a);
-        hipLaunchKernelGGL((k_back_join<DK, true, VEC>), dim3(pairs * a.VB), dim3(DK * 2), 0, s, a);
+    if (both) {
+        hipLaunchKernelGGL((k_back_chains<DK, TA, RETR, VEC, false>), dim3(2 * chains), block, 0, s, a, (int)chains);
+    } else {
+        hipLaunchKernelGGL((k_back_states<DK, TA, RETR, VEC, false>), dim3(chains), block, 0, s, a);
+        hipLaunchKernelGGL((k_back_chain<DK, TA, RETR, VEC, false>), dim3(chains), block, 0, s, a);
     }
-    hipLaunchKernelGGL((k_back_chain<DK, TA, RETR, VEC, false>), chains, block, 0, s, a);
     hipLaunchKernelGGL((k_back_grad<DK, TA, RETR, VEC>), dim3(per_chunk), dim3(512), 0, s, a);
     if (RETR || a.decays)
         hipLaunchKernelGGL((k_back_gate<Geo<DK>::C, RETR>), dim3(((unsigned)a.chunks * p.HV + 3) / 4), dim3(256), 0, s, a);

@@ -39,13 +39,15 @@ struct BackParams {
     // workspace
     int32_t *off;               // (B + 1) first chunk of each request; off[B] = chunks in use
     int32_t *tok;               // (B, 2) first token and length of each request
+    int32_t *order;             // (B) requests, the longest first
     int32_t *where;             // (chunks, 2) first token and length of each chunk
     uint16_t *act;              // fp32 activations, per (chunk, q/k head): operand fragments of k^T, q^T
     uint16_t *tri;              // per (chunk, value head): P^T, and with retrieval (I + diag(b) L)^-T, (I + L diag(b))^-1
     float *sc, *s, *ds, *e, *y; // scalars; S0, dS1, E, Y as fp32 fragments
     float *gx;                  // see BackGateRow
-    // between the segments of a chain (nseg > 1): M by rows and by columns, carries, states at their starts
-    float *seg_m, *seg_mt, *seg_carry, *seg_state;
+    // between the segments of the chains (nseg > 1): M by rows and by columns,
+    // carries, states at their starts, and the same of the backward chain
+    float *seg_m, *seg_mt, *seg_carry, *seg_state, *seg_dcarry, *seg_dstate;
     int32_t nseg;
     int32_t chunks;             // chunk budget: ceil(T / C) + B
     int32_t VB;                 // 16-row blocks of dv, a multiple of 4
