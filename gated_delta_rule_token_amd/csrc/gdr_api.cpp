@@ -372,25 +372,25 @@ gdr_status check_backward(const gdr_problem *p)
     return GDR_OK;
 }
 
-// Segments of the backward pass's chains, `chains` workgroups of them.  With n
+// Segments of the backward pass's chains, `chains` workgroups of each.  With n
 // segments the two chains of N steps take about 2 N / n steps each (a segment's
 // map first, then its results) and n hand-overs from segment to segment, worth
 // one step together with the later launches' latency; workgroups past one per
-// CU only slow each other, but for bf16's (two a CU) in long chains.  Measured,
-// bf16, dk = dv = 128, one request, 1 segment against the rule's choice: 4,096
-// tokens x 8 heads 697 / 246 us (n = 16; n = 32: 291), 512 x 4 heads 140 / 127
-// (5), 16,384 x 64 heads 4618 / 4214 (4), 65,536 x 16 heads 15.7 / 4.74 ms (16;
-// n = 8: 5.0); and where it stays at 1: 512 x 32 heads 162 / 175 with 4, four
-// requests of 2,048 x 16 heads 684 / 701 with 4, 8,192 x 128 heads 3160 / 4113
-// with 4.
+// CU of each chain only slow each other.  Few segments gain little and pay in
+// long chains only (bf16's two chains, which run side by side, from four on).
+// Measured, dk = dv = 128, one request, 1 segment against the rule's choice:
+// bf16, 16,384 tokens x 8 heads 1795 / 645 us (16; 32: 669), 4,096 x 8 heads
+// 443 / 215 (16), 1,024 x 8 heads 161 / 121 (8), 512 x 4 heads 100 / 91 (5),
+// 16,384 x 32 heads 2623 / 2305 (4); f32, 2 x 4,096 x 8 heads 966 / 735 (8); and
+// where it stays at 1: bf16, 1,024 x 32 heads 176 / 207 with 4, 16,384 x 64 heads
+// 3508 / 4305 with 4, four requests of 2,048 x 16 heads 556 / 713 with 4.
 int32_t back_segments(const gdr_problem *p, int64_t chains)
 {
     if (chains < 1) return 1;
-    const int64_t N = (p->total_tokens + p->batch - 1) / p->batch / gdr::back_chunk(p->head_dim_k);
-    const bool two = N >= 128 && p->act_dtype == GDR_BF16 && p->head_dim_k <= 128;
-    int64_t n = (two ? 512 : 256) / chains;
-    n = std::min(std::min(n, (int64_t)(2.0 * std::sqrt((double)N))), (int64_t)64);
-    return n >= 3 && n * N >= 40 ? (int32_t)n : 1;
+    const int64_t N = (p->total_tokens + p->batch - 1) / p->batch / gdr::back_chunk(p->head_dim_k), room = 256 / chains;
+    const int64_t n = std::min(std::min(room, (int64_t)(2.0 * std::sqrt((double)N))), (int64_t)64);
+    const bool pays = room >= 8 ? n >= 3 && n * N >= 40 : room >= (p->act_dtype == GDR_BF16 ? 4 : 3) && N >= 64;
+    return pays ? (int32_t)n : 1;
 }
 
 // Carve the workspace (256-byte aligned pieces) at `base` into `a`, with the
