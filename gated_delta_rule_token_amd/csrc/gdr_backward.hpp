@@ -1907,10 +1907,12 @@ hipError_t launch_back_typed(const BackParams &a, hipStream_t s)
     const dim3 block(256);
     hipLaunchKernelGGL((k_back_prep<DK, TA, RETR, VEC>), dim3((unsigned)a.chunks * p.HV), block, 0, s, a);
     if (p.B == 0) return hipGetLastError();
-    // one launch where both kernels have the same workgroups a CU (bf16, two), or
-    // all find a CU of their own; the forward chain of fp16 has two a CU by itself
-    // and one beside the other
-    const bool both = planes_of<TA> == 1 || 2 * chains <= 256;
+    // One launch for both, but for many chains of fp16 and fp32 rows of 128: their
+    // forward chain has two workgroups a CU (fp32: leaves room for a second) by
+    // itself, and one in the joint kernel.  The ragged batch's lengths, one launch
+    // against two: 32 heads of 128 fp16 3.96 / 3.80 ms, fp32 6.05 / 5.75; of 64
+    // fp16 1.91 / 2.23, fp32 2.34 / 2.69; 8 heads of 256 bf16 4.42 / 4.91.
+    const bool both = planes_of<TA> == 1 || DK != 128 || 2 * chains <= 256;
     if (a.nseg > 1) {
         if (both) {
             hipLaunchKernelGGL((k_back_chains<DK, TA, RETR, VEC, true>), dim3(chains + carry), block, 0, s, a, (int)chains);
