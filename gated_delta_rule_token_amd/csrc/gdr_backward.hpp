@@ -31,13 +31,14 @@
 //   k_back_prep    per chunk and value head: the two triangular inverses, P, decay factors
 //   k_back_states  per request, head and 64 state rows: forward chain, keeps S0 and E of every chunk
 //   k_back_chain   the same backwards: dS1, Y, dV
+//   k_back_chains  both of them in one launch, where that is faster
 //   k_back_join    between the segments of a chain, where it is cut (see there)
 //   k_back_grad    per chunk and q/k head: dQ, dK (summed over the value heads that share them)
 //   k_back_gate    per chunk and value head: dg, db
 // and the sums over chunks or heads (k_back_gate_sums, k_back_rate_sums).
 //
 // Figures at the kernels are of a ragged batch of 8 requests, 29,273 tokens, 16
-// q/k and 32 value heads, dk = dv = 128, bf16: 3.2 ms, of which 0.23 ms are the
+// q/k and 32 value heads, dk = dv = 128, bf16: 2.93 ms, of which 0.23 ms are the
 // floor of its inputs and outputs at the copy rate (5.2 TB/s) and 1.0 ms that of
 // its products, in planes, at the rate of a large bf16 product (1234 TFLOP/s).
 // What the kernels hand on (S0 and dS1 64 KB each, E and Y 32 KB each, the
@@ -1057,9 +1058,10 @@ __global__ __launch_bounds__(DK * 2) void k_back_join(const BackParams a)
 // 16 rows in its accumulators over the whole chain.  Everything that a step
 // reads from memory is loaded one step ahead: within the step there are only
 // LDS reads, and stores that nothing waits for.  Two workgroups a CU where
-// registers allow.  656 us: 1.45 GB written and 1.3 GB read, 4.2 TB/s over all,
-// but the longest request's 109 steps, 6 us each, are what it waits for: while
-// all 512 chains run it is bound by memory and VALU, at the end by latency.
+// registers allow.  656 us by itself: 1.45 GB written and 1.3 GB read, 4.2 TB/s
+// over all, but the longest request's 109 steps, 6 us each, are what it waits
+// for: while all 512 chains run it is bound by memory and VALU, at the end by
+// latency.
 template <int DK, typename TA, bool RETR> struct StatesLds {
     __align__(16) uint16_t Kr[planes_of<TA> * Rows<DK>::PLANE];
     __align__(16) uint16_t T[RETR ? 3 * Geo<DK>::NT * BLOCK : 8];
@@ -1183,7 +1185,7 @@ __device__ __forceinline__ void states_chain(const BackParams &a, int block, Sta
 
 // ---------------------------------------------------------------- backward chain
 // As the forward chain; a step has two triangular products and the update of
-// dS by q and by k.  1.03 ms: 1.7 GB written and 2.4 GB read, 3.9 TB/s; 109 steps
+// dS by q and by k.  1.03 ms by itself: 1.7 GB written and 2.4 GB read, 3.9 TB/s; 109 steps
 // of 9.4 us, of which a wave's 198 matrix instructions take 1.3 us and its 1100
 // VALU instructions (planes, transposes) 2 us: 56 % of the waves' time is waiting
 // for LDS and the step before.  Transposes across banks instead of quads spared
