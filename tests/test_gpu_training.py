@@ -199,6 +199,18 @@ def test_backward_many_requests_and_an_empty_call():
     assert got.q.shape == (0, 1, 8)
 
 
+@pytest.mark.parametrize("dtype", [np.float32, np.float16, "bf16"], ids=["f32", "f16", "bf16"])
+@pytest.mark.parametrize("lens,H,HV,DK,DV", [([3, 0, 70, 1] * 35, 1, 1, 128, 16), ([1300], 2, 8, 100, 200),
+                                             ([2, 0, 1] * 400, 1, 1, 8, 8)],
+                         ids=["many_chains", "many_segments", "1200_requests"])
+def test_backward_in_one_launch_and_in_two(lens, H, HV, DK, DV, dtype):
+    """More chains than CUs: of keys of 128 in fp16 and fp32 the two chains are
+    launched one after the other, whole and in segments; else side by side."""
+    case = workloads.random_case(42, lengths=lens, H=H, HV=HV, DK=DK, DV=DV, dtype=dtype, update_rule="gated_delta", qk_l2_norm=1)
+    case["gate"] = case["gate"] * np.float32(0.05)
+    check(case, what="launches")
+
+
 @pytest.mark.parametrize("cu", [[0, 50, 20, 90], [30, 10, 60, 999], [-5, 40, 40, 70]])
 def test_backward_of_any_cu_seqlens(cu):
     """Entries out of order or out of range: the running maximum, clamped; rows
