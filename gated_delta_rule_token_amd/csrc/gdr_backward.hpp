@@ -1850,7 +1850,9 @@ __global__ __launch_bounds__(256) void k_back_gate(const BackParams a)
     const bool mine = lane < C;
     const size_t th = (size_t)(t0 + (lane < cnt ? lane : cnt - 1)) * p.HV + h;
     const float raw = a.decays && p.gate_qwen ? load_gate(p, th) + p.dt_bias[h] : 0.f;
-    const float rate = RETR ? a.sc[(size_t)rec * (BACK_SC * C) + SC_B * C + n0] : 0.f;
+    // e^-|x| of the rate's logit x: the sigmoid's derivative is t / (1 + t)^2,
+    // formed so because 1 - rate loses all its digits where the rate is near 1
+    const float t = RETR && p.beta_sigmoid ? expf(-fabsf(p.beta[beta_index(p, th)])) : 0.f;
     const float col = x[GX_COL * C + n0], state = x[GX_STATE * C], db = x[GX_DB * C + n0];
     float pre = mine ? x[GX_U * C + n0] : 0.f, suf = mine ? x[GX_W * C + n0] : 0.f;
     float rows[MB];
@@ -1884,7 +1886,10 @@ __global__ __launch_bounds__(256) void k_back_gate(const BackParams a)
             else if (p.gate_dt == 2) static_cast<bf16_t *>(a.d_gate)[th] = from_f32<bf16_t>(g);
             else static_cast<float *>(a.d_gate)[th] = g;
         }
-        if (RETR) a.d_beta[th] = p.beta_sigmoid ? db * rate * (1.f - rate) : db;
+        if (RETR) {
+            const float r = 1.f / (1.f + t);
+            a.d_beta[th] = p.beta_sigmoid ? db * (t * r * r) : db;
+        }
     }
     if (a.decays && p.gate_qwen) {
 #pragma unroll
