@@ -453,9 +453,11 @@ def backward(q, k, v, d_o, *, gate=None, beta=None, a_log=None, dt_bias=None, ga
     The gradients have their tensors' shapes and dtypes; beta and a raw gate
     get theirs as given (through the sigmoid, the softplus and the L2 norm).
     ``want_initial_state``: whether the initial states' gradient is returned
-    (default: when there is an initial state).  Rows of tokens that no request
-    covers are zero, or left as they are in a gradient passed in ``out`` (a
-    ``Gradients`` whose tensors are filled; None entries are allocated).
+    (default: when there is an initial state, or ``out`` holds a tensor for
+    it; with False such a tensor is left alone).  Rows of tokens that no
+    request covers are zero, or left as they are in a gradient passed in
+    ``out`` (a ``Gradients`` whose tensors are filled; None entries are
+    allocated; a tensor for an input that the call does not have is refused).
     ``workspace``: a uint8 device tensor of ``backward_workspace_size`` bytes
     (allocated here when not given)."""
     lib = load_library()
@@ -483,11 +485,13 @@ def backward(q, k, v, d_o, *, gate=None, beta=None, a_log=None, dt_bias=None, ga
                                   gate_scale=gate_scale, cu_seqlens=cu_seqlens, seq_lens=seq_lens,
                                   initial_state=initial_state, final_state=d_final_state))
     if want_initial_state is None:
-        want_initial_state = initial_state is not None
+        want_initial_state = initial_state is not None or (out is not None and out.initial_state is not None)
     grads, zero_rest = {}, out is None
     for name, like in (("q", q), ("k", k), ("v", v), ("gate", gate), ("beta", beta), ("initial_state", None),
                        ("a_log", a_log), ("dt_bias", dt_bias), ("gate_scale", gate_scale)):
         if like is None and not (name == "initial_state" and want_initial_state):
+            if out is not None and getattr(out, name) is not None and name != "initial_state":
+                raise GDRError("GDR_E_INVALID", "out.%s given, but the call has no %s" % (name, name))
             grads[name] = None
             continue
         shape, dtype = (states, torch.float32) if like is None else (tuple(like.shape), like.dtype)

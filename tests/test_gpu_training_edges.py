@@ -43,3 +43,30 @@ def test_rate_gradient_of_saturated_sigmoids(shared, dtype):
     err = np.abs(got / factor - rate).max()
     say("  d_beta over r (1 - r): max err %.3e (bound %.1e)" % (err, bar))
     assert err <= bar
+
+
+def test_caller_buffers_of_every_gradient():
+    """A buffer given for the initial states' gradient is filled, with an
+    initial state or without one; one for a tensor that the call does not have
+    is refused, as nothing would be written to it."""
+    from gated_delta_rule_token_amd import api
+    none = dict.fromkeys(api.Gradients._fields)
+    for with_initial in (True, False):
+        case = workloads.random_case(51, lengths=[70, 0, 5], H=1, HV=2, DK=16, DV=24, update_rule="gated_delta",
+                                     with_initial=with_initial)
+        d_o, d_st = draw_gradients(case, False)
+        want = gpu_backward(case, d_o, d_st, want_initial_state=True)
+        buf = torch.full((3, 2, 24, 16), 7.0, device="cuda")
+        got = gpu_backward(case, d_o, d_st, out=api.Gradients(**dict(none, initial_state=buf)))
+        assert got.initial_state is buf and torch.equal(buf, want.initial_state)
+        buf.fill_(7.0)
+        left = gpu_backward(case, d_o, d_st, want_initial_state=False, out=api.Gradients(**dict(none, initial_state=buf)))
+        assert left.initial_state is None and torch.all(buf == 7)
+        for name in ("a_log", "dt_bias", "gate_scale"):
+            with pytest.raises(api.GDRError, match=name):
+                gpu_backward(case, d_o, d_st, out=api.Gradients(**dict(none, **{name: torch.zeros(2, device="cuda")})))
+    case = workloads.random_case(52, lengths=[8], H=1, HV=2, DK=16, DV=16, update_rule="linear")
+    d_o, d_st = draw_gradients(case, False)
+    for name in ("gate", "beta"):
+        with pytest.raises(api.GDRError, match=name):
+            gpu_backward(case, d_o, d_st, out=api.Gradients(**dict(none, **{name: torch.zeros(8, 2, device="cuda")})))
