@@ -329,10 +329,11 @@ gdr_status gdr_gate_backward(int64_t count, int32_t heads, int32_t dtype, const 
  * or NULL) receives inv, which the backward pass takes.  y has out_dtype:
  * dtype, or GDR_E4M3 with scales.  Then scale (rows, ceil(width / group)),
  * or (rows, 1) with group = 0, receives max |y| / 448 over each `group`
- * columns of a row (1 where that is 0), and y holds y / scale, rounded to
- * nearest even; group is 0 or a power of two from 8 to 512.  Arithmetic and
- * sums in fp32.  A row that holds NaN or an infinity gives what the formulas
- * give, and so does one whose squares pass fp32's range (inv = 0). */
+ * columns of a row (1 where that is 0), and y holds the fp32 quotient
+ * y / scale, rounded to nearest even; group is 0 or a power of two from 8 to
+ * 512.  Arithmetic and sums in fp32.  A row that holds NaN or an infinity
+ * gives what the formulas give, and so does one whose squares pass fp32's
+ * range (inv = 0). */
 gdr_status gdr_rms_norm(int64_t rows, int32_t width, int32_t dtype, int32_t weight_dtype, int32_t out_dtype,
                         int32_t group, float eps, const void *x, const void *residual, const void *weight,
                         void *y, float *scale, void *residual_out, float *inv_rms, void *stream);

@@ -70,3 +70,40 @@ def test_caller_buffers_of_every_gradient():
     for name in ("gate", "beta"):
         with pytest.raises(api.GDRError, match=name):
             gpu_backward(case, d_o, d_st, out=api.Gradients(**dict(none, **{name: torch.zeros(8, 2, device="cuda")})))
+
+
+def _quotient_codes(y, scale, group):
+    """e4m3 of the fp32 quotient y / scale, nearest even, on the host."""
+    width = y.shape[1]
+    s = scale.cpu().repeat_interleave(group or width, 1)[:, :width]
+    return (y.cpu() / s).clamp(-448, 448).to(torch.float8_e4m3fn).float()
+
+
+@pytest.mark.parametrize("width,group", [(64, 0), (256, 32), (1001, 128), (4096, 0), (16400, 512)])
+def test_norm_in_8_bits_rounds_the_quotient(width, group):
+    """y8 is the fp32 quotient of the y and the scale that are returned,
+    rounded to nearest even: bit for bit, also for values placed on the
+    midpoints of two codes and on the floats beside them."""
+    from gated_delta_rule_token_amd import api
+    rng = np.random.Generator(np.random.PCG64(width))
+    x = torch.from_numpy(rng.standard_normal((40, width)).astype(np.float32)).cuda()
+    w = torch.from_numpy(rng.standard_normal(width).astype(np.float32)).cuda()
+    y = api.rms_norm(x, w).y
+    got = api.rms_norm(x, w, out_dtype=torch.float8_e4m3fn, group=group)
+    assert torch.equal(got.y.cpu().float(), _quotient_codes(y, got.scale, group))
+    # rows of 2^-30 and eps = 1: inv is 1 and y is x
+    g = group or width
+    n = -(-width // g)
+    top = (448 * 2.0 ** -30 * (1 + rng.random((40, n, 1)))).astype(np.float32)
+    scale = top / np.float32(448)
+    code = rng.integers(1, 126, (40, n, g))
+    mag = np.where(code < 8, code * 2.0 ** -9, (8 + code % 8) * 2.0 ** (code // 8 - 10.0))
+    step = np.where(code < 8, 2.0 ** -9, 2.0 ** (code // 8 - 10.0))
+    v = ((mag + step / 2) * scale).astype(np.float32)
+    v = (v.view(np.int32) + rng.integers(-2, 3, v.shape).astype(np.int32)).view(np.float32)
+    v[..., :1] = top
+    x = torch.from_numpy((v * rng.choice(np.float32([-1, 1]), v.shape)).reshape(40, n * g)[:, :width].copy()).cuda()
+    got = api.rms_norm(x, eps=1.0, out_dtype=torch.float8_e4m3fn, group=group)
+    assert torch.equal(api.rms_norm(x, eps=1.0).y, x)
+    assert torch.equal(got.scale.cpu(), torch.from_numpy(scale[..., 0]))
+    assert torch.equal(got.y.cpu().float(), _quotient_codes(x, got.scale, group))
