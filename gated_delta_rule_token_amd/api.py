@@ -194,6 +194,14 @@ def _need(t, name, dtype=None, device=None):
     return t
 
 
+def _int32(value, name):
+    """``value`` as the C ABI's int32: ctypes would cut it to its low 32 bits."""
+    value = int(value)
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise GDRError("GDR_E_INVALID", "%s (%d) does not fit in 32 bits" % (name, value))
+    return value
+
+
 def build_problem(q, k, v, *, gate=None, beta=None, erase=None, a_log=None, dt_bias=None,
                   cu_seqlens=None, initial_state=None, slot_ids=None, state=None,
                   update_rule="gated_delta", gate_activation="none", beta_activation="none",
@@ -530,7 +538,7 @@ def gate_backward(a, dt_bias, decay_scale, d_decay, b=None, d_beta=None, workspa
     lib = load_library()
     dev = a.device
     _need(a, "a", device=dev)
-    heads = a.shape[-1] if a.dim() else 0
+    heads = _int32(a.shape[-1] if a.dim() else 0, "the last axis of a")
     if (b is None) != (d_beta is None):
         raise GDRError("GDR_E_INVALID", "b and d_beta must be given together")
     for name, t in (("d_decay", d_decay), ("b", b), ("d_beta", d_beta)):
@@ -566,7 +574,7 @@ def _norm_rows(x, weight):
     _need(x, "x", device=x.device)
     if x.dim() < 1 or x.shape[-1] < 1:
         raise GDRError("GDR_E_INVALID", "x needs a last axis of at least one column")
-    width = x.shape[-1]
+    width = _int32(x.shape[-1], "the last axis of x")
     if weight is not None:
         _need(weight, "weight", device=x.device)
         if tuple(weight.shape) != (width,):
@@ -586,6 +594,7 @@ def rms_norm(x, weight=None, *, residual=None, eps=1e-6, out_dtype=None, group=0
     return 1 / sqrt(mean(r^2) + eps) per row, which ``rms_norm_backward`` takes."""
     lib = load_library()
     dev = x.device
+    group = _int32(group, "group")
     rows, width = _norm_rows(x, weight)
     _need(residual, "residual", x.dtype, dev)
     if residual is not None and residual.shape != x.shape:
@@ -608,7 +617,7 @@ def rms_norm(x, weight=None, *, residual=None, eps=1e-6, out_dtype=None, group=0
         raise GDRError("GDR_E_INVALID", "out_dtype must be x's dtype or torch.float8_e4m3fn, got %s" % out_dtype)
     inv = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if want_inv_rms else None
     _enqueue(lib.gdr_rms_norm, dev, rows, width, code, code if weight is None else _dtype_code(weight.dtype), out_code,
-             int(group), float(eps), _ptr(x), _ptr(residual), _ptr(weight), _ptr(y), _ptr(scale), _ptr(residual_out),
+             group, float(eps), _ptr(x), _ptr(residual), _ptr(weight), _ptr(y), _ptr(scale), _ptr(residual_out),
              _ptr(inv))
     return NormOutput(y, scale, residual_out, inv)
 

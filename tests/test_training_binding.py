@@ -1,0 +1,33 @@
+"""Checks of the training operators' binding that come before any device
+access, so that host tensors reach them."""
+import os
+
+import pytest
+import torch
+
+from gated_delta_rule_token_amd import api
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _library():
+    if not os.path.exists(api.library_path()):
+        from gated_delta_rule_token_amd import build
+        build.build()
+
+
+@pytest.mark.parametrize("group", [2 ** 31, 2 ** 32 + 8, -2 ** 32 + 8, 2 ** 40 + 64])
+def test_norm_refuses_a_group_past_32_bits(group):
+    """ctypes would hand the library the low 32 bits: a group of 8 columns for
+    scales that were allocated for one group a row."""
+    with pytest.raises(api.GDRError, match="group"):
+        api.rms_norm(torch.zeros(4, 64), out_dtype=torch.float8_e4m3fn, group=group)
+
+
+@pytest.mark.parametrize("value,fits", [(0, True), (2 ** 31 - 1, True), (-2 ** 31, True), (2 ** 31, False),
+                                        (2 ** 32, False), (-2 ** 31 - 1, False)])
+def test_sizes_handed_to_the_library_fit_32_bits(value, fits):
+    if fits:
+        assert api._int32(value, "size") == value
+    else:
+        with pytest.raises(api.GDRError, match="size"):
+            api._int32(value, "size")
