@@ -68,6 +68,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "gdr_backward_launch.hpp"
 #include "gdr_device.hpp"
 
@@ -1919,22 +1921,23 @@ hipError_t launch_back_typed(const BackParams &a, hipStream_t s)
     // itself, and one in the joint kernel.  The ragged batch's lengths, one launch
     // against two: 32 heads of 128 fp16 3.96 / 3.80 ms, fp32 6.05 / 5.75; of 64
     // fp16 1.91 / 2.23, fp32 2.34 / 2.69; 8 heads of 256 bf16 4.42 / 4.91.
-    const bool both = planes_of<TA> == 1 || DK != 128 || 2 * chains <= 256;
-    if (a.nseg > 1) {
-        if (both) {
-            hipLaunchKernelGGL((k_back_chains<DK, TA, RETR, VEC, true>), dim3(chains + carry), block, 0, s, a, (int)chains);
-        } else {
-            hipLaunchKernelGGL((k_back_states<DK, TA, RETR, VEC, true>), dim3(carry), block, 0, s, a);
-            hipLaunchKernelGGL((k_back_chain<DK, TA, RETR, VEC, true>), dim3(chains), block, 0, s, a);
+    constexpr bool SPLITS = planes_of<TA> > 1 && DK == 128;
+    const auto launch_chains = [&](auto first_pass, unsigned backward, unsigned forward) {
+        constexpr bool CARRY = decltype(first_pass)::value;
+        if constexpr (SPLITS) {
+            if (2 * chains > 256) {
+                hipLaunchKernelGGL((k_back_states<DK, TA, RETR, VEC, CARRY>), dim3(forward), block, 0, s, a);
+                hipLaunchKernelGGL((k_back_chain<DK, TA, RETR, VEC, CARRY>), dim3(backward), block, 0, s, a);
+                return;
+            }
         }
+        hipLaunchKernelGGL((k_back_chains<DK, TA, RETR, VEC, CARRY>), dim3(backward + forward), block, 0, s, a, (int)backward);
+    };
+    if (a.nseg > 1) {
+        launch_chains(std::true_type(), chains, carry);
         hipLaunchKernelGGL((k_back_join<DK, VEC>), dim3(2 * pairs * a.VB), dim3(DK * 2), 0, s, a);
     }
-    if (both) {
-        hipLaunchKernelGGL((k_back_chains<DK, TA, RETR, VEC, false>), dim3(2 * chains), block, 0, s, a, (int)chains);
-    } else {
-        hipLaunchKernelGGL((k_back_states<DK, TA, RETR, VEC, false>), dim3(chains), block, 0, s, a);
-        hipLaunchKernelGGL((k_back_chain<DK, TA, RETR, VEC, false>), dim3(chains), block, 0, s, a);
-    }
+    launch_chains(std::false_type(), chains, chains);
     hipLaunchKernelGGL((k_back_grad<DK, TA, RETR, VEC>), dim3(per_chunk), dim3(512), 0, s, a);
     if (RETR || a.decays)
         hipLaunchKernelGGL((k_back_gate<Geo<DK>::C, RETR>), dim3(((unsigned)a.chunks * p.HV + 3) / 4), dim3(256), 0, s, a);

@@ -386,9 +386,10 @@ hipError_t by_width(int64_t width, F &&f)
     if (v <= 32) return f(integral_constant<int, 32>(), integral_constant<int, 1>());
     if (v <= 64) return f(integral_constant<int, 64>(), integral_constant<int, 1>());
     if (v <= 128) return f(integral_constant<int, 64>(), integral_constant<int, 2>());
-    if constexpr (WAVE >= 4)
-        if (v <= 256) return f(integral_constant<int, 64>(), integral_constant<int, 4>());
-    if (v <= 256) return f(integral_constant<int, 256>(), integral_constant<int, 1>());
+    if (v <= 256) {
+        if constexpr (WAVE >= 4) return f(integral_constant<int, 64>(), integral_constant<int, 4>());
+        else return f(integral_constant<int, 256>(), integral_constant<int, 1>());
+    }
     if (v <= 512) return f(integral_constant<int, 256>(), integral_constant<int, 2>());
     if (v <= 1024) return f(integral_constant<int, 256>(), integral_constant<int, 4>());
     if (v <= 2048) return f(integral_constant<int, 1024>(), integral_constant<int, 2>());

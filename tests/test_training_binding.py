@@ -1,6 +1,7 @@
 """Checks of the training operators' binding that come before any device
 access, so that host tensors reach them."""
 import os
+import re
 
 import pytest
 import torch
@@ -31,3 +32,17 @@ def test_sizes_handed_to_the_library_fit_32_bits(value, fits):
     else:
         with pytest.raises(api.GDRError, match="size"):
             api._int32(value, "size")
+
+
+def test_no_kernel_that_no_call_launches():
+    """The chains have kernels of their own only where the launch rule can
+    choose them (keys of 65 to 128 in fp16 and fp32), and the norm's forward
+    pass one form of rows for each width.  By the kernels' names in the library."""
+    with open(api.library_path(), "rb") as f:
+        code = f.read()
+    instances = lambda kernel: set(re.findall(kernel + rb"ILi(\d+)E(DF16b|DF16_|f)", code))  # noqa: E731
+    everything = {(dk, t) for dk in (b"64", b"128", b"256") for t in (b"DF16b", b"DF16_", b"f")}
+    assert instances(rb"k_back_chains") == everything and instances(rb"k_back_grad") == everything
+    assert instances(rb"k_back_states") == instances(rb"k_back_chain") == {(b"128", b"DF16_"), (b"128", b"f")}
+    forms = set(re.findall(rb"6k_normI(?:DF16b|DF16_|f)+Li(\d+)ELi(\d+)E", code))
+    assert (b"64", b"4") in forms and (b"256", b"1") not in forms
