@@ -6,7 +6,7 @@ import pytest
 
 from gated_delta_rule_token_amd import workloads
 from tests.gpu_helpers import say
-from tests.test_gpu_training import FP32, draw_gradients, gpu_backward, host, oracle_backward
+from tests.test_gpu_training import FP32, HALF_STEP, check, draw_gradients, gpu_backward, host, oracle_backward
 
 pytestmark = pytest.mark.gpu
 
@@ -107,3 +107,75 @@ def test_norm_in_8_bits_rounds_the_quotient(width, group):
     assert torch.equal(api.rms_norm(x, eps=1.0).y, x)
     assert torch.equal(got.scale.cpu(), torch.from_numpy(scale[..., 0]))
     assert torch.equal(got.y.cpu().float(), _quotient_codes(x, got.scale, group))
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e-37, 1e-38, 1e-41, 1e-43, 1e-45])
+@pytest.mark.parametrize("group", [0, 32])
+def test_norm_in_8_bits_of_tiny_rows_has_their_scale(size, group):
+    """Scales down to denormal ones: max / 448 in fp32, 1 only where that rounds
+    to 0, and the codes of the quotients, so that the largest of a group lies
+    at 448 but for the rounding of a denormal scale."""
+    from gated_delta_rule_token_amd import api
+    rng = np.random.Generator(np.random.PCG64(8))
+    x = torch.from_numpy((rng.standard_normal((5, 200)) * size).astype(np.float32)).cuda()
+    got = api.rms_norm(x, eps=1.0, out_dtype=torch.float8_e4m3fn, group=group)  # inv = 1: y = x
+    for c, s in enumerate(got.scale.cpu().double().unbind(1)):
+        part = x[:, c * group:(c + 1) * group] if group else x
+        top = part.abs().amax(1).cpu().double() / 448
+        zero = top <= 2.0 ** -150
+        assert torch.all(s[zero] == 1)
+        assert torch.all((s - top).abs()[~zero] <= 2.0 ** -24 * top[~zero] + 2.0 ** -150)
+        full = (top > 2.0 ** -126) & ~zero
+        q = got.y[:, c * group:(c + 1) * group] if group else got.y
+        assert torch.all(q.cpu().float().abs().amax(1)[full] == 448)
+    assert torch.equal(got.y.cpu().float(), _quotient_codes(x, got.scale, group))
+
+
+# more rows than 2,048 workgroups of 16, 8, 4 or 1 rows take at once, and no multiple of that
+MANY = [(33001, 128, 64), (16500, 250, 0), (9000, 512, 128), (8300, 2048, 0), (2500, 4096, 128), (2500, 4100, 0),
+        (2100, 8200, 512), (2100, 16400, 256)]
+
+
+@pytest.mark.parametrize("rows,width,group", MANY)
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+def test_norm_of_more_rows_than_one_launch_holds(rows, width, group, dtype):
+    """A workgroup's further rows, with the next one on its way: in place, in
+    8 bits and backwards, against fp64 (the bars of the small calls)."""
+    from gated_delta_rule_token_amd import api
+    dt, half = getattr(torch, dtype), HALF_STEP[dtype]
+    gen = torch.Generator(device="cuda").manual_seed(rows + width)
+    draw = lambda *s: torch.randn(s, generator=gen, device="cuda").to(dt)  # noqa: E731
+    x, res, w, dy = draw(rows, width), draw(rows, width), draw(width), draw(rows, width)
+    r = (x.float() + res.float()).to(dt)
+    inv = torch.rsqrt(r.double().square().mean(-1, keepdim=True) + 1e-6)
+    h = r.double() * inv
+    y = h * w.double()
+    kept = res.clone()
+    got = api.rms_norm(x, w, residual=kept, residual_out=kept, want_inv_rms=True)
+    assert torch.equal(kept, r)
+    assert torch.all((got.inv_rms.double()[:, None] - inv).abs() <= 1e-5 * inv)
+    assert torch.all((got.y.double() - y).abs() <= (half + 1e-5) * y.abs() + 2.0 ** -25)  # half of fp16's smallest value
+    kept = res.clone()
+    eight = api.rms_norm(x, w, residual=kept, residual_out=kept, out_dtype=torch.float8_e4m3fn, group=group)
+    assert torch.equal(kept, r)
+    g = group or width
+    amax = torch.nn.functional.pad(y.abs(), (0, -width % g)).view(rows, -1, g).amax(-1)
+    assert torch.all((eight.scale.double() - amax / 448).abs() <= 1e-5 * amax / 448)
+    t = y / eight.scale.double().repeat_interleave(g, 1)[:, :width]
+    step = torch.exp2(torch.floor(torch.log2(t.abs().clamp(min=2.0 ** -6))) - 3)
+    assert torch.all((eight.y.double() - t).abs() <= step / 2 + 2e-5 * t.abs())
+    back = api.rms_norm_backward(dy, r, w, got.inv_rms)
+    d = dy.double() * w.double()
+    dx = inv * (d - h * (d * h).mean(-1, keepdim=True))
+    assert (back.x.double() - dx).abs().max() <= (half + FP32) * dx.abs().max()
+    dw = (dy.double() * h).sum(0)
+    assert (back.weight.double() - dw).abs().max() <= FP32 * dw.abs().max()
+
+
+def test_raw_gate_sums_over_many_chunks():
+    """More chunks than the 256 threads that add up a head's sums."""
+    rng = np.random.Generator(np.random.PCG64(9))
+    check(workloads.random_case(53, lengths=rng.integers(0, 4, 700), H=1, HV=2, DK=16, DV=8, update_rule="gated_delta",
+                                gate_activation="qwen", beta_activation="sigmoid", qk_l2_norm=1), what="700 requests")
+    check(workloads.random_case(54, lengths=rng.integers(1, 3, 400), H=1, HV=3, DK=200, DV=8, update_rule="gated",
+                                gate_activation="qwen", folded_scale=True), what="400 requests")
