@@ -179,3 +179,27 @@ def test_raw_gate_sums_over_many_chunks():
                                 gate_activation="qwen", beta_activation="sigmoid", qk_l2_norm=1), what="700 requests")
     check(workloads.random_case(54, lengths=rng.integers(1, 3, 400), H=1, HV=3, DK=200, DV=8, update_rule="gated",
                                 gate_activation="qwen", folded_scale=True), what="400 requests")
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("where", ["q", "k", "v", "d_o", "initial_state", "d_final_state"])
+def test_backward_keeps_a_bad_value_in_its_request(where, bad):
+    """A NaN or an infinity in one request: the rows and states of the others
+    have the bits that they have without it."""
+    case = workloads.random_case(55, lengths=[70, 100, 0, 65], H=1, HV=2, DK=32, DV=16, update_rule="gated_delta",
+                                 gate_activation="qwen", beta_activation="sigmoid", qk_l2_norm=1)
+    d_o, d_st = draw_gradients(case, True)
+    good = gpu_backward(case, d_o, d_st)
+    case = {name: x.copy() if isinstance(x, np.ndarray) else x for name, x in case.items()}
+    d_o, d_st = d_o.copy(), d_st.copy()
+    if where in ("initial_state", "d_final_state"):
+        (case["initial_state"] if where == "initial_state" else d_st)[1, 0, 3, 5] = bad
+    else:
+        (d_o if where == "d_o" else case[where])[70 + 40, 0, 7] = bad
+    got = gpu_backward(case, d_o, d_st)
+    assert not torch.isfinite(got.q[70:170]).all() or not torch.isfinite(got.k[70:170]).all()
+    for name in ("q", "k", "v", "gate", "beta"):
+        for rows in (slice(0, 70), slice(170, 235)):
+            assert torch.equal(getattr(got, name)[rows], getattr(good, name)[rows]), name
+    for b in (0, 2, 3):
+        assert torch.equal(got.initial_state[b], good.initial_state[b])
