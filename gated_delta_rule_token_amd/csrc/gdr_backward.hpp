@@ -31,7 +31,8 @@
 //   k_back_prep    per chunk and value head: the two triangular inverses, P, decay factors
 //   k_back_states  per request, head and 64 state rows: forward chain, keeps S0 and E of every chunk
 //   k_back_chain   the same backwards: dS1, Y, dV
-//   k_back_chains  both of them in one launch, where that is faster
+//   k_back_chains  both of them in one launch; by themselves only where that is
+//                  faster (fp16 and fp32 rows of 65 to 128, many chains)
 //   k_back_join    between the segments of a chain, where it is cut (see there)
 //   k_back_grad    per chunk and q/k head: dQ, dK (summed over the value heads that share them)
 //   k_back_gate    per chunk and value head: dg, db
@@ -1063,7 +1064,7 @@ __global__ __launch_bounds__(DK * 2) void k_back_join(const BackParams a)
 // registers allow.  656 us by itself: 1.45 GB written and 1.3 GB read, 4.2 TB/s
 // over all, but the longest request's 109 steps, 6 us each, are what it waits
 // for: while all 512 chains run it is bound by memory and VALU, at the end by
-// latency.
+// latency (beside the other chain: see k_back_chains).
 template <int DK, typename TA, bool RETR> struct StatesLds {
     __align__(16) uint16_t Kr[planes_of<TA> * Rows<DK>::PLANE];
     __align__(16) uint16_t T[RETR ? 3 * Geo<DK>::NT * BLOCK : 8];
@@ -1190,9 +1191,12 @@ __device__ __forceinline__ void states_chain(const BackParams &a, int block, Sta
 // dS by q and by k.  1.03 ms by itself: 1.7 GB written and 2.4 GB read, 3.9 TB/s; 109 steps
 // of 9.4 us, of which a wave's 198 matrix instructions take 1.3 us and its 1100
 // VALU instructions (planes, transposes) 2 us: 56 % of the waves' time is waiting
-// for LDS and the step before.  Transposes across banks instead of quads spared
-// 300 of the latter and were no faster; nor was one XCD for the workgroups that
-// share operands (1041 us against 1047).
+// for LDS, memory and the step before.  By itself it gained nothing from
+// transposes across banks instead of quads, which spared 300 of the latter, nor
+// from one XCD for the workgroups that share operands (1041 us against 1047);
+// neither was tried in the joint launch, which memory bounds.
+// fp16 rows lie in LDS as two planes: 112 KB and one workgroup a CU, where bf16
+// has 75 KB and two.
 template <int DK, typename TA, bool RETR> struct ChainLds {
     __align__(16) uint16_t Kr[planes_of<TA> * Rows<DK>::PLANE], Qr[planes_of<TA> * Rows<DK>::PLANE];
     __align__(16) uint16_t T[(RETR ? 6 : 3) * Geo<DK>::NT * BLOCK];  // P^T, then (I + diag(b) L)^-T
@@ -1324,9 +1328,11 @@ __device__ __forceinline__ void gradient_chain(const BackParams &a, int block, C
 
 // ---------------------------------------------------------------- the chains' kernels
 // Neither chain reads what the other writes, so one launch may hold both: the
-// long requests of one run while the other's end.  Ragged batch: 1.42 ms for both
-// (one after the other 1.69; in the requests' own order 1.54), 16 tokens 9.8 us
-// (17.4).
+// long requests of one run while the other's end.  Ragged batch: 1.41 ms for both
+// (one after the other 1.69; in the requests' own order 1.54), 3.7 GB read and
+// 3.2 GB written: 4.9 TB/s, bound by memory at 95 % of a copy's rate.  16 tokens
+// 9.8 us (17.4).  252 registers of bf16 rows of 128, 256 and 8 bytes of scratch
+// in the first pass of segments; odd widths 8 to 32 bytes.
 template <int DK, typename TA, bool RETR, bool VEC, bool CARRY>
 __global__ __launch_bounds__(256, planes_of<TA> <= 2 && DK <= 128 ? 2 : 1) void k_back_states(const BackParams a)
 {
@@ -1363,10 +1369,17 @@ __global__ __launch_bounds__(256, planes_of<TA> == 1 && DK <= 128 ? 2 : 1) void 
 // registers, those over tokens (d_o, Y, E) through LDS, cut into planes once
 // for all waves, 32 state rows a step, double buffered.  Of the chunk x chunk
 // products wave (ft, part) forms column blocks part * SBW .. of row block ft.
-// 1.34 ms: 3.9 GB read and 0.33 GB written, 3.2 TB/s, one workgroup a CU (151 KB of
+// 1.34 ms: 3.5 GB read and 0.3 GB written, 2.8 TB/s, one workgroup a CU (152 KB of
 // LDS, 256 VGPRs); matrix and VALU instructions fill two thirds of the SIMDs'
 // cycles, the rest is waiting between a head's phases.  Keeping the rows of q
 // and k in LDS spared 0.4 ms against reading them again for each head.
+// The registers do not hold everything: with retrieval, 16-bit rows of 65 to 128
+// channels put 12 to 56 bytes a lane in scratch memory, fp32 ones (whose q and k
+// stay in registers over all heads) 344 to 360 (160 to 200 without retrieval),
+// and above 128 channels, where a wave has twice the accumulators, every type
+// 240 to 736.  Up to 64 channels nothing spills.  That and the chunks of 32 are
+// what those widths pay for (the batch's lengths, whole calls: 8 heads of 256 in
+// bf16 4.4 ms and fp32 6.4, 32 heads of 128 in fp32 5.7).
 template <int DK, typename TA, bool RETR, bool VEC>
 __global__ __launch_bounds__(512, 2) void k_back_grad(const BackParams a)
 {
@@ -1832,7 +1845,7 @@ __global__ __launch_bounds__(512, 2) void k_back_grad(const BackParams a)
 }
 
 // ---------------------------------------------------------------- dg and db
-// A wave per (chunk, value head), a lane a token (24 us):
+// A wave per (chunk, value head), a lane a token (28 us):
 //   dg_s = e^Gamma <dS1, S0> + sum_{t<s} u_t + sum_{t>=s} w_t + sum_{t>=s>r} M_tr
 // the last from the sums over r of whole blocks before s's own (rows) and
 // within it (col); then the raw gate's and the rate's activation.

@@ -375,8 +375,10 @@ __global__ __launch_bounds__(256) void k_norm_back_sums(const NormBackParams p, 
 // pass takes 92 us with a row a wave (four vectors a lane); the backward pass
 // 100 us so and 88 us with a row a workgroup, as its lanes then hold a quarter
 // of the three rows and the weight's gradient.  The widest rows (above 16,384)
-// do not fit a workgroup's registers backwards: 3,000 rows of 32,768 in bf16
-// take 641 us, 4 times the copy rate's 152 (forward 159 us).
+// do not fit a workgroup's registers: 60 to 144 bytes a lane lie in scratch
+// memory forwards (3,000 rows of 32,768 in bf16: 159 us) and 324 to 520 backwards
+// (642 us, 4 times the copy rate's 152, where 6,000 rows of 16,384 take 145); rows of
+// 8,193 to 16,384 backwards put 12 bytes there in bf16 and 52 to 68 in fp32.
 template <int WAVE, typename F>
 hipError_t by_width(int64_t width, F &&f)
 {
@@ -438,7 +440,13 @@ hipError_t by_types(const P &p, F &&f)
 int norm_back_blocks(int64_t rows, int64_t width)
 {
     // 16,384 elements a workgroup, up to two workgroups a CU (29,273 rows of
-    // 2,048 in bf16: 88 us; with four, whose partial rows are twice as many, 97 us)
+    // 2,048 in bf16: 88 us; with four, whose partial rows are twice as many, 97 us).
+    // 8,192, 16,384 and 32,768 elements, on the device (a graph's replay): 1,217 rows of
+    // 1,001 in fp32 10.9, 14.0 and 18.9 us, 256 of 2,048 in bf16 8.7, 11.7 and
+    // 18.9, 300 of 8,192 in fp32 21.5, 15.4 and 16.8, 1,000 of 4,096 in bf16 17.1,
+    // 16.9 and 21.6.  Calls one by one take 16.7 to 17.0 us in all of the first two
+    // forms, the host's time, but for the 300 rows (20.0 and 16.7), and up to 21
+    // in the third.
     const int64_t n = rows * width / 16384;
     return n < 1 ? 1 : n > 512 ? 512 : (int)n;
 }

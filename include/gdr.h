@@ -265,7 +265,11 @@ gdr_status gdr_forward_noalloc(const gdr_problem *problem, const gdr_tensors *te
  *
  * All arithmetic and every sum is in fp32 (cumulative decays in fp64);
  * gradients are rounded to nearest once, on store.  Sums over tokens and
- * shared heads have a fixed order: equal calls give equal bits. */
+ * shared heads have a fixed order: equal calls give equal bits.  An infinity or
+ * a NaN in a request's tensors or incoming gradients makes NaN of gradients of
+ * that request, of tokens before and after it (a chunk's masked products are
+ * formed and multiplied by 0), and of the sums it enters; other requests' rows
+ * are as without it.  A gate of -inf (a reset) is no such value. */
 typedef struct {
     const void *d_o;              /* (T, HV, dv) act dtype: gradient of o */
     const float *d_final_state;   /* (B, HV, dv, dk): gradient of the final states, or NULL (zero) */
@@ -278,17 +282,22 @@ typedef struct {
     int32_t zero_rest;            /* 1: zero in the rows (of d_q .. d_beta) of tokens that no request covers */
 } gdr_gradients;
 
-/* Bytes of device workspace gdr_backward needs for `problem`: about 256 KB per
- * 64 tokens of a request and value head at dk = dv = 128 (3.8 GB at 29,273
- * tokens in 8 requests, 32 heads), more for fp32 activations, and less without
- * retrieval.  Calls that overlap in time need workspaces of their own; nothing
- * in it has to start at zero or be kept between calls. */
+/* Bytes of device workspace gdr_backward needs for `problem`: at dk = dv = 128
+ * about 256 KB for each value head and chunk, of which ceil(T / 64) + B are
+ * counted (chunks of 32 tokens above dk = 128), as a request's last chunk is
+ * kept whole: 3.8 GB at 29,273 tokens in 8 requests and 32 heads, 0.3 GB at 949
+ * tokens in 24, and 83 GB for 10,000 requests of one token: split such a batch
+ * over several calls.  More for fp32 activations, less without retrieval.
+ * Calls that overlap in time need workspaces of their own; nothing in it has to
+ * start at zero or be kept between calls. */
 gdr_status gdr_backward_workspace_size(const gdr_problem *problem, size_t *bytes);
 
 /* Enqueue the backward pass on `stream`.  Arguments are checked on the host
  * as in gdr_forward; no output may overlap an input, the workspace or another
  * output (GDR_E_ALIAS; d_final_state and d_initial_state may be the same
- * buffer). */
+ * buffer).  Few requests and heads have their chains of chunks cut into
+ * segments by the average length; one long request among many short ones does
+ * not, and is several times faster in a call of its own. */
 gdr_status gdr_backward(const gdr_problem *problem, const gdr_tensors *tensors, const gdr_gradients *gradients,
                         void *workspace, size_t workspace_bytes, void *stream);
 
@@ -308,8 +317,9 @@ gdr_status gdr_gate(int64_t count, int32_t heads, int32_t dtype, const void *a,
  *   d_b[n] = d_beta[n] * beta[n] * (1 - beta[n])     (with b, d_beta and d_b, all or none)
  *   d_dt_bias[h] = sum of d_a,  d_decay_scale[h] = sum of d_decay * softplus(a + dt_bias)
  * the sums over every row (n / heads), in fp32, in a fixed order.  a, b,
- * d_decay, d_beta, d_a, d_b share `dtype` and are 16-byte aligned; d_dt_bias
- * and d_decay_scale are fp32 (heads), written also when count is 0.
+ * d_decay, d_beta, d_a, d_b share `dtype`; d_dt_bias and d_decay_scale are fp32
+ * (heads, up to 65,535), written also when count is 0.  Every pointer is 16-byte
+ * aligned.
  * `workspace`: gdr_gate_backward_workspace_size bytes of device memory.  No
  * output may overlap an input, the workspace or another output. */
 gdr_status gdr_gate_backward_workspace_size(int64_t count, int32_t heads, size_t *bytes);
@@ -333,7 +343,8 @@ gdr_status gdr_gate_backward(int64_t count, int32_t heads, int32_t dtype, const 
  * y / scale, rounded to nearest even; group is 0 or a power of two from 8 to
  * 512.  Arithmetic and sums in fp32.  A row that holds NaN or an infinity
  * gives what the formulas give, and so does one whose squares pass fp32's
- * range (inv = 0). */
+ * range (inv = 0).  Every pointer is 16-byte aligned (rows need not be: a width
+ * may be odd). */
 gdr_status gdr_rms_norm(int64_t rows, int32_t width, int32_t dtype, int32_t weight_dtype, int32_t out_dtype,
                         int32_t group, float eps, const void *x, const void *residual, const void *weight,
                         void *y, float *scale, void *residual_out, float *inv_rms, void *stream);
@@ -343,8 +354,8 @@ gdr_status gdr_rms_norm(int64_t rows, int32_t width, int32_t dtype, int32_t weig
  *   d_x = inv * (t - h * mean(t * h)) + d_residual,  h = x * inv, t = weight * d_y
  *   d_weight = sum over rows of d_y * h   (fp32; non-NULL iff weight is)
  * d_residual, the gradient that reaches r besides through y, may be NULL; d_x
- * is the gradient of x and of the residual alike.  The sum over rows has a
- * fixed order.  `workspace`: gdr_rms_norm_backward_workspace_size bytes (not
+ * is the gradient of x and of the residual alike.  Pointers are 16-byte
+ * aligned.  The sum over rows has a fixed order.  `workspace`: gdr_rms_norm_backward_workspace_size bytes (not
  * needed without a weight). */
 gdr_status gdr_rms_norm_backward_workspace_size(int64_t rows, int32_t width, size_t *bytes);
 gdr_status gdr_rms_norm_backward(int64_t rows, int32_t width, int32_t dtype, int32_t weight_dtype, const void *d_y,
