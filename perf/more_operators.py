@@ -1,0 +1,403 @@
+"""Positions of queries and keys, and the state cache in fewer bits, as they are measured: cases, inputs, plain forms
+and 64-bit results.
+
+``own`` False computes each operator in its plain form (elementary torch operations in 32 bits, angles in 64); True
+makes the framework's calls.
+
+Operators (key ``op`` of a case):
+  rotary           root-mean-square norm of every head of q and k and the rotation by the positions
+  rotary_backward  its gradients
+  pack             fp32 states written into slots of a cache of 8 or 16 bits
+  unpack           slots of such a cache read back
+  decode           one to eight tokens for each request, on the states in the cache, which is updated in place
+"""
+import math
+
+import torch
+
+own = False
+
+DTYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}
+SIZE = {"f32": 4, "f16": 2, "bf16": 2, "e4m3": 1}
+E4M3_MAX = 448.0
+EPS = 1e-6
+
+
+def listed():
+    rotary = dict(dim=128, rotary=128, weight="f32", pairs="halves", axes=1, far=0, fused=False)
+    decode = dict(op="decode", heads=16, heads_v=32, dk=128, dv=128, rule="gated_delta", per_key=False)
+    return [
+        # serving: one token of each of 256 requests, at positions up to 32,768
+        dict(rotary, op="rotary", name="rotary_decode", tokens=256, heads=16, heads_k=16, dtype="bf16", far=32768),
+        # the ragged prefill batch; q and k are views of the projection's output
+        dict(rotary, op="rotary", name="rotary_prefill", tokens=29273, heads=16, heads_k=16, dtype="f16", fused=True),
+        # a video's patches: time, height and width, half of each head rotated, fewer key heads
+        dict(rotary, op="rotary", name="rotary_video", tokens=32760, heads=16, heads_k=4, dtype="bf16", rotary=64,
+             axes=3, weight="bf16"),
+        # the training step's gradients for the same ragged batch
+        dict(rotary, op="rotary_backward", name="rotary_backward_train", tokens=29273, heads=16, heads_k=16,
+             dtype="bf16", weight="bf16"),
+        # odd sizes in fp32, neighbours paired, positions past a million
+        dict(rotary, op="rotary_backward", name="rotary_backward_odd", tokens=1217, heads=9, heads_k=3, dim=72,
+             rotary=40, dtype="f32", pairs="neighbours", far=2000000),
+        # the final states of a prefill batch of eight requests, into the cache that decoding goes on with
+        dict(op="pack", name="pack_prefill", batch=8, heads_v=32, dk=128, dv=128, cache="f16"),
+        # a whole batch's states parked in 8 bits
+        dict(op="pack", name="pack_batch_8bit", batch=256, heads_v=32, dk=128, dv=128, cache="e4m3"),
+        # a few parked requests taken up again
+        dict(op="unpack", name="unpack_resume_8bit", batch=24, heads_v=32, dk=128, dv=128, cache="e4m3"),
+        # odd sizes
+        dict(op="unpack", name="unpack_odd", batch=37, heads_v=9, dk=72, dv=40, cache="bf16"),
+        # a handful of requests: latency
+        dict(decode, name="decode_few", batch=4, length=1, dtype="bf16", cache="bf16"),
+        # the decode batch, one token each, the cache in 8 bits
+        dict(decode, name="decode_batch_8bit", batch=256, length=1, dtype="f16", cache="e4m3"),
+        # the same batch with four tokens each to verify, the cache in 16 bits
+        dict(decode, name="decode_verify_16bit", batch=256, length=4, dtype="bf16", cache="f16"),
+    ]
+
+
+def _spread(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["rotary", "rotary", "rotary_backward", "rotary_backward", "pack", "unpack", "decode", "decode", "decode"])
+    if op.startswith("rotary"):
+        dtype = rng.choice(["f32", "f16", "bf16", "bf16"])
+        dim = rng.choice([64, 128, 128, 256, _spread(rng, 8, 256)])
+        rotary = 2 * rng.randint(1, dim // 2) if rng.random() < 0.2 else dim // rng.choice([1, 1, 2, 4]) // 2 * 2
+        heads = _spread(rng, 1, 32)
+        heads_k = rng.choice([heads, heads, 1, _spread(rng, 1, 32)])
+        most = 29273 * 32 * 128 // ((heads + heads_k) * dim * (2 if dtype == "f32" else 1))
+        return dict(op=op, tokens=_spread(rng, 1, min(most, 100000)), heads=heads, heads_k=heads_k, dim=dim, rotary=max(2, rotary),
+                    dtype=dtype, weight=rng.choice([dtype, "f32", "none"]), pairs=rng.choice(["halves", "halves", "neighbours"]),
+                    axes=rng.choice([1, 1, 2, 3]), far=rng.choice([0, 4096, 131072, 2000000]), fused=rng.random() < 0.4)
+    dk = rng.choice([64, 128, 128, 128, 256, _spread(rng, 8, 256)])
+    dv = dk if rng.random() < 0.7 else rng.choice([64, 128, 256, _spread(rng, 8, 256)])
+    heads = _spread(rng, 1, 16)
+    heads_v = heads * rng.choice([1, 2, 4])
+    batch = _spread(rng, 1, min(512, max(1, 256 * 32 * 128 * 128 // (heads_v * dk * dv))))
+    cache = rng.choice(["e4m3", "e4m3", "f16", "bf16"])
+    if op != "decode":
+        return dict(op=op, batch=batch, heads_v=heads_v, dk=dk, dv=dv, cache=cache)
+    rule = rng.choice(["gated_delta", "gated_delta", "gated_delta", "delta", "gated", "gated_delta_v2"])
+    return dict(op=op, batch=batch, length=rng.choice([1, 1, 1, 2, 4, 7]), heads=heads, heads_v=heads_v, dk=dk, dv=dv,
+                dtype=rng.choice(["f16", "bf16"]), cache=cache, rule=rule,
+                per_key=rule in ("gated", "gated_delta", "gated_delta_v2") and rng.random() < 0.3)
+
+
+# ------------------------------------------------------------------ inputs
+
+def prepare(case, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    dev = "cuda"
+
+    def normal(*shape, std=1.0, dtype=torch.float32):
+        return (torch.randn(shape, generator=gen, device=dev) * std).to(dtype)
+
+    def uniform(lo, hi, *shape):
+        return torch.rand(shape, generator=gen, device=dev) * (hi - lo) + lo
+
+    s = {"case": case}
+    if case["op"].startswith("rotary"):
+        dtype = DTYPES[case["dtype"]]
+        T, H, HK, d, R = case["tokens"], case["heads"], case["heads_k"], case["dim"], case["rotary"]
+        if case["fused"]:  # the projection's output: q, k and a value part beside them
+            rows = normal(T, (H + HK) * d + 2 * d, dtype=dtype)
+            q, k = rows[:, : H * d].view(T, H, d), rows[:, H * d: (H + HK) * d].view(T, HK, d)
+        else:
+            q, k = normal(T, H, d, dtype=dtype), normal(T, HK, d, dtype=dtype)
+        s.update(q=q, k=k, q_weight=None, k_weight=None)
+        if case["weight"] != "none":
+            s["q_weight"] = (1 + normal(d, std=0.1)).to(DTYPES[case["weight"]])
+            s["k_weight"] = (1 + normal(d, std=0.1)).to(DTYPES[case["weight"]])
+        at = torch.arange(T, device=dev)
+        if case["far"]:
+            at = at % 777 + torch.randint(0, case["far"], (1 + T // 777,), generator=gen, device=dev)[at // 777]
+        # one axis: the token's place; more: a video's frame, row and column
+        axes = [at] if case["axes"] == 1 else [at // 1560, at % 1560 // 52, at % 52][: case["axes"]]
+        s["positions"] = torch.stack(axes).to(torch.int32) if len(axes) > 1 else axes[0].to(torch.int32)
+        s["freqs"] = torch.exp(torch.arange(R // 2, device=dev, dtype=torch.float64) * (-math.log(10000.0) * 2 / R)).float()
+        s["axes"] = (torch.arange(R // 2, device=dev) % len(axes)).to(torch.int32) if len(axes) > 1 else None
+        if case["op"] == "rotary_backward":
+            s["d_q"], s["d_k"] = normal(T, H, d, std=0.01, dtype=dtype), normal(T, HK, d, std=0.01, dtype=dtype)
+        return s
+    B, HV, dk, dv, cache = case["batch"], case["heads_v"], case["dk"], case["dv"], case["cache"]
+    slots = 2 * B
+    # rows of different sizes, as value channels have them
+    states = normal(B, HV, dv, dk, std=0.05) * torch.exp(normal(B, HV, dv, 1))
+    slot_ids = torch.randperm(slots, generator=gen, device=dev)[:B]
+    s["data"] = torch.zeros(slots, HV, dv, dk, dtype=DTYPES[cache], device=dev)
+    s["scale"] = torch.full((slots, HV, dv), 27, dtype=torch.uint8, device=dev).view(torch.float8_e8m0fnu) if cache == "e4m3" else None
+    s.update(slot_ids=slot_ids.to(torch.int32), states=states if case["op"] == "pack" else None)
+    if case["op"] == "pack":
+        return s
+    _plain_write(s, slot_ids, states)
+    if case["op"] == "unpack":
+        return s
+    L, H, dtype, rule = case["length"], case["heads"], DTYPES[case["dtype"]], case["rule"]
+    decays, rate = rule != "delta", rule in ("gated_delta", "delta")
+    k = normal(B, L, H, dk)
+    s.update(q=normal(B, L, H, dk, dtype=dtype), k=(k / k.norm(dim=-1, keepdim=True)).to(dtype), v=normal(B, L, HV, dv, dtype=dtype),
+             gate=None, a_log=None, dt_bias=None, beta=None, erase=None)
+    if decays:  # the projection's raw gate
+        key = (dk,) if case["per_key"] else ()
+        s.update(gate=normal(B, L, HV, *key, dtype=dtype), a_log=uniform(-4.0, 1.0, HV), dt_bias=uniform(0, 1, HV, *key))
+    if rate:
+        s["beta"] = normal(B, L, HV)
+    if rule == "gated_delta_v2":
+        s["erase"] = torch.sigmoid(normal(B, L, HV, dk))
+    return s
+
+
+# ------------------------------------------------------------------ plain forms
+
+def _angles(s):
+    """cos and sin of every token's pairs, (T, 1, R/2), from products in 64 bits."""
+    pos = s["positions"].double()
+    at = pos[:, None] if s["axes"] is None else pos[s["axes"].long()].T
+    a = at * s["freqs"].double()
+    return torch.cos(a).float()[:, None], torch.sin(a).float()[:, None]
+
+
+def _turn(x, cos, sin, pairs):
+    R = 2 * cos.shape[-1]
+    if pairs == "halves":
+        a, b = x[..., : R // 2], x[..., R // 2: R]
+        return torch.cat([a * cos - b * sin, b * cos + a * sin, x[..., R:]], -1)
+    a, b = x[..., 0:R:2], x[..., 1:R:2]
+    both = torch.stack([a * cos - b * sin, b * cos + a * sin], -1).flatten(-2)
+    return torch.cat([both, x[..., R:]], -1)
+
+
+def _plain_rotary(s):
+    cos, sin = _angles(s)
+    out = {}
+    for name in ("q", "k"):
+        x = s[name].float()
+        h = x * torch.rsqrt(x.square().mean(-1, keepdim=True) + EPS)
+        if s[name + "_weight"] is not None:
+            h = h * s[name + "_weight"].float()
+        out[name] = _turn(h, cos, sin, s["case"]["pairs"]).to(s[name].dtype)
+    return out
+
+
+def _plain_rotary_backward(s):
+    cos, sin = _angles(s)
+    out = {}
+    for name in ("q", "k"):
+        x, w = s[name].float(), s[name + "_weight"]
+        inv = torch.rsqrt(x.square().mean(-1, keepdim=True) + EPS)
+        g, n = _turn(s["d_" + name].float(), cos, -sin, s["case"]["pairs"]), x * inv
+        t = g
+        if w is not None:
+            t, out["d_%s_weight" % name] = g * w.float(), (g * n).sum((0, 1))
+        out["d_" + name] = (inv * (t - n * (t * n).mean(-1, keepdim=True))).to(s[name].dtype)
+    return out
+
+
+def _plain_write(s, at, states):
+    """The states rounded to the cache's type; with 8 bits by each row's least power of two under which they fit."""
+    if s["scale"] is None:
+        s["data"][at] = states.to(s["data"].dtype)
+        return
+    m, e = torch.frexp(states.abs().amax(-1))  # 448 is 0.875 * 2^9
+    scale = torch.ldexp(torch.ones_like(m), (e - torch.where(m > 0.875, 8, 9)).clamp(min=-100))
+    s["data"][at] = (states / scale[..., None]).to(s["data"].dtype)
+    s["scale"][at] = scale.to(s["scale"].dtype)
+
+
+def _plain_read(s, at):
+    x = s["data"][at].float()
+    return x if s["scale"] is None else x * s["scale"][at].float()[..., None]
+
+
+def _cache(s):
+    return {"data": s["data"]} if s["scale"] is None else {"data": s["data"], "scale": s["scale"]}
+
+
+def _plain_pack(s):
+    _plain_write(s, s["slot_ids"].long(), s["states"])
+    return _cache(s)
+
+
+def _plain_unpack(s):
+    return {"states": _plain_read(s, s["slot_ids"].long())}
+
+
+def _plain_decode(s):
+    case, at = s["case"], s["slot_ids"].long()
+    rule, R, dk = case["rule"], case["heads_v"] // case["heads"], case["dk"]
+    S, outs = _plain_read(s, at), []
+    for t in range(case["length"]):
+        q, k = (s[n][:, t].float().repeat_interleave(R, 1)[..., None, :] for n in ("q", "k"))
+        v = s["v"][:, t].float()
+        if s["gate"] is not None:
+            x = s["gate"][:, t].float() + s["dt_bias"]
+            soft = x.clamp(min=0) + torch.log1p(torch.exp(-x.abs()))
+            if case["per_key"]:
+                S = S * torch.exp(-torch.exp(s["a_log"])[:, None] * soft)[..., None, :]
+            else:
+                S = S * torch.exp(-torch.exp(s["a_log"]) * soft)[..., None, None]
+        if s["beta"] is not None:
+            v = torch.sigmoid(s["beta"][:, t])[..., None] * (v - (S * k).sum(-1))
+        elif rule == "gated_delta_v2":
+            v = v - (S * (k * s["erase"][:, t][..., None, :])).sum(-1)
+        S = S + v[..., None] * k
+        outs.append((S * q).sum(-1) / math.sqrt(dk))
+    _plain_write(s, at, S)
+    return dict(_cache(s), o=torch.stack(outs, 1).to(s["q"].dtype))
+
+
+# ------------------------------------------------------------------ the framework's calls
+
+def _own_rotary(s):
+    from gated_delta_rule_token_amd import api
+    r = api.qk_rotary(s["q"], s["k"], s["positions"], s["freqs"], axes=s["axes"], q_weight=s["q_weight"],
+                      k_weight=s["k_weight"], eps=EPS, interleaved=s["case"]["pairs"] == "neighbours")
+    return {"q": r.q, "k": r.k}
+
+
+def _own_rotary_backward(s):
+    from gated_delta_rule_token_amd import api
+    g = api.qk_rotary_backward(s["d_q"], s["d_k"], s["q"], s["k"], s["positions"], s["freqs"], axes=s["axes"],
+                               q_weight=s["q_weight"], k_weight=s["k_weight"], eps=EPS,
+                               interleaved=s["case"]["pairs"] == "neighbours")
+    out = {"d_q": g.q, "d_k": g.k, "d_q_weight": g.q_weight, "d_k_weight": g.k_weight}
+    return {name: t for name, t in out.items() if t is not None}
+
+
+def _own_pack(s):
+    from gated_delta_rule_token_amd import api
+    api.state_pack(s["states"], api.PackedSlab(s["data"], s["scale"]), s["slot_ids"])
+    return _cache(s)
+
+
+def _own_unpack(s):
+    from gated_delta_rule_token_amd import api
+    return {"states": api.state_unpack(api.PackedSlab(s["data"], s["scale"]), s["slot_ids"])}
+
+
+def _own_decode(s):
+    from gated_delta_rule_token_amd import api
+    o = api.forward_packed(s["q"], s["k"], s["v"], slab=api.PackedSlab(s["data"], s["scale"]), slot_ids=s["slot_ids"],
+                           gate=s["gate"], a_log=s["a_log"], dt_bias=s["dt_bias"], beta=s["beta"], erase=s["erase"],
+                           update_rule=s["case"]["rule"], gate_activation="none" if s["gate"] is None else "qwen",
+                           beta_activation="none" if s["beta"] is None else "sigmoid")
+    return dict(_cache(s), o=o)
+
+
+def run(state):
+    op = state["case"]["op"]
+    if own:
+        return {"rotary": _own_rotary, "rotary_backward": _own_rotary_backward, "pack": _own_pack, "unpack": _own_unpack,
+                "decode": _own_decode}[op](state)
+    return {"rotary": _plain_rotary, "rotary_backward": _plain_rotary_backward, "pack": _plain_pack,
+            "unpack": _plain_unpack, "decode": _plain_decode}[op](state)
+
+
+# ------------------------------------------------------------------ work
+
+def work(case):
+    if case["op"].startswith("rotary"):
+        n = case["tokens"] * (case["heads"] + case["heads_k"]) * case["dim"]
+        back = case["op"] == "rotary_backward"
+        weights = 0 if case["weight"] == "none" else 2 * case["dim"] * (SIZE[case["weight"]] + (4 if back else 0))
+        small = 4 * case["tokens"] * case["axes"] + 2 * case["rotary"] + weights
+        return {"bytes": n * SIZE[case["dtype"]] * (3 if back else 2) + small, "flops": n * (14 if back else 8)}
+    B, HV, dk, dv = case["batch"], case["heads_v"], case["dk"], case["dv"]
+    rows = B * HV * dv
+    cache = rows * (dk * SIZE[case["cache"]] + (1 if case["cache"] == "e4m3" else 0))
+    if case["op"] != "decode":
+        return {"bytes": cache + rows * dk * 4 + 4 * B, "flops": 2 * rows * dk}
+    T, H, a = B * case["length"], case["heads"], SIZE[case["dtype"]]
+    size = 2 * cache + 2 * T * H * dk * a + 2 * T * HV * dv * a + 4 * B
+    key = dk if case["per_key"] else 1
+    size += T * HV * key * a if case["rule"] != "delta" else 0
+    size += T * HV * 4 if case["rule"] in ("gated_delta", "delta") else 0
+    size += T * HV * dk * 4 if case["rule"] == "gated_delta_v2" else 0
+    return {"bytes": size, "flops": 7 * T * HV * dk * dv}
+
+
+# ------------------------------------------------------------------ 64 bits
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    if case["op"].startswith("rotary"):
+        return _exact_rotary(s)
+    at = s["slot_ids"].long()
+
+    def written(states):  # in units of the rows' scales, not rounded
+        data = s["data"].double()
+        if s["scale"] is None:
+            data[at] = states
+            return {"data": data}
+        scale = s["scale"].double()
+        fit = torch.exp2(torch.ceil(torch.log2(states.abs().max(-1).values / E4M3_MAX)).clamp(min=-100))
+        data[at], scale[at] = states / fit[..., None], fit
+        return {"data": data, "scale": scale}
+
+    if case["op"] == "pack":
+        return written(s["states"].double())
+    S = s["data"][at].double()
+    if s["scale"] is not None:
+        S = S * s["scale"][at].double()[..., None]
+    return {"states": S} if case["op"] == "unpack" else _exact_decode(s, S, written)
+
+
+def _exact_rotary(s):
+    case = s["case"]
+    T, d, R = case["tokens"], case["dim"], case["rotary"]
+    pos = s["positions"].double().reshape(-1, T)
+    which = torch.zeros(R // 2, dtype=torch.long, device=pos.device) if s["axes"] is None else s["axes"].long()
+    turn = torch.polar(torch.ones_like(pos[which].T), pos[which].T * s["freqs"].double())[:, None]
+
+    def rotate(x, by):
+        y = x.clone()
+        first = slice(0, R // 2) if case["pairs"] == "halves" else slice(0, R, 2)
+        second = slice(R // 2, R) if case["pairs"] == "halves" else slice(1, R, 2)
+        z = torch.complex(x[..., first].contiguous(), x[..., second].contiguous()) * by
+        y[..., first], y[..., second] = z.real, z.imag
+        return y
+
+    out = {}
+    for name in ("q", "k"):
+        x = s[name].double()
+        root = torch.sqrt((x * x).sum(-1, keepdim=True) / d + EPS)
+        w = torch.ones(d, dtype=torch.float64, device=x.device)
+        w = w if s[name + "_weight"] is None else s[name + "_weight"].double()
+        if case["op"] == "rotary":
+            out[name] = rotate(x / root * w, turn)
+            continue
+        g = rotate(s["d_" + name].double(), turn.conj())
+        out["d_" + name] = g * w / root - x * (g * w * x).sum(-1, keepdim=True) / (d * root ** 3)
+        if s[name + "_weight"] is not None:
+            out["d_%s_weight" % name] = (g * x / root).sum(0).sum(0)
+    return out
+
+
+def _exact_decode(s, S, written):
+    case = s["case"]
+    B, L, H, HV, dk = case["batch"], case["length"], case["heads"], case["heads_v"], case["dk"]
+    head = torch.arange(HV, device=S.device) * H // HV
+    q, k, v = s["q"].double()[:, :, head], s["k"].double()[:, :, head], s["v"].double()
+    keep = S.new_ones(B, L, HV, 1)
+    if s["gate"] is not None:
+        x = s["gate"].double() + s["dt_bias"].double()
+        rate = torch.exp(s["a_log"].double())
+        g = -torch.logaddexp(x, torch.zeros_like(x)) * (rate[:, None] if case["per_key"] else rate)
+        keep = torch.exp(g).reshape(B, L, HV, -1)
+    take = torch.zeros_like(k)
+    if s["erase"] is not None:
+        take, write = s["erase"].double() * k, S.new_ones(B, L, HV, 1)
+    else:
+        write = S.new_ones(B, L, HV, 1) if s["beta"] is None else 1 / (1 + torch.exp(-s["beta"].double()))[..., None]
+        take = take if s["beta"] is None else k
+    o = torch.empty_like(v)
+    for t in range(L):
+        S = S * keep[:, t, :, None]
+        new = write[:, t] * (v[:, t] - torch.matmul(S, take[:, t, :, :, None])[..., 0])
+        S = S + new[..., :, None] * k[:, t, :, None, :]
+        o[:, t] = torch.matmul(S, q[:, t, :, :, None])[..., 0] * dk ** -0.5
+    return dict(written(S), o=o)
