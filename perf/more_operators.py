@@ -77,7 +77,8 @@ def draw(rng):
     dv = dk if rng.random() < 0.7 else rng.choice([64, 128, 256, _spread(rng, 8, 256)])
     heads = _spread(rng, 1, 16)
     heads_v = heads * rng.choice([1, 2, 4])
-    batch = _spread(rng, 1, min(512, max(1, 256 * 32 * 128 * 128 // (heads_v * dk * dv))))
+    most = 256 * 32 * 128 * 128 * (4 if op == "decode" else 3) // 4
+    batch = _spread(rng, 1, min(512, max(1, most // (heads_v * dk * dv))))
     cache = rng.choice(["e4m3", "e4m3", "f16", "bf16"])
     if op != "decode":
         return dict(op=op, batch=batch, heads_v=heads_v, dk=dk, dv=dv, cache=cache)
