@@ -9,16 +9,24 @@ never a fallback.
 """
 from .api import (  # noqa: F401
     GDRError,
+    PackedSlab,
     backward,
     forward,
+    forward_packed,
     gate,
     gate_backward,
     library_path,
     load_library,
+    packed_slab,
+    qk_rotary,
+    qk_rotary_backward,
     rms_norm,
     rms_norm_backward,
+    state_pack,
+    state_unpack,
     workspace_size,
 )
 
-__all__ = ["GDRError", "backward", "forward", "gate", "gate_backward", "library_path", "load_library", "rms_norm",
-           "rms_norm_backward", "workspace_size"]
+__all__ = ["GDRError", "PackedSlab", "backward", "forward", "forward_packed", "gate", "gate_backward", "library_path",
+           "load_library", "packed_slab", "qk_rotary", "qk_rotary_backward", "rms_norm", "rms_norm_backward",
+           "state_pack", "state_unpack", "workspace_size"]

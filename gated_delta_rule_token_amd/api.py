@@ -77,11 +77,27 @@ class GradientPointers(ctypes.Structure):
         "d_dt_bias", "d_gate_scale")] + [("zero_rest", ctypes.c_int32)]
 
 
+class RotaryArguments(ctypes.Structure):
+    """gdr_rotary"""
+    _fields_ = ([("tokens", ctypes.c_int64)]
+                + [(name, ctypes.c_int32) for name in ("heads_q", "heads_k", "head_dim", "rotary_dim", "axes",
+                                                       "interleaved", "norm", "dtype", "weight_dtype")]
+                + [("eps", ctypes.c_float), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64)]
+                + [(name, ctypes.c_void_p) for name in ("q", "k", "q_weight", "k_weight", "positions", "inv_freq",
+                                                        "axis_of")])
+
+
+class SlabPointers(ctypes.Structure):
+    """gdr_packed_slab"""
+    _fields_ = [("data", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("dtype", ctypes.c_int32)]
+
+
 EXPORTS = ("gdr_abi_version", "gdr_status_str", "gdr_last_error", "gdr_validate",
            "gdr_workspace_size", "gdr_select_algo", "gdr_forward", "gdr_forward_noalloc",
            "gdr_backward_workspace_size", "gdr_backward", "gdr_gate", "gdr_gate_backward_workspace_size",
            "gdr_gate_backward", "gdr_rms_norm", "gdr_rms_norm_backward_workspace_size", "gdr_rms_norm_backward",
-           "gdr_slab_stream")
+           "gdr_qk_rotary", "gdr_qk_rotary_backward_workspace_size", "gdr_qk_rotary_backward", "gdr_state_pack",
+           "gdr_state_unpack", "gdr_packed_workspace_size", "gdr_forward_packed", "gdr_slab_stream")
 NOALLOC_SCRATCH_BYTES = 256 << 20  # GDR_NOALLOC_SCRATCH_BYTES of include/gdr.h
 
 
@@ -141,6 +157,22 @@ def load_library():
         lib.gdr_rms_norm_backward.argtypes = ([ctypes.c_int64] + [ctypes.c_int32] * 3 + [ctypes.c_void_p] * 8
                                               + [ctypes.c_size_t, ctypes.c_void_p])
         lib.gdr_rms_norm_backward.restype = ctypes.c_int
+        ptr, i32, i64, size = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+        rotary, slab = ctypes.POINTER(RotaryArguments), ctypes.POINTER(SlabPointers)
+        lib.gdr_qk_rotary.argtypes = [rotary, ptr, i64, ptr, i64, ptr]
+        lib.gdr_qk_rotary.restype = ctypes.c_int
+        lib.gdr_qk_rotary_backward_workspace_size.argtypes = [rotary, ctypes.POINTER(size)]
+        lib.gdr_qk_rotary_backward_workspace_size.restype = ctypes.c_int
+        lib.gdr_qk_rotary_backward.argtypes = [rotary, ptr, ptr, ptr, i64, ptr, i64, ptr, ptr, ptr, size, ptr]
+        lib.gdr_qk_rotary_backward.restype = ctypes.c_int
+        lib.gdr_state_pack.argtypes = [i32] * 5 + [ptr, ptr, slab, ptr]
+        lib.gdr_state_pack.restype = ctypes.c_int
+        lib.gdr_state_unpack.argtypes = [i32] * 5 + [slab, ptr, ptr, ptr]
+        lib.gdr_state_unpack.restype = ctypes.c_int
+        lib.gdr_packed_workspace_size.argtypes = [ctypes.POINTER(Problem), ctypes.POINTER(size)]
+        lib.gdr_packed_workspace_size.restype = ctypes.c_int
+        lib.gdr_forward_packed.argtypes = [ctypes.POINTER(Problem), ctypes.POINTER(Tensors), slab, ptr, size, ptr]
+        lib.gdr_forward_packed.restype = ctypes.c_int
         lib.gdr_slab_stream.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
                                         ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_void_p]
         lib.gdr_slab_stream.restype = ctypes.c_int
@@ -659,6 +691,285 @@ def rms_norm_backward(d_y, x, weight, inv_rms, *, d_residual=None, workspace=Non
              _ptr(d_y), _ptr(x), _ptr(weight), _ptr(inv_rms), _ptr(d_residual), _ptr(d_x), _ptr(d_weight),
              _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
     return NormGradients(d_x, d_weight)
+
+
+class RotaryOutput(NamedTuple):
+    """Results of ``qk_rotary``; ``k`` is None without one."""
+    q: torch.Tensor
+    k: Optional[torch.Tensor]
+
+
+class RotaryGradients(NamedTuple):
+    """Results of ``qk_rotary_backward``; None where the call has no such input."""
+    q: torch.Tensor
+    k: Optional[torch.Tensor]
+    q_weight: Optional[torch.Tensor]
+    k_weight: Optional[torch.Tensor]
+
+
+def _token_stride(t, name, dtype, dev, lead, dim):
+    """Elements from token to token of a tensor (..., heads, dim) whose heads
+    lie one after the other (a view of a wider projection's output may)."""
+    if not isinstance(t, torch.Tensor):
+        raise GDRError("GDR_E_INVALID", "%s must be a torch.Tensor" % name)
+    if t.device != dev or not t.is_cuda:
+        raise GDRError("GDR_E_INVALID", "%s is on %s, expected %s (a GPU)" % (name, t.device, dev))
+    if t.dtype != dtype:
+        raise GDRError("GDR_E_INVALID", "%s must be %s, got %s" % (name, dtype, t.dtype))
+    shape = t.shape
+    if tuple(shape[:-2]) != lead or shape[-1] != dim:
+        raise GDRError("GDR_E_INVALID", "%s has shape %s, expected %s + (heads, %d)" % (name, tuple(shape), lead, dim))
+    st, heads = t.stride(), shape[-2]
+    token = st[-3] if shape[-3] > 1 else heads * dim
+    if len(lead) == 2 and shape[-3] == 1:
+        token = st[0] if shape[0] > 1 else token
+    ok = st[-1] == 1 and (heads <= 1 or st[-2] == dim)
+    if len(lead) == 2 and shape[0] > 1 and shape[-3] > 1:
+        ok = ok and st[0] == shape[-3] * token
+    if t.numel() and not ok:
+        raise GDRError("GDR_E_INVALID", "%s has strides %s: a token's heads must lie one after the other, and tokens be "
+                       "evenly apart" % (name, tuple(st)))
+    return max(token, heads * dim) if t.numel() == 0 else token
+
+
+def _rotary_arguments(q, k, positions, inv_freq, axes, q_weight, k_weight, eps, interleaved, norm):
+    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
+        raise GDRError("GDR_E_INVALID", "q must be a tensor (T, H, d) or (B, L, H, d)")
+    dev, lead, dim = q.device, tuple(q.shape[:-2]), q.shape[-1]
+    code = _dtype_code(q.dtype)
+    q_stride = _token_stride(q, "q", q.dtype, dev, lead, dim)
+    k_stride = 0 if k is None else _token_stride(k, "k", q.dtype, dev, lead, dim)
+    _need(positions, "positions", torch.int32, dev)
+    _need(inv_freq, "inv_freq", torch.float32, dev)
+    _need(axes, "axes", torch.int32, dev)
+    if positions is None or inv_freq is None:
+        raise GDRError("GDR_E_INVALID", "positions and inv_freq are required")
+    shape = tuple(positions.shape)
+    if shape != lead and shape[1:] != lead:
+        raise GDRError("GDR_E_INVALID", "positions has shape %s, expected %s or (axes,) + %s" % (shape, lead, lead))
+    n_axes = 1 if shape == lead else shape[0]
+    if inv_freq.dim() != 1:
+        raise GDRError("GDR_E_INVALID", "inv_freq must have one axis")
+    half = inv_freq.shape[0]
+    if axes is not None and tuple(axes.shape) != (half,):
+        raise GDRError("GDR_E_INVALID", "axes has shape %s, expected %s" % (tuple(axes.shape), (half,)))
+    if axes is None and n_axes > 1:
+        raise GDRError("GDR_E_INVALID", "positions of several axes need axes (an axis for each pair)")
+    weight_code = code
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is None:
+            continue
+        if tuple(_need(w, name, None, dev).shape) != (dim,):
+            raise GDRError("GDR_E_INVALID", "%s has shape %s, expected %s" % (name, tuple(w.shape), (dim,)))
+        weight_code = _dtype_code(w.dtype)
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise GDRError("GDR_E_INVALID", "q_weight and k_weight must have one dtype")
+    if k_weight is not None and k is None:
+        raise GDRError("GDR_E_INVALID", "k_weight given without k")
+    tokens = 1
+    for n in lead:
+        tokens *= n
+    return RotaryArguments(
+        tokens, _int32(q.shape[-2], "q's heads"), 0 if k is None else _int32(k.shape[-2], "k's heads"),
+        _int32(dim, "the last axis of q"), 2 * _int32(half, "inv_freq's length") if half < 2 ** 30 else -1,
+        _int32(n_axes, "the axes"), int(bool(interleaved)), int(bool(norm)), code, weight_code, float(eps), q_stride,
+        k_stride, _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq), _ptr(axes))
+
+
+def _rotary_out(out, q, k, what):
+    """The (q, k) tensors that a call writes, and their token strides."""
+    if out is None:
+        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device),
+               None if k is None else torch.empty(k.shape, dtype=q.dtype, device=q.device))
+    oq, ok = out[0], out[1]
+    if (ok is None) != (k is None):
+        raise GDRError("GDR_E_INVALID", "%s needs a tensor for k exactly when the call has one" % what)
+    strides = []
+    for t, like, name in ((oq, q, "q"), (ok, k, "k")):
+        if like is None:
+            strides.append(0)
+            continue
+        strides.append(_token_stride(t, "%s of %s" % (what, name), q.dtype, q.device, tuple(q.shape[:-2]), q.shape[-1]))
+        if t.shape != like.shape:
+            raise GDRError("GDR_E_INVALID", "%s of %s must have its shape" % (what, name))
+    return oq, ok, strides
+
+
+def qk_rotary(q, k, positions, inv_freq, *, axes=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+              norm=True, out=None) -> RotaryOutput:
+    """Root-mean-square norm of every head of ``q`` (T,H,d) or (B,L,H,d) and
+    ``k`` (the same with its own number of heads, or None), and the rotation of
+    its first 2 * len(inv_freq) columns by the tokens' positions, in one pass.
+
+    ``positions``: int32 (T,) or (B,L), or with several axes (A,T) / (A,B,L)
+    and ``axes`` (len(inv_freq),) int32: the axis of each pair.  ``inv_freq``:
+    fp32, the angle of a pair for each position.  Pairs are columns (i, i +
+    len(inv_freq)), or neighbours (2i, 2i + 1) with ``interleaved``.
+    ``q_weight`` and ``k_weight`` (d,), of one dtype: q's or fp32.
+    ``norm=False`` leaves the norm out.
+
+    q and k may be views of one projection's output (a token's heads one after
+    the other, tokens evenly apart).  ``out``: (q, k) tensors to fill, which may
+    be q and k themselves; allocated without gaps when not given, as ``forward``
+    takes them."""
+    lib = load_library()
+    r = _rotary_arguments(q, k, positions, inv_freq, axes, q_weight, k_weight, eps, interleaved, norm)
+    oq, ok, strides = _rotary_out(out, q, k, "out")
+    _enqueue(lib.gdr_qk_rotary, q.device, ctypes.byref(r), _ptr(oq), strides[0], _ptr(ok), strides[1])
+    return RotaryOutput(oq, ok)
+
+
+def qk_rotary_backward(d_q_out, d_k_out, q, k, positions, inv_freq, *, axes=None, q_weight=None, k_weight=None,
+                       eps=1e-6, interleaved=False, norm=True, out=None, workspace=None) -> RotaryGradients:
+    """Gradients of ``qk_rotary``: ``d_q_out`` and ``d_k_out`` are those of its
+    results (contiguous, of q's dtype), the rest are its arguments; nothing of
+    that call has to be kept.  The weights' gradients are sums over every token
+    and head, in fp32.  ``out``: (q, k) tensors for the gradients of q and k,
+    which may be views of one projection's gradient; allocated without gaps
+    when not given."""
+    lib = load_library()
+    r = _rotary_arguments(q, k, positions, inv_freq, axes, q_weight, k_weight, eps, interleaved, norm)
+    dev = q.device
+    for name, d, like in (("d_q_out", d_q_out, q), ("d_k_out", d_k_out, k)):
+        if (d is None) != (like is None):
+            raise GDRError("GDR_E_INVALID", "d_q_out is required, and d_k_out exactly with k")
+        if d is not None and _need(d, name, q.dtype, dev).shape != like.shape:
+            raise GDRError("GDR_E_INVALID", "%s has shape %s, expected %s" % (name, tuple(d.shape), tuple(like.shape)))
+    dq, dk, strides = _rotary_out(out, q, k, "out")
+    dqw = None if q_weight is None else torch.empty(q.shape[-1], dtype=torch.float32, device=dev)
+    dkw = None if k_weight is None else torch.empty(q.shape[-1], dtype=torch.float32, device=dev)
+    n = ctypes.c_size_t(0)
+    check(lib.gdr_qk_rotary_backward_workspace_size(ctypes.byref(r), ctypes.byref(n)))
+    if workspace is None and n.value:
+        workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", device=dev)
+    _enqueue(lib.gdr_qk_rotary_backward, dev, ctypes.byref(r), _ptr(d_q_out), _ptr(d_k_out), _ptr(dq), strides[0],
+             _ptr(dk), strides[1], _ptr(dqw), _ptr(dkw), _ptr(workspace),
+             0 if workspace is None else workspace.numel() * workspace.element_size())
+    return RotaryGradients(dq, dk, dqw, dkw)
+
+
+class PackedSlab(NamedTuple):
+    """A slab of states in fewer bits: ``data`` (num_slots, HV, dv, dk) in
+    float16, bfloat16 or float8_e4m3fn, and with the last ``scale``
+    (num_slots, HV, dv) in float8_e8m0fnu, a power of two for each row."""
+    data: torch.Tensor
+    scale: Optional[torch.Tensor] = None
+
+
+_CACHE_DTYPES = {torch.float16: F16, torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3}
+
+
+def packed_slab(num_slots, heads, dv, dk, dtype=torch.bfloat16, device="cuda") -> PackedSlab:
+    """A packed slab of zero states."""
+    if dtype not in _CACHE_DTYPES:
+        raise GDRError("GDR_E_INVALID", "a packed slab is float16, bfloat16 or float8_e4m3fn, got %s" % dtype)
+    data = torch.zeros(num_slots, heads, dv, dk, dtype=dtype, device=device)
+    if dtype != torch.float8_e4m3fn:
+        return PackedSlab(data)
+    scale = torch.full((num_slots, heads, dv), 27, dtype=torch.uint8, device=device)  # 2^-100, as for rows of zeros
+    return PackedSlab(data, scale.view(torch.float8_e8m0fnu))
+
+
+def _slab_pointers(slab, dev):
+    data, scale = slab
+    _need(data, "slab.data", device=dev)
+    code = _CACHE_DTYPES.get(data.dtype)
+    if code is None or data.dim() != 4:
+        raise GDRError("GDR_E_INVALID", "slab.data must be (num_slots, HV, dv, dk) in float16, bfloat16 or "
+                       "float8_e4m3fn, got %s %s" % (tuple(data.shape), data.dtype))
+    if (scale is not None) != (code == E4M3):
+        raise GDRError("GDR_E_INVALID", "a slab has scales exactly with float8_e4m3fn")
+    if scale is not None and _need(scale, "slab.scale", torch.float8_e8m0fnu, dev).shape != data.shape[:3]:
+        raise GDRError("GDR_E_INVALID", "slab.scale has shape %s, expected %s" % (tuple(scale.shape), tuple(data.shape[:3])))
+    return SlabPointers(data.data_ptr(), _ptr(scale), code)
+
+
+def _slots(slot_ids, dev):
+    _need(slot_ids, "slot_ids", torch.int32, dev)
+    if slot_ids is None or slot_ids.dim() != 1:
+        raise GDRError("GDR_E_INVALID", "slot_ids must be (B,) int32")
+    return _int32(slot_ids.shape[0], "the batch")
+
+
+def state_pack(states, slab, slot_ids) -> None:
+    """Write ``states`` (B,HV,dv,dk) fp32 into the rows ``slot_ids`` (B,) int32
+    of a ``PackedSlab``, rounded to nearest even (in 8 bits: in units of a power
+    of two for each row).  Out-of-range ids are skipped."""
+    lib = load_library()
+    dev = slab.data.device
+    p = _slab_pointers(slab, dev)
+    B, (slots, HV, dv, dk) = _slots(slot_ids, dev), slab.data.shape
+    if states is None or tuple(_need(states, "states", torch.float32, dev).shape) != (B, HV, dv, dk):
+        raise GDRError("GDR_E_INVALID", "states must be %s" % ((B, HV, dv, dk),))
+    _enqueue(lib.gdr_state_pack, dev, B, _int32(HV, "HV"), dv, dk, _int32(slots, "num_slots"), _ptr(states),
+             _ptr(slot_ids), ctypes.byref(p))
+
+
+def state_unpack(slab, slot_ids, out=None):
+    """The states (B,HV,dv,dk) fp32 that the rows ``slot_ids`` of a
+    ``PackedSlab`` hold, in ``out`` when given; zeros for out-of-range ids."""
+    lib = load_library()
+    dev = slab.data.device
+    p = _slab_pointers(slab, dev)
+    B, (slots, HV, dv, dk) = _slots(slot_ids, dev), slab.data.shape
+    if out is None:
+        out = torch.empty((B, HV, dv, dk), dtype=torch.float32, device=dev)
+    elif tuple(_need(out, "out", torch.float32, dev).shape) != (B, HV, dv, dk):
+        raise GDRError("GDR_E_INVALID", "out must be %s" % ((B, HV, dv, dk),))
+    _enqueue(lib.gdr_state_unpack, dev, B, _int32(HV, "HV"), dv, dk, _int32(slots, "num_slots"), ctypes.byref(p),
+             _ptr(slot_ids), _ptr(out))
+    return out
+
+
+def packed_workspace_size(problem: Problem) -> int:
+    n = ctypes.c_size_t(0)
+    check(load_library().gdr_packed_workspace_size(ctypes.byref(problem), ctypes.byref(n)))
+    return int(n.value)
+
+
+def forward_packed(q, k, v, *, slab, slot_ids, gate=None, beta=None, erase=None, a_log=None, dt_bias=None,
+                   gate_scale=None, cu_seqlens=None, seq_lens=None, update_rule="gated_delta", gate_activation="none",
+                   beta_activation="none", qk_l2_norm=False, scale=0.0, chunk_size=64, algo="auto", scan_segments=0,
+                   out=None, workspace=None):
+    """``forward`` on a ``PackedSlab``, whose rows ``slot_ids`` (B,) are read
+    and updated in place: in fp32 over all tokens of a request, rounded once on
+    the way back.  A request without tokens leaves its row as it is.  The other
+    arguments are ``forward``'s.  ``workspace``: a uint8 device tensor of
+    ``packed_workspace_size`` bytes, which calls of more than 8 tokens a request
+    need (allocated here when not given).  Returns o."""
+    lib = load_library()
+    dev = q.device
+    s = _slab_pointers(slab, dev)
+    _need(q, "q", device=dev)
+    act, f32, i32 = q.dtype, torch.float32, torch.int32
+    for name, t, dt in (("k", k, act), ("v", v, act), ("gate", gate, None), ("beta", beta, f32), ("erase", erase, f32),
+                        ("a_log", a_log, f32), ("dt_bias", dt_bias, f32), ("gate_scale", gate_scale, f32),
+                        ("cu_seqlens", cu_seqlens, i32), ("seq_lens", seq_lens, i32), ("slot_ids", slot_ids, i32),
+                        ("out", out, act)):
+        _need(t, name, dt, dev)
+    if k is None or v is None or slot_ids is None or q.dim() not in (3, 4) or v.dim() != q.dim():
+        raise GDRError("GDR_E_INVALID", "q, k, v of three or four axes and slot_ids are required")
+    p = build_problem(q, k, v, gate=gate, beta=beta, erase=erase, a_log=a_log, dt_bias=dt_bias, cu_seqlens=cu_seqlens,
+                      slot_ids=slot_ids, state=slab.data, update_rule=update_rule, gate_activation=gate_activation,
+                      beta_activation=beta_activation, qk_l2_norm=qk_l2_norm, scale=scale, chunk_size=chunk_size,
+                      algo=algo, gate_scale=gate_scale, seq_lens=seq_lens, scan_segments=scan_segments)
+    lead = tuple(q.shape[:-2])
+    if out is None:
+        out = torch.empty(lead + tuple(v.shape[-2:]), dtype=act, device=dev)
+    check_shapes(p, lead, _shapes(q=q, k=k, v=v, out=out, gate=gate, beta=beta, erase=erase, a_log=a_log,
+                                  gate_scale=gate_scale, dt_bias=dt_bias, cu_seqlens=cu_seqlens, seq_lens=seq_lens,
+                                  slot_ids=slot_ids, state=slab.data))
+    need = packed_workspace_size(p)
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", device=dev)
+    t = Tensors(q=_ptr(q), k=_ptr(k), v=_ptr(v), o=_ptr(out), gate=_ptr(gate), beta=_ptr(beta), erase=_ptr(erase),
+                a_log=_ptr(a_log), dt_bias=_ptr(dt_bias), cu_seqlens=_ptr(cu_seqlens), slot_ids=_ptr(slot_ids),
+                gate_scale=_ptr(gate_scale), seq_lens=_ptr(seq_lens))
+    _enqueue(lib.gdr_forward_packed, dev, ctypes.byref(p), ctypes.byref(t), ctypes.byref(s), _ptr(workspace),
+             0 if workspace is None else workspace.numel() * workspace.element_size())
+    return out
 
 
 def slab_stream(slab, slot_ids, factor=1.0):

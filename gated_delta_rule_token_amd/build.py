@@ -23,7 +23,8 @@ ARCH = os.environ.get("GDR_OFFLOAD_ARCH", "gfx950")
 
 SOURCES = ["gdr_api.cpp", "gdr_decode.hip", "gdr_recurrent.hip", "gdr_chunked.hip", "gdr_chunked_bf16.hip",
            "gdr_gate.hip", "gdr_stream.hip", "gdr_backward.hip", "gdr_backward_f32.hip", "gdr_backward_f16.hip",
-           "gdr_backward_bf16.hip", "gdr_norm.hip"]
+           "gdr_backward_bf16.hip", "gdr_norm.hip", "gdr_rotary.hip", "gdr_packed.hip", "gdr_packed_f16.hip",
+           "gdr_packed_bf16.hip", "gdr_packed_e4m3.hip"]
 
 # Packed fp32 VALU forms are switched off for the device code; every kernel
 # is ordinary fp32 arithmetic.

@@ -15,6 +15,8 @@
 #include "gdr_backward_launch.hpp"
 #include "gdr_launch.hpp"
 #include "gdr_norm_launch.hpp"
+#include "gdr_packed_launch.hpp"
+#include "gdr_rotary_launch.hpp"
 
 // Workspace of gdr_forward_noalloc, one copy per GPU (see include/gdr.h).  In
 // host code `scratch` is only a handle: its device address comes from
@@ -115,8 +117,33 @@ Range range_of(const char *name, const void *ptr, size_t bytes)
     return Range{name, lo, ptr ? lo + bytes : lo};
 }
 
-// `backward`: the tensors of a backward pass, which reads neither o nor final_state.
-gdr_status check_tensors(const gdr_problem *p, const gdr_tensors *t, bool backward = false)
+// Every input of a forward call.
+constexpr int INPUTS = 13;
+void input_ranges(const gdr_problem *p, const gdr_tensors *t, Range (&ins)[INPUTS])
+{
+    const int64_t T = p->total_tokens, H = p->num_heads_qk, HV = p->num_heads_v, dk = p->head_dim_k, dv = p->head_dim_v;
+    const size_t a = dsize(p->act_dtype);
+    const Range all[INPUTS] = {
+        range_of("q", t->q, (size_t)T * H * dk * a),
+        range_of("k", t->k, (size_t)T * H * dk * a),
+        range_of("v", t->v, (size_t)T * HV * dv * a),
+        range_of("gate", t->gate, (size_t)T * HV * (p->decay_per_key ? dk : 1) * dsize(p->gate_dtype)),
+        range_of("beta", t->beta, (size_t)T * (p->beta_per_token ? 1 : HV) * 4),
+        range_of("erase", t->erase, (size_t)T * HV * dk * 4),
+        range_of("a_log", t->a_log, (size_t)HV * 4),
+        range_of("gate_scale", t->gate_scale, (size_t)HV * 4),
+        range_of("dt_bias", t->dt_bias, (size_t)HV * (p->decay_per_key ? dk : 1) * 4),
+        range_of("seq_lens", t->seq_lens, (size_t)p->batch * 4),
+        range_of("cu_seqlens", t->cu_seqlens, (size_t)(p->batch + 1) * 4),
+        range_of("slot_ids", t->slot_ids, (size_t)p->batch * 4),
+        range_of("initial_state", t->initial_state, (size_t)p->batch * HV * dv * dk * 4),
+    };
+    std::copy(all, all + INPUTS, ins);
+}
+
+// `backward`: the tensors of a backward pass, which reads neither o nor
+// final_state.  state_value: bytes of a value of final_state.
+gdr_status check_tensors(const gdr_problem *p, const gdr_tensors *t, bool backward = false, size_t state_value = 4)
 {
     const int rule = p->update_rule;
     const bool decays = gdr::rule_decays(rule);
@@ -164,27 +191,11 @@ gdr_status check_tensors(const gdr_problem *p, const gdr_tensors *t, bool backwa
     if (backward) return GDR_OK;
 
     // aliasing: outputs must not overlap inputs or each other; final == initial is the in-place case
-    const int64_t H = p->num_heads_qk, HV = p->num_heads_v, dk = p->head_dim_k, dv = p->head_dim_v;
-    const size_t a = dsize(p->act_dtype);
-    const size_t state_bytes = (size_t)state_rows(p) * HV * dv * dk * 4;
-    const auto rng = range_of;
-    const Range out_o = rng("o", t->o, (size_t)T * HV * dv * a);
-    const Range out_s = rng("final_state", t->final_state, state_bytes);
-    const Range ins[] = {
-        rng("q", t->q, (size_t)T * H * dk * a),
-        rng("k", t->k, (size_t)T * H * dk * a),
-        rng("v", t->v, (size_t)T * HV * dv * a),
-        rng("gate", t->gate, (size_t)T * HV * (p->decay_per_key ? dk : 1) * dsize(p->gate_dtype)),
-        rng("beta", t->beta, (size_t)T * (p->beta_per_token ? 1 : HV) * 4),
-        rng("erase", t->erase, (size_t)T * HV * dk * 4),
-        rng("a_log", t->a_log, (size_t)HV * 4),
-        rng("gate_scale", t->gate_scale, (size_t)HV * 4),
-        rng("dt_bias", t->dt_bias, (size_t)HV * (p->decay_per_key ? dk : 1) * 4),
-        rng("seq_lens", t->seq_lens, (size_t)p->batch * 4),
-        rng("cu_seqlens", t->cu_seqlens, (size_t)(p->batch + 1) * 4),
-        rng("slot_ids", t->slot_ids, (size_t)p->batch * 4),
-        rng("initial_state", t->initial_state, (size_t)p->batch * HV * dv * dk * 4),
-    };
+    const int64_t HV = p->num_heads_v, dk = p->head_dim_k, dv = p->head_dim_v;
+    const Range out_o = range_of("o", t->o, (size_t)T * HV * dv * dsize(p->act_dtype));
+    const Range out_s = range_of("final_state", t->final_state, (size_t)state_rows(p) * HV * dv * dk * state_value);
+    Range ins[INPUTS];
+    input_ranges(p, t, ins);
     if (overlaps(out_o, out_s)) return fail(GDR_E_ALIAS, "o overlaps final_state");
     for (const Range &r : ins) {
         if (overlaps(out_o, r)) return fail(GDR_E_ALIAS, "o overlaps %s", r.name);
@@ -517,6 +528,225 @@ gdr_status check_norm(int64_t rows, int32_t width, int32_t dtype, int32_t weight
     return GDR_OK;
 }
 
+// Whether rows of `width` bytes, `stride` bytes apart, may share a byte; exact
+// for equal strides.
+struct Rows {
+    const char *name;
+    uintptr_t lo;
+    size_t stride, width;
+    int64_t count;
+};
+
+bool overlaps(const Rows &a, const Rows &b)
+{
+    if (a.count == 0 || b.count == 0 || a.width == 0 || b.width == 0) return false;
+    const uintptr_t a_end = a.lo + (a.count - 1) * a.stride + a.width, b_end = b.lo + (b.count - 1) * b.stride + b.width;
+    if (a.lo >= b_end || b.lo >= a_end) return false;
+    if (a.stride != b.stride || a.count == 1 || b.count == 1) return true;
+    const size_t apart = a.lo <= b.lo ? (b.lo - a.lo) % a.stride : (a.stride - (a.lo - b.lo) % a.stride) % a.stride;
+    return apart < a.width || apart + b.width > a.stride;
+}
+
+bool same(const Rows &a, const Rows &b) { return a.lo == b.lo && (a.stride == b.stride || a.count == 1) && a.width == b.width; }
+
+bool aligned_to(const void *p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+gdr_status check_rotary(const gdr_rotary *r)
+{
+    if (!r) return fail(GDR_E_INVALID, "rotary is NULL");
+    if (r->tokens < 0 || r->tokens > INT32_MAX) return fail(GDR_E_INVALID, "tokens must lie in [0, 2^31 - 1]");
+    if (r->heads_q < 1 || r->heads_k < 0 || r->heads_q > 65536 || r->heads_k > 65536)
+        return fail(GDR_E_INVALID, "heads_q must lie in [1, 65536] and heads_k in [0, 65536]");
+    if (r->head_dim < 2 || r->head_dim > gdr::ROTARY_MAX_DIM)
+        return fail(GDR_E_INVALID, "head_dim (%d) must lie in [2, %d]", r->head_dim, gdr::ROTARY_MAX_DIM);
+    if (r->rotary_dim < 2 || r->rotary_dim % 2 != 0 || r->rotary_dim > r->head_dim)
+        return fail(GDR_E_INVALID, "rotary_dim (%d) must be even and lie in [2, head_dim]", r->rotary_dim);
+    if (r->axes < 1 || r->axes > gdr::ROTARY_MAX_AXES)
+        return fail(GDR_E_INVALID, "axes (%d) must lie in [1, %d]", r->axes, gdr::ROTARY_MAX_AXES);
+    if (r->interleaved != 0 && r->interleaved != 1) return fail(GDR_E_INVALID, "interleaved must be 0 or 1");
+    if (r->norm != 0 && r->norm != 1) return fail(GDR_E_INVALID, "norm must be 0 or 1");
+    if (r->dtype != GDR_F32 && r->dtype != GDR_F16 && r->dtype != GDR_BF16)
+        return fail(GDR_E_INVALID, "dtype must be GDR_F32, GDR_F16 or GDR_BF16");
+    const bool weight = r->q_weight || r->k_weight;
+    if (weight && r->weight_dtype != r->dtype && r->weight_dtype != GDR_F32)
+        return fail(GDR_E_INVALID, "weight_dtype must be dtype or GDR_F32");
+    if (!std::isfinite(r->eps) || r->eps < 0.f) return fail(GDR_E_INVALID, "eps must be finite and >= 0");
+    return GDR_OK;
+}
+
+size_t rotary_width(const gdr_rotary *r, int heads) { return (size_t)heads * r->head_dim * dsize(r->dtype); }
+
+Rows rotary_rows(const gdr_rotary *r, const char *name, const void *ptr, int64_t stride, int heads)
+{
+    return Rows{name, reinterpret_cast<uintptr_t>(ptr), (size_t)stride * dsize(r->dtype), rotary_width(r, heads),
+                heads && ptr ? r->tokens : 0};
+}
+
+// Rows without gaps, or a plain buffer as one row.
+Rows plain(const char *name, const void *ptr, size_t bytes)
+{
+    return Rows{name, reinterpret_cast<uintptr_t>(ptr), bytes, bytes, ptr ? 1 : 0};
+}
+
+// Pointers, strides and overlaps of a call with the strided outputs outs[0]
+// (of q) and outs[1] (of k), `more` inputs and plain outputs.  in_place: an
+// output may be its own input.
+gdr_status check_rotary_tensors(const gdr_rotary *r, const void *q_out, int64_t q_out_stride, const void *k_out,
+                                int64_t k_out_stride, bool in_place, const Rows *more_ins, int n_ins,
+                                const Rows *more_outs, int n_outs)
+{
+    const bool any = r->tokens > 0;
+    if ((r->heads_k == 0 && (r->k || k_out || r->k_weight)) || (any && r->heads_k > 0 && (!r->k || !k_out)))
+        return fail(GDR_E_INVALID, "k and its result must be given exactly when heads_k > 0");
+    if (any && (!r->q || !q_out || !r->positions)) return fail(GDR_E_INVALID, "q, its result and positions are required");
+    if (!r->inv_freq) return fail(GDR_E_INVALID, "inv_freq is required");
+    const size_t e = dsize(r->dtype);
+    for (const void *ptr : {r->q, r->k, q_out, k_out})
+        if (!aligned_to(ptr, e)) return fail(GDR_E_INVALID, "q, k and their results must be aligned to their elements");
+    const size_t we = dsize(r->weight_dtype);
+    if (!aligned_to(r->q_weight, we) || !aligned_to(r->k_weight, we) || !aligned_to(r->positions, 4) ||
+        !aligned_to(r->inv_freq, 4) || !aligned_to(r->axis_of, 4))
+        return fail(GDR_E_INVALID, "weights, positions, inv_freq and axis_of must be aligned to their elements");
+    const int64_t wq = (int64_t)r->heads_q * r->head_dim, wk = (int64_t)r->heads_k * r->head_dim;
+    const int64_t most = INT64_MAX / 8 / (r->tokens > 0 ? r->tokens : 1);
+    for (int64_t s : {r->q_stride, q_out_stride})
+        if (r->tokens > 1 && (s < wq || s > most)) return fail(GDR_E_INVALID, "strides of q must be at least heads_q * head_dim");
+    for (int64_t s : {r->k_stride, k_out_stride})
+        if (r->tokens > 1 && r->heads_k > 0 && (s < wk || s > most))
+            return fail(GDR_E_INVALID, "strides of k must be at least heads_k * head_dim");
+    const size_t half = (size_t)r->rotary_dim / 2 * 4, weight = (size_t)r->head_dim * we;
+    Rows ins[10] = {rotary_rows(r, "q", r->q, r->q_stride, r->heads_q), rotary_rows(r, "k", r->k, r->k_stride, r->heads_k),
+                    plain("q_weight", r->q_weight, weight), plain("k_weight", r->k_weight, weight),
+                    plain("positions", r->positions, (size_t)r->axes * r->tokens * 4),
+                    plain("inv_freq", r->inv_freq, half), plain("axis_of", r->axis_of, half)};
+    std::copy(more_ins, more_ins + n_ins, ins + 7);
+    Rows outs[5] = {rotary_rows(r, "q's result", q_out, q_out_stride, r->heads_q),
+                    rotary_rows(r, "k's result", k_out, k_out_stride, r->heads_k)};
+    std::copy(more_outs, more_outs + n_outs, outs + 2);
+    for (int i = 0; i < 2 + n_outs; ++i) {
+        for (int j = i + 1; j < 2 + n_outs; ++j)
+            if (overlaps(outs[i], outs[j])) return fail(GDR_E_ALIAS, "%s overlaps %s", outs[i].name, outs[j].name);
+        for (int j = 0; j < 7 + n_ins; ++j) {
+            if (in_place && i == j && same(outs[i], ins[j])) continue;
+            if (overlaps(outs[i], ins[j])) return fail(GDR_E_ALIAS, "%s overlaps %s", outs[i].name, ins[j].name);
+        }
+    }
+    return GDR_OK;
+}
+
+gdr::RotaryParams rotary_params(const gdr_rotary *r)
+{
+    gdr::RotaryParams p{};
+    const bool weight = r->q_weight || r->k_weight;
+    p.part[0].x = r->q;
+    p.part[0].weight = r->q_weight;
+    p.part[0].stride = r->q_stride;
+    p.part[0].heads = r->heads_q;
+    p.part[1].x = r->k;
+    p.part[1].weight = r->k_weight;
+    p.part[1].stride = r->k_stride;
+    p.part[1].heads = r->heads_k;
+    p.tokens = r->tokens;
+    p.dim = r->head_dim;
+    p.half = r->rotary_dim / 2;
+    p.axes = r->axes;
+    p.neighbours = r->interleaved;
+    p.norm = r->norm;
+    p.dt = dtype_code(r->dtype);
+    p.weight_dt = weight ? dtype_code(r->weight_dtype) : p.dt;
+    p.eps = r->eps;
+    p.positions = r->positions;
+    p.axis_of = r->axis_of;
+    p.freq = r->inv_freq;
+    return p;
+}
+
+gdr_status check_slab(const gdr_packed_slab *slab)
+{
+    if (!slab) return fail(GDR_E_INVALID, "slab is NULL");
+    if (slab->dtype != GDR_F16 && slab->dtype != GDR_BF16 && slab->dtype != GDR_E4M3)
+        return fail(GDR_E_INVALID, "a packed slab's dtype must be GDR_F16, GDR_BF16 or GDR_E4M3");
+    return GDR_OK;
+}
+
+// The slab's pointers, for a call that addresses it (slots > 0).
+gdr_status check_slab_pointers(const gdr_packed_slab *slab)
+{
+    if (!slab->data) return fail(GDR_E_INVALID, "the slab's data is required");
+    if ((slab->scale != nullptr) != (slab->dtype == GDR_E4M3))
+        return fail(GDR_E_INVALID, "a packed slab has scales exactly with GDR_E4M3");
+    if (!aligned16(slab->data)) return fail(GDR_E_INVALID, "the slab's data must be 16-byte aligned");
+    return GDR_OK;
+}
+
+size_t slab_value(const gdr_packed_slab *slab) { return slab->dtype == GDR_E4M3 ? 1 : 2; }
+
+Range scale_range(const gdr_packed_slab *slab, int64_t rows)
+{
+    return range_of("the slab's scales", slab->scale, (size_t)rows);
+}
+
+// Check a pack or unpack call and set up its kernel; *go: there is work.
+gdr_status packed_params(int32_t batch, int32_t heads, int32_t dv, int32_t dk, int32_t num_slots, const float *states,
+                         const int32_t *slot_ids, const gdr_packed_slab *slab, bool pack, gdr::PackedParams *a, bool *go)
+{
+    *go = false;
+    gdr_status st = check_slab(slab);
+    if (st != GDR_OK) return st;
+    if (batch < 0 || heads < 1 || num_slots < 0) return fail(GDR_E_INVALID, "batch and num_slots must be >= 0, heads >= 1");
+    if (dk < 1 || dk > 256 || dv < 1 || dv > 256) return fail(GDR_E_INVALID, "head dims must lie in [1, 256] (dk=%d, dv=%d)", dk, dv);
+    if (gdr::pack_blocks(batch, heads, dv) > INT32_MAX) return fail(GDR_E_INVALID, "batch * heads too large");
+    if (batch == 0 || num_slots == 0) return GDR_OK;
+    st = check_slab_pointers(slab);
+    if (st != GDR_OK) return st;
+    if (!states || !slot_ids) return fail(GDR_E_INVALID, "states and slot_ids are required");
+    if (!aligned16(states) || !aligned_to(slot_ids, 4))
+        return fail(GDR_E_INVALID, "states must be 16-byte aligned and slot_ids 4-byte aligned");
+    const int64_t rows = (int64_t)num_slots * heads * dv;
+    const Range data = range_of("the slab's data", slab->data, (size_t)rows * dk * slab_value(slab));
+    const Range scale = scale_range(slab, rows), ids = range_of("slot_ids", slot_ids, (size_t)batch * 4);
+    const Range all = range_of("states", states, (size_t)batch * heads * dv * dk * 4);
+    const Range cache[] = {data, scale}, state[] = {all}, with_ids[] = {all, ids}, with_cache[] = {data, scale, ids};
+    st = pack ? check_overlap(cache, 2, with_ids, 2) : check_overlap(state, 1, with_cache, 3);
+    if (st != GDR_OK) return st;
+    a->p.slot_ids = slot_ids;
+    a->p.num_slots = num_slots;
+    a->p.B = batch;
+    a->p.HV = heads;
+    a->p.dv = dv;
+    a->p.dk = dk;
+    a->data = slab->data;
+    a->scale = slab->scale;
+    a->type = slab->dtype;
+    a->states = const_cast<float *>(states);
+    *go = true;
+    return GDR_OK;
+}
+
+// Whether a call on a packed slab runs as one pass over it: as pick_algo
+// chooses the decode kernel, with the key dims the pass takes.
+bool packed_step(const gdr_problem *p)
+{
+    if (p->algo == GDR_ALGO_DECODE) return true;  // checked: dk = dv = 128
+    const int64_t per_req = p->batch > 0 ? (p->total_tokens + p->batch - 1) / p->batch : 0;
+    return p->algo == GDR_ALGO_AUTO && gdr::packed_step_ok(p->head_dim_k) && per_req <= 8;
+}
+
+// The call on fp32 states in the workspace: slot b of a slab of B.
+gdr_problem unpacked_problem(const gdr_problem *p)
+{
+    gdr_problem q = *p;
+    q.num_slots = p->batch;
+    return q;
+}
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+size_t state_bytes(const gdr_problem *p)
+{
+    return up256((size_t)p->batch * p->num_heads_v * p->head_dim_v * p->head_dim_k * 4);
+}
+
 // Enqueue every kernel of a validated call on `stream`; `workspace` holds at
 // least gdr_workspace_size bytes.
 gdr_status launch_all(const gdr_problem *problem, const gdr_tensors *tensors, void *workspace, void *stream)
@@ -809,6 +1039,182 @@ gdr_status gdr_rms_norm_backward(int64_t rows, int32_t width, int32_t dtype, int
     p.d_weight = d_weight;
     p.partial = d_weight ? static_cast<float *>(workspace) : nullptr;
     hipError_t err = gdr::launch_norm_backward(p, static_cast<hipStream_t>(stream));
+    if (err != hipSuccess) return fail(GDR_E_HIP, "kernel launch failed: %s", hipGetErrorString(err));
+    return GDR_OK;
+}
+
+gdr_status gdr_qk_rotary(const gdr_rotary *rotary, void *q_out, int64_t q_out_stride, void *k_out,
+                         int64_t k_out_stride, void *stream)
+{
+    g_last_error.clear();
+    gdr_status st = check_rotary(rotary);
+    if (st != GDR_OK) return st;
+    st = check_rotary_tensors(rotary, q_out, q_out_stride, k_out, k_out_stride, true, nullptr, 0, nullptr, 0);
+    if (st != GDR_OK) return st;
+    gdr::RotaryParams p = rotary_params(rotary);
+    p.part[0].y = q_out;
+    p.part[0].out_stride = q_out_stride;
+    p.part[1].y = k_out;
+    p.part[1].out_stride = k_out_stride;
+    hipError_t err = gdr::launch_rotary(p, static_cast<hipStream_t>(stream));
+    if (err != hipSuccess) return fail(GDR_E_HIP, "kernel launch failed: %s", hipGetErrorString(err));
+    return GDR_OK;
+}
+
+gdr_status gdr_qk_rotary_backward_workspace_size(const gdr_rotary *rotary, size_t *bytes)
+{
+    g_last_error.clear();
+    if (!bytes) return fail(GDR_E_INVALID, "bytes is NULL");
+    gdr_status st = check_rotary(rotary);
+    if (st != GDR_OK) return st;
+    const int64_t heads = std::max(rotary->heads_q, rotary->heads_k);
+    const size_t part = (size_t)gdr::rotary_back_blocks(rotary->tokens, heads, rotary->head_dim) * rotary->head_dim * 4;
+    *bytes = part * ((rotary->q_weight != nullptr) + (rotary->k_weight != nullptr));
+    return GDR_OK;
+}
+
+gdr_status gdr_qk_rotary_backward(const gdr_rotary *rotary, const void *d_q_out, const void *d_k_out, void *d_q,
+                                  int64_t d_q_stride, void *d_k, int64_t d_k_stride, float *d_q_weight,
+                                  float *d_k_weight, void *workspace, size_t workspace_bytes, void *stream)
+{
+    g_last_error.clear();
+    gdr_status st = check_rotary(rotary);
+    if (st != GDR_OK) return st;
+    const gdr_rotary &r = *rotary;
+    if (r.tokens > 0 && (!d_q_out || (r.heads_k > 0) != (d_k_out != nullptr)))
+        return fail(GDR_E_INVALID, "d_q_out is required, and d_k_out exactly when heads_k > 0");
+    if ((d_q_weight != nullptr) != (r.q_weight != nullptr) || (d_k_weight != nullptr) != (r.k_weight != nullptr))
+        return fail(GDR_E_INVALID, "d_q_weight and d_k_weight must be given exactly when the weights are");
+    if (!aligned_to(d_q_out, dsize(r.dtype)) || !aligned_to(d_k_out, dsize(r.dtype)) || !aligned_to(d_q_weight, 4) ||
+        !aligned_to(d_k_weight, 4) || !aligned16(workspace))
+        return fail(GDR_E_INVALID, "gradients must be aligned to their elements, the workspace to 16 bytes");
+    size_t need = 0;
+    gdr_qk_rotary_backward_workspace_size(rotary, &need);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return fail(GDR_E_WORKSPACE, "workspace of %zu bytes required", need);
+    const Rows ins[] = {plain("d_q_out", d_q_out, (size_t)r.tokens * rotary_width(rotary, r.heads_q)),
+                        plain("d_k_out", d_k_out, (size_t)r.tokens * rotary_width(rotary, r.heads_k))};
+    const Rows outs[] = {plain("d_q_weight", d_q_weight, (size_t)r.head_dim * 4),
+                         plain("d_k_weight", d_k_weight, (size_t)r.head_dim * 4), plain("workspace", workspace, need)};
+    st = check_rotary_tensors(rotary, d_q, d_q_stride, d_k, d_k_stride, false, ins, 2, outs, 3);
+    if (st != GDR_OK) return st;
+    gdr::RotaryParams p = rotary_params(rotary);
+    float *partial = static_cast<float *>(workspace);
+    p.part[0].y = d_q;
+    p.part[0].out_stride = d_q_stride;
+    p.part[0].d_y = d_q_out;
+    p.part[0].d_weight = d_q_weight;
+    p.part[0].partial = d_q_weight ? partial : nullptr;
+    p.part[1].y = d_k;
+    p.part[1].out_stride = d_k_stride;
+    p.part[1].d_y = d_k_out;
+    p.part[1].d_weight = d_k_weight;
+    p.part[1].partial = d_k_weight ? partial + (d_q_weight ? need / 8 : 0) : nullptr;  // the second half, in floats
+    hipError_t err = gdr::launch_rotary_backward(p, static_cast<hipStream_t>(stream));
+    if (err != hipSuccess) return fail(GDR_E_HIP, "kernel launch failed: %s", hipGetErrorString(err));
+    return GDR_OK;
+}
+
+gdr_status gdr_state_pack(int32_t batch, int32_t heads, int32_t dv, int32_t dk, int32_t num_slots,
+                          const float *states, const int32_t *slot_ids, const gdr_packed_slab *slab, void *stream)
+{
+    g_last_error.clear();
+    gdr::PackedParams a{};
+    bool go = false;
+    gdr_status st = packed_params(batch, heads, dv, dk, num_slots, states, slot_ids, slab, true, &a, &go);
+    if (st != GDR_OK || !go) return st;
+    hipError_t err = gdr::launch_pack(a, static_cast<hipStream_t>(stream));
+    if (err != hipSuccess) return fail(GDR_E_HIP, "kernel launch failed: %s", hipGetErrorString(err));
+    return GDR_OK;
+}
+
+gdr_status gdr_state_unpack(int32_t batch, int32_t heads, int32_t dv, int32_t dk, int32_t num_slots,
+                            const gdr_packed_slab *slab, const int32_t *slot_ids, float *states, void *stream)
+{
+    g_last_error.clear();
+    gdr::PackedParams a{};
+    bool go = false;
+    gdr_status st = packed_params(batch, heads, dv, dk, num_slots, states, slot_ids, slab, false, &a, &go);
+    if (st != GDR_OK || !go) return st;
+    hipError_t err = gdr::launch_unpack(a, static_cast<hipStream_t>(stream));
+    if (err != hipSuccess) return fail(GDR_E_HIP, "kernel launch failed: %s", hipGetErrorString(err));
+    return GDR_OK;
+}
+
+gdr_status gdr_packed_workspace_size(const gdr_problem *problem, size_t *bytes)
+{
+    g_last_error.clear();
+    if (!bytes) return fail(GDR_E_INVALID, "bytes is NULL");
+    gdr_status st = check_problem(problem);
+    if (st != GDR_OK) return st;
+    *bytes = 0;
+    if (packed_step(problem) || problem->batch == 0) return GDR_OK;
+    const gdr_problem inner = unpacked_problem(problem);
+    size_t more = 0;
+    st = gdr_workspace_size(&inner, &more);
+    if (st != GDR_OK) return st;
+    *bytes = up256((size_t)problem->batch * 4) + state_bytes(problem) + more;
+    return GDR_OK;
+}
+
+gdr_status gdr_forward_packed(const gdr_problem *problem, const gdr_tensors *tensors, const gdr_packed_slab *slab,
+                              void *workspace, size_t workspace_bytes, void *stream)
+{
+    g_last_error.clear();
+    if (!tensors) return fail(GDR_E_INVALID, "tensors is NULL");
+    gdr_status st = check_problem(problem);
+    if (st != GDR_OK) return st;
+    st = check_slab(slab);
+    if (st != GDR_OK) return st;
+    if (problem->num_slots < 1) return fail(GDR_E_INVALID, "a packed slab needs num_slots >= 1");
+    if (tensors->initial_state || tensors->final_state)
+        return fail(GDR_E_INVALID, "with a packed slab initial_state and final_state must be NULL");
+    if (problem->batch == 0) return GDR_OK;  // slot_ids has no entries, and may be NULL
+    st = check_slab_pointers(slab);
+    if (st != GDR_OK) return st;
+    gdr_tensors t = *tensors;
+    t.final_state = static_cast<float *>(slab->data);
+    st = check_tensors(problem, &t, false, slab_value(slab));
+    if (st != GDR_OK) return st;
+    size_t need = 0;
+    gdr_packed_workspace_size(problem, &need);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return fail(GDR_E_WORKSPACE, "workspace of %zu bytes required", need);
+    if (need > 0 && !aligned16(workspace)) return fail(GDR_E_INVALID, "the workspace must be 16-byte aligned");
+    const gdr_problem &p = *problem;
+    const int64_t rows = (int64_t)p.num_slots * p.num_heads_v * p.head_dim_v;
+    const Range outs[] = {range_of("o", t.o, (size_t)p.total_tokens * p.num_heads_v * p.head_dim_v * dsize(p.act_dtype)),
+                          range_of("the slab's data", slab->data, (size_t)rows * p.head_dim_k * slab_value(slab)),
+                          scale_range(slab, rows), range_of("workspace", workspace, need)};
+    Range ins[INPUTS];
+    input_ranges(problem, &t, ins);
+    st = check_overlap(outs, 4, ins, INPUTS);
+    if (st != GDR_OK) return st;
+
+    gdr::PackedParams a{};
+    a.p = kernel_params(problem, &t);
+    a.data = slab->data;
+    a.scale = slab->scale;
+    a.type = slab->dtype;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    hipError_t err;
+    if (packed_step(problem)) {
+        err = gdr::launch_packed_step(a, p.update_rule, p.decay_per_key != 0, dtype_code(p.act_dtype), s);
+    } else {
+        char *ws = static_cast<char *>(workspace);
+        const size_t ids = up256((size_t)p.batch * 4);
+        a.ids = reinterpret_cast<int32_t *>(ws);
+        a.states = reinterpret_cast<float *>(ws + ids);
+        a.skip_empty = 1;
+        err = gdr::launch_unpack(a, s);
+        if (err == hipSuccess) {
+            const gdr_problem inner = unpacked_problem(problem);
+            t.slot_ids = a.ids;
+            t.final_state = a.states;
+            st = launch_all(&inner, &t, ws + ids + state_bytes(problem), stream);
+            if (st != GDR_OK) return st;
+            a.ids = nullptr;
+            err = gdr::launch_pack(a, s);
+        }
+    }
     if (err != hipSuccess) return fail(GDR_E_HIP, "kernel launch failed: %s", hipGetErrorString(err));
     return GDR_OK;
 }

@@ -1,0 +1,415 @@
+// gdr_rotary.hip -- root-mean-square norm of every head of q and k and the
+// rotation by the tokens' positions in one pass, and its backward pass.
+//
+//   h = x inv w,  inv = 1 / sqrt(mean x^2 + eps)      (inv = 1 without the norm)
+//   a = position[axis_i] freq_i;  pair i of h turned by a:
+//   (y_0, y_1) = (h_0 cos a - h_1 sin a, h_1 cos a + h_0 sin a)
+// and backwards, with g the pairs of dy turned by -a, t = w g and n = x inv,
+//   dx = inv (t - n mean(t n)),   dw = sum over tokens and heads of g n
+// (the norm's statistics are formed again: a sum more, nothing kept).
+//
+// Bound by memory: a head's row lies in the registers of LPR lanes between its
+// load and its store.  A lane holds both values of its pairs: VEC elements
+// from each half of the turned columns, or 2 VEC neighbours.  The angles of a
+// workgroup's tokens are formed once, by all its threads, and lie in LDS for
+// every head.  An angle is the product of an int32 and an fp32 value, taken in
+// turns and in 64 bits: at position 10^6 an fp32 product is off by 0.03.
+#include "gdr_rotary_launch.hpp"
+
+namespace gdr {
+namespace {
+
+constexpr int THREADS = 256;
+constexpr int ANGLES = 2048;  // pairs of (token, frequency) whose cos and sin LDS holds
+
+// 16 bytes from any even address.
+typedef uint32_t v4 __attribute__((ext_vector_type(4), aligned(2)));
+
+// VEC elements as they lie in memory.
+template <typename T, int VEC> struct Raw {
+    static constexpr int WORDS = (VEC * sizeof(T) + 3) / 4;
+    uint32_t w[WORDS];
+    __device__ __forceinline__ void load(const T *src)
+    {
+        if constexpr (WORDS == 4) {
+            const v4 x = *reinterpret_cast<const v4 *>(src);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = x[i];
+        } else if constexpr (sizeof(T) == 4) {
+            w[0] = __builtin_bit_cast(uint32_t, src[0]);
+        } else {
+            w[0] = __builtin_bit_cast(uint16_t, src[0]);
+        }
+    }
+    __device__ __forceinline__ float get(int i) const
+    {
+        if constexpr (sizeof(T) == 4) return __builtin_bit_cast(float, w[i]);
+        else return to_f32(__builtin_bit_cast(T, (uint16_t)(w[i / 2] >> (16 * (i % 2)))));
+    }
+};
+
+template <typename T, int VEC>
+__device__ __forceinline__ void store(T *dst, const float *v)
+{
+    if constexpr (VEC * sizeof(T) == 16) {
+        v4 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) o[i] = __builtin_bit_cast(uint32_t, v[i]);
+            else o[i] = __builtin_bit_cast(uint16_t, from_f32<T>(v[2 * i])) |
+                        (uint32_t)__builtin_bit_cast(uint16_t, from_f32<T>(v[2 * i + 1])) << 16;
+        }
+        *reinterpret_cast<v4 *>(dst) = o;
+    } else {
+        dst[0] = from_f32<T>(v[0]);
+    }
+}
+
+// Where a lane's vector lies in a head: `at` the columns of its two parts of
+// VEC elements, `pair` its first turned pair (or -1: not turned).
+template <int VEC> struct Place {
+    int at[2], pair;
+    bool on, second;  // second: the second part lies inside the head
+    __device__ __forceinline__ Place(const RotaryParams &p, int vector)
+    {
+        const int base = vector * VEC;
+        const bool turned = base < p.half;
+        on = 2 * base < p.dim;
+        at[0] = turned && !p.neighbours ? base : 2 * base;
+        at[1] = turned && !p.neighbours ? p.half + base : 2 * base + VEC;
+        second = VEC > 1 || at[1] < p.dim;
+        pair = turned ? base : -1;
+    }
+};
+
+// Pair i of a lane's 2 VEC values: both halves' i-th, or two neighbours.
+template <int VEC>
+__device__ __forceinline__ void turn(float (&x)[2 * VEC], const float *cs, const float *sn, bool neighbours, float sign)
+{
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        const float c = cs[i], s = sign * sn[i];
+        float &a0 = x[i], &b0 = x[VEC + i], &a1 = x[2 * i], &b1 = x[2 * i + 1];
+        if (neighbours) {
+            const float a = a1, b = b1;
+            a1 = a * c - b * s;
+            b1 = b * c + a * s;
+        } else {
+            const float a = a0, b = b0;
+            a0 = a * c - b * s;
+            b0 = b * c + a * s;
+        }
+    }
+}
+
+template <int LPR>
+__device__ __forceinline__ float row_sum(float x)
+{
+#pragma unroll
+    for (int o = 1; o < LPR; o <<= 1) x += __shfl_xor(x, o);
+    return x;
+}
+
+// cos and sin of the angles of tokens t0 .. t0 + n - 1.
+__device__ __forceinline__ void angles(const RotaryParams &p, int64_t t0, int n, float *cs, float *sn)
+{
+    for (int i = threadIdx.x; i < n * p.half; i += THREADS) {
+        const int token = i / p.half, f = i - token * p.half;
+        int axis = p.axis_of ? p.axis_of[f] : 0;
+        axis = axis < 0 ? 0 : axis < p.axes ? axis : p.axes - 1;
+        const double turns = (double)p.positions[axis * p.tokens + t0 + token] * ((double)p.freq[f] * 0.15915494309189535);
+        sincospif((float)(2 * (turns - rint(turns))), &sn[i], &cs[i]);
+    }
+}
+
+// A workgroup takes p.block tokens, all heads of q and then of k for each.
+template <typename T, typename TW, int VEC, int LPR, int NV>
+__global__ __launch_bounds__(THREADS) void k_rotary(const RotaryParams p)
+{
+    __shared__ float s_cos[ANGLES], s_sin[ANGLES], s_w[2][ROTARY_MAX_DIM];
+    constexpr int ROWS = THREADS / LPR;
+    const int lane = threadIdx.x % LPR;
+    const int heads = p.part[0].heads + p.part[1].heads;
+    const int64_t t0 = (int64_t)blockIdx.x * p.block;
+    const int n = (int)(p.tokens - t0 < p.block ? p.tokens - t0 : p.block);
+    const int step_t = ROWS / heads, step_h = ROWS - step_t * heads;
+    int token = threadIdx.x / LPR / heads, head = threadIdx.x / LPR - token * heads;
+    Raw<T, VEC> x[NV][2];
+    auto fetch = [&](int token, int head) {
+        const int z = head >= p.part[0].heads;
+        const RotaryPart &part = p.part[z];
+        const T *row = static_cast<const T *>(part.x) + (t0 + token) * part.stride +
+                       (int64_t)(z ? head - p.part[0].heads : head) * p.dim;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const Place<VEC> at(p, lane + LPR * v);
+            if (!at.on) continue;
+            x[v][0].load(row + at.at[0]);
+            x[v][1].load(row + (at.second ? at.at[1] : at.at[0]));
+        }
+    };
+    if (token < n) fetch(token, head);
+    angles(p, t0, n, s_cos, s_sin);
+    for (int i = threadIdx.x; i < 2 * p.dim; i += THREADS) {
+        const int z = i >= p.dim, c = z ? i - p.dim : i;
+        s_w[z][c] = p.part[z].weight ? to_f32(static_cast<const TW *>(p.part[z].weight)[c]) : 1.f;
+    }
+    lds_barrier();
+    while (token < n) {
+        const int z = head >= p.part[0].heads;
+        const RotaryPart &part = p.part[z];
+        float h[NV][2 * VEC], sum = 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const Place<VEC> at(p, lane + LPR * v);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                h[v][i] = at.on ? x[v][0].get(i) : 0.f;
+                h[v][VEC + i] = at.on && at.second ? x[v][1].get(i) : 0.f;
+                sum += h[v][i] * h[v][i] + h[v][VEC + i] * h[v][VEC + i];
+            }
+        }
+        T *row = static_cast<T *>(part.y) + (t0 + token) * part.out_stride +
+                 (int64_t)(z ? head - p.part[0].heads : head) * p.dim;
+        const int now = token;
+        token += step_t;
+        head += step_h;
+        if (head >= heads) {
+            head -= heads;
+            ++token;
+        }
+        if (token < n) fetch(token, head);
+        const float inv = p.norm ? 1.f / sqrtf(row_sum<LPR>(sum) / (float)p.dim + p.eps) : 1.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const Place<VEC> at(p, lane + LPR * v);
+            if (!at.on) continue;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                h[v][i] *= inv * s_w[z][at.at[0] + i];
+                if (at.second) h[v][VEC + i] *= inv * s_w[z][at.at[1] + i];
+            }
+            if (at.pair >= 0)
+                turn<VEC>(h[v], &s_cos[now * p.half + at.pair], &s_sin[now * p.half + at.pair], p.neighbours, 1.f);
+            store<T, VEC>(row + at.at[0], &h[v][0]);
+            if (at.second) store<T, VEC>(row + at.at[1], &h[v][VEC]);
+        }
+    }
+}
+
+// blockIdx.y: q or k.  A workgroup takes p.block tokens, + gridDim.x *
+// p.block, ...; the weight's gradient stays in a lane's registers, as its
+// columns are the same for every row, and its sums over the workgroup's rows
+// and then over the workgroups have a fixed order.
+template <typename T, typename TW, int VEC, int LPR, int NV>
+__global__ __launch_bounds__(THREADS) void k_rotary_back(const RotaryParams p)
+{
+    __shared__ float s_cos[ANGLES], s_sin[ANGLES], s_w[ROTARY_MAX_DIM], s_dw[THREADS][2 * VEC + 1];
+    constexpr int ROWS = THREADS / LPR;
+    const int lane = threadIdx.x % LPR, group = threadIdx.x / LPR;
+    const RotaryPart &part = p.part[blockIdx.y];
+    const int heads = part.heads;
+    if (heads == 0) return;
+    float dw[NV][2 * VEC] = {};
+    for (int i = threadIdx.x; i < p.dim; i += THREADS)
+        s_w[i] = part.weight ? to_f32(static_cast<const TW *>(part.weight)[i]) : 1.f;
+    const int step_t = ROWS / heads, step_h = ROWS - step_t * heads;
+    for (int64_t t0 = (int64_t)blockIdx.x * p.block; t0 < p.tokens; t0 += (int64_t)gridDim.x * p.block) {
+        const int n = (int)(p.tokens - t0 < p.block ? p.tokens - t0 : p.block);
+        int token = group / heads, head = group - token * heads;
+        Raw<T, VEC> x[NV][2], y[NV][2];
+        auto fetch = [&](int token, int head) {
+            const T *row = static_cast<const T *>(part.x) + (t0 + token) * part.stride + (int64_t)head * p.dim;
+            const T *dy = static_cast<const T *>(part.d_y) + ((t0 + token) * heads + head) * p.dim;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const Place<VEC> at(p, lane + LPR * v);
+                if (!at.on) continue;
+                x[v][0].load(row + at.at[0]);
+                x[v][1].load(row + (at.second ? at.at[1] : at.at[0]));
+                y[v][0].load(dy + at.at[0]);
+                y[v][1].load(dy + (at.second ? at.at[1] : at.at[0]));
+            }
+        };
+        if (token < n) fetch(token, head);
+        lds_barrier();  // the last tokens' angles have been used
+        angles(p, t0, n, s_cos, s_sin);
+        lds_barrier();
+        while (token < n) {
+            float h[NV][2 * VEC], g[NV][2 * VEC], sum = 0.f, dot = 0.f;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const Place<VEC> at(p, lane + LPR * v);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    h[v][i] = at.on ? x[v][0].get(i) : 0.f;
+                    h[v][VEC + i] = at.on && at.second ? x[v][1].get(i) : 0.f;
+                    g[v][i] = at.on ? y[v][0].get(i) : 0.f;
+                    g[v][VEC + i] = at.on && at.second ? y[v][1].get(i) : 0.f;
+                }
+                if (at.on && at.pair >= 0)
+                    turn<VEC>(g[v], &s_cos[token * p.half + at.pair], &s_sin[token * p.half + at.pair], p.neighbours, -1.f);
+#pragma unroll
+                for (int i = 0; i < 2 * VEC; ++i) {
+                    sum += h[v][i] * h[v][i];
+                    if (at.on && (i < VEC || at.second)) dot += g[v][i] * s_w[at.at[i / VEC] + i % VEC] * h[v][i];
+                }
+            }
+            T *row = static_cast<T *>(part.y) + (t0 + token) * part.out_stride + (int64_t)head * p.dim;
+            token += step_t;
+            head += step_h;
+            if (head >= heads) {
+                head -= heads;
+                ++token;
+            }
+            if (token < n) fetch(token, head);
+            float inv = 1.f, mean = 0.f;
+            if (p.norm) {
+                inv = 1.f / sqrtf(row_sum<LPR>(sum) / (float)p.dim + p.eps);
+                mean = row_sum<LPR>(dot) * inv / (float)p.dim;
+            }
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const Place<VEC> at(p, lane + LPR * v);
+                if (!at.on) continue;
+#pragma unroll
+                for (int i = 0; i < 2 * VEC; ++i) {
+                    if (i >= VEC && !at.second) continue;
+                    const float nx = h[v][i] * inv;
+                    dw[v][i] += g[v][i] * nx;
+                    g[v][i] = inv * (g[v][i] * s_w[at.at[i / VEC] + i % VEC] - nx * mean);
+                }
+                store<T, VEC>(row + at.at[0], &g[v][0]);
+                if (at.second) store<T, VEC>(row + at.at[1], &g[v][VEC]);
+            }
+        }
+    }
+    if (!part.partial) return;
+    float *out = part.partial + (size_t)blockIdx.x * p.dim;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2 * VEC; ++i) s_dw[threadIdx.x][i] = dw[v][i];
+        __syncthreads();
+        // value i of lane l of this vector: one thread each
+        for (int e = threadIdx.x; e < LPR * 2 * VEC; e += THREADS) {
+            const int l = e / (2 * VEC), i = e % (2 * VEC);
+            const Place<VEC> at(p, l + LPR * v);
+            if (!at.on || (i >= VEC && !at.second)) continue;
+            float sum = 0.f;
+            for (int r = 0; r < ROWS; ++r) sum += s_dw[r * LPR + l][i];
+            out[at.at[i / VEC] + i % VEC] = sum;
+        }
+    }
+}
+
+// Workgroup: 16 columns, 16 threads a column, each every 16th partial row.
+__global__ __launch_bounds__(256) void k_rotary_back_sums(const RotaryParams p, int blocks)
+{
+    __shared__ float s[16][17];
+    const RotaryPart &part = p.part[blockIdx.y];
+    if (!part.d_weight) return;
+    const int c = threadIdx.x & 15, r = threadIdx.x >> 4, col = blockIdx.x * 16 + c;
+    float sum = 0.f;
+    if (col < p.dim && part.heads > 0)
+        for (int b = r; b < blocks; b += 16) sum += part.partial[(size_t)b * p.dim + col];
+    s[r][c] = sum;
+    __syncthreads();
+    if (r == 0 && col < p.dim) {
+        for (int n = 1; n < 16; ++n) sum += s[n][c];
+        part.d_weight[col] = sum;
+    }
+}
+
+// Lanes and vectors of a head: vectors of 16 bytes where head and turned part
+// consist of whole pairs of them, else single pairs.
+template <typename T, typename F>
+hipError_t by_form(const RotaryParams &p, F &&f)
+{
+    using std::integral_constant;
+    constexpr int V = 16 / sizeof(T);
+    using vec = integral_constant<int, V>;
+    using one = integral_constant<int, 1>;
+    if (p.dim % (2 * V) == 0 && p.half % V == 0) {
+        const int vectors = p.dim / (2 * V);
+        if (vectors <= 8) return f(vec(), integral_constant<int, 8>(), one());
+        if (vectors <= 16) return f(vec(), integral_constant<int, 16>(), one());
+        if constexpr (V == 4) return f(vec(), integral_constant<int, 32>(), one());
+    }
+    if (p.dim <= 64) return f(one(), integral_constant<int, 32>(), one());
+    if (p.dim <= 128) return f(one(), integral_constant<int, 64>(), one());
+    return f(one(), integral_constant<int, 64>(), integral_constant<int, 2>());
+}
+
+template <typename F>
+hipError_t by_types(const RotaryParams &p, F &&f)
+{
+    if (p.dt == 1) return p.weight_dt == 1 ? f(half_t(), half_t()) : f(half_t(), float());
+    if (p.dt == 2) return p.weight_dt == 2 ? f(bf16_t(), bf16_t()) : f(bf16_t(), float());
+    return f(float(), float());
+}
+
+// Tokens a workgroup takes at a time: about `rows` heads, and no more angles
+// than LDS holds.
+int token_block(const RotaryParams &p, int64_t heads, int64_t rows)
+{
+    int64_t n = (rows + heads - 1) / heads;
+    if (n * p.half > ANGLES) n = ANGLES / p.half;
+    return (int)(n < 1 ? 1 : n);
+}
+
+}  // namespace
+
+int rotary_back_blocks(int64_t tokens, int64_t heads, int64_t dim)
+{
+    const int64_t n = tokens * heads * dim / 16384;
+    return n < 1 ? 1 : n > 512 ? 512 : (int)n;
+}
+
+hipError_t launch_rotary(const RotaryParams &params, hipStream_t s)
+{
+    RotaryParams p = params;
+    const int64_t heads = (int64_t)p.part[0].heads + p.part[1].heads;
+    if (p.tokens == 0 || heads == 0) return hipSuccess;
+    p.block = token_block(p, heads, 128);
+    const int64_t spread = (p.tokens + 511) / 512;  // few tokens: a workgroup each
+    if (p.block > spread) p.block = (int)spread;
+    const dim3 blocks((unsigned)((p.tokens + p.block - 1) / p.block));
+    return by_types(p, [&](auto t, auto w) {
+        using T = decltype(t);
+        using TW = decltype(w);
+        return by_form<T>(p, [&](auto vec, auto lpr, auto nv) {
+            hipLaunchKernelGGL((k_rotary<T, TW, decltype(vec)::value, decltype(lpr)::value, decltype(nv)::value>),
+                               blocks, dim3(THREADS), 0, s, p);
+            return hipGetLastError();
+        });
+    });
+}
+
+hipError_t launch_rotary_backward(const RotaryParams &params, hipStream_t s)
+{
+    RotaryParams p = params;
+    const int64_t heads = std::max(p.part[0].heads, p.part[1].heads);
+    const int blocks = rotary_back_blocks(p.tokens, heads, p.dim);
+    if (p.tokens > 0 && heads > 0) {
+        p.block = token_block(p, heads, 64);
+        hipError_t err = by_types(p, [&](auto t, auto w) {
+            using T = decltype(t);
+            using TW = decltype(w);
+            return by_form<T>(p, [&](auto vec, auto lpr, auto nv) {
+                hipLaunchKernelGGL((k_rotary_back<T, TW, decltype(vec)::value, decltype(lpr)::value, decltype(nv)::value>),
+                                   dim3((unsigned)blocks, 2), dim3(THREADS), 0, s, p);
+                return hipGetLastError();
+            });
+        });
+        if (err != hipSuccess) return err;
+    }
+    if (p.part[0].d_weight || p.part[1].d_weight) {
+        const int have = p.tokens > 0 ? blocks : 0;
+        hipLaunchKernelGGL(k_rotary_back_sums, dim3((unsigned)((p.dim + 15) / 16), 2), dim3(256), 0, s, p, have);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace gdr

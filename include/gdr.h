@@ -105,7 +105,8 @@ typedef enum {
  * per-key form. */
 typedef enum {
     GDR_F32 = 0, GDR_F16 = 1, GDR_BF16 = 2,
-    GDR_E4M3 = 3  /* 8 bits (4 exponent, 3 mantissa, largest 448, no infinities): gdr_rms_norm's output only */
+    GDR_E4M3 = 3  /* 8 bits (4 exponent, 3 mantissa, largest 448, no infinities): gdr_rms_norm's output
+                   * and the state cache of gdr_packed_slab only */
 } gdr_dtype;
 
 typedef enum {
@@ -361,6 +362,105 @@ gdr_status gdr_rms_norm_backward_workspace_size(int64_t rows, int32_t width, siz
 gdr_status gdr_rms_norm_backward(int64_t rows, int32_t width, int32_t dtype, int32_t weight_dtype, const void *d_y,
                                  const void *x, const void *weight, const float *inv_rms, const void *d_residual,
                                  void *d_x, float *d_weight, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- Norm and rotation of queries and keys --------------------------------
+ *
+ * In front of the recurrence (or of any attention): for every token and head
+ * of q (tokens, heads_q, head_dim) and k (tokens, heads_k, head_dim)
+ *   h = x * inv * weight,  inv = 1 / sqrt(mean(x^2) + eps)   (inv = 1 with norm = 0)
+ * and the first rotary_dim columns of h turned in pairs, pair i (i < rotary_dim / 2)
+ * by the angle a = positions[axis_of[i]][token] * inv_freq[i]:
+ *   (y0, y1) = (h0 cos a - h1 sin a, h1 cos a + h0 sin a)
+ * where a pair is columns (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with
+ * interleaved; the other columns pass.  Several axes (time, height, width)
+ * have a row of positions each.  The angle is the exact product of its int32
+ * and fp32 factors to within 1e-6, at any position; arithmetic is in fp32 and
+ * rounded to nearest once, on store.  An axis_of entry outside [0, axes) counts
+ * as the nearest that is inside.  NaN and infinities stay in their heads (a
+ * norm spreads them over the head).
+ *
+ * q and k may be views of one projection's output: q_stride and k_stride count
+ * elements from token to token (at least heads * head_dim; a token's heads lie
+ * one after the other), and tensors need the alignment of their elements only. */
+typedef struct {
+    int64_t tokens;
+    int32_t heads_q, heads_k;   /* heads_q >= 1, heads_k >= 0, 65,536 at most */
+    int32_t head_dim;           /* 2 to 256 */
+    int32_t rotary_dim;         /* even, 2 to head_dim */
+    int32_t axes;               /* 1 to 4 */
+    int32_t interleaved;        /* 1: pairs of neighbours */
+    int32_t norm;               /* 0: no norm (weights still apply) */
+    int32_t dtype;              /* of q, k and the results: F32, F16 or BF16 */
+    int32_t weight_dtype;       /* dtype or F32 */
+    float eps;
+    int64_t q_stride, k_stride;
+    const void *q, *k;          /* k: NULL iff heads_k = 0 */
+    const void *q_weight, *k_weight; /* (head_dim), each or NULL for ones */
+    const int32_t *positions;   /* (axes, tokens) */
+    const float *inv_freq;      /* (rotary_dim / 2) */
+    const int32_t *axis_of;     /* (rotary_dim / 2), or NULL: every pair on axis 0 */
+} gdr_rotary;
+
+/* Results with token strides of their own.  A result may be its input's buffer
+ * with the same stride (in place); no other overlap with an input or the other
+ * result is accepted (rows of one buffer whose columns are disjoint are no
+ * overlap, given equal strides). */
+gdr_status gdr_qk_rotary(const gdr_rotary *rotary, void *q_out, int64_t q_out_stride, void *k_out,
+                         int64_t k_out_stride, void *stream);
+
+/* Gradients of gdr_qk_rotary, whose arguments `rotary` holds (nothing of that
+ * call is kept).  d_q_out (tokens, heads_q, head_dim) and d_k_out, the results'
+ * gradients, have no gaps; d_q and d_k have token strides.
+ *   g = d_out with its pairs turned back, t = weight * g, n = x * inv:
+ *   d_x = inv * (t - n * mean(t * n))   (t without the norm)
+ *   d_weight = sum over tokens and heads of g * n  (fp32, in a fixed order;
+ *              non-NULL iff the weight is)
+ * No output may overlap an input, the workspace or another output.
+ * `workspace`: gdr_qk_rotary_backward_workspace_size bytes, 16-byte aligned. */
+gdr_status gdr_qk_rotary_backward_workspace_size(const gdr_rotary *rotary, size_t *bytes);
+gdr_status gdr_qk_rotary_backward(const gdr_rotary *rotary, const void *d_q_out, const void *d_k_out, void *d_q,
+                                  int64_t d_q_stride, void *d_k, int64_t d_k_stride, float *d_q_weight,
+                                  float *d_k_weight, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- A state cache in 16 or 8 bits -----------------------------------------
+ *
+ * The slab of states (num_slots, HV, dv, dk) held in fp16, in bf16, or in e4m3
+ * with a power of two for each row (slot, head, value channel): `scale` holds
+ * its exponent plus 127 in a byte, (num_slots, HV, dv), and the values are in
+ * its units.  The exponent is the least with max |row| <= 448 * 2^exponent, but
+ * not below -100 (a row of zeros has that).  Values are rounded to nearest
+ * even whenever a state is written.  fp16 holds magnitudes up to 65,504 (more
+ * becomes an infinity); in e4m3 an infinity becomes NaN, a NaN stays in its
+ * place, and what rounds to 2^128 (above 1.9375 * 2^127) reads as an infinity.  Each call that updates a state rounds it anew, by up to 2^-11 (fp16),
+ * 2^-8 (bf16) or 2^-4 (e4m3) of a value; a decay a per token lets the errors of
+ * about 1 / (1 - a^2) calls stand side by side, so 8 bits suit parked states
+ * and heads that forget, 16 bits any decoding.
+ * data and states are 16-byte aligned, slab, slot ids and their contract as in
+ * gdr_forward. */
+typedef struct {
+    void *data;                 /* (num_slots, HV, dv, dk) */
+    uint8_t *scale;             /* non-NULL iff dtype is GDR_E4M3 */
+    int32_t dtype;              /* GDR_F16, GDR_BF16 or GDR_E4M3 */
+} gdr_packed_slab;
+
+/* Write states (batch, heads, dv, dk) fp32 into the slab's rows slot_ids[b], or
+ * read those rows back.  A slot id out of range is skipped, and its states read as
+ * zeros. */
+gdr_status gdr_state_pack(int32_t batch, int32_t heads, int32_t dv, int32_t dk, int32_t num_slots,
+                          const float *states, const int32_t *slot_ids, const gdr_packed_slab *slab, void *stream);
+gdr_status gdr_state_unpack(int32_t batch, int32_t heads, int32_t dv, int32_t dk, int32_t num_slots,
+                            const gdr_packed_slab *slab, const int32_t *slot_ids, float *states, void *stream);
+
+/* gdr_forward on a packed slab, updated in place: problem->num_slots is the
+ * slab's, tensors->slot_ids is required, tensors->initial_state and final_state
+ * are NULL.  The states are read, updated in fp32 over all tokens of their
+ * request and rounded once, on the way back; a request without tokens leaves
+ * its states as they are.  Few tokens a request (8 on average, with dk 64, 128
+ * or 256) run in one pass over the packed states, without workspace; everything
+ * else runs gdr_forward's kernels on fp32 states in the workspace. */
+gdr_status gdr_packed_workspace_size(const gdr_problem *problem, size_t *bytes);
+gdr_status gdr_forward_packed(const gdr_problem *problem, const gdr_tensors *tensors, const gdr_packed_slab *slab,
+                              void *workspace, size_t workspace_bytes, void *stream);
 
 /* Memory-traffic floor of a decode step over a state slab: a measurement
  * aid beside the operation, which computes nothing of it.  Multiplies in place
