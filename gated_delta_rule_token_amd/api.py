@@ -108,6 +108,8 @@ def library_path() -> str:
 def load_library():
     """Open libgdr.so (once).  Raises GDRError when it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -194,7 +196,8 @@ def _enqueue(fn, dev, *args):
     """Call a library function on torch's current stream of ``dev``, with that
     device current (a launch needs its stream's device to be)."""
     if dev.index == torch.cuda.current_device():
-        check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+        # the stream's handle without the Stream object, whose making takes 1.9 of a small call's 10 us
+        check(fn(*args, torch._C._cuda_getCurrentRawStream(dev.index)))
     else:
         with torch.cuda.device(dev):
             check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
@@ -224,6 +227,19 @@ def _need(t, name, dtype=None, device=None):
     if dtype is not None and t.dtype != dtype:
         raise GDRError("GDR_E_INVALID", "%s must be %s, got %s" % (name, dtype, t.dtype))
     return t
+
+
+def _fits(t, name, dtype, dev, shape):
+    """``t`` has this dtype, device and shape, and no gaps."""
+    try:
+        if t.shape == shape and t.dtype == dtype and t.device == dev and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    if t is None:
+        raise GDRError("GDR_E_INVALID", "%s is required" % name)
+    _need(t, name, dtype, dev)
+    raise GDRError("GDR_E_INVALID", "%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
 
 
 def _int32(value, name):
@@ -717,82 +733,87 @@ def _token_stride(t, name, dtype, dev, lead, dim):
     if t.dtype != dtype:
         raise GDRError("GDR_E_INVALID", "%s must be %s, got %s" % (name, dtype, t.dtype))
     shape = t.shape
-    if tuple(shape[:-2]) != lead or shape[-1] != dim:
-        raise GDRError("GDR_E_INVALID", "%s has shape %s, expected %s + (heads, %d)" % (name, tuple(shape), lead, dim))
-    st, heads = t.stride(), shape[-2]
+    if shape[:-2] != lead or shape[-1] != dim:
+        raise GDRError("GDR_E_INVALID", "%s has shape %s, expected %s + (heads, %d)" % (name, tuple(shape), tuple(lead), dim))
+    heads = shape[-2]
+    if t.is_contiguous():
+        return heads * dim
+    st = t.stride()
     token = st[-3] if shape[-3] > 1 else heads * dim
-    if len(lead) == 2 and shape[-3] == 1:
-        token = st[0] if shape[0] > 1 else token
-    ok = st[-1] == 1 and (heads <= 1 or st[-2] == dim)
+    if len(lead) == 2 and shape[-3] == 1 and shape[0] > 1:
+        token = st[0]
+    ok = st[-1] == 1 and (heads == 1 or st[-2] == dim)
     if len(lead) == 2 and shape[0] > 1 and shape[-3] > 1:
         ok = ok and st[0] == shape[-3] * token
-    if t.numel() and not ok:
+    if not ok:
         raise GDRError("GDR_E_INVALID", "%s has strides %s: a token's heads must lie one after the other, and tokens be "
                        "evenly apart" % (name, tuple(st)))
-    return max(token, heads * dim) if t.numel() == 0 else token
+    return token
 
 
 def _rotary_arguments(q, k, positions, inv_freq, axes, q_weight, k_weight, eps, interleaved, norm):
     if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
         raise GDRError("GDR_E_INVALID", "q must be a tensor (T, H, d) or (B, L, H, d)")
-    dev, lead, dim = q.device, tuple(q.shape[:-2]), q.shape[-1]
-    code = _dtype_code(q.dtype)
-    q_stride = _token_stride(q, "q", q.dtype, dev, lead, dim)
-    k_stride = 0 if k is None else _token_stride(k, "k", q.dtype, dev, lead, dim)
-    _need(positions, "positions", torch.int32, dev)
-    _need(inv_freq, "inv_freq", torch.float32, dev)
-    _need(axes, "axes", torch.int32, dev)
+    dev, act, shape = q.device, q.dtype, q.shape
+    lead, heads, dim = shape[:-2], shape[-2], shape[-1]
+    code = _dtype_code(act)
+    q_stride = _token_stride(q, "q", act, dev, lead, dim)
+    k_heads = k_stride = 0
+    if k is not None:
+        k_stride, k_heads = _token_stride(k, "k", act, dev, lead, dim), k.shape[-2]
     if positions is None or inv_freq is None:
         raise GDRError("GDR_E_INVALID", "positions and inv_freq are required")
-    shape = tuple(positions.shape)
-    if shape != lead and shape[1:] != lead:
-        raise GDRError("GDR_E_INVALID", "positions has shape %s, expected %s or (axes,) + %s" % (shape, lead, lead))
-    n_axes = 1 if shape == lead else shape[0]
+    _need(positions, "positions", torch.int32, dev)
+    _need(inv_freq, "inv_freq", torch.float32, dev)
+    at = positions.shape
+    n_axes = 1
+    if at != lead:
+        if at[1:] != lead:
+            raise GDRError("GDR_E_INVALID", "positions has shape %s, expected %s or (axes,) + %s"
+                           % (tuple(at), tuple(lead), tuple(lead)))
+        n_axes = at[0]
     if inv_freq.dim() != 1:
         raise GDRError("GDR_E_INVALID", "inv_freq must have one axis")
     half = inv_freq.shape[0]
-    if axes is not None and tuple(axes.shape) != (half,):
-        raise GDRError("GDR_E_INVALID", "axes has shape %s, expected %s" % (tuple(axes.shape), (half,)))
-    if axes is None and n_axes > 1:
+    if axes is not None:
+        _fits(axes, "axes", torch.int32, dev, (half,))
+    elif n_axes > 1:
         raise GDRError("GDR_E_INVALID", "positions of several axes need axes (an axis for each pair)")
-    weight_code = code
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is None:
-            continue
-        if tuple(_need(w, name, None, dev).shape) != (dim,):
-            raise GDRError("GDR_E_INVALID", "%s has shape %s, expected %s" % (name, tuple(w.shape), (dim,)))
-        weight_code = _dtype_code(w.dtype)
-    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
-        raise GDRError("GDR_E_INVALID", "q_weight and k_weight must have one dtype")
-    if k_weight is not None and k is None:
-        raise GDRError("GDR_E_INVALID", "k_weight given without k")
-    tokens = 1
-    for n in lead:
-        tokens *= n
-    return RotaryArguments(
-        tokens, _int32(q.shape[-2], "q's heads"), 0 if k is None else _int32(k.shape[-2], "k's heads"),
-        _int32(dim, "the last axis of q"), 2 * _int32(half, "inv_freq's length") if half < 2 ** 30 else -1,
-        _int32(n_axes, "the axes"), int(bool(interleaved)), int(bool(norm)), code, weight_code, float(eps), q_stride,
-        k_stride, _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq), _ptr(axes))
+    weight = code
+    if q_weight is not None:
+        weight = _dtype_code(q_weight.dtype)
+        _fits(q_weight, "q_weight", q_weight.dtype, dev, (dim,))
+    if k_weight is not None:
+        if k is None:
+            raise GDRError("GDR_E_INVALID", "k_weight given without k")
+        if q_weight is not None and q_weight.dtype != k_weight.dtype:
+            raise GDRError("GDR_E_INVALID", "q_weight and k_weight must have one dtype")
+        weight = _dtype_code(k_weight.dtype)
+        _fits(k_weight, "k_weight", k_weight.dtype, dev, (dim,))
+    tokens = lead[0] if len(lead) == 1 else lead[0] * lead[1]
+    for value in (heads, k_heads, dim, 2 * half, n_axes):
+        if value >= 2 ** 31:
+            raise GDRError("GDR_E_INVALID", "a size (%d) does not fit in 32 bits" % value)
+    return RotaryArguments(tokens, heads, k_heads, dim, 2 * half, n_axes, 1 if interleaved else 0, 1 if norm else 0, code,
+                           weight, eps, q_stride, k_stride, q.data_ptr(), _ptr(k), _ptr(q_weight), _ptr(k_weight),
+                           positions.data_ptr(), inv_freq.data_ptr(), _ptr(axes))
 
 
-def _rotary_out(out, q, k, what):
-    """The (q, k) tensors that a call writes, and their token strides."""
+def _rotary_out(out, q, k):
+    """The tensors for q and k that a call writes, each with its token stride."""
     if out is None:
-        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device),
-               None if k is None else torch.empty(k.shape, dtype=q.dtype, device=q.device))
-    oq, ok = out[0], out[1]
-    if (ok is None) != (k is None):
-        raise GDRError("GDR_E_INVALID", "%s needs a tensor for k exactly when the call has one" % what)
-    strides = []
-    for t, like, name in ((oq, q, "q"), (ok, k, "k")):
-        if like is None:
-            strides.append(0)
-            continue
-        strides.append(_token_stride(t, "%s of %s" % (what, name), q.dtype, q.device, tuple(q.shape[:-2]), q.shape[-1]))
-        if t.shape != like.shape:
-            raise GDRError("GDR_E_INVALID", "%s of %s must have its shape" % (what, name))
-    return oq, ok, strides
+        oq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k is None:
+            return oq, q.shape[-2] * q.shape[-1], None, 0
+        return oq, q.shape[-2] * q.shape[-1], torch.empty(k.shape, dtype=q.dtype, device=q.device), k.shape[-2] * k.shape[-1]
+    found = []
+    for t, like, name in ((out[0], q, "out of q"), (out[1], k, "out of k")):
+        if (t is None) != (like is None):
+            raise GDRError("GDR_E_INVALID", "%s must be given exactly when the call has it" % name)
+        found += [t, 0 if t is None else _token_stride(t, name, q.dtype, q.device, q.shape[:-2], q.shape[-1])]
+        if t is not None and t.shape != like.shape:
+            raise GDRError("GDR_E_INVALID", "%s must have its shape" % name)
+    return found
 
 
 def qk_rotary(q, k, positions, inv_freq, *, axes=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
@@ -814,8 +835,8 @@ def qk_rotary(q, k, positions, inv_freq, *, axes=None, q_weight=None, k_weight=N
     takes them."""
     lib = load_library()
     r = _rotary_arguments(q, k, positions, inv_freq, axes, q_weight, k_weight, eps, interleaved, norm)
-    oq, ok, strides = _rotary_out(out, q, k, "out")
-    _enqueue(lib.gdr_qk_rotary, q.device, ctypes.byref(r), _ptr(oq), strides[0], _ptr(ok), strides[1])
+    oq, q_stride, ok, k_stride = _rotary_out(out, q, k)
+    _enqueue(lib.gdr_qk_rotary, q.device, ctypes.byref(r), oq.data_ptr(), q_stride, _ptr(ok), k_stride)
     return RotaryOutput(oq, ok)
 
 
@@ -830,21 +851,21 @@ def qk_rotary_backward(d_q_out, d_k_out, q, k, positions, inv_freq, *, axes=None
     lib = load_library()
     r = _rotary_arguments(q, k, positions, inv_freq, axes, q_weight, k_weight, eps, interleaved, norm)
     dev = q.device
-    for name, d, like in (("d_q_out", d_q_out, q), ("d_k_out", d_k_out, k)):
-        if (d is None) != (like is None):
-            raise GDRError("GDR_E_INVALID", "d_q_out is required, and d_k_out exactly with k")
-        if d is not None and _need(d, name, q.dtype, dev).shape != like.shape:
-            raise GDRError("GDR_E_INVALID", "%s has shape %s, expected %s" % (name, tuple(d.shape), tuple(like.shape)))
-    dq, dk, strides = _rotary_out(out, q, k, "out")
+    _fits(d_q_out, "d_q_out", q.dtype, dev, q.shape)
+    if k is not None:
+        _fits(d_k_out, "d_k_out", q.dtype, dev, k.shape)
+    elif d_k_out is not None:
+        raise GDRError("GDR_E_INVALID", "d_k_out given without k")
+    dq, q_stride, dk, k_stride = _rotary_out(out, q, k)
     dqw = None if q_weight is None else torch.empty(q.shape[-1], dtype=torch.float32, device=dev)
     dkw = None if k_weight is None else torch.empty(q.shape[-1], dtype=torch.float32, device=dev)
-    n = ctypes.c_size_t(0)
-    check(lib.gdr_qk_rotary_backward_workspace_size(ctypes.byref(r), ctypes.byref(n)))
-    if workspace is None and n.value:
+    if workspace is None and (dqw is not None or dkw is not None):
+        n = ctypes.c_size_t(0)
+        check(lib.gdr_qk_rotary_backward_workspace_size(ctypes.byref(r), ctypes.byref(n)))
         workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
     _need(workspace, "workspace", device=dev)
-    _enqueue(lib.gdr_qk_rotary_backward, dev, ctypes.byref(r), _ptr(d_q_out), _ptr(d_k_out), _ptr(dq), strides[0],
-             _ptr(dk), strides[1], _ptr(dqw), _ptr(dkw), _ptr(workspace),
+    _enqueue(lib.gdr_qk_rotary_backward, dev, ctypes.byref(r), d_q_out.data_ptr(), _ptr(d_k_out), dq.data_ptr(), q_stride,
+             _ptr(dk), k_stride, _ptr(dqw), _ptr(dkw), _ptr(workspace),
              0 if workspace is None else workspace.numel() * workspace.element_size())
     return RotaryGradients(dq, dk, dqw, dkw)
 
@@ -880,16 +901,24 @@ def _slab_pointers(slab, dev):
                        "float8_e4m3fn, got %s %s" % (tuple(data.shape), data.dtype))
     if (scale is not None) != (code == E4M3):
         raise GDRError("GDR_E_INVALID", "a slab has scales exactly with float8_e4m3fn")
-    if scale is not None and _need(scale, "slab.scale", torch.float8_e8m0fnu, dev).shape != data.shape[:3]:
-        raise GDRError("GDR_E_INVALID", "slab.scale has shape %s, expected %s" % (tuple(scale.shape), tuple(data.shape[:3])))
-    return SlabPointers(data.data_ptr(), _ptr(scale), code)
+    if scale is None:
+        return SlabPointers(data.data_ptr(), None, code)
+    _fits(scale, "slab.scale", torch.float8_e8m0fnu, dev, data.shape[:3])
+    return SlabPointers(data.data_ptr(), scale.data_ptr(), code)
 
 
-def _slots(slot_ids, dev):
+def _slab_call(slab, slot_ids):
+    """Device, C struct and sizes of a call that writes or reads a slab's rows."""
+    dev = slab.data.device
+    p = _slab_pointers(slab, dev)
     _need(slot_ids, "slot_ids", torch.int32, dev)
     if slot_ids is None or slot_ids.dim() != 1:
         raise GDRError("GDR_E_INVALID", "slot_ids must be (B,) int32")
-    return _int32(slot_ids.shape[0], "the batch")
+    slots, HV, dv, dk = slab.data.shape
+    sizes = (slot_ids.shape[0], HV, dv, dk, slots)
+    if max(sizes) >= 2 ** 31:
+        raise GDRError("GDR_E_INVALID", "a size of %s does not fit in 32 bits" % (sizes,))
+    return dev, p, sizes
 
 
 def state_pack(states, slab, slot_ids) -> None:
@@ -897,28 +926,21 @@ def state_pack(states, slab, slot_ids) -> None:
     of a ``PackedSlab``, rounded to nearest even (in 8 bits: in units of a power
     of two for each row).  Out-of-range ids are skipped."""
     lib = load_library()
-    dev = slab.data.device
-    p = _slab_pointers(slab, dev)
-    B, (slots, HV, dv, dk) = _slots(slot_ids, dev), slab.data.shape
-    if states is None or tuple(_need(states, "states", torch.float32, dev).shape) != (B, HV, dv, dk):
-        raise GDRError("GDR_E_INVALID", "states must be %s" % ((B, HV, dv, dk),))
-    _enqueue(lib.gdr_state_pack, dev, B, _int32(HV, "HV"), dv, dk, _int32(slots, "num_slots"), _ptr(states),
-             _ptr(slot_ids), ctypes.byref(p))
+    dev, p, sizes = _slab_call(slab, slot_ids)
+    _fits(states, "states", torch.float32, dev, sizes[:4])
+    _enqueue(lib.gdr_state_pack, dev, *sizes, states.data_ptr(), slot_ids.data_ptr(), ctypes.byref(p))
 
 
 def state_unpack(slab, slot_ids, out=None):
     """The states (B,HV,dv,dk) fp32 that the rows ``slot_ids`` of a
     ``PackedSlab`` hold, in ``out`` when given; zeros for out-of-range ids."""
     lib = load_library()
-    dev = slab.data.device
-    p = _slab_pointers(slab, dev)
-    B, (slots, HV, dv, dk) = _slots(slot_ids, dev), slab.data.shape
+    dev, p, sizes = _slab_call(slab, slot_ids)
     if out is None:
-        out = torch.empty((B, HV, dv, dk), dtype=torch.float32, device=dev)
-    elif tuple(_need(out, "out", torch.float32, dev).shape) != (B, HV, dv, dk):
-        raise GDRError("GDR_E_INVALID", "out must be %s" % ((B, HV, dv, dk),))
-    _enqueue(lib.gdr_state_unpack, dev, B, _int32(HV, "HV"), dv, dk, _int32(slots, "num_slots"), ctypes.byref(p),
-             _ptr(slot_ids), _ptr(out))
+        out = torch.empty(sizes[:4], dtype=torch.float32, device=dev)
+    else:
+        _fits(out, "out", torch.float32, dev, sizes[:4])
+    _enqueue(lib.gdr_state_unpack, dev, *sizes, ctypes.byref(p), slot_ids.data_ptr(), out.data_ptr())
     return out
 
 
@@ -939,36 +961,55 @@ def forward_packed(q, k, v, *, slab, slot_ids, gate=None, beta=None, erase=None,
     ``packed_workspace_size`` bytes, which calls of more than 8 tokens a request
     need (allocated here when not given).  Returns o."""
     lib = load_library()
-    dev = q.device
+    dev, act, f32, i32 = q.device, q.dtype, torch.float32, torch.int32
     s = _slab_pointers(slab, dev)
-    _need(q, "q", device=dev)
-    act, f32, i32 = q.dtype, torch.float32, torch.int32
-    for name, t, dt in (("k", k, act), ("v", v, act), ("gate", gate, None), ("beta", beta, f32), ("erase", erase, f32),
-                        ("a_log", a_log, f32), ("dt_bias", dt_bias, f32), ("gate_scale", gate_scale, f32),
-                        ("cu_seqlens", cu_seqlens, i32), ("seq_lens", seq_lens, i32), ("slot_ids", slot_ids, i32),
-                        ("out", out, act)):
-        _need(t, name, dt, dev)
-    if k is None or v is None or slot_ids is None or q.dim() not in (3, 4) or v.dim() != q.dim():
+    if not isinstance(v, torch.Tensor) or q.dim() not in (3, 4) or v.dim() != q.dim() or slot_ids is None:
         raise GDRError("GDR_E_INVALID", "q, k, v of three or four axes and slot_ids are required")
-    p = build_problem(q, k, v, gate=gate, beta=beta, erase=erase, a_log=a_log, dt_bias=dt_bias, cu_seqlens=cu_seqlens,
-                      slot_ids=slot_ids, state=slab.data, update_rule=update_rule, gate_activation=gate_activation,
-                      beta_activation=beta_activation, qk_l2_norm=qk_l2_norm, scale=scale, chunk_size=chunk_size,
-                      algo=algo, gate_scale=gate_scale, seq_lens=seq_lens, scan_segments=scan_segments)
-    lead = tuple(q.shape[:-2])
+    lead, (H, dk), (HV, dv), slots = q.shape[:-2], q.shape[-2:], v.shape[-2:], slab.data.shape[0]
+    rank4 = len(lead) == 2
+    if rank4:
+        B, L = lead
+        T = B * L
+    else:
+        T = lead[0]
+        B = slot_ids.shape[0] if cu_seqlens is None else cu_seqlens.shape[0] - 1
+        L = T // B if cu_seqlens is None and B > 0 else 0
+    per_key = gate is not None and gate.dim() == len(lead) + 2
+    per_token = beta is not None and HV > 1 and beta.shape[-1] == 1
+    key = (dk,) if per_key else ()
+    if max(T, B, H, HV, dk, dv, slots, chunk_size, scan_segments) >= 2 ** 31 or min(chunk_size, scan_segments) < 0:
+        raise GDRError("GDR_E_INVALID", "a size does not fit in 32 bits, or is negative")
+    if slab.data.shape != (slots, HV, dv, dk):
+        raise GDRError("GDR_E_INVALID", "the slab's state has shape %s, expected (num_slots,) + %s" % (tuple(slab.data.shape), (HV, dv, dk)))
     if out is None:
-        out = torch.empty(lead + tuple(v.shape[-2:]), dtype=act, device=dev)
-    check_shapes(p, lead, _shapes(q=q, k=k, v=v, out=out, gate=gate, beta=beta, erase=erase, a_log=a_log,
-                                  gate_scale=gate_scale, dt_bias=dt_bias, cu_seqlens=cu_seqlens, seq_lens=seq_lens,
-                                  slot_ids=slot_ids, state=slab.data))
-    need = packed_workspace_size(p)
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        out = torch.empty(lead + (HV, dv), dtype=act, device=dev)
+    _fits(q, "q", act, dev, lead + (H, dk))
+    _fits(k, "k", act, dev, lead + (H, dk))
+    _fits(v, "v", act, dev, lead + (HV, dv))
+    _fits(out, "out", act, dev, lead + (HV, dv))
+    _fits(slot_ids, "slot_ids", i32, dev, (B,))
+    for name, t, dtype, shape in (("gate", gate, None, lead + (HV,) + key), ("beta", beta, f32, lead + (1 if per_token else HV,)),
+                                  ("erase", erase, f32, lead + (HV, dk)), ("a_log", a_log, f32, (HV,)),
+                                  ("gate_scale", gate_scale, f32, (HV,)), ("dt_bias", dt_bias, f32, (HV,) + key),
+                                  ("cu_seqlens", cu_seqlens, i32, (B + 1,)), ("seq_lens", seq_lens, i32, (B,))):
+        if t is not None:
+            _fits(t, name, dtype or t.dtype, dev, shape)
+    p = Problem(T, B, L, H, HV, dk, dv, slots, _dtype_code(act), F32 if gate is None else _dtype_code(gate.dtype),
+                RULES[update_rule], GATES[gate_activation], BETAS[beta_activation], 1 if qk_l2_norm else 0, int(per_key),
+                int(rank4), chunk_size, ALGOS[algo], 0, int(per_token), scale, scan_segments)
+    t = Tensors(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(gate), _ptr(beta), _ptr(erase), _ptr(a_log),
+                _ptr(dt_bias), _ptr(cu_seqlens), slot_ids.data_ptr(), None, None, _ptr(gate_scale), _ptr(seq_lens))
     _need(workspace, "workspace", device=dev)
-    t = Tensors(q=_ptr(q), k=_ptr(k), v=_ptr(v), o=_ptr(out), gate=_ptr(gate), beta=_ptr(beta), erase=_ptr(erase),
-                a_log=_ptr(a_log), dt_bias=_ptr(dt_bias), cu_seqlens=_ptr(cu_seqlens), slot_ids=_ptr(slot_ids),
-                gate_scale=_ptr(gate_scale), seq_lens=_ptr(seq_lens))
-    _enqueue(lib.gdr_forward_packed, dev, ctypes.byref(p), ctypes.byref(t), ctypes.byref(s), _ptr(workspace),
-             0 if workspace is None else workspace.numel() * workspace.element_size())
+    for size in (0 if workspace is None else workspace.numel() * workspace.element_size(), None):
+        if size is None:  # asked for only when the call turned out to need one: few tokens a request do not
+            size = packed_workspace_size(p)
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        try:
+            _enqueue(lib.gdr_forward_packed, dev, ctypes.byref(p), ctypes.byref(t), ctypes.byref(s), _ptr(workspace), size)
+            break
+        except GDRError as e:
+            if e.status != "GDR_E_WORKSPACE" or workspace is not None:
+                raise
     return out
 
 

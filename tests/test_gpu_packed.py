@@ -445,8 +445,8 @@ def test_refusals_on_the_gpu():
                        ("overlaps", dict(out=d["v"]))):
         with pytest.raises(api.GDRError, match=text):
             api.forward_packed(*qkv, slab=slab, **dict(args, **over))
-    for text, states in (("states must be", torch.zeros(2, 4, 128, 64, device="cuda")), ("states must be", torch.zeros(2, 4, 128, 128, device="cuda").half())):
+    for text, states in (("states has shape", torch.zeros(2, 4, 128, 64, device="cuda")), ("states must be", torch.zeros(2, 4, 128, 128, device="cuda").half())):
         with pytest.raises(api.GDRError, match=text):
             api.state_pack(states, slab, args["slot_ids"])
-    with pytest.raises(api.GDRError, match="out must be"):
+    with pytest.raises(api.GDRError, match="out has shape"):
         api.state_unpack(slab, args["slot_ids"], out=torch.zeros(1, 4, 128, 128, device="cuda"))
