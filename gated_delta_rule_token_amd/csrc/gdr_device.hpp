@@ -86,10 +86,11 @@ __device__ __forceinline__ void lds_barrier()
 }
 
 // ---------------------------------------------------------------- gate math (fp32)
-// softplus(x) = log(1 + e^x), evaluated without overflow on either side.
+// softplus(x) = log(1 + e^x), evaluated without overflow on either side (and
+// without a branch, both sides of which a wave would run).
 __device__ __forceinline__ float softplus_f32(float x)
 {
-    return x > 0.f ? x + log1pf(expf(-x)) : log1pf(expf(x));
+    return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));
 }
 
 __device__ __forceinline__ float sigmoid_f32(float x) { return 1.f / (1.f + expf(-x)); }

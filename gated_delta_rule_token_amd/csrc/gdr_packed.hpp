@@ -16,6 +16,9 @@
 
 #include "gdr_packed_launch.hpp"
 
+#include <type_traits>
+#include <utility>
+
 namespace gdr {
 
 typedef uint32_t w4 __attribute__((ext_vector_type(4)));
@@ -81,29 +84,47 @@ __device__ __forceinline__ float row_reduce(float x, Op op)
 template <int TYPE> struct CacheType { using T = half_t; };
 template <> struct CacheType<CACHE_BF16> { using T = bf16_t; };
 
-// A workgroup (4 waves) holds packed_step_rows(DK) rows of one (request, value
-// head) state.  LANES lanes hold a row, 16 values each: with e4m3 16
-// neighbouring bytes, with 16 bits 8 values of each half of the row, so that
-// every access is a 16-byte vector and a wave's vectors are contiguous.
-template <typename TA, int TYPE, int DK, bool VD>
-__global__ __launch_bounds__(256) void k_packed_step(const PackedParams a, int rule, int per_key)
+// ---------------------------------------------------------------- any tokens, on the vector units
+// LANES lanes hold a row, 16 values each: with e4m3 16 neighbouring bytes, with
+// 16 bits 8 values of each half of the row, so that every access is a 16-byte
+// vector and a wave's vectors are contiguous.  A wave holds G times 64 / LANES
+// rows.  With single tokens (ONE) each row group is widened, stepped and rounded
+// by itself, so few registers are live beside the packed values; more tokens
+// keep all groups in fp32 between them.
+// Bound by memory for single tokens (256 requests x 32 heads of 128): 8 bits
+// 60 us for 283 MB, 16 bits 96 us for 547 MB.  Waves and rows, in us for 8 and
+// 16 bits: 2 waves of 64 rows 60 and 109, 4 of 32 rows 63 and 104, 4 of 16 rows
+// 73 and 96; as the form for more tokens 68 and 102.
+template <int TYPE, int DK, bool ONE> struct StepForm {
+    static constexpr bool EIGHT = TYPE == CACHE_E4M3;
+    static constexpr int WAVES = ONE && EIGHT ? 2 : 4;
+    static constexpr int ROWS = DK == 128 && (EIGHT || !ONE) ? 128 : 64;  // of a workgroup
+};
+
+// Requests of fewer than `least` tokens are left alone.
+template <typename TA, int TYPE, int DK, bool VD, bool ONE>
+__global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packed_step(const PackedParams a, int rule,
+                                                                                       int per_key, int least)
 {
+    using Form = StepForm<TYPE, DK, ONE>;
     constexpr bool EIGHT = TYPE == CACHE_E4M3;
     using TC = typename CacheType<TYPE>::T;
-    constexpr int C = 16, LANES = DK / C, RPW = 64 / LANES, G = packed_step_rows(DK) / (4 * RPW), V = EIGHT ? 1 : 2;
+    constexpr int C = 16, LANES = DK / C, RPW = 64 / LANES, G = Form::ROWS / (Form::WAVES * RPW), V = EIGHT ? 1 : 2;
+    constexpr int ROW = DK * (EIGHT ? 1 : 2);  // bytes
     const Params &p = a.p;
-    const int parts = (p.dv + packed_step_rows(DK) - 1) / packed_step_rows(DK);
+    const int parts = (p.dv + Form::ROWS - 1) / Form::ROWS;
     const int part = blockIdx.x % parts, h = (blockIdx.x / parts) % p.HV, b = blockIdx.x / (parts * p.HV);
     const int slot = p.slot_ids[b];
     if (slot < 0 || slot >= p.num_slots) return;
     int64_t s, e;
     request_range(p, b, s, e);
-    if (e <= s) return;  // the states stay as they are, to the bit
+    if (e - s < least) return;  // without tokens the states stay as they are, to the bit
     const int lane = threadIdx.x & 63, l = lane % LANES, r = lane / LANES, wave = threadIdx.x >> 6;
-    const int row0 = part * packed_step_rows(DK) + wave * G * RPW + r;  // + RPW for each row group
+    const int row0 = part * Form::ROWS + wave * G * RPW + r;  // + RPW for each row group
     const int qh = (int)(((int64_t)h * p.H) / p.HV);
     const bool retrieves = rule_retrieves(rule), decays = rule_decays(rule), rate = rule_has_beta(rule);
     const auto column = [&](int c) { return EIGHT ? l * C + c : (c < 8 ? 0 : DK / 2) + l * 8 + c % 8; };
+    const auto add = [](float x, float y) { return x + y; };
     const TA *q = static_cast<const TA *>(p.q), *k = static_cast<const TA *>(p.k), *v = static_cast<const TA *>(p.v);
     TA *o = static_cast<TA *>(p.o);
 
@@ -134,7 +155,7 @@ __global__ __launch_bounds__(256) void k_packed_step(const PackedParams a, int r
             vw[g] = to_f32(v[(t * p.HV + h) * p.dv + (row < p.dv ? row : p.dv - 1)]);
         }
     };
-    fetch(s);
+    fetch(s);  // before the states, so that waiting for it does not wait for them
 
     const size_t head = ((size_t)slot * p.HV + h) * p.dv;
     w4 raw[G][V];
@@ -142,26 +163,48 @@ __global__ __launch_bounds__(256) void k_packed_step(const PackedParams a, int r
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         const int row = row0 + g * RPW, at = row < p.dv ? row : p.dv - 1;
-        const char *src = static_cast<const char *>(a.data) + (head + at) * DK * (EIGHT ? 1 : 2) + l * 16;
+        const char *src = static_cast<const char *>(a.data) + (head + at) * ROW + l * 16;
 #pragma unroll
         for (int n = 0; n < V; ++n) raw[g][n] = __builtin_nontemporal_load(reinterpret_cast<const w4 *>(src + n * DK));
         ex[g] = EIGHT ? a.scale[head + at] : 0;
     }
-    float S[G][C];
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
+    const auto widen = [&](int g, float (&S)[C]) {
         if constexpr (EIGHT) {
 #pragma unroll
-            for (int n = 0; n < 4; ++n) from_codes(raw[g][0][n], scale_of(ex[g]), &S[g][4 * n]);
+            for (int n = 0; n < 4; ++n) from_codes(raw[g][0][n], scale_of(ex[g]), &S[4 * n]);
         } else {
 #pragma unroll
-            for (int c = 0; c < C; ++c) S[g][c] = half_of<TC>(raw[g][c / 8][c % 8 / 2], c % 2);
+            for (int c = 0; c < C; ++c) S[c] = half_of<TC>(raw[g][c / 8][c % 8 / 2], c % 2);
         }
-    }
+    };
+    const auto put_back = [&](int g, const float (&S)[C]) {
+        const int row = row0 + g * RPW;
+        w4 out[V];
+        uint32_t eo = 0;
+        if constexpr (EIGHT) {
+            float top = 0.f;
+#pragma unroll
+            for (int c = 0; c < C; ++c) top = fmaxf(top, fabsf(S[c]));
+            eo = scale_byte(row_reduce<LANES>(top, [](float x, float y) { return fmaxf(x, y); }));
+#pragma unroll
+            for (int n = 0; n < 4; ++n) out[0][n] = to_codes(&S[4 * n], scale_of(eo));
+        } else {
+#pragma unroll
+            for (int c = 0; c < C; c += 2) out[c / 8][c % 8 / 2] = two_halves<TC>(S[c], S[c + 1]);
+        }
+        if (row >= p.dv) return;
+        char *dst = static_cast<char *>(a.data) + (head + row) * ROW + l * 16;
+#pragma unroll
+        for (int n = 0; n < V; ++n) __builtin_nontemporal_store(out[n], reinterpret_cast<w4 *>(dst + n * DK));
+        if (EIGHT && l == 0) a.scale[head + row] = (uint8_t)eo;
+    };
 
-    for (int64_t t = s; t < e; ++t) {
+    // One token: its vectors and scalars, then each row group's step.
+    float qv[C], kv[C], av[C], kb[C], vi[G], qk, alpha, bt;
+    const auto token = [&](int64_t t) {
         const size_t th = (size_t)t * p.HV + h;
-        float qv[C], kv[C], vi[G], qq = 0.f, kk = 0.f, qk = 0.f;
+        float qq = 0.f, kk = 0.f;
+        qk = 0.f;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             qv[c] = get8(qw[c / 8], c % 8);
@@ -172,8 +215,7 @@ __global__ __launch_bounds__(256) void k_packed_step(const PackedParams a, int r
         }
 #pragma unroll
         for (int g = 0; g < G; ++g) vi[g] = vw[g];
-        if (t + 1 < e) fetch(t + 1);
-        const auto add = [](float x, float y) { return x + y; };
+        if (!ONE && t + 1 < e) fetch(t + 1);
         qk = row_reduce<LANES>(qk, add);
         if (p.qk_l2_norm) {
             const float inq = 1.f / sqrtf(row_reduce<LANES>(qq, add) + 1e-12f);
@@ -185,10 +227,9 @@ __global__ __launch_bounds__(256) void k_packed_step(const PackedParams a, int r
                 kv[c] *= ink;
             }
         }
-        float alpha = 1.f, av[C], kb[C];  // decay: one, or for each key
-        if (decays && !per_key) alpha = expf(log_decay(p, th, h));
-        const float bt = rate ? update_rate(p, th) : 1.f;
-        if constexpr (VD) {
+        alpha = decays && !per_key ? expf(log_decay(p, th, h)) : 1.f;
+        bt = rate ? update_rate(p, th) : 1.f;
+        if constexpr (VD) {  // a decay for each key, or the erase gate
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 av[c] = per_key ? expf(log_decay_key(p, th, h, column(c))) : alpha;
@@ -196,61 +237,452 @@ __global__ __launch_bounds__(256) void k_packed_step(const PackedParams a, int r
                 qv[c] *= av[c];
             }
         }
+    };
+    const auto step = [&](int64_t t, int g, float (&S)[C]) {
+        float get = 0.f, u = 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            get = fmaf(S[c], VD ? kb[c] : kv[c], get);
+            u = fmaf(S[c], qv[c], u);
+        }
+        get = row_reduce<LANES>(get, add);
+        u = row_reduce<LANES>(u, add);
+        if constexpr (!VD) {
+            get *= alpha;
+            u *= alpha;
+        }
+        const float put = retrieves ? bt * (vi[g] - get) : vi[g];
+#pragma unroll
+        for (int c = 0; c < C; ++c) S[c] = fmaf(VD ? av[c] : alpha, S[c], put * kv[c]);
+        const int row = row0 + g * RPW;
+        if (l == 0 && row < p.dv) o[((size_t)t * p.HV + h) * p.dv + row] = from_f32<TA>(p.scale * (u + qk * put));
+    };
+    if constexpr (ONE) {
+        token(s);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            float get = 0.f, u = 0.f;
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                get = fmaf(S[g][c], VD ? kb[c] : kv[c], get);
-                u = fmaf(S[g][c], qv[c], u);
-            }
-            get = row_reduce<LANES>(get, add);
-            u = row_reduce<LANES>(u, add);
-            if constexpr (!VD) {
-                get *= alpha;
-                u *= alpha;
-            }
-            const float put = retrieves ? bt * (vi[g] - get) : vi[g];
-#pragma unroll
-            for (int c = 0; c < C; ++c) S[g][c] = fmaf(VD ? av[c] : alpha, S[g][c], put * kv[c]);
-            const int row = row0 + g * RPW;
-            if (l == 0 && row < p.dv) o[th * p.dv + row] = from_f32<TA>(p.scale * (u + qk * put));
+            float S[C];
+            widen(g, S);
+            step(s, g, S);
+            put_back(g, S);
         }
-    }
-
+    } else {
+        float S[G][C];
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-        const int row = row0 + g * RPW;
-        if constexpr (EIGHT) {
+        for (int g = 0; g < G; ++g) widen(g, S[g]);
+        for (int64_t t = s; t < e; ++t) {
+            token(t);
+#pragma unroll
+            for (int g = 0; g < G; ++g) step(t, g, S[g]);
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g) put_back(g, S[g]);
+    }
+}
+
+// ---------------------------------------------------------------- 1 to 8 tokens, on the matrix cores
+// A request's tokens together, for 16-bit activations and one decay a head.
+// With S the packed states, x_n the vectors k_0 .. k_7, q_0 .. q_7 and
+// a_t the decays, per row
+//   z_n = S . x_n for all 16 n                         (matrix product)
+//   for each token t:  z <- a_t z,  d_t = beta_t (v_t - z_t),  z <- z + d_t (k_t . x_n)
+// so that z_n is at every step the dot of x_n with the state of the moment, d_t
+// the new value that token t writes, and z of q_t after step t its output; then
+//   S <- (prod a) S + sum_t (prod of the later a) d_t k_t       (matrix product)
+// (the norms of q and k are factors of z and d).  So the states are read once
+// from registers, whatever the number of tokens: on the vector units each
+// token takes 3 operations a value, which at 4 tokens is 1.5 times the memory's
+// time.  256 requests x 32 heads of 128, vector units and this, in us: 16 bits
+// 2 tokens 115 and 104, 4 tokens 157 and 108 (562 MB), 7 tokens 237 and 116;
+// 8 bits, 4 tokens 143 and 76; but single tokens 60 and 67 in 8 bits, 96 and 102
+// in 16, which the vector units take where every request has one.
+//
+// Operands.  The states are an operand as they are: 16-bit values, or codes
+// as fp16 or bf16 (either holds every code), with the row's scale a factor of
+// z.  Vectors of the other 16-bit type go in as two planes, exact for fp16 in
+// bf16; bf16 in fp16 is scaled by a power of two that brings the largest to
+// [2^14, 2^15), where two planes hold 2^-39 of it.  d (fp32) goes into the
+// second product as bf16 planes: three, all 24 bits, beside a bf16 k; two (to
+// 2^-17, a sixty-fourth of fp16's rounding of the state) beside an fp16 k, which
+// takes two planes itself.  The planes share one product: its 32 inner places
+// hold 8 tokens of four plane pairs.
+//
+// A tile is 16 rows: lane (c, kb) of a wave holds row c, 8 keys of every 32 (with
+// codes 16 of 64) at the kb-th place, which is the first product's operand; the
+// second product is transposed (keys by rows), with the keys in the order that
+// gives each lane the values it holds.  So a row's 64-byte pieces lie with 4
+// lanes; whole 128-byte lines come from loading an even and an odd row's line
+// with 8 lanes each and exchanging pieces between lanes c and c ^ 1 (without it
+// 4 tokens on 16 bits take 129 us).
+typedef float f4v __attribute__((ext_vector_type(4)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+
+// Lane N's value, in each 16 neighbours.
+template <int N> __device__ __forceinline__ float lane_of(float x) { return dpp_mov<0x150 + N>(x); }
+
+__device__ __forceinline__ f4v mfma(h8 a, h8 b, f4v c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+__device__ __forceinline__ f4v mfma(b8 a, b8 b, f4v c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+template <typename T> struct Vec8;
+template <> struct Vec8<half_t> { using V = h8; };
+template <> struct Vec8<bf16_t> { using V = b8; };
+
+// Orders a wave's own LDS accesses: writes of other lanes before it, reads after.
+__device__ __forceinline__ void wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+template <typename F, int... I> __device__ __forceinline__ void each(F &&f, std::integer_sequence<int, I...>)
+{
+    (f(std::integral_constant<int, I>()), ...);
+}
+
+// Own row's two 64-byte pieces (of 16 bytes a lane) from the lines of an even
+// and of an odd row, and back: lanes c and c ^ 1 exchange one vector.
+__device__ __forceinline__ void exchange(w4 &x, w4 &y, bool odd)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t got = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(odd ? x[i] : y[i]), 0xB1, 0xF, 0xF, false);
+        x[i] = odd ? got : x[i];
+        y[i] = odd ? y[i] : got;
+    }
+}
+
+// A wave takes the tiles of 16 rows wave, wave + `waves`, ... of one state, by
+// itself (its LDS is its own), the next PRE of them on their way.  (At least two
+// waves a SIMD asked for: with one, products would accumulate in registers that
+// the vector units do not reach, 64 moves a tile.)
+template <typename TA, int TYPE, int DK, int PRE>
+__global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int rule, int waves)
+{
+    constexpr bool EIGHT = TYPE == CACHE_E4M3, BF = std::is_same<TA, bf16_t>::value;
+    constexpr int KS = DK / 32, NV = EIGHT ? KS / 2 : KS, T = 8, ROW = DK * (EIGHT ? 1 : 2);
+    using TC = typename std::conditional<EIGHT, TA, typename CacheType<TYPE>::T>::type;  // type of the dots' operands
+    constexpr bool SAME = std::is_same<TC, TA>::value;
+    using VA = typename Vec8<TA>::V;
+    using VC = typename Vec8<TC>::V;
+    __shared__ __align__(16) bf16_t s_k4[4][BF ? 1 : 2][DK][T];
+    __shared__ __align__(16) float s_d4[4][T][16];
+    const Params &p = a.p;
+    const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), gw = blockIdx.x * 4 + wid;
+    const int bh = gw / waves, wave = gw - bh * waves;
+    if (bh >= p.B * p.HV) return;
+    const int b = bh / p.HV, h = bh - b * p.HV;
+    auto &s_k = s_k4[wid];
+    auto &s_d = s_d4[wid];
+    const int slot = p.slot_ids[b];
+    if (slot < 0 || slot >= p.num_slots) return;
+    int64_t s, e;
+    request_range(p, b, s, e);
+    if (e <= s || e - s > T) return;
+    const int n = (int)(e - s);
+    const int lane = threadIdx.x & 63, c = lane & 15, kb = lane >> 4;
+    const int tiles = (p.dv + 15) / 16;
+    const int qh = (int)(((int64_t)h * p.H) / p.HV);
+    const auto key = [](int f, int kb) { return EIGHT ? 64 * (f / 2) + 16 * kb + 8 * (f % 2) : 32 * f + 8 * kb; };
+
+    // vector c: k of token c, q of token c - 8
+    const int own = c & 7, tt = own < n ? own : n - 1;
+    const size_t th = (size_t)(s + tt) * p.HV + h;
+    w4 xr[KS];
+    {
+        const TA *x = static_cast<const TA *>(c < 8 ? p.k : p.q) + ((size_t)(s + tt) * p.H + qh) * DK;
+#pragma unroll
+        for (int f = 0; f < KS; ++f) xr[f] = *reinterpret_cast<const w4 *>(x + key(f, kb));
+    }
+    const size_t head = ((size_t)slot * p.HV + h) * p.dv;
+    char *const mat = static_cast<char *>(a.data) + head * DK * (EIGHT ? 1 : 2);
+    uint8_t *const scales = EIGHT ? a.scale + head : nullptr;
+    const TA *const vv = static_cast<const TA *>(p.v) + th * p.dv;
+    w4 raw[PRE][NV];
+    uint32_t ex[PRE], exr[PRE][4];
+    TA vr[PRE][4];
+    const auto fetch = [&](int j, int tile) {
+        if (tile >= tiles) return;
+        const int row = 16 * tile + c, at = row < p.dv ? row : p.dv - 1;
+#pragma unroll
+        for (int m = 0; m < NV; ++m) {
+            const int r = NV > 1 ? 16 * tile + (c & ~1) + m % 2 : row, rr = r < p.dv ? r : p.dv - 1;
+            raw[j][m] = __builtin_nontemporal_load(reinterpret_cast<const w4 *>(mat + rr * ROW + m / 2 * 128 + (NV > 1 ? (c & 1) * 64 : 0) + kb * 16));
+        }
+        if (EIGHT) ex[j] = scales[at];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int r = 16 * tile + 4 * kb + m, rr = r < p.dv ? r : p.dv - 1;
+            if (EIGHT) exr[j][m] = scales[rr];
+            vr[j][m] = vv[rr];
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < PRE; ++j) fetch(j, wave + j * waves);
+    const bool decays = rule_decays(rule), retrieves = rule_retrieves(rule);
+    const float alpha = decays ? expf(log_decay(p, th, h)) : 1.f;
+    const float beta = rule_has_beta(rule) ? update_rate(p, th) : 1.f;
+
+    VA x[KS];
+#pragma unroll
+    for (int f = 0; f < KS; ++f) x[f] = __builtin_bit_cast(VA, xr[f]);
+    // k by keys, tokens together
+    if (c < 8) {
+#pragma unroll
+        for (int f = 0; f < KS; ++f)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float kf = c < n ? to_f32((TA)x[f][j]) : 0.f;
+                const bf16_t hi = from_f32<bf16_t>(kf);
+                s_k[0][key(f, kb) + j][c] = hi;
+                if constexpr (!BF) s_k[1][key(f, kb) + j][c] = from_f32<bf16_t>(kf - to_f32(hi));
+            }
+    }
+    s_d[lane / 16][lane % 16] = 0.f;
+    s_d[4 + lane / 16][lane % 16] = 0.f;
+    f4v gram = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int f = 0; f < KS; ++f) gram = mfma(x[f], x[f], gram);
+    // x as operands of the cache's type
+    VC y[SAME ? 1 : 2][KS];
+    float back = 1.f;
+    if constexpr (SAME) {
+#pragma unroll
+        for (int f = 0; f < KS; ++f) y[0][f] = __builtin_bit_cast(VC, xr[f]);
+    } else {
+        float up = 1.f;
+        if constexpr (BF) {  // bf16 in two fp16 planes: scaled to fp16's upper range
             float top = 0.f;
 #pragma unroll
-            for (int c = 0; c < C; ++c) top = fmaxf(top, fabsf(S[g][c]));
-            top = row_reduce<LANES>(top, [](float x, float y) { return fmaxf(x, y); });
-            ex[g] = scale_byte(top);
+            for (int f = 0; f < KS; ++f)
 #pragma unroll
-            for (int n = 0; n < 4; ++n) raw[g][0][n] = to_codes(&S[g][4 * n], scale_of(ex[g]));
-        } else {
-#pragma unroll
-            for (int c = 0; c < C; c += 2) raw[g][c / 8][c % 8 / 2] = two_halves<TC>(S[g][c], S[g][c + 1]);
+                for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(to_f32((TA)x[f][j])));
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            int e2 = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127 - 14;
+            e2 = top > 0.f ? (e2 < -120 ? -120 : e2 > 120 ? 120 : e2) : 0;
+            up = __builtin_bit_cast(float, (uint32_t)(127 - e2) << 23);
+            back = __builtin_bit_cast(float, (uint32_t)(127 + e2) << 23);
         }
-        if (row >= p.dv) continue;
-        char *dst = static_cast<char *>(a.data) + (head + row) * DK * (EIGHT ? 1 : 2) + l * 16;
 #pragma unroll
-        for (int n = 0; n < V; ++n) __builtin_nontemporal_store(raw[g][n], reinterpret_cast<w4 *>(dst + n * DK));
-        if (EIGHT && l == 0) a.scale[head + row] = (uint8_t)ex[g];
+        for (int f = 0; f < KS; ++f)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float v = to_f32((TA)x[f][j]) * up;
+                const TC hi = from_f32<TC>(v);
+                y[0][f][j] = hi;
+                y[1][f][j] = from_f32<TC>(v - to_f32(hi));
+            }
     }
+    // norms and the products of the tokens' vectors
+    float inv = 1.f;
+    if (p.qk_l2_norm) {
+        const float mine = c % 4 == 0 ? gram[0] : c % 4 == 1 ? gram[1] : c % 4 == 2 ? gram[2] : gram[3];
+        inv = 1.f / sqrtf(__shfl(mine, 16 * (c / 4) + c) + 1e-12f);
+    }
+    float al[T], cl[T], all = 1.f, later = 1.f;
+    each([&](auto t_) {
+        constexpr int t = decltype(t_)::value;
+        if (t < n) {
+            const float at = lane_of<t>(alpha), kt = lane_of<t>(inv), g = __shfl(gram[t % 4], 16 * (t / 4) + c);
+            const bool past = c >= 8 && t > c - 8;  // q of a token before t
+            al[t] = past ? 1.f : at;
+            cl[t] = past ? 0.f : kt * g;
+            all *= at;
+            if (t > own) later *= at;
+        }
+    }, std::make_integer_sequence<int, T>());
+    const float put_own = later * inv, oscale = p.scale * inv, binv = retrieves ? beta * inv : 0.f;
+    float put[T];
+    each([&](auto t_) {
+        constexpr int t = decltype(t_)::value;
+        if (t < n) put[t] = lane_of<t>(put_own);
+    }, std::make_integer_sequence<int, T>());
+    wave_sync();
+
+    for (int t0 = wave; t0 < tiles; t0 += PRE * waves)
+#pragma unroll
+        for (int i = 0; i < PRE; ++i) {
+            const int tile = t0 + i * waves;
+            if (tile >= tiles) break;
+            if constexpr (NV > 1)
+#pragma unroll
+                for (int m = 0; m < NV; m += 2) exchange(raw[i][m], raw[i][m + 1], c & 1);
+            // dots of the states with every vector: rows 4 kb + j, column c
+            f4v z = {0.f, 0.f, 0.f, 0.f}, z1 = z;
+#pragma unroll
+            for (int f = 0; f < KS; ++f) {
+                VC sv;
+                if constexpr (EIGHT) {
+                    const uint32_t w0 = raw[i][f / 2][f % 2 * 2], w1 = raw[i][f / 2][f % 2 * 2 + 1];
+                    w4 o;
+                    if constexpr (BF) {
+                        o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.f, false));
+                        o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.f, true));
+                        o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.f, false));
+                        o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.f, true));
+                    } else {
+                        o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.f, false));
+                        o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.f, true));
+                        o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.f, false));
+                        o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.f, true));
+                    }
+                    sv = __builtin_bit_cast(VC, o);
+                } else {
+                    const w4 o = raw[i][f];
+                    sv = __builtin_bit_cast(VC, o);
+                }
+                if constexpr (SAME) {
+                    if (f % 2) z1 = mfma(sv, y[0][f], z1);
+                    else z = mfma(sv, y[0][f], z);
+                } else {
+                    z = mfma(sv, y[0][f], z);
+                    z1 = mfma(sv, y[1][f], z1);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) z[j] += z1[j];
+            // decayed states, to which the update is added
+            float S[KS][8];
+#pragma unroll
+            for (int f = 0; f < KS; ++f) {
+                if constexpr (EIGHT) {
+                    from_codes(raw[i][f / 2][f % 2 * 2], scale_of(ex[i]), &S[f][0]);
+                    from_codes(raw[i][f / 2][f % 2 * 2 + 1], scale_of(ex[i]), &S[f][4]);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) S[f][j] *= all;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) S[f][j] = fmaf(half_of<TC>(raw[i][f][j / 2], j % 2), all, 0.f);
+                }
+            }
+            float vj[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                z[j] *= EIGHT ? scale_of(exr[i][j]) : back;
+                vj[j] = beta * to_f32(vr[i][j]);
+            }
+            fetch(i, tile + PRE * waves);
+            // the tokens in order: the new values d, and the dots with the states after them
+            each([&](auto t_) {
+                constexpr int t = decltype(t_)::value;
+                if (t < n) {
+                    float d[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        z[j] *= al[t];
+                        d[j] = retrieves ? fmaf(-binv, z[j], vj[j]) : vj[j];
+                    }
+                    if (c == t) *reinterpret_cast<f4v *>(&s_d[t][4 * kb]) = f4v{d[0], d[1], d[2], d[3]};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) z[j] = fmaf(lane_of<t>(d[j]), cl[t], z[j]);
+                }
+            }, std::make_integer_sequence<int, T>());
+            if (c >= 8 && c - 8 < n) {
+                TA *o = static_cast<TA *>(p.o) + th * p.dv + 16 * tile + 4 * kb;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (16 * tile + 4 * kb + j < p.dv) o[j] = from_f32<TA>(oscale * z[j]);
+            }
+            wave_sync();
+            // d of row c in planes: hi, mid, lo (and k is exact), or hi, mid for both planes of k
+            const bool plane1 = BF ? kb > 0 : (kb & 1), plane2 = kb > 1;
+            b8 dv8;
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                dv8[t] = from_f32<bf16_t>(0.f);
+                if (t < n) {
+                    float d = s_d[t][c] * put[t];
+                    d -= plane1 ? to_f32(from_f32<bf16_t>(d)) : 0.f;
+                    if constexpr (BF) {
+                        d -= plane2 ? to_f32(from_f32<bf16_t>(d)) : 0.f;
+                        d = kb == 3 ? 0.f : d;
+                    }
+                    dv8[t] = from_f32<bf16_t>(d);
+                }
+            }
+            wave_sync();
+#pragma unroll
+            for (int f = 0; f < KS; ++f)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const b8 k8 = *reinterpret_cast<const b8 *>(&s_k[BF ? 0 : kb >> 1][key(f, c / 4) + 4 * j + c % 4][0]);
+                    f4v acc = {S[f][4 * j], S[f][4 * j + 1], S[f][4 * j + 2], S[f][4 * j + 3]};
+                    acc = mfma(k8, dv8, acc);
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) S[f][4 * j + m] = acc[m];
+                }
+            const int row = 16 * tile + c;
+            w4 out[NV];
+            uint32_t eo = 0;
+            if constexpr (EIGHT) {
+                float top = 0.f;
+#pragma unroll
+                for (int f = 0; f < KS; ++f)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(S[f][j]));
+                top = fmaxf(top, __shfl_xor(top, 16));
+                top = fmaxf(top, __shfl_xor(top, 32));
+                eo = scale_byte(top);
+#pragma unroll
+                for (int f = 0; f < KS; ++f) {
+                    out[f / 2][f % 2 * 2] = to_codes(&S[f][0], scale_of(eo));
+                    out[f / 2][f % 2 * 2 + 1] = to_codes(&S[f][4], scale_of(eo));
+                }
+            } else {
+#pragma unroll
+                for (int f = 0; f < KS; ++f)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) out[f][j] = two_halves<TC>(S[f][2 * j], S[f][2 * j + 1]);
+            }
+            if constexpr (NV > 1)
+#pragma unroll
+                for (int m = 0; m < NV; m += 2) exchange(out[m], out[m + 1], c & 1);
+#pragma unroll
+            for (int m = 0; m < NV; ++m) {
+                const int r = NV > 1 ? 16 * tile + (c & ~1) + m % 2 : row;
+                if (r < p.dv) __builtin_nontemporal_store(out[m], reinterpret_cast<w4 *>(mat + r * ROW + m / 2 * 128 + (NV > 1 ? (c & 1) * 64 : 0) + kb * 16));
+            }
+            if (EIGHT && kb == 0 && row < p.dv) scales[row] = (uint8_t)eo;
+        }
+}
+
+template <typename TA, int TYPE, int DK, bool VD, bool ONE>
+hipError_t launch_step(const PackedParams &a, int rule, bool per_key, int least, hipStream_t s)
+{
+    using Form = StepForm<TYPE, DK, ONE>;
+    const int64_t blocks = (int64_t)a.p.B * a.p.HV * ((a.p.dv + Form::ROWS - 1) / Form::ROWS);
+    hipLaunchKernelGGL((k_packed_step<TA, TYPE, DK, VD, ONE>), dim3((unsigned)blocks), dim3(64 * Form::WAVES), 0, s, a, rule,
+                       (int)per_key, least);
+    return hipGetLastError();
 }
 
 template <typename TA, int TYPE, int DK>
 hipError_t packed_step_at(const PackedParams &a, int rule, bool per_key, hipStream_t s)
 {
-    const int64_t blocks = (int64_t)a.p.B * a.p.HV * ((a.p.dv + packed_step_rows(DK) - 1) / packed_step_rows(DK));
-    const dim3 grid((unsigned)blocks), threads(256);
-    if (per_key || rule == GATED_DELTA_V2)
-        hipLaunchKernelGGL((k_packed_step<TA, TYPE, DK, true>), grid, threads, 0, s, a, rule, (int)per_key);
-    else
-        hipLaunchKernelGGL((k_packed_step<TA, TYPE, DK, false>), grid, threads, 0, s, a, rule, 0);
-    return hipGetLastError();
+    const Params &p = a.p;
+    const bool keyed = per_key || rule == GATED_DELTA_V2;  // per-key vectors
+    const bool one = !p.cu_seqlens && p.L == 1;            // no request has more than a token
+    if (one)
+        return keyed ? launch_step<TA, TYPE, DK, true, true>(a, rule, per_key, 1, s)
+                     : launch_step<TA, TYPE, DK, false, true>(a, rule, per_key, 1, s);
+    if (keyed) return launch_step<TA, TYPE, DK, true, false>(a, rule, per_key, 1, s);
+    if constexpr (sizeof(TA) == 2 && DK <= 128) {
+        // Waves of a state: one, which spares the tokens' own work, until too few
+        // states leave SIMDs idle: 2,048 waves, two a SIMD.  4 tokens, 32 heads of
+        // 128, in us with 1,024, 2,048, 4,096 and 8,192 waves at least: 8-bit states of
+        // 32 requests 19.4, 16.0, 18.8 and 22.2, of 64 25.3, 25.5, 26.8 and 30.7;
+        // 16-bit ones 21.1, 20.8, 23.9 and 26.2, 32.1, 32.2, 36.5 and 37.2.
+        const int64_t states = (int64_t)p.B * p.HV;
+        int waves = 1;
+        while (waves < 8 && waves * 16 < p.dv && states * waves < 2048) waves *= 2;
+        const dim3 blocks((unsigned)((states * waves + 3) / 4));
+        hipLaunchKernelGGL((k_packed_few<TA, TYPE, DK, TYPE == CACHE_E4M3 ? 2 : 1>), blocks, dim3(256), 0, s, a, rule, waves);
+        hipError_t err = hipGetLastError();
+        if (err != hipSuccess || (p.cu_seqlens ? p.T : p.L) <= 8) return err;
+        return launch_step<TA, TYPE, DK, false, false>(a, rule, false, 9, s);  // requests of more than 8 tokens
+    }
+    return launch_step<TA, TYPE, DK, false, false>(a, rule, false, 1, s);
 }
 
 template <typename TA, int TYPE>

@@ -23,7 +23,6 @@ struct PackedParams {
 
 // Head dims of the keys that the step's kernel takes.
 constexpr bool packed_step_ok(int dk) { return dk == 64 || dk == 128 || dk == 256; }
-constexpr int packed_step_rows(int dk) { return dk == 128 ? 128 : 64; }  // state rows a workgroup
 int64_t pack_blocks(int batch, int heads, int dv);
 
 hipError_t launch_pack(const PackedParams &a, hipStream_t s);
