@@ -634,6 +634,13 @@ gdr_status check_rotary_tensors(const gdr_rotary *r, const void *q_out, int64_t 
     return GDR_OK;
 }
 
+// Bytes of the weight gradient's sums over workgroups, for q or k.
+size_t rotary_partial(const gdr_rotary *r, int heads)
+{
+    const int64_t all = (int64_t)r->heads_q + r->heads_k;
+    return (size_t)gdr::rotary_back_blocks(r->tokens, heads, all, r->head_dim) * r->head_dim * 4;
+}
+
 gdr::RotaryParams rotary_params(const gdr_rotary *r)
 {
     gdr::RotaryParams p{};
@@ -1067,9 +1074,8 @@ gdr_status gdr_qk_rotary_backward_workspace_size(const gdr_rotary *rotary, size_
     if (!bytes) return fail(GDR_E_INVALID, "bytes is NULL");
     gdr_status st = check_rotary(rotary);
     if (st != GDR_OK) return st;
-    const int64_t heads = std::max(rotary->heads_q, rotary->heads_k);
-    const size_t part = (size_t)gdr::rotary_back_blocks(rotary->tokens, heads, rotary->head_dim) * rotary->head_dim * 4;
-    *bytes = part * ((rotary->q_weight != nullptr) + (rotary->k_weight != nullptr));
+    *bytes = (rotary->q_weight ? rotary_partial(rotary, rotary->heads_q) : 0) +
+             (rotary->k_weight ? rotary_partial(rotary, rotary->heads_k) : 0);
     return GDR_OK;
 }
 
@@ -1108,7 +1114,7 @@ gdr_status gdr_qk_rotary_backward(const gdr_rotary *rotary, const void *d_q_out,
     p.part[1].out_stride = d_k_stride;
     p.part[1].d_y = d_k_out;
     p.part[1].d_weight = d_k_weight;
-    p.part[1].partial = d_k_weight ? partial + (d_q_weight ? need / 8 : 0) : nullptr;  // the second half, in floats
+    p.part[1].partial = d_k_weight ? partial + (d_q_weight ? rotary_partial(rotary, r.heads_q) / 4 : 0) : nullptr;
     hipError_t err = gdr::launch_rotary_backward(p, static_cast<hipStream_t>(stream));
     if (err != hipSuccess) return fail(GDR_E_HIP, "kernel launch failed: %s", hipGetErrorString(err));
     return GDR_OK;

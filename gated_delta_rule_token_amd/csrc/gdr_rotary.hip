@@ -22,21 +22,27 @@ namespace {
 constexpr int THREADS = 256;
 constexpr int ANGLES = 2048;  // pairs of (token, frequency) whose cos and sin LDS holds
 
-// 16 bytes from any even address.
+// 16, 8 and 4 bytes from any even address.
 typedef uint32_t v4 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t v2 __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t v1 __attribute__((aligned(2)));
 
 // VEC elements as they lie in memory.
 template <typename T, int VEC> struct Raw {
-    static constexpr int WORDS = (VEC * sizeof(T) + 3) / 4;
+    static constexpr int BYTES = VEC * sizeof(T), WORDS = (BYTES + 3) / 4;
     uint32_t w[WORDS];
     __device__ __forceinline__ void load(const T *src)
     {
-        if constexpr (WORDS == 4) {
+        if constexpr (BYTES == 16) {
             const v4 x = *reinterpret_cast<const v4 *>(src);
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = x[i];
-        } else if constexpr (sizeof(T) == 4) {
-            w[0] = __builtin_bit_cast(uint32_t, src[0]);
+        } else if constexpr (BYTES == 8) {
+            const v2 x = *reinterpret_cast<const v2 *>(src);
+            w[0] = x[0];
+            w[1] = x[1];
+        } else if constexpr (BYTES == 4) {
+            w[0] = *reinterpret_cast<const v1 *>(src);
         } else {
             w[0] = __builtin_bit_cast(uint16_t, src[0]);
         }
@@ -51,17 +57,20 @@ template <typename T, int VEC> struct Raw {
 template <typename T, int VEC>
 __device__ __forceinline__ void store(T *dst, const float *v)
 {
-    if constexpr (VEC * sizeof(T) == 16) {
-        v4 o;
+    constexpr int BYTES = VEC * sizeof(T), WORDS = (BYTES + 3) / 4;
+    if constexpr (BYTES == 2) {
+        dst[0] = from_f32<T>(v[0]);
+    } else {
+        uint32_t o[WORDS];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < WORDS; ++i) {
             if constexpr (sizeof(T) == 4) o[i] = __builtin_bit_cast(uint32_t, v[i]);
             else o[i] = __builtin_bit_cast(uint16_t, from_f32<T>(v[2 * i])) |
                         (uint32_t)__builtin_bit_cast(uint16_t, from_f32<T>(v[2 * i + 1])) << 16;
         }
-        *reinterpret_cast<v4 *>(dst) = o;
-    } else {
-        dst[0] = from_f32<T>(v[0]);
+        if constexpr (BYTES == 16) *reinterpret_cast<v4 *>(dst) = v4{o[0], o[1], o[2], o[3]};
+        else if constexpr (BYTES == 8) *reinterpret_cast<v2 *>(dst) = v2{o[0], o[1]};
+        else *reinterpret_cast<v1 *>(dst) = o[0];
     }
 }
 
@@ -197,8 +206,7 @@ __global__ __launch_bounds__(THREADS) void k_rotary(const RotaryParams p)
     }
 }
 
-// blockIdx.y: q or k.  A workgroup takes p.block tokens, + gridDim.x *
-// p.block, ...; the weight's gradient stays in a lane's registers, as its
+// blockIdx.y: q or k.  A workgroup takes part.block tokens at a time; the weight's gradient stays in a lane's registers, as its
 // columns are the same for every row, and its sums over the workgroup's rows
 // and then over the workgroups have a fixed order.
 template <typename T, typename TW, int VEC, int LPR, int NV>
@@ -209,13 +217,13 @@ __global__ __launch_bounds__(THREADS) void k_rotary_back(const RotaryParams p)
     const int lane = threadIdx.x % LPR, group = threadIdx.x / LPR;
     const RotaryPart &part = p.part[blockIdx.y];
     const int heads = part.heads;
-    if (heads == 0) return;
+    if ((int)blockIdx.x >= part.blocks) return;
     float dw[NV][2 * VEC] = {};
     for (int i = threadIdx.x; i < p.dim; i += THREADS)
         s_w[i] = part.weight ? to_f32(static_cast<const TW *>(part.weight)[i]) : 1.f;
     const int step_t = ROWS / heads, step_h = ROWS - step_t * heads;
-    for (int64_t t0 = (int64_t)blockIdx.x * p.block; t0 < p.tokens; t0 += (int64_t)gridDim.x * p.block) {
-        const int n = (int)(p.tokens - t0 < p.block ? p.tokens - t0 : p.block);
+    for (int64_t t0 = (int64_t)blockIdx.x * part.block; t0 < p.tokens; t0 += (int64_t)part.blocks * part.block) {
+        const int n = (int)(p.tokens - t0 < part.block ? p.tokens - t0 : part.block);
         int token = group / heads, head = group - token * heads;
         Raw<T, VEC> x[NV][2], y[NV][2];
         auto fetch = [&](int token, int head) {
@@ -304,41 +312,55 @@ __global__ __launch_bounds__(THREADS) void k_rotary_back(const RotaryParams p)
     }
 }
 
-// Workgroup: 16 columns, 16 threads a column, each every 16th partial row.
-__global__ __launch_bounds__(256) void k_rotary_back_sums(const RotaryParams p, int blocks)
+// Workgroup: 16 columns, 64 threads a column, each every 64th partial row.
+__global__ __launch_bounds__(1024) void k_rotary_back_sums(const RotaryParams p)
 {
-    __shared__ float s[16][17];
+    __shared__ float s[64][17];
     const RotaryPart &part = p.part[blockIdx.y];
     if (!part.d_weight) return;
     const int c = threadIdx.x & 15, r = threadIdx.x >> 4, col = blockIdx.x * 16 + c;
     float sum = 0.f;
-    if (col < p.dim && part.heads > 0)
-        for (int b = r; b < blocks; b += 16) sum += part.partial[(size_t)b * p.dim + col];
+    if (col < p.dim) {
+#pragma unroll 8
+        for (int b = r; b < part.blocks; b += 64) sum += part.partial[(size_t)b * p.dim + col];
+    }
     s[r][c] = sum;
     __syncthreads();
-    if (r == 0 && col < p.dim) {
-        for (int n = 1; n < 16; ++n) sum += s[n][c];
-        part.d_weight[col] = sum;
+    if (r < 4) {
+        for (int n = r + 4; n < 64; n += 4) sum += s[n][c];
+        s[r][c] = sum;
     }
+    __syncthreads();
+    if (r == 0 && col < p.dim) part.d_weight[col] = s[0][c] + s[1][c] + s[2][c] + s[3][c];
 }
 
-// Lanes and vectors of a head: vectors of 16 bytes where head and turned part
-// consist of whole pairs of them, else single pairs.
+// Vectors, lanes and vectors a lane of a head: vectors of 16, 8 or 4 bytes (16
+// and 8 in fp32) where the head and its turned part consist of whole pairs of
+// them, else single pairs.
 template <typename T, typename F>
 hipError_t by_form(const RotaryParams &p, F &&f)
 {
     using std::integral_constant;
     constexpr int V = 16 / sizeof(T);
-    using vec = integral_constant<int, V>;
-    using one = integral_constant<int, 1>;
-    if (p.dim % (2 * V) == 0 && p.half % V == 0) {
-        const int vectors = p.dim / (2 * V);
-        if (vectors <= 8) return f(vec(), integral_constant<int, 8>(), one());
-        if (vectors <= 16) return f(vec(), integral_constant<int, 16>(), one());
-        if constexpr (V == 4) return f(vec(), integral_constant<int, 32>(), one());
+    const auto fits = [&](int v) { return p.dim % (2 * v) == 0 && p.half % v == 0; };
+    const auto lanes = [&](auto vec) {
+        const int vectors = p.dim / (2 * vec());
+        if (vectors <= 8) return f(vec, integral_constant<int, 8>(), integral_constant<int, 1>());
+        if (vectors <= 16) return f(vec, integral_constant<int, 16>(), integral_constant<int, 1>());
+        if constexpr (vec() < 8) {
+            if (vec() == 4 || vectors <= 32) return f(vec, integral_constant<int, 32>(), integral_constant<int, 1>());
+        }
+        return f(vec, integral_constant<int, vec() < 4 ? 64 : 16>(), integral_constant<int, 1>());
+    };
+    if (fits(V)) return lanes(integral_constant<int, V>());
+    if (fits(V / 2)) return lanes(integral_constant<int, V / 2>());
+    if constexpr (V == 8) {
+        if (fits(2)) return lanes(integral_constant<int, 2>());
     }
+    using one = integral_constant<int, 1>;
+    if (p.dim <= 32) return f(one(), integral_constant<int, 16>(), one());
     if (p.dim <= 64) return f(one(), integral_constant<int, 32>(), one());
-    if (p.dim <= 128) return f(one(), integral_constant<int, 64>(), one());
+    if (p.dim <= 128) return f(one(), integral_constant<int, 32>(), integral_constant<int, 2>());
     return f(one(), integral_constant<int, 64>(), integral_constant<int, 2>());
 }
 
@@ -361,10 +383,17 @@ int token_block(const RotaryParams &p, int64_t heads, int64_t rows)
 
 }  // namespace
 
-int rotary_back_blocks(int64_t tokens, int64_t heads, int64_t dim)
+int rotary_back_blocks(int64_t tokens, int64_t heads, int64_t all_heads, int64_t dim)
 {
-    const int64_t n = tokens * heads * dim / 16384;
-    return n < 1 ? 1 : n > 512 ? 512 : (int)n;
+    // 4,096 elements a workgroup, up to four workgroups a CU for q and k together.
+    // 16,384, 4,096 and 2,048: 1,217 tokens x 9 and 3 heads of 72 in fp32 32, 23 and
+    // 23 us (21 of them the host's), in fp16 68, 23 and 24; 2,000 x 16 + 16 heads of
+    // 128 in bf16 33, 29 and 29; 29,273 of them 145.3 each, 146.1 with twice as many.
+    const int64_t n = tokens * heads * dim / 4096;
+    // A part of few heads still forms every token's angles: 29,273 tokens x 16 and 1
+    // heads of 128 with 60, 128, 256 and 512 workgroups for the one 127, 116, 98 and 92 us.
+    const int64_t most = std::max<int64_t>(512, 1024 * heads / std::max<int64_t>(all_heads, 1));
+    return n < 1 ? 1 : n > most ? (int)most : (int)n;
 }
 
 hipError_t launch_rotary(const RotaryParams &params, hipStream_t s)
@@ -372,7 +401,10 @@ hipError_t launch_rotary(const RotaryParams &params, hipStream_t s)
     RotaryParams p = params;
     const int64_t heads = (int64_t)p.part[0].heads + p.part[1].heads;
     if (p.tokens == 0 || heads == 0) return hipSuccess;
-    p.block = token_block(p, heads, 128);
+    // 16 KB of rows a workgroup: 29,273 tokens x 32 heads of 128 in fp16 with 8, 16,
+    // 32 and 64 KB 103, 94, 96 and 100 us; 14,000 in fp32 with 16, 32 and 64 87, 92
+    // and 92.
+    p.block = token_block(p, heads, 16384 / (p.dim * (p.dt == 0 ? 4 : 2)));
     const int64_t spread = (p.tokens + 511) / 512;  // few tokens: a workgroup each
     if (p.block > spread) p.block = (int)spread;
     const dim3 blocks((unsigned)((p.tokens + p.block - 1) / p.block));
@@ -390,25 +422,28 @@ hipError_t launch_rotary(const RotaryParams &params, hipStream_t s)
 hipError_t launch_rotary_backward(const RotaryParams &params, hipStream_t s)
 {
     RotaryParams p = params;
-    const int64_t heads = std::max(p.part[0].heads, p.part[1].heads);
-    const int blocks = rotary_back_blocks(p.tokens, heads, p.dim);
+    const int64_t heads = (int64_t)p.part[0].heads + p.part[1].heads;
     if (p.tokens > 0 && heads > 0) {
-        p.block = token_block(p, heads, 64);
+        // 64 heads at a time (32, 64 and 128: 29,273 tokens x 16 + 16 heads of 128 in
+        // bf16 147.9, 145.3 and 144.9 us; 1,217 of 9 + 3 of 72 in fp16 23, 23 and 37)
+        for (RotaryPart &part : p.part) {
+            part.block = token_block(p, std::max(part.heads, 1), 64);
+            part.blocks = part.heads ? rotary_back_blocks(p.tokens, part.heads, heads, p.dim) : 0;
+        }
+        const dim3 blocks((unsigned)std::max(p.part[0].blocks, p.part[1].blocks), 2);
         hipError_t err = by_types(p, [&](auto t, auto w) {
             using T = decltype(t);
             using TW = decltype(w);
             return by_form<T>(p, [&](auto vec, auto lpr, auto nv) {
                 hipLaunchKernelGGL((k_rotary_back<T, TW, decltype(vec)::value, decltype(lpr)::value, decltype(nv)::value>),
-                                   dim3((unsigned)blocks, 2), dim3(THREADS), 0, s, p);
+                                   blocks, dim3(THREADS), 0, s, p);
                 return hipGetLastError();
             });
         });
         if (err != hipSuccess) return err;
     }
-    if (p.part[0].d_weight || p.part[1].d_weight) {
-        const int have = p.tokens > 0 ? blocks : 0;
-        hipLaunchKernelGGL(k_rotary_back_sums, dim3((unsigned)((p.dim + 15) / 16), 2), dim3(256), 0, s, p, have);
-    }
+    if (p.part[0].d_weight || p.part[1].d_weight)
+        hipLaunchKernelGGL(k_rotary_back_sums, dim3((unsigned)((p.dim + 15) / 16), 2), dim3(1024), 0, s, p);
     return hipGetLastError();
 }
 

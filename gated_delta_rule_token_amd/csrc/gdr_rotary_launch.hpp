@@ -23,6 +23,7 @@ struct RotaryPart {
     float *d_weight, *partial;  // backward: rotary_back_blocks x dim floats, or nullptr
     int64_t stride, out_stride;
     int32_t heads;
+    int32_t block, blocks;          // backward: tokens a workgroup takes at a time, workgroups
 };
 
 // dt, weight_dt: 0 fp32, 1 fp16, 2 bf16; weight_dt is dt or 0.
@@ -31,13 +32,13 @@ struct RotaryParams {
     int64_t tokens;
     int32_t dim, half, axes;        // half: pairs that are turned
     int32_t neighbours, norm, dt, weight_dt;
-    int32_t block;                  // tokens a workgroup takes at a time
+    int32_t block;                  // forward: tokens a workgroup takes
     float eps;
     const int32_t *positions, *axis_of;
     const float *freq;
 };
 
-int rotary_back_blocks(int64_t tokens, int64_t heads, int64_t dim);
+int rotary_back_blocks(int64_t tokens, int64_t heads, int64_t all_heads, int64_t dim);
 hipError_t launch_rotary(const RotaryParams &p, hipStream_t s);
 hipError_t launch_rotary_backward(const RotaryParams &p, hipStream_t s);
 
