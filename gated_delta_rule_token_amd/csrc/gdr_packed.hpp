@@ -22,6 +22,7 @@
 namespace gdr {
 
 typedef uint32_t w4 __attribute__((ext_vector_type(4)));
+typedef uint32_t Any4 __attribute__((ext_vector_type(4), aligned(1)));  // 16 bytes from any address
 typedef float f2 __attribute__((ext_vector_type(2)));
 typedef short s2 __attribute__((ext_vector_type(2)));
 
@@ -101,8 +102,11 @@ template <int TYPE, int DK, bool ONE> struct StepForm {
     static constexpr int ROWS = DK == 128 && (EIGHT || !ONE) ? 128 : 64;  // of a workgroup
 };
 
+// EXACT: p.dk is DK; else it lies between 16 and DK, and a lane's vector that
+// would pass the row's end starts earlier: the columns that it then shares with
+// another lane count in that lane's sums only, and both write the same bytes.
 // Requests of fewer than `least` tokens are left alone.
-template <typename TA, int TYPE, int DK, bool VD, bool ONE>
+template <typename TA, int TYPE, int DK, bool VD, bool ONE, bool EXACT>
 __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packed_step(const PackedParams a, int rule,
                                                                                        int per_key, int least)
 {
@@ -110,8 +114,9 @@ __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packe
     constexpr bool EIGHT = TYPE == CACHE_E4M3;
     using TC = typename CacheType<TYPE>::T;
     constexpr int C = 16, LANES = DK / C, RPW = 64 / LANES, G = Form::ROWS / (Form::WAVES * RPW), V = EIGHT ? 1 : 2;
-    constexpr int ROW = DK * (EIGHT ? 1 : 2);  // bytes
+    constexpr int VC = EIGHT ? 16 : 8;  // values of a vector
     const Params &p = a.p;
+    const int dk = EXACT ? DK : p.dk, ROW = dk * (EIGHT ? 1 : 2);  // values and bytes of a row
     const int parts = (p.dv + Form::ROWS - 1) / Form::ROWS;
     const int part = blockIdx.x % parts, h = (blockIdx.x / parts) % p.HV, b = blockIdx.x / (parts * p.HV);
     const int slot = p.slot_ids[b];
@@ -123,7 +128,16 @@ __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packe
     const int row0 = part * Form::ROWS + wave * G * RPW + r;  // + RPW for each row group
     const int qh = (int)(((int64_t)h * p.H) / p.HV);
     const bool retrieves = rule_retrieves(rule), decays = rule_decays(rule), rate = rule_has_beta(rule);
-    const auto column = [&](int c) { return EIGHT ? l * C + c : (c < 8 ? 0 : DK / 2) + l * 8 + c % 8; };
+    // this lane's vectors: the first column, and how many of the columns are another lane's
+    int at[V], others[V];
+#pragma unroll
+    for (int n = 0; n < V; ++n) {
+        const int want = n * (DK / 2) + l * VC;
+        at[n] = EXACT || want + VC <= dk ? want : dk - VC;
+        others[n] = EXACT ? 0 : want - at[n];
+    }
+    const auto column = [&](int c) { return at[c / VC] + c % VC; };
+    const auto own = [&](int c) { return EXACT || c % VC >= others[c / VC]; };
     const auto add = [](float x, float y) { return x + y; };
     const TA *q = static_cast<const TA *>(p.q), *k = static_cast<const TA *>(p.k), *v = static_cast<const TA *>(p.v);
     TA *o = static_cast<TA *>(p.o);
@@ -133,7 +147,7 @@ __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packe
     const auto load8 = [](const TA *src) {
         Eight x;
 #pragma unroll
-        for (unsigned i = 0; i < sizeof(TA) / 2; ++i) x.w[i] = reinterpret_cast<const w4 *>(src)[i];
+        for (unsigned i = 0; i < sizeof(TA) / 2; ++i) x.w[i] = reinterpret_cast<const Any4 *>(src)[i];
         return x;
     };
     const auto get8 = [](const Eight &x, int i) {
@@ -143,7 +157,7 @@ __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packe
     Eight qw[2], kw[2];
     float vw[G];
     const auto fetch = [&](int64_t t) {
-        const TA *qr = q + (t * p.H + qh) * DK, *kr = k + (t * p.H + qh) * DK;
+        const TA *qr = q + (t * p.H + qh) * dk, *kr = k + (t * p.H + qh) * dk;
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
             qw[n] = load8(qr + column(8 * n));
@@ -162,11 +176,11 @@ __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packe
     uint32_t ex[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-        const int row = row0 + g * RPW, at = row < p.dv ? row : p.dv - 1;
-        const char *src = static_cast<const char *>(a.data) + (head + at) * ROW + l * 16;
+        const int row = row0 + g * RPW, from = row < p.dv ? row : p.dv - 1;
+        const char *src = static_cast<const char *>(a.data) + (head + from) * ROW;
 #pragma unroll
-        for (int n = 0; n < V; ++n) raw[g][n] = __builtin_nontemporal_load(reinterpret_cast<const w4 *>(src + n * DK));
-        ex[g] = EIGHT ? a.scale[head + at] : 0;
+        for (int n = 0; n < V; ++n) raw[g][n] = __builtin_nontemporal_load(reinterpret_cast<const Any4 *>(src + at[n] * (16 / VC)));
+        ex[g] = EIGHT ? a.scale[head + from] : 0;
     }
     const auto widen = [&](int g, float (&S)[C]) {
         if constexpr (EIGHT) {
@@ -193,25 +207,40 @@ __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packe
             for (int c = 0; c < C; c += 2) out[c / 8][c % 8 / 2] = two_halves<TC>(S[c], S[c + 1]);
         }
         if (row >= p.dv) return;
-        char *dst = static_cast<char *>(a.data) + (head + row) * ROW + l * 16;
+        char *dst = static_cast<char *>(a.data) + (head + row) * ROW;
 #pragma unroll
-        for (int n = 0; n < V; ++n) __builtin_nontemporal_store(out[n], reinterpret_cast<w4 *>(dst + n * DK));
+        for (int n = 0; n < V; ++n)
+            if (EXACT || others[n] < VC) __builtin_nontemporal_store(out[n], reinterpret_cast<Any4 *>(dst + at[n] * (16 / VC)));
         if (EIGHT && l == 0) a.scale[head + row] = (uint8_t)eo;
     };
 
+    // A decay for each key or the erase gate: the workgroup forms a token's
+    // factors once, for all its rows, a token ahead of their use.  (Formed by the
+    // lanes for themselves, 256 requests x 32 heads of 128 on 16-bit states took
+    // 316 us for a token and 830 for four.)
+    __shared__ __align__(16) float s_decay[VD ? 2 : 1][VD ? DK : 1], s_erase[VD ? 2 : 1][VD ? DK : 1];
+    const auto stage = [&](int64_t t) {
+        const size_t th = (size_t)t * p.HV + h;
+        for (int j = threadIdx.x; j < dk; j += 64 * Form::WAVES) {
+            s_decay[(t - s) & 1][j] = expf(per_key ? log_decay_key(p, th, h, j) : decays ? log_decay(p, th, h) : 0.f);
+            s_erase[(t - s) & 1][j] = p.erase ? p.erase[th * dk + j] : 1.f;
+        }
+    };
     // One token: its vectors and scalars, then each row group's step.
-    float qv[C], kv[C], av[C], kb[C], vi[G], qk, alpha, bt;
+    float qv[C], kv[C], av[C], kb[C], vi[G], qk, alpha, bt;  // qv and kb: for dots
     const auto token = [&](int64_t t) {
         const size_t th = (size_t)t * p.HV + h;
         float qq = 0.f, kk = 0.f;
         qk = 0.f;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            qv[c] = get8(qw[c / 8], c % 8);
+            const float qc = get8(qw[c / 8], c % 8);
             kv[c] = get8(kw[c / 8], c % 8);
+            qv[c] = own(c) ? qc : 0.f;
+            kb[c] = own(c) ? kv[c] : 0.f;
             qq = fmaf(qv[c], qv[c], qq);
-            kk = fmaf(kv[c], kv[c], kk);
-            qk = fmaf(qv[c], kv[c], qk);
+            kk = fmaf(kb[c], kb[c], kk);
+            qk = fmaf(qv[c], kb[c], qk);
         }
 #pragma unroll
         for (int g = 0; g < G; ++g) vi[g] = vw[g];
@@ -225,15 +254,18 @@ __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packe
             for (int c = 0; c < C; ++c) {
                 qv[c] *= inq;
                 kv[c] *= ink;
+                kb[c] *= ink;
             }
         }
-        alpha = decays && !per_key ? expf(log_decay(p, th, h)) : 1.f;
+        alpha = !VD && decays ? expf(log_decay(p, th, h)) : 1.f;
         bt = rate ? update_rate(p, th) : 1.f;
-        if constexpr (VD) {  // a decay for each key, or the erase gate
+        if constexpr (VD) {
+            lds_barrier();
+            if (!ONE && t + 1 < e) stage(t + 1);
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                av[c] = per_key ? expf(log_decay_key(p, th, h, column(c))) : alpha;
-                kb[c] = av[c] * kv[c] * (p.erase ? p.erase[th * DK + column(c)] : 1.f);
+                av[c] = s_decay[(t - s) & 1][column(c)];
+                kb[c] = av[c] * kb[c] * s_erase[(t - s) & 1][column(c)];
                 qv[c] *= av[c];
             }
         }
@@ -242,7 +274,7 @@ __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packe
         float get = 0.f, u = 0.f;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            get = fmaf(S[c], VD ? kb[c] : kv[c], get);
+            get = fmaf(S[c], kb[c], get);
             u = fmaf(S[c], qv[c], u);
         }
         get = row_reduce<LANES>(get, add);
@@ -257,6 +289,7 @@ __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packe
         const int row = row0 + g * RPW;
         if (l == 0 && row < p.dv) o[((size_t)t * p.HV + h) * p.dv + row] = from_f32<TA>(p.scale * (u + qk * put));
     };
+    if constexpr (VD) stage(s);
     if constexpr (ONE) {
         token(s);
 #pragma unroll
@@ -651,9 +684,12 @@ template <typename TA, int TYPE, int DK, bool VD, bool ONE>
 hipError_t launch_step(const PackedParams &a, int rule, bool per_key, int least, hipStream_t s)
 {
     using Form = StepForm<TYPE, DK, ONE>;
-    const int64_t blocks = (int64_t)a.p.B * a.p.HV * ((a.p.dv + Form::ROWS - 1) / Form::ROWS);
-    hipLaunchKernelGGL((k_packed_step<TA, TYPE, DK, VD, ONE>), dim3((unsigned)blocks), dim3(64 * Form::WAVES), 0, s, a, rule,
-                       (int)per_key, least);
+    const dim3 blocks((unsigned)((int64_t)a.p.B * a.p.HV * ((a.p.dv + Form::ROWS - 1) / Form::ROWS)));
+    const dim3 threads(64 * Form::WAVES);
+    if (a.p.dk == DK)
+        hipLaunchKernelGGL((k_packed_step<TA, TYPE, DK, VD, ONE, true>), blocks, threads, 0, s, a, rule, (int)per_key, least);
+    else
+        hipLaunchKernelGGL((k_packed_step<TA, TYPE, DK, VD, ONE, false>), blocks, threads, 0, s, a, rule, (int)per_key, least);
     return hipGetLastError();
 }
 
@@ -668,19 +704,21 @@ hipError_t packed_step_at(const PackedParams &a, int rule, bool per_key, hipStre
                      : launch_step<TA, TYPE, DK, false, true>(a, rule, per_key, 1, s);
     if (keyed) return launch_step<TA, TYPE, DK, true, false>(a, rule, per_key, 1, s);
     if constexpr (sizeof(TA) == 2 && DK <= 128) {
-        // Waves of a state: one, which spares the tokens' own work, until too few
-        // states leave SIMDs idle: 2,048 waves, two a SIMD.  4 tokens, 32 heads of
-        // 128, in us with 1,024, 2,048, 4,096 and 8,192 waves at least: 8-bit states of
-        // 32 requests 19.4, 16.0, 18.8 and 22.2, of 64 25.3, 25.5, 26.8 and 30.7;
-        // 16-bit ones 21.1, 20.8, 23.9 and 26.2, 32.1, 32.2, 36.5 and 37.2.
-        const int64_t states = (int64_t)p.B * p.HV;
-        int waves = 1;
-        while (waves < 8 && waves * 16 < p.dv && states * waves < 2048) waves *= 2;
-        const dim3 blocks((unsigned)((states * waves + 3) / 4));
-        hipLaunchKernelGGL((k_packed_few<TA, TYPE, DK, TYPE == CACHE_E4M3 ? 2 : 1>), blocks, dim3(256), 0, s, a, rule, waves);
-        hipError_t err = hipGetLastError();
-        if (err != hipSuccess || (p.cu_seqlens ? p.T : p.L) <= 8) return err;
-        return launch_step<TA, TYPE, DK, false, false>(a, rule, false, 9, s);  // requests of more than 8 tokens
+        if (p.dk == DK) {
+            // Waves of a state: one, which spares the tokens' own work, until too few
+            // states leave SIMDs idle: 2,048 waves, two a SIMD.  4 tokens, 32 heads of
+            // 128, in us with 1,024, 2,048, 4,096 and 8,192 waves at least: 8-bit states of
+            // 32 requests 19.4, 16.0, 18.8 and 22.2, of 64 25.3, 25.5, 26.8 and 30.7;
+            // 16-bit ones 21.1, 20.8, 23.9 and 26.2, 32.1, 32.2, 36.5 and 37.2.
+            const int64_t states = (int64_t)p.B * p.HV;
+            int waves = 1;
+            while (waves < 8 && waves * 16 < p.dv && states * waves < 2048) waves *= 2;
+            const dim3 blocks((unsigned)((states * waves + 3) / 4));
+            hipLaunchKernelGGL((k_packed_few<TA, TYPE, DK, TYPE == CACHE_E4M3 ? 2 : 1>), blocks, dim3(256), 0, s, a, rule, waves);
+            hipError_t err = hipGetLastError();
+            if (err != hipSuccess || (p.cu_seqlens ? p.T : p.L) <= 8) return err;
+            return launch_step<TA, TYPE, DK, false, false>(a, rule, false, 9, s);  // requests of more than 8 tokens
+        }
     }
     return launch_step<TA, TYPE, DK, false, false>(a, rule, false, 1, s);
 }
@@ -688,8 +726,8 @@ hipError_t packed_step_at(const PackedParams &a, int rule, bool per_key, hipStre
 template <typename TA, int TYPE>
 hipError_t packed_step_by_dk(const PackedParams &a, int rule, bool per_key, hipStream_t s)
 {
-    if (a.p.dk == 64) return packed_step_at<TA, TYPE, 64>(a, rule, per_key, s);
-    if (a.p.dk == 128) return packed_step_at<TA, TYPE, 128>(a, rule, per_key, s);
+    if (a.p.dk <= 64) return packed_step_at<TA, TYPE, 64>(a, rule, per_key, s);
+    if (a.p.dk <= 128) return packed_step_at<TA, TYPE, 128>(a, rule, per_key, s);
     return packed_step_at<TA, TYPE, 256>(a, rule, per_key, s);
 }
 

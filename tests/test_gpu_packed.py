@@ -274,19 +274,44 @@ RULES = [dict(update_rule="gated_delta", gate_activation="qwen", beta_activation
 @pytest.mark.parametrize("dtype", DT)
 @pytest.mark.parametrize("rule", range(len(RULES)))
 def test_single_tokens_of_every_rule(dtype, rule):
-    for act, dim in ((np.float16, 128), ("bf16", 64), (np.float32, 256)):
+    for act, dim in ((np.float16, 128), ("bf16", 64), (np.float32, 256), ("bf16", 72), (np.float32, 97)):
         case = workloads.random_case(50 + rule, rank4_batch=(3, 1), H=2, HV=4, DK=dim, DV=dim, dtype=act, slots=(7,), **RULES[rule])
         step_and_check(case, dtype)
 
 
 @pytest.mark.parametrize("dtype", DT)
 @pytest.mark.parametrize("dk,dv,H,HV,L", [(128, 128, 1, 1, 1), (128, 72, 2, 6, 2), (64, 256, 3, 3, 4), (256, 1, 1, 2, 3),
-                                          (256, 130, 1, 4, 8), (64, 33, 2, 2, 7), (128, 256, 1, 3, 5)])
+                                          (256, 130, 1, 4, 8), (64, 33, 2, 2, 7), (128, 256, 1, 3, 5),
+                                          (96, 96, 2, 4, 1), (17, 40, 1, 2, 3), (255, 9, 1, 1, 2), (33, 33, 2, 2, 1),
+                                          (16, 16, 1, 4, 5), (130, 64, 1, 2, 8), (72, 40, 3, 9, 1)])
 def test_dims_heads_and_several_tokens(dtype, dk, dv, H, HV, L):
     for act in (np.float16, np.float32):
         case = workloads.random_case(dk + dv + L, rank4_batch=(2, L), H=H, HV=HV, DK=dk, DV=dv, dtype=act, slots=(5,),
                                      qk_l2_norm=1, **RULES[0])
         step_and_check(case, dtype, tokens=L)
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("rule", [1, 6, 7])
+def test_several_tokens_with_per_key_factors(dtype, rule):
+    for act, dim, L in (("bf16", 128, 5), (np.float16, 40, 3), (np.float32, 256, 2)):
+        case = workloads.random_case(60 + rule, rank4_batch=(2, L), H=2, HV=4, DK=dim, DV=dim, dtype=act, slots=(4,), **RULES[rule])
+        step_and_check(case, dtype, tokens=L)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_tiny_and_huge_values_on_the_matrix_cores(dtype):
+    """States and values in fp16's denormal range, and keys whose planes are
+    scaled: products of small operands are not lost."""
+    for act, size, keys in ((np.float16, 2.0 ** -13, 1.0), ("bf16", 2.0 ** -13, 1.0), ("bf16", 1.0, 2.0 ** 9),
+                            ("bf16", 1.0, 2.0 ** -20), (np.float16, 1.0, 2.0 ** -6)):
+        case = workloads.random_case(95, rank4_batch=(2, 3), H=2, HV=2, DK=128, DV=64, dtype=act, slots=(3,), qk_l2_norm=1, **RULES[0])
+        to16 = (lambda x: x.astype(np.float16)) if act == np.float16 else (lambda x: x)
+        case["v"] = to16(np.asarray(case["v"], np.float32) * np.float32(size))
+        case["slab"] = case["slab"] * np.float32(size)
+        for name in ("q", "k"):
+            case[name] = to16(np.asarray(case[name], np.float32) * np.float32(keys))
+        step_and_check(case, dtype, tokens=3)
 
 
 @pytest.mark.parametrize("dtype", DT)
