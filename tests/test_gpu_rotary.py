@@ -164,6 +164,31 @@ def test_rows_around_a_result_stay():
     assert bool((rest == 3.0).all())
 
 
+def test_rows_past_32_bit_offsets():
+    """Views whose last rows lie past 2^31 elements."""
+    from gated_delta_rule_token_amd import api
+    T, stride = 70000, 40000
+    wide = torch.zeros(T, stride, dtype=torch.bfloat16, device="cuda")
+    c = dev(make(5, 16, 2, 1, 64, 64, "bf16", far=4096))
+    q, k = wide[:, 100:228].view(T, 2, 64), wide[:, 39900:39964].view(T, 1, 64)
+    q[-16:], k[-16:] = c["q"], c["k"]
+    pos = torch.zeros(T, dtype=torch.int32, device="cuda")
+    pos[-16:] = c["positions"]
+    want = call(c)
+    kw = dict(q_weight=c["q_weight"], k_weight=c["k_weight"])
+    got = api.qk_rotary(q, k, pos, c["inv_freq"], **kw)
+    assert torch.equal(got.q[-16:], want.q) and torch.equal(got.k[-16:], want.k) and not bool(got.q[:-16].any())
+    dq, dk = torch.zeros(T, 2, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(T, 1, 64, dtype=torch.bfloat16, device="cuda")
+    dq[-16:], dk[-16:] = want.q, want.k
+    small = back(c, want.q, want.k)
+    big = api.qk_rotary_backward(dq, dk, q, k, pos, c["inv_freq"], **kw)
+    assert torch.equal(big.q[-16:], small.q) and torch.equal(big.k[-16:], small.k)
+    api.qk_rotary(q, k, pos, c["inv_freq"], out=(q, k), **kw)  # in place
+    assert torch.equal(q[-16:], want.q) and torch.equal(k[-16:], want.k) and not bool(wide[:-16].any())
+    del wide, q, k
+    torch.cuda.empty_cache()
+
+
 def test_no_tokens_and_bad_axes():
     c = make(7, 0, 2, 1, 64, 64, "bf16")
     r = call(dev(c))
