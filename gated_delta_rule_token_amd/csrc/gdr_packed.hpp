@@ -327,7 +327,8 @@ __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packe
 // token takes 3 operations a value, which at 4 tokens is 1.5 times the memory's
 // time.  256 requests x 32 heads of 128, vector units and this, in us: 16 bits
 // 2 tokens 115 and 104, 4 tokens 157 and 108 (562 MB), 7 tokens 237 and 116;
-// 8 bits, 4 tokens 143 and 76; but single tokens 60 and 67 in 8 bits, 96 and 102
+// 8 bits, 4 tokens 143 and 76; 64 requests x 32 heads of 256, 4 tokens, 159 and 116
+// in 16 bits, 146 and 68 in 8; but single tokens 60 and 67 in 8 bits, 96 and 102
 // in 16, which the vector units take where every request has one.
 //
 // Operands.  The states are an operand as they are: 16-bit values, or codes
@@ -703,7 +704,7 @@ hipError_t packed_step_at(const PackedParams &a, int rule, bool per_key, hipStre
         return keyed ? launch_step<TA, TYPE, DK, true, true>(a, rule, per_key, 1, s)
                      : launch_step<TA, TYPE, DK, false, true>(a, rule, per_key, 1, s);
     if (keyed) return launch_step<TA, TYPE, DK, true, false>(a, rule, per_key, 1, s);
-    if constexpr (sizeof(TA) == 2 && DK <= 128) {
+    if constexpr (sizeof(TA) == 2) {
         if (p.dk == DK) {
             // Waves of a state: one, which spares the tokens' own work, until too few
             // states leave SIMDs idle: 2,048 waves, two a SIMD.  4 tokens, 32 heads of
