@@ -795,7 +795,7 @@ def _rotary_arguments(q, k, positions, inv_freq, axes, q_weight, k_weight, eps, 
     if max(heads, k_heads, dim, 2 * half, n_axes) >= 2 ** 31:
         raise GDRError("GDR_E_INVALID", "a size does not fit in 32 bits")
     return RotaryArguments(lead.numel(), heads, k_heads, dim, 2 * half, n_axes, 1 if interleaved else 0, 1 if norm else 0,
-                           code, weight, eps, q_stride, k_stride, q.data_ptr(), k_ptr, qw_ptr, kw_ptr,
+                           code, weight, float(eps), q_stride, k_stride, q.data_ptr(), k_ptr, qw_ptr, kw_ptr,
                            positions.data_ptr(), inv_freq.data_ptr(), axes_ptr)
 
 
@@ -1020,8 +1020,8 @@ def forward_packed(q, k, v, *, slab, slot_ids, gate=None, beta=None, erase=None,
         _fits(seq_lens, "seq_lens", i32, dev, (B,))
         lens_ptr = seq_lens.data_ptr()
     p = Problem(T, B, L, H, HV, dk, dv, slots, code, gate_code, RULES[update_rule], GATES[gate_activation],
-                BETAS[beta_activation], 1 if qk_l2_norm else 0, 1 if per_key else 0, 1 if rank4 else 0, chunk_size,
-                ALGOS[algo], 0, 1 if per_token else 0, scale, scan_segments)
+                BETAS[beta_activation], 1 if qk_l2_norm else 0, 1 if per_key else 0, 1 if rank4 else 0, int(chunk_size),
+                ALGOS[algo], 0, 1 if per_token else 0, float(scale), int(scan_segments))
     t = Tensors(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), gate_ptr, beta_ptr, erase_ptr, log_ptr, bias_ptr,
                 cu_ptr, slot_ids.data_ptr(), 0, 0, scale_ptr, lens_ptr)
     if workspace is not None:

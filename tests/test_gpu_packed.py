@@ -314,6 +314,55 @@ def test_tiny_and_huge_values_on_the_matrix_cores(dtype):
         step_and_check(case, dtype, tokens=3)
 
 
+@pytest.mark.parametrize("seed", range(36))
+def test_random_steps(seed):
+    """Any dims, heads, lengths, rules, activations and packings of short requests."""
+    rng = np.random.default_rng(1000 + seed)
+    dk = int(rng.choice([64, 128, 256, rng.integers(16, 257)]))
+    dv = int(rng.choice([64, 128, dk, rng.integers(1, 257)]))
+    H = int(rng.integers(1, 4))
+    B = int(rng.integers(1, 5))
+    rule = dict(RULES[int(rng.integers(len(RULES)))])
+    if rule["update_rule"] in ("gated", "gated_delta") and not rule.get("per_key") and rng.random() < 0.5:
+        rule.update(gate_activation="qwen", folded_scale=bool(rng.random() < 0.5))
+    packing = [dict(rank4_batch=(B, int(rng.integers(1, 9)))), dict(rank4_batch=(B, 1)),
+               dict(lengths=[int(n) for n in rng.integers(0, 13, B)])][int(rng.integers(3))]
+    if "lengths" in packing and sum(packing["lengths"]) > 8 * B:
+        packing["lengths"][0] = 0
+    act = [np.float16, "bf16", np.float32][int(rng.integers(3))]
+    case = workloads.random_case(2000 + seed, H=H, HV=H * int(rng.choice([1, 2, 3])), DK=dk, DV=dv, dtype=act, slots=(B + 2,),
+                                 qk_l2_norm=int(rng.random() < 0.5), **packing, **rule)
+    if "lengths" in packing and sum(packing["lengths"]) > 8 * B:
+        pytest.skip("a prompt")
+    if case["beta"] is not None and rng.random() < 0.3:
+        case["beta"] = np.ascontiguousarray(case["beta"][..., :1])  # one rate a token
+    step_and_check(case, ["f16", "bf16", "e4m3"][seed % 3], tokens=max(1, max(request_lengths(case))))
+
+
+@pytest.mark.parametrize("dtype", DT)
+def test_spellings_and_kernels_agree(dtype):
+    """Rank 3 with a token a request is rank 4 with one, to the bit; the other
+    kernels' results on unpacked states differ by their arithmetic alone."""
+    from gated_delta_rule_token_amd import api
+    case = workloads.random_case(96, rank4_batch=(5, 1), H=2, HV=4, DK=128, DV=128, dtype=np.float16, slots=(8,), **RULES[0])
+    d, args = gpu_tensors(case)
+    a, b, c = (slab_of(case["slab"], dtype) for _ in range(3))
+    oa = api.forward_packed(d["q"], d["k"], d["v"], slab=a, **args)
+    flat = {n: t[:, 0].contiguous() if n in ("gate", "beta") and t is not None else t for n, t in args.items()}
+    ob = api.forward_packed(d["q"][:, 0].contiguous(), d["k"][:, 0].contiguous(), d["v"][:, 0].contiguous(), slab=b, **flat)
+    assert torch.equal(oa[:, 0], ob) and same(a, b)
+    cu = torch.arange(6, dtype=torch.int32, device="cuda")
+    for kw in (dict(algo="recurrent"), dict(algo="decode"), dict(cu_seqlens=cu)):
+        rank4 = "cu_seqlens" not in kw
+        c = slab_of(case["slab"], dtype)
+        q, k, v = (d[n] if rank4 else d[n][:, 0].contiguous() for n in "qkv")
+        oc = api.forward_packed(q, k, v, slab=c, **dict(args if rank4 else flat, **kw))
+        assert float((oc.float().view(-1) - oa.float().view(-1)).abs().max()) <= 2e-3 * float(oa.float().abs().max())
+        x, y = read(c.data, c.scale), read(a.data, a.scale)
+        # a value may fall on the other side of a border between two codes
+        assert bool(((x - y).abs() <= 2.1 * HALF[dtype] * y.abs() + 1e-4 * y.abs().amax(-1, keepdim=True) + 2 * LEAST[dtype]).all())
+
+
 @pytest.mark.parametrize("dtype", DT)
 def test_ragged_requests_empty_ones_and_ids_out_of_range(dtype):
     case = workloads.random_case(70, lengths=[1, 0, 3, 1, 2, 0, 1, 9], H=2, HV=4, DK=128, DV=128, dtype=np.float16, slots=(12,), **RULES[0])
