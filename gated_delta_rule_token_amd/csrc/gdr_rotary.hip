@@ -119,17 +119,47 @@ __device__ __forceinline__ float row_sum(float x)
     return x;
 }
 
-// cos and sin of the angles of tokens t0 .. t0 + n - 1.
-__device__ __forceinline__ void angles(const RotaryParams &p, int64_t t0, int n, float *cs, float *sn)
+// Sine and cosine of `turns` whole turns, by the Taylor series within an eighth
+// of a turn (their first terms left out are under 3e-8).
+__device__ __forceinline__ void sincos_turns(double turns, float &sn, float &cs)
 {
-    for (int i = threadIdx.x; i < n * p.half; i += THREADS) {
-        const int token = i / p.half, f = i - token * p.half;
+    const float f = (float)(turns - rint(turns)), n = rintf(4.f * f), r = fmaf(n, -0.25f, f), y = r * r;
+    const float s = r * fmaf(y, fmaf(y, fmaf(y, fmaf(y, 42.058693944897653f, -76.705859753061386f), 81.605249276075054f),
+                                     -41.341702240399755f), 6.2831853071795865f);
+    const float c = fmaf(y, fmaf(y, fmaf(y, fmaf(y, 60.244641371876664f, -85.456817206693732f), 64.939394022668291f),
+                                 -19.739208802178716f), 1.f);
+    const int quarter = (int)n & 3;
+    const float a = quarter & 1 ? c : s, b = quarter & 1 ? s : c;
+    sn = quarter & 2 ? -a : a;
+    cs = (quarter + 1) & 2 ? -b : b;
+}
+
+// cos and sin of the angles of a workgroup's tokens: a thread takes one
+// frequency, and every groups-th token.  (With both found by division in a loop
+// over all pairs, and the library's sincospi, gradients of 40,021 tokens and one
+// head of q and k took 41 us.)
+struct Angles {
+    double turn;  // of a position
+    const int32_t *positions;
+    int f, group, groups;
+    __device__ __forceinline__ Angles(const RotaryParams &p)
+    {
+        groups = THREADS / p.half;
+        group = threadIdx.x / p.half;
+        f = threadIdx.x - group * p.half;
         int axis = p.axis_of ? p.axis_of[f] : 0;
         axis = axis < 0 ? 0 : axis < p.axes ? axis : p.axes - 1;
-        const double turns = (double)p.positions[axis * p.tokens + t0 + token] * ((double)p.freq[f] * 0.15915494309189535);
-        sincospif((float)(2 * (turns - rint(turns))), &sn[i], &cs[i]);
+        positions = p.positions + axis * p.tokens;
+        turn = (double)p.freq[f] * 0.15915494309189535;
     }
-}
+    // tokens t0 .. t0 + n - 1
+    __device__ __forceinline__ void fill(const RotaryParams &p, int64_t t0, int n, float *cs, float *sn) const
+    {
+        if (group >= groups) return;
+        for (int token = group; token < n; token += groups)
+            sincos_turns((double)positions[t0 + token] * turn, sn[token * p.half + f], cs[token * p.half + f]);
+    }
+};
 
 // A workgroup takes p.block tokens, all heads of q and then of k for each.
 template <typename T, typename TW, int VEC, int LPR, int NV>
@@ -157,8 +187,9 @@ __global__ __launch_bounds__(THREADS) void k_rotary(const RotaryParams p)
             x[v][1].load(row + (at.second ? at.at[1] : at.at[0]));
         }
     };
+    const Angles angles(p);
     if (token < n) fetch(token, head);
-    angles(p, t0, n, s_cos, s_sin);
+    angles.fill(p, t0, n, s_cos, s_sin);
     for (int i = threadIdx.x; i < 2 * p.dim; i += THREADS) {
         const int z = i >= p.dim, c = z ? i - p.dim : i;
         s_w[z][c] = p.part[z].weight ? to_f32(static_cast<const TW *>(p.part[z].weight)[c]) : 1.f;
@@ -219,6 +250,7 @@ __global__ __launch_bounds__(THREADS) void k_rotary_back(const RotaryParams p)
     const int heads = part.heads;
     if ((int)blockIdx.x >= part.blocks) return;
     float dw[NV][2 * VEC] = {};
+    const Angles angles(p);
     for (int i = threadIdx.x; i < p.dim; i += THREADS)
         s_w[i] = part.weight ? to_f32(static_cast<const TW *>(part.weight)[i]) : 1.f;
     const int step_t = ROWS / heads, step_h = ROWS - step_t * heads;
@@ -241,7 +273,7 @@ __global__ __launch_bounds__(THREADS) void k_rotary_back(const RotaryParams p)
         };
         if (token < n) fetch(token, head);
         lds_barrier();  // the last tokens' angles have been used
-        angles(p, t0, n, s_cos, s_sin);
+        angles.fill(p, t0, n, s_cos, s_sin);
         lds_barrier();
         while (token < n) {
             float h[NV][2 * VEC], g[NV][2 * VEC], sum = 0.f, dot = 0.f;
@@ -345,6 +377,7 @@ hipError_t by_form(const RotaryParams &p, F &&f)
     const auto fits = [&](int v) { return p.dim % (2 * v) == 0 && p.half % v == 0; };
     const auto lanes = [&](auto vec) {
         const int vectors = p.dim / (2 * vec());
+        if (vectors <= 4) return f(vec, integral_constant<int, 4>(), integral_constant<int, 1>());
         if (vectors <= 8) return f(vec, integral_constant<int, 8>(), integral_constant<int, 1>());
         if (vectors <= 16) return f(vec, integral_constant<int, 16>(), integral_constant<int, 1>());
         if constexpr (vec() < 8) {
