@@ -369,7 +369,7 @@ __global__ __launch_bounds__(1024) void k_rotary_back_sums(const RotaryParams p)
 // Vectors, lanes and vectors a lane of a head: vectors of 16, 8 or 4 bytes (16
 // and 8 in fp32) where the head and its turned part consist of whole pairs of
 // them, else single pairs.
-template <typename T, typename F>
+template <typename T, bool BACK, typename F>
 hipError_t by_form(const RotaryParams &p, F &&f)
 {
     using std::integral_constant;
@@ -377,6 +377,13 @@ hipError_t by_form(const RotaryParams &p, F &&f)
     const auto fits = [&](int v) { return p.dim % (2 * v) == 0 && p.half % v == 0; };
     const auto lanes = [&](auto vec) {
         const int vectors = p.dim / (2 * vec());
+        // Three vectors a lane where they fill more lanes (29,273 tokens, 32 heads of 72,
+        // 72 and 36 columns turned, in fp16 86 -> 74 and 114 -> 82 us; of 80 with 20
+        // 117 -> 97, gradients 198 -> 147; but gradients of 72 with 72 131 -> 159).
+        if constexpr (vec() < V && (!BACK || vec() <= 2)) {
+            if (vectors > 8 && vectors <= 12) return f(vec, integral_constant<int, 4>(), integral_constant<int, 3>());
+            if (vectors > 16 && vectors <= 24) return f(vec, integral_constant<int, 8>(), integral_constant<int, 3>());
+        }
         if (vectors <= 4) return f(vec, integral_constant<int, 4>(), integral_constant<int, 1>());
         if (vectors <= 8) return f(vec, integral_constant<int, 8>(), integral_constant<int, 1>());
         if (vectors <= 16) return f(vec, integral_constant<int, 16>(), integral_constant<int, 1>());
@@ -444,7 +451,7 @@ hipError_t launch_rotary(const RotaryParams &params, hipStream_t s)
     return by_types(p, [&](auto t, auto w) {
         using T = decltype(t);
         using TW = decltype(w);
-        return by_form<T>(p, [&](auto vec, auto lpr, auto nv) {
+        return by_form<T, false>(p, [&](auto vec, auto lpr, auto nv) {
             hipLaunchKernelGGL((k_rotary<T, TW, decltype(vec)::value, decltype(lpr)::value, decltype(nv)::value>),
                                blocks, dim3(THREADS), 0, s, p);
             return hipGetLastError();
@@ -467,7 +474,7 @@ hipError_t launch_rotary_backward(const RotaryParams &params, hipStream_t s)
         hipError_t err = by_types(p, [&](auto t, auto w) {
             using T = decltype(t);
             using TW = decltype(w);
-            return by_form<T>(p, [&](auto vec, auto lpr, auto nv) {
+            return by_form<T, true>(p, [&](auto vec, auto lpr, auto nv) {
                 hipLaunchKernelGGL((k_rotary_back<T, TW, decltype(vec)::value, decltype(lpr)::value, decltype(nv)::value>),
                                    blocks, dim3(THREADS), 0, s, p);
                 return hipGetLastError();
