@@ -860,8 +860,8 @@ def qk_rotary_backward(d_q_out, d_k_out, q, k, positions, inv_freq, *, axes=None
     elif d_k_out is not None:
         raise GDRError("GDR_E_INVALID", "d_k_out given without k")
     dq, q_stride, dk, k_stride = _rotary_out(out, q, k, r)
-    dqw = None if q_weight is None else torch.empty(q.shape[-1], dtype=torch.float32, device=dev)
-    dkw = None if k_weight is None else torch.empty(q.shape[-1], dtype=torch.float32, device=dev)
+    dqw = None if q_weight is None else torch.empty_like(q_weight, dtype=torch.float32)
+    dkw = None if k_weight is None else torch.empty_like(k_weight, dtype=torch.float32)
     if workspace is None and (dqw is not None or dkw is not None):
         n = ctypes.c_size_t(0)
         check(lib.gdr_qk_rotary_backward_workspace_size(ctypes.byref(r), ctypes.byref(n)))
