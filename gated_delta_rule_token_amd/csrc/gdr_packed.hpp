@@ -314,7 +314,7 @@ __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packe
 }
 
 // ---------------------------------------------------------------- 1 to 8 tokens, on the matrix cores
-// A request's tokens together, for 16-bit activations and one decay a head.
+// A request's tokens together.  First for 16-bit activations and one decay a head.
 // With S the packed states, x_n the vectors k_0 .. k_7, q_0 .. q_7 and
 // a_t the decays, per row
 //   z_n = S . x_n for all 16 n                         (matrix product)
@@ -341,6 +341,17 @@ __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packe
 // takes two planes itself.  The planes share one product: its 32 inner places
 // hold 8 tokens of four plane pairs.
 //
+// Any other call (GEN: fp32 activations, a decay for each key, the erase gate)
+// takes the decays into the vectors.  With D_t the product of the decays up to
+// token t (a vector over the keys), x_n is D_n o e_n o k_n and D_n o q_n, token
+// t's write enters a later x_n's dot by sum_j k_t (D_n / D_t) e_n k_n, and S by
+// d_t (D_T / D_t) o k_t: a lane forms these for its two keys, the quotients as
+// running products of the later decays, which do not overflow.  x_n in fp32 goes
+// in as planes (two of scaled fp16, three of bf16), k_t and d_t as two of bf16
+// each.  256 requests x 32 heads of 128, 4 tokens, vector units and this, in us: a
+// decay for each key on 16 and 8 bits 229 and 134, 210 and 124; fp32 activations
+// 211 and 130, 205 and 121.
+//
 // A tile is 16 rows: lane (c, kb) of a wave holds row c, 8 keys of every 32 (with
 // codes 16 of 64) at the kb-th place, which is the first product's operand; the
 // second product is transposed (keys by rows), with the keys in the order that
@@ -357,9 +368,36 @@ template <int N> __device__ __forceinline__ float lane_of(float x) { return dpp_
 
 __device__ __forceinline__ f4v mfma(h8 a, h8 b, f4v c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 __device__ __forceinline__ f4v mfma(b8 a, b8 b, f4v c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
-template <typename T> struct Vec8;
-template <> struct Vec8<half_t> { using V = h8; };
+template <typename T> struct Vec8 { using V = h8; };
 template <> struct Vec8<bf16_t> { using V = b8; };
+
+// Over a wave, to every lane.
+__device__ __forceinline__ float wave_sum(float x)
+{
+    x = sum16(x);
+    const auto past = [](float x, auto ctrl, auto rows) {  // other rows get 0
+        return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), ctrl(), rows(), 0xF, false));
+    };
+    x += past(x, std::integral_constant<int, 0x142>(), std::integral_constant<int, 0xA>());  // lane 15 of the row before
+    x += past(x, std::integral_constant<int, 0x143>(), std::integral_constant<int, 0xC>());  // lane 31
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
+}
+
+__device__ __forceinline__ float wave_max(float x)
+{
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) x = fmaxf(x, __shfl_xor(x, o));
+    return x;
+}
+
+// The power of two that brings `top` to [2^14, 2^15), and its inverse.
+__device__ __forceinline__ void half_scale(float top, float &up, float &back)
+{
+    int e = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127 - 14;
+    e = top > 0.f ? (e < -120 ? -120 : e > 120 ? 120 : e) : 0;
+    up = __builtin_bit_cast(float, (uint32_t)(127 - e) << 23);
+    back = __builtin_bit_cast(float, (uint32_t)(127 + e) << 23);
+}
 
 // Orders a wave's own LDS accesses: writes of other lanes before it, reads after.
 __device__ __forceinline__ void wave_sync()
@@ -390,24 +428,31 @@ __device__ __forceinline__ void exchange(w4 &x, w4 &y, bool odd)
 // itself (its LDS is its own), the next PRE of them on their way.  (At least two
 // waves a SIMD asked for: with one, products would accumulate in registers that
 // the vector units do not reach, 64 moves a tile.)
-template <typename TA, int TYPE, int DK, int PRE>
-__global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int rule, int waves)
+template <typename TA, int TYPE, int DK, int PRE, bool GEN>
+__global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int rule, int per_key, int waves)
 {
-    constexpr bool EIGHT = TYPE == CACHE_E4M3, BF = std::is_same<TA, bf16_t>::value;
+    constexpr bool EIGHT = TYPE == CACHE_E4M3, BF = !GEN && std::is_same<TA, bf16_t>::value;
     constexpr int KS = DK / 32, NV = EIGHT ? KS / 2 : KS, T = 8, ROW = DK * (EIGHT ? 1 : 2);
-    using TC = typename std::conditional<EIGHT, TA, typename CacheType<TYPE>::T>::type;  // type of the dots' operands
-    constexpr bool SAME = std::is_same<TC, TA>::value;
+    // type of the dots' operands, and planes of x
+    using TE = typename std::conditional<GEN, bf16_t, TA>::type;
+    using TC = typename std::conditional<EIGHT, TE, typename CacheType<TYPE>::T>::type;
+    constexpr bool CB = std::is_same<TC, bf16_t>::value, SAME = !GEN && std::is_same<TC, TA>::value;
+    constexpr int PX = GEN ? (CB ? 3 : 2) : SAME ? 1 : 2, PK = BF ? 1 : 2;
     using VA = typename Vec8<TA>::V;
     using VC = typename Vec8<TC>::V;
-    __shared__ __align__(16) bf16_t s_k4[4][BF ? 1 : 2][DK][T];
-    __shared__ __align__(16) float s_d4[4][T][16];
+    // a wave's k by keys (and before it, where x does not come from memory, x)
+    constexpr int K_BYTES = PK * DK * T * 2, X_BYTES = GEN ? PX * 16 * DK * 2 : 0;
+    __shared__ __align__(16) char s_kx4[4][K_BYTES > X_BYTES ? K_BYTES : X_BYTES];
+    __shared__ __align__(16) float s_d4[4][T][16], s_all4[4][GEN ? DK : 4];
     const Params &p = a.p;
     const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), gw = blockIdx.x * 4 + wid;
     const int bh = gw / waves, wave = gw - bh * waves;
     if (bh >= p.B * p.HV) return;
     const int b = bh / p.HV, h = bh - b * p.HV;
-    auto &s_k = s_k4[wid];
+    auto &s_k = *reinterpret_cast<bf16_t (*)[PK][DK][T]>(s_kx4[wid]);
+    auto &s_x = *reinterpret_cast<TC (*)[PX][16][DK]>(s_kx4[wid]);
     auto &s_d = s_d4[wid];
+    auto &s_all = s_all4[wid];
     const int slot = p.slot_ids[b];
     if (slot < 0 || slot >= p.num_slots) return;
     int64_t s, e;
@@ -423,7 +468,7 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
     const int own = c & 7, tt = own < n ? own : n - 1;
     const size_t th = (size_t)(s + tt) * p.HV + h;
     w4 xr[KS];
-    {
+    if constexpr (!GEN) {
         const TA *x = static_cast<const TA *>(c < 8 ? p.k : p.q) + ((size_t)(s + tt) * p.H + qh) * DK;
 #pragma unroll
         for (int f = 0; f < KS; ++f) xr[f] = *reinterpret_cast<const w4 *>(x + key(f, kb));
@@ -454,8 +499,127 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
 #pragma unroll
     for (int j = 0; j < PRE; ++j) fetch(j, wave + j * waves);
     const bool decays = rule_decays(rule), retrieves = rule_retrieves(rule);
-    const float alpha = decays ? expf(log_decay(p, th, h)) : 1.f;
     const float beta = rule_has_beta(rule) ? update_rate(p, th) : 1.f;
+    // x as operands; what z, d and the states are multiplied by
+    VC y[PX][KS];
+    float back = 1.f, al[T], cl[T], put[T], all = 1.f, oscale = p.scale, binv = retrieves ? beta : 0.f;
+    s_d[lane / 16][lane % 16] = 0.f;
+    s_d[4 + lane / 16][lane % 16] = 0.f;
+
+    if constexpr (GEN) {
+        // Lane: keys lane, lane + 64.  With D_t the product of the decays up to token t,
+        // x_n is D_n o (e_n o k_n), D_n o q_n, and the rest is relative to a token.
+        constexpr int KL = DK / 64;
+        const TA *q = static_cast<const TA *>(p.q), *k = static_cast<const TA *>(p.k);
+        float kv[T][KL], rv[T][KL], qv[T][KL], av[T][KL];
+        each([&](auto t_) {
+            constexpr int t = decltype(t_)::value;
+            if (t < n) {
+                const size_t tq = ((size_t)(s + t) * p.H + qh) * DK, tv = (size_t)(s + t) * p.HV + h;
+                float qq = 0.f, kk = 0.f;
+#pragma unroll
+                for (int m = 0; m < KL; ++m) {
+                    const int j = lane + 64 * m;
+                    kv[t][m] = to_f32(k[tq + j]);
+                    qv[t][m] = to_f32(q[tq + j]);
+                    av[t][m] = expf(per_key ? log_decay_key(p, tv, h, j) : decays ? log_decay(p, tv, h) : 0.f);
+                    rv[t][m] = p.erase ? p.erase[tv * DK + j] : 1.f;
+                    qq = fmaf(qv[t][m], qv[t][m], qq);
+                    kk = fmaf(kv[t][m], kv[t][m], kk);
+                }
+                if (p.qk_l2_norm) {
+                    const float inq = 1.f / sqrtf(wave_sum(qq) + 1e-12f), ink = 1.f / sqrtf(wave_sum(kk) + 1e-12f);
+#pragma unroll
+                    for (int m = 0; m < KL; ++m) {
+                        qv[t][m] *= inq;
+                        kv[t][m] *= ink;
+                    }
+                }
+#pragma unroll
+                for (int m = 0; m < KL; ++m) rv[t][m] *= kv[t][m];
+            }
+        }, std::make_integer_sequence<int, T>());
+        float gone[KL];
+#pragma unroll
+        for (int m = 0; m < KL; ++m) gone[m] = 1.f;
+        each([&](auto t_) {
+            constexpr int t = decltype(t_)::value;
+            if (t < n) {
+                float xr_[KL], xq_[KL], topr = 0.f, topq = 0.f, upr = 1.f, upq = 1.f, backr = 1.f, backq = 1.f;
+#pragma unroll
+                for (int m = 0; m < KL; ++m) {
+                    gone[m] *= av[t][m];
+                    xr_[m] = gone[m] * rv[t][m];
+                    xq_[m] = gone[m] * qv[t][m];
+                    topr = fmaxf(topr, fabsf(xr_[m]));
+                    topq = fmaxf(topq, fabsf(xq_[m]));
+                }
+                if constexpr (!CB) {
+                    half_scale(wave_max(topr), upr, backr);
+                    half_scale(wave_max(topq), upq, backq);
+                    back = c == t ? backr : c == 8 + t ? backq : back;
+                }
+#pragma unroll
+                for (int m = 0; m < KL; ++m) {
+                    float r = xr_[m] * upr, w = xq_[m] * upq;
+#pragma unroll
+                    for (int x = 0; x < PX; ++x) {
+                        const TC hr = from_f32<TC>(r), hq = from_f32<TC>(w);
+                        s_x[x][t][lane + 64 * m] = hr;
+                        s_x[x][8 + t][lane + 64 * m] = hq;
+                        r -= to_f32(hr);
+                        w -= to_f32(hq);
+                    }
+                }
+                cl[t] = 0.f;
+                float since[KL];  // decays after token t
+#pragma unroll
+                for (int m = 0; m < KL; ++m) since[m] = kv[t][m];
+                each([&](auto u_) {
+                    constexpr int u = decltype(u_)::value;
+                    if (u >= t && u < n) {
+                        float cr = 0.f, cq = 0.f;
+#pragma unroll
+                        for (int m = 0; m < KL; ++m) {
+                            if (u > t) since[m] *= av[u][m];
+                            cr = fmaf(since[m], rv[u][m], cr);
+                            cq = fmaf(since[m], qv[u][m], cq);
+                        }
+                        cq = wave_sum(cq);
+                        cl[t] = c == 8 + u ? cq : cl[t];
+                        if (u > t) {
+                            cr = wave_sum(cr);
+                            cl[t] = c == u ? cr : cl[t];
+                        }
+                    }
+                }, std::make_integer_sequence<int, T>());
+#pragma unroll
+                for (int m = 0; m < KL; ++m) kv[t][m] = since[m];
+            }
+        }, std::make_integer_sequence<int, T>());
+#pragma unroll
+        for (int m = 0; m < KL; ++m) s_all[lane + 64 * m] = gone[m];
+        wave_sync();
+#pragma unroll
+        for (int x = 0; x < PX; ++x)
+#pragma unroll
+            for (int f = 0; f < KS; ++f) y[x][f] = *reinterpret_cast<const VC *>(&s_x[x][c][key(f, kb)]);
+        wave_sync();
+#pragma unroll
+        for (int m = 0; m < KL; ++m) {
+            b8 hi, mid;
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                const float v = t < n ? kv[t][m] : 0.f;
+                hi[t] = from_f32<bf16_t>(v);
+                mid[t] = from_f32<bf16_t>(v - to_f32(hi[t]));
+            }
+            *reinterpret_cast<b8 *>(&s_k[0][lane + 64 * m][0]) = hi;
+            *reinterpret_cast<b8 *>(&s_k[PK - 1][lane + 64 * m][0]) = mid;
+        }
+        wave_sync();
+    } else {
+    const float alpha = decays ? expf(log_decay(p, th, h)) : 1.f;
 
     VA x[KS];
 #pragma unroll
@@ -472,14 +636,10 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
                 if constexpr (!BF) s_k[1][key(f, kb) + j][c] = from_f32<bf16_t>(kf - to_f32(hi));
             }
     }
-    s_d[lane / 16][lane % 16] = 0.f;
-    s_d[4 + lane / 16][lane % 16] = 0.f;
     f4v gram = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int f = 0; f < KS; ++f) gram = mfma(x[f], x[f], gram);
     // x as operands of the cache's type
-    VC y[SAME ? 1 : 2][KS];
-    float back = 1.f;
     if constexpr (SAME) {
 #pragma unroll
         for (int f = 0; f < KS; ++f) y[0][f] = __builtin_bit_cast(VC, xr[f]);
@@ -493,10 +653,7 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
                 for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(to_f32((TA)x[f][j])));
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
-            int e2 = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127 - 14;
-            e2 = top > 0.f ? (e2 < -120 ? -120 : e2 > 120 ? 120 : e2) : 0;
-            up = __builtin_bit_cast(float, (uint32_t)(127 - e2) << 23);
-            back = __builtin_bit_cast(float, (uint32_t)(127 + e2) << 23);
+            half_scale(top, up, back);
         }
 #pragma unroll
         for (int f = 0; f < KS; ++f)
@@ -514,7 +671,7 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
         const float mine = c % 4 == 0 ? gram[0] : c % 4 == 1 ? gram[1] : c % 4 == 2 ? gram[2] : gram[3];
         inv = 1.f / sqrtf(__shfl(mine, 16 * (c / 4) + c) + 1e-12f);
     }
-    float al[T], cl[T], all = 1.f, later = 1.f;
+    float later = 1.f;
     each([&](auto t_) {
         constexpr int t = decltype(t_)::value;
         if (t < n) {
@@ -526,13 +683,15 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
             if (t > own) later *= at;
         }
     }, std::make_integer_sequence<int, T>());
-    const float put_own = later * inv, oscale = p.scale * inv, binv = retrieves ? beta * inv : 0.f;
-    float put[T];
+    const float put_own = later * inv;
+    oscale = p.scale * inv;
+    binv = retrieves ? beta * inv : 0.f;
     each([&](auto t_) {
         constexpr int t = decltype(t_)::value;
         if (t < n) put[t] = lane_of<t>(put_own);
     }, std::make_integer_sequence<int, T>());
     wave_sync();
+    }
 
     for (int t0 = wave; t0 < tiles; t0 += PRE * waves)
 #pragma unroll
@@ -550,7 +709,7 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
                 if constexpr (EIGHT) {
                     const uint32_t w0 = raw[i][f / 2][f % 2 * 2], w1 = raw[i][f / 2][f % 2 * 2 + 1];
                     w4 o;
-                    if constexpr (BF) {
+                    if constexpr (CB) {
                         o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.f, false));
                         o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.f, true));
                         o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.f, false));
@@ -566,12 +725,13 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
                     const w4 o = raw[i][f];
                     sv = __builtin_bit_cast(VC, o);
                 }
-                if constexpr (SAME) {
+                if constexpr (PX == 1) {
                     if (f % 2) z1 = mfma(sv, y[0][f], z1);
                     else z = mfma(sv, y[0][f], z);
                 } else {
                     z = mfma(sv, y[0][f], z);
                     z1 = mfma(sv, y[1][f], z1);
+                    if constexpr (PX == 3) z1 = mfma(sv, y[2][f], z1);
                 }
             }
 #pragma unroll
@@ -580,14 +740,20 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
             float S[KS][8];
 #pragma unroll
             for (int f = 0; f < KS; ++f) {
+                f4v each_all[2];
+                if constexpr (GEN) {
+                    each_all[0] = *reinterpret_cast<const f4v *>(&s_all[key(f, kb)]);
+                    each_all[1] = *reinterpret_cast<const f4v *>(&s_all[key(f, kb) + 4]);
+                }
                 if constexpr (EIGHT) {
                     from_codes(raw[i][f / 2][f % 2 * 2], scale_of(ex[i]), &S[f][0]);
                     from_codes(raw[i][f / 2][f % 2 * 2 + 1], scale_of(ex[i]), &S[f][4]);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) S[f][j] *= all;
+                    for (int j = 0; j < 8; ++j) S[f][j] *= GEN ? each_all[j / 4][j % 4] : all;
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) S[f][j] = fmaf(half_of<TC>(raw[i][f][j / 2], j % 2), all, 0.f);
+                    for (int j = 0; j < 8; ++j)
+                        S[f][j] = fmaf(half_of<TC>(raw[i][f][j / 2], j % 2), GEN ? each_all[j / 4][j % 4] : all, 0.f);
                 }
             }
             float vj[4];
@@ -604,7 +770,7 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
                     float d[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        z[j] *= al[t];
+                        if constexpr (!GEN) z[j] *= al[t];
                         d[j] = retrieves ? fmaf(-binv, z[j], vj[j]) : vj[j];
                     }
                     if (c == t) *reinterpret_cast<f4v *>(&s_d[t][4 * kb]) = f4v{d[0], d[1], d[2], d[3]};
@@ -626,7 +792,7 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
             for (int t = 0; t < T; ++t) {
                 dv8[t] = from_f32<bf16_t>(0.f);
                 if (t < n) {
-                    float d = s_d[t][c] * put[t];
+                    float d = GEN ? s_d[t][c] : s_d[t][c] * put[t];
                     d -= plane1 ? to_f32(from_f32<bf16_t>(d)) : 0.f;
                     if constexpr (BF) {
                         d -= plane2 ? to_f32(from_f32<bf16_t>(d)) : 0.f;
@@ -703,25 +869,37 @@ hipError_t packed_step_at(const PackedParams &a, int rule, bool per_key, hipStre
     if (one)
         return keyed ? launch_step<TA, TYPE, DK, true, true>(a, rule, per_key, 1, s)
                      : launch_step<TA, TYPE, DK, false, true>(a, rule, per_key, 1, s);
-    if (keyed) return launch_step<TA, TYPE, DK, true, false>(a, rule, per_key, 1, s);
-    if constexpr (sizeof(TA) == 2) {
-        if (p.dk == DK) {
-            // Waves of a state: one, which spares the tokens' own work, until too few
-            // states leave SIMDs idle: 2,048 waves, two a SIMD.  4 tokens, 32 heads of
-            // 128, in us with 1,024, 2,048, 4,096 and 8,192 waves at least: 8-bit states of
-            // 32 requests 19.4, 16.0, 18.8 and 22.2, of 64 25.3, 25.5, 26.8 and 30.7;
-            // 16-bit ones 21.1, 20.8, 23.9 and 26.2, 32.1, 32.2, 36.5 and 37.2.
-            const int64_t states = (int64_t)p.B * p.HV;
-            int waves = 1;
-            while (waves < 8 && waves * 16 < p.dv && states * waves < 2048) waves *= 2;
-            const dim3 blocks((unsigned)((states * waves + 3) / 4));
-            hipLaunchKernelGGL((k_packed_few<TA, TYPE, DK, TYPE == CACHE_E4M3 ? 2 : 1>), blocks, dim3(256), 0, s, a, rule, waves);
-            hipError_t err = hipGetLastError();
-            if (err != hipSuccess || (p.cu_seqlens ? p.T : p.L) <= 8) return err;
-            return launch_step<TA, TYPE, DK, false, false>(a, rule, false, 9, s);  // requests of more than 8 tokens
+    // Up to 8 tokens on the matrix cores: 16-bit activations with one decay a head,
+    // or (to 128 keys, where its registers suffice) any.
+    constexpr bool PLAIN = sizeof(TA) == 2, ANY = DK <= 128;
+    const bool plain = PLAIN && !keyed;
+    if (p.dk == DK && (plain || ANY)) {
+        // Waves of a state: one, which spares the tokens' own work, until too few
+        // states leave SIMDs idle: 2,048 waves, two a SIMD.  4 tokens, 32 heads of
+        // 128, in us with 1,024, 2,048, 4,096 and 8,192 waves at least: 8-bit states of
+        // 32 requests 19.4, 16.0, 18.8 and 22.2, of 64 25.3, 25.5, 26.8 and 30.7;
+        // 16-bit ones 21.1, 20.8, 23.9 and 26.2, 32.1, 32.2, 36.5 and 37.2.
+        const int64_t states = (int64_t)p.B * p.HV;
+        int waves = 1;
+        while (waves < 8 && waves * 16 < p.dv && states * waves < 2048) waves *= 2;
+        const dim3 blocks((unsigned)((states * waves + 3) / 4)), threads(256);
+        constexpr int PRE = TYPE == CACHE_E4M3 ? 2 : 1;
+        if constexpr (PLAIN) {
+            if (plain)
+                hipLaunchKernelGGL((k_packed_few<TA, TYPE, DK, PRE, false>), blocks, threads, 0, s, a, rule, 0, waves);
         }
+        if constexpr (ANY) {
+            if (!plain)
+                hipLaunchKernelGGL((k_packed_few<TA, TYPE, DK, PRE, true>), blocks, threads, 0, s, a, rule, (int)per_key, waves);
+        }
+        hipError_t err = hipGetLastError();
+        if (err != hipSuccess || (p.cu_seqlens ? p.T : p.L) <= 8) return err;
+        // requests of more than 8 tokens
+        return keyed ? launch_step<TA, TYPE, DK, true, false>(a, rule, per_key, 9, s)
+                     : launch_step<TA, TYPE, DK, false, false>(a, rule, false, 9, s);
     }
-    return launch_step<TA, TYPE, DK, false, false>(a, rule, false, 1, s);
+    return keyed ? launch_step<TA, TYPE, DK, true, false>(a, rule, per_key, 1, s)
+                 : launch_step<TA, TYPE, DK, false, false>(a, rule, false, 1, s);
 }
 
 template <typename TA, int TYPE>
