@@ -731,12 +731,12 @@ gdr_status packed_params(int32_t batch, int32_t heads, int32_t dv, int32_t dk, i
 }
 
 // Whether a call on a packed slab runs as one pass over it: as pick_algo
-// chooses the decode kernel, with the key dims the pass takes.
+// chooses the decode kernel, with any dims.
 bool packed_step(const gdr_problem *p)
 {
     if (p->algo == GDR_ALGO_DECODE) return true;  // checked: dk = dv = 128
     const int64_t per_req = p->batch > 0 ? (p->total_tokens + p->batch - 1) / p->batch : 0;
-    return p->algo == GDR_ALGO_AUTO && gdr::packed_step_ok(p->head_dim_k) && per_req <= 8;
+    return p->algo == GDR_ALGO_AUTO && per_req <= 8;
 }
 
 // The call on fp32 states in the workspace: slot b of a slab of B.

@@ -71,12 +71,12 @@ template <typename T> __device__ __forceinline__ uint32_t two_halves(float a, fl
     return __builtin_bit_cast(uint16_t, from_f32<T>(a)) | (uint32_t)__builtin_bit_cast(uint16_t, from_f32<T>(b)) << 16;
 }
 
-// Over the LANES (4, 8 or 16) neighbours that hold a row.
+// Over the LANES (1, 4, 8 or 16) neighbours that hold a row.
 template <int LANES, typename Op>
 __device__ __forceinline__ float row_reduce(float x, Op op)
 {
-    x = op(x, dpp_mov<0xB1>(x));                            // lane ^ 1
-    x = op(x, dpp_mov<0x4E>(x));                            // lane ^ 2
+    if constexpr (LANES > 1) x = op(x, dpp_mov<0xB1>(x));   // lane ^ 1
+    if constexpr (LANES > 1) x = op(x, dpp_mov<0x4E>(x));   // lane ^ 2
     if constexpr (LANES > 4) x = op(x, dpp_mov<0x141>(x));  // i <-> 7 - i within 8
     if constexpr (LANES > 8) x = op(x, dpp_mov<0x140>(x));  // i <-> 15 - i within 16
     return x;
@@ -88,23 +88,25 @@ template <> struct CacheType<CACHE_BF16> { using T = bf16_t; };
 // ---------------------------------------------------------------- any tokens, on the vector units
 // LANES lanes hold a row, 16 values each: with e4m3 16 neighbouring bytes, with
 // 16 bits 8 values of each half of the row, so that every access is a 16-byte
-// vector and a wave's vectors are contiguous.  A wave holds G times 64 / LANES
-// rows.  With single tokens (ONE) each row group is widened, stepped and rounded
-// by itself, so few registers are live beside the packed values; more tokens
-// keep all groups in fp32 between them.
+// vector and a wave's vectors are contiguous.  To 16 keys that is a lane a row
+// (142 requests x 32 heads of 15 by 256 in 8 bits 49 us; 117 in the form of 64
+// keys).  A wave holds G times 64 / LANES rows.  With single tokens (ONE) each row
+// group is widened, stepped and rounded by itself, so few registers are live beside
+// the packed values; more tokens keep all groups in fp32 between them.
 // Bound by memory for single tokens (256 requests x 32 heads of 128): 8 bits
 // 60 us for 283 MB, 16 bits 96 us for 547 MB.  Waves and rows, in us for 8 and
 // 16 bits: 2 waves of 64 rows 60 and 109, 4 of 32 rows 63 and 104, 4 of 16 rows
 // 73 and 96; as the form for more tokens 68 and 102.
 template <int TYPE, int DK, bool ONE> struct StepForm {
     static constexpr bool EIGHT = TYPE == CACHE_E4M3;
-    static constexpr int WAVES = ONE && EIGHT ? 2 : 4;
+    static constexpr int WAVES = DK == 16 ? 1 : ONE && EIGHT ? 2 : 4;
     static constexpr int ROWS = DK == 128 && (EIGHT || !ONE) ? 128 : 64;  // of a workgroup
 };
 
-// EXACT: p.dk is DK; else it lies between 16 and DK, and a lane's vector that
-// would pass the row's end starts earlier: the columns that it then shares with
-// another lane count in that lane's sums only, and both write the same bytes.
+// EXACT: p.dk is DK; else it is less, and a lane's vector that would pass the
+// row's end starts earlier: the columns that it then shares with another lane
+// count in that lane's sums only, and both write the same bytes.  Rows of under
+// 16 values have a lane each, which takes them value by value.
 // Requests of fewer than `least` tokens are left alone.
 template <typename TA, int TYPE, int DK, bool VD, bool ONE, bool EXACT>
 __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packed_step(const PackedParams a, int rule,
@@ -129,25 +131,35 @@ __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packe
     const int qh = (int)(((int64_t)h * p.H) / p.HV);
     const bool retrieves = rule_retrieves(rule), decays = rule_decays(rule), rate = rule_has_beta(rule);
     // this lane's vectors: the first column, and how many of the columns are another lane's
+    constexpr bool narrow = !EXACT && DK == 16;
     int at[V], others[V];
 #pragma unroll
     for (int n = 0; n < V; ++n) {
         const int want = n * (DK / 2) + l * VC;
-        at[n] = EXACT || want + VC <= dk ? want : dk - VC;
+        at[n] = EXACT || narrow || want + VC <= dk ? want : dk - VC;
         others[n] = EXACT ? 0 : want - at[n];
     }
     const auto column = [&](int c) { return at[c / VC] + c % VC; };
-    const auto own = [&](int c) { return EXACT || c % VC >= others[c / VC]; };
+    const auto own = [&](int c) { return EXACT || (narrow ? column(c) < dk : c % VC >= others[c / VC]); };
     const auto add = [](float x, float y) { return x + y; };
     const TA *q = static_cast<const TA *>(p.q), *k = static_cast<const TA *>(p.k), *v = static_cast<const TA *>(p.v);
     TA *o = static_cast<TA *>(p.o);
 
     // Eight neighbouring values of q or k as they lie in memory.
     struct Eight { w4 w[sizeof(TA) / 2]; };
-    const auto load8 = [](const TA *src) {
+    const auto load8 = [&](const TA *row, int col) {
         Eight x;
+        if constexpr (narrow) {
 #pragma unroll
-        for (unsigned i = 0; i < sizeof(TA) / 2; ++i) x.w[i] = reinterpret_cast<const Any4 *>(src)[i];
+            for (int i = 0; i < 8; ++i) {
+                const TA v = col + i < dk ? row[col + i] : from_f32<TA>(0.f);
+                if constexpr (sizeof(TA) == 4) x.w[i / 4][i % 4] = __builtin_bit_cast(uint32_t, v);
+                else x.w[0][i / 2] = (i % 2 ? x.w[0][i / 2] : 0) | (uint32_t)__builtin_bit_cast(uint16_t, v) << (16 * (i % 2));
+            }
+        } else {
+#pragma unroll
+            for (unsigned i = 0; i < sizeof(TA) / 2; ++i) x.w[i] = reinterpret_cast<const Any4 *>(row + col)[i];
+        }
         return x;
     };
     const auto get8 = [](const Eight &x, int i) {
@@ -160,8 +172,8 @@ __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packe
         const TA *qr = q + (t * p.H + qh) * dk, *kr = k + (t * p.H + qh) * dk;
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-            qw[n] = load8(qr + column(8 * n));
-            kw[n] = load8(kr + column(8 * n));
+            qw[n] = load8(qr, column(8 * n));
+            kw[n] = load8(kr, column(8 * n));
         }
 #pragma unroll
         for (int g = 0; g < G; ++g) {
@@ -179,7 +191,19 @@ __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packe
         const int row = row0 + g * RPW, from = row < p.dv ? row : p.dv - 1;
         const char *src = static_cast<const char *>(a.data) + (head + from) * ROW;
 #pragma unroll
-        for (int n = 0; n < V; ++n) raw[g][n] = __builtin_nontemporal_load(reinterpret_cast<const Any4 *>(src + at[n] * (16 / VC)));
+        for (int n = 0; n < V; ++n) {
+            if constexpr (narrow) {
+                using Code = typename std::conditional<EIGHT, uint8_t, uint16_t>::type;
+                constexpr int PER = 4 / sizeof(Code);  // values of a word
+#pragma unroll
+                for (int i = 0; i < VC; ++i) {
+                    const uint32_t v = at[n] + i < dk ? reinterpret_cast<const Code *>(src)[at[n] + i] : 0;
+                    raw[g][n][i / PER] = (i % PER ? raw[g][n][i / PER] : 0) | v << (32 / PER * (i % PER));
+                }
+            } else {
+                raw[g][n] = __builtin_nontemporal_load(reinterpret_cast<const Any4 *>(src + at[n] * (16 / VC)));
+            }
+        }
         ex[g] = EIGHT ? a.scale[head + from] : 0;
     }
     const auto widen = [&](int g, float (&S)[C]) {
@@ -209,8 +233,17 @@ __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packe
         if (row >= p.dv) return;
         char *dst = static_cast<char *>(a.data) + (head + row) * ROW;
 #pragma unroll
-        for (int n = 0; n < V; ++n)
-            if (EXACT || others[n] < VC) __builtin_nontemporal_store(out[n], reinterpret_cast<Any4 *>(dst + at[n] * (16 / VC)));
+        for (int n = 0; n < V; ++n) {
+            if constexpr (narrow) {
+                using Code = typename std::conditional<EIGHT, uint8_t, uint16_t>::type;
+                constexpr int PER = 4 / sizeof(Code);
+#pragma unroll
+                for (int i = 0; i < VC; ++i)
+                    if (at[n] + i < dk) reinterpret_cast<Code *>(dst)[at[n] + i] = (Code)(out[n][i / PER] >> (32 / PER * (i % PER)));
+            } else if (EXACT || others[n] < VC) {
+                __builtin_nontemporal_store(out[n], reinterpret_cast<Any4 *>(dst + at[n] * (16 / VC)));
+            }
+        }
         if (EIGHT && l == 0) a.scale[head + row] = (uint8_t)eo;
     };
 
@@ -264,8 +297,9 @@ __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packe
             if (!ONE && t + 1 < e) stage(t + 1);
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                av[c] = s_decay[(t - s) & 1][column(c)];
-                kb[c] = av[c] * kb[c] * s_erase[(t - s) & 1][column(c)];
+                const int j = EXACT || column(c) < dk ? column(c) : 0;
+                av[c] = s_decay[(t - s) & 1][j];
+                kb[c] = av[c] * kb[c] * s_erase[(t - s) & 1][j];
                 qv[c] *= av[c];
             }
         }
@@ -871,7 +905,7 @@ hipError_t packed_step_at(const PackedParams &a, int rule, bool per_key, hipStre
                      : launch_step<TA, TYPE, DK, false, true>(a, rule, per_key, 1, s);
     // Up to 8 tokens on the matrix cores: 16-bit activations with one decay a head,
     // or (to 128 keys, where its registers suffice) any.
-    constexpr bool PLAIN = sizeof(TA) == 2, ANY = DK <= 128;
+    constexpr bool PLAIN = DK >= 64 && sizeof(TA) == 2, ANY = DK >= 64 && DK <= 128;
     const bool plain = PLAIN && !keyed;
     if (p.dk == DK && (plain || ANY)) {
         // Waves of a state: one, which spares the tokens' own work, until too few
@@ -905,6 +939,7 @@ hipError_t packed_step_at(const PackedParams &a, int rule, bool per_key, hipStre
 template <typename TA, int TYPE>
 hipError_t packed_step_by_dk(const PackedParams &a, int rule, bool per_key, hipStream_t s)
 {
+    if (a.p.dk <= 16) return packed_step_at<TA, TYPE, 16>(a, rule, per_key, s);
     if (a.p.dk <= 64) return packed_step_at<TA, TYPE, 64>(a, rule, per_key, s);
     if (a.p.dk <= 128) return packed_step_at<TA, TYPE, 128>(a, rule, per_key, s);
     return packed_step_at<TA, TYPE, 256>(a, rule, per_key, s);

@@ -21,9 +21,6 @@ struct PackedParams {
     int32_t skip_empty;  // pack: requests without tokens keep their slots
 };
 
-// Head dims of the keys that the step's kernel takes (up to 256): a row holds a
-// lane's vector at least.
-constexpr bool packed_step_ok(int dk) { return dk >= 16; }
 int64_t pack_blocks(int batch, int heads, int dv);
 
 hipError_t launch_pack(const PackedParams &a, hipStream_t s);

@@ -207,10 +207,10 @@ def test_forward_packed_workspace(lib):
     state = 4 * 4 * 128 * 128 * 4
     assert size() == 0 and size(seq_len=8, total_tokens=32) == 0
     assert size(head_dim_k=64) == 0 and size(head_dim_k=256, head_dim_v=72) == 0  # one pass
-    assert size(head_dim_k=72) == 0 and size(head_dim_k=16) == 0
-    assert size(batch=0, total_tokens=0, head_dim_k=9) == 0
+    assert size(head_dim_k=72) == 0 and size(head_dim_k=1, head_dim_v=9) == 0
+    assert size(batch=0, total_tokens=0, algo=1) == 0
     assert size(seq_len=9, total_tokens=36) >= state  # fp32 states in the workspace
-    assert 0 < size(head_dim_k=9) < state and size(head_dim_k=15) > 0
+    assert 0 < size(head_dim_k=9, seq_len=9, total_tokens=36) < state and size(algo=1) >= state
     long = size(seq_len=4096, total_tokens=4 * 4096)
     p, _ = _step(dict(seq_len=4096, total_tokens=4 * 4096, num_slots=4))
     assert long == api.workspace_size(p) + state + 256
