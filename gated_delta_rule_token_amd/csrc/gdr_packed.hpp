@@ -808,8 +808,12 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
                         d[j] = retrieves ? fmaf(-binv, z[j], vj[j]) : vj[j];
                     }
                     if (c == t) *reinterpret_cast<f4v *>(&s_d[t][4 * kb]) = f4v{d[0], d[1], d[2], d[3]};
+                    // (not into a q of a token before t: nothing of t, a NaN neither, reaches that output)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) z[j] = fmaf(lane_of<t>(d[j]), cl[t], z[j]);
+                    for (int j = 0; j < 4; ++j) {
+                        const float dt = lane_of<t>(d[j]);
+                        z[j] = t > 0 && c >= 8 && c < 8 + t ? z[j] : fmaf(dt, cl[t], z[j]);
+                    }
                 }
             }, std::make_integer_sequence<int, T>());
             if (c >= 8 && c - 8 < n) {

@@ -316,6 +316,81 @@ def test_tiny_and_huge_values_on_the_matrix_cores(dtype):
         step_and_check(case, dtype, tokens=3)
 
 
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("act", [np.float16, "bf16", np.float32])
+@pytest.mark.parametrize("dk,rule", [(128, 0), (64, 0), (256, 0), (40, 0), (128, 1), (64, 6), (9, 7)])
+def test_nan_and_infinities_reach_later_tokens_only(dtype, act, dk, rule):
+    """What a token brings does not reach the outputs before it, other requests,
+    or, through v, other rows; what its q holds reaches its own output alone."""
+    from gated_delta_rule_token_amd import api
+    case = workloads.random_case(97, rank4_batch=(2, 5), H=1, HV=2, DK=dk, DV=40, dtype=act, slots=(4,), **RULES[rule])
+    d, args = gpu_tensors(case)
+    one, other = (int(i) for i in case["slot_ids"])
+
+    def run(name=None, where=None, value=0.0):
+        a, x = dict(args), {n: d[n] for n in ("q", "k", "v")}
+        if name is not None:
+            bad = (x[name] if name in x else a[name]).clone()
+            bad[where] = value
+            (x if name in x else a)[name] = bad
+        slab = slab_of(case["slab"], dtype)
+        o = api.forward_packed(x["q"], x["k"], x["v"], slab=slab, **a)
+        return o, bits(slab.data), None if slab.scale is None else bits(slab.scale)
+
+    o, data, scale = run()
+    for value in (float("nan"), float("inf")):
+        for name in ("q", "k", "v", "gate", "beta", "erase"):
+            if name not in ("q", "k", "v") and args[name] is None:
+                continue
+            oo, dd, ss = run(name, (0, 3, 0, 3) if name in ("q", "k", "v") else (0, 3, 0), value)
+            assert torch.equal(bits(oo[0, :3]), bits(o[0, :3])) and torch.equal(bits(oo[1]), bits(o[1])), name
+            assert torch.equal(dd[other], data[other]) and (scale is None or torch.equal(ss[other], scale[other])), name
+            assert value == float("inf") or not bool(oo[0, 3:].isfinite().all()), name  # (an infinite gate forgets)
+            if name == "v":
+                rows = torch.arange(40) != 3
+                assert torch.equal(bits(oo[0][..., rows]), bits(o[0][..., rows])) and torch.equal(dd[one][:, rows], data[one][:, rows])
+                assert torch.equal(dd[one, 1], data[one, 1])
+            if name == "q":
+                assert torch.equal(dd, data) and torch.equal(bits(oo[0, 4]), bits(o[0, 4]))
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("act,dk,rule", [("bf16", 128, 0), (np.float32, 64, 0), (np.float16, 64, 1), (np.float16, 72, 0), ("bf16", 5, 6)])
+@pytest.mark.parametrize("algo", ["auto", "recurrent"])
+def test_padding_is_neither_read_nor_written(dtype, act, dk, rule, algo):
+    """Tokens past seq_lens, before the first and behind the last packed request."""
+    from gated_delta_rule_token_amd import api
+    case = workloads.random_case(98, rank4_batch=(3, 6), H=1, HV=2, DK=dk, DV=24, dtype=act, slots=(5,), **RULES[rule])
+    d, args = gpu_tensors(case)
+    names = ("q", "k", "v", "gate", "beta", "erase")
+
+    def run(used, o, flat, **kw):
+        x = {}
+        for n in names:
+            t = d[n] if n in d and d[n] is not None else None
+            if t is not None:
+                t = t.flatten(0, 1)
+                t = torch.where(used.view(-1, *[1] * (t.dim() - 1)), t, torch.full_like(t, float("nan")))
+                t = t.contiguous() if flat else t.unflatten(0, (3, 6)).contiguous()
+            x[n] = t
+        a = dict(args, algo=algo, out=o, **kw)
+        a.update({n: x[n] for n in names[3:]})
+        slab = slab_of(case["slab"], dtype)
+        api.forward_packed(x["q"], x["k"], x["v"], slab=slab, **a)
+        return o, slab
+
+    at = torch.arange(18, device="cuda")
+    used = at % 6 < torch.tensor([4, 0, 6], device="cuda")[at // 6]
+    like = d["v"]
+    runs = [run(used, torch.full_like(like, 7.0), False, seq_lens=ids(4, 0, 6))]
+    gap = (at >= 2) & (at < 9)
+    runs.append(run(gap, torch.full_like(like, 7.0).flatten(0, 1), True, cu_seqlens=ids(2, 2, 5, 9)))
+    for (o, slab), u in zip(runs, (used, gap)):
+        o = o.reshape(18, 2, 24)
+        assert bool(o[u].isfinite().all()) and bool((o[~u] == 7).all())
+        assert bool(read(slab.data, slab.scale).isfinite().all())
+
+
 @pytest.mark.parametrize("seed", range(36))
 def test_random_steps(seed):
     """Any dims, heads, lengths, rules, activations and packings of short requests."""
