@@ -554,7 +554,7 @@ bool aligned_to(const void *p, size_t bytes) { return reinterpret_cast<uintptr_t
 gdr_status check_rotary(const gdr_rotary *r)
 {
     if (!r) return fail(GDR_E_INVALID, "rotary is NULL");
-    if (r->tokens < 0 || r->tokens > INT32_MAX) return fail(GDR_E_INVALID, "tokens must lie in [0, 2^31 - 1]");
+    if (r->tokens < 0 || r->tokens >= 1 << 28) return fail(GDR_E_INVALID, "tokens must lie in [0, 2^28 - 1]");
     if (r->heads_q < 1 || r->heads_k < 0 || r->heads_q > 65536 || r->heads_k > 65536)
         return fail(GDR_E_INVALID, "heads_q must lie in [1, 65536] and heads_k in [0, 65536]");
     if (r->head_dim < 2 || r->head_dim > gdr::ROTARY_MAX_DIM)
@@ -702,7 +702,7 @@ gdr_status packed_params(int32_t batch, int32_t heads, int32_t dv, int32_t dk, i
     if (st != GDR_OK) return st;
     if (batch < 0 || heads < 1 || num_slots < 0) return fail(GDR_E_INVALID, "batch and num_slots must be >= 0, heads >= 1");
     if (dk < 1 || dk > 256 || dv < 1 || dv > 256) return fail(GDR_E_INVALID, "head dims must lie in [1, 256] (dk=%d, dv=%d)", dk, dv);
-    if (gdr::pack_blocks(batch, heads, dv) > INT32_MAX) return fail(GDR_E_INVALID, "batch * heads too large");
+    if (gdr::pack_blocks(batch, heads, dv) > gdr::PACK_BLOCKS_MAX) return fail(GDR_E_INVALID, "batch * heads * dv too large");
     if (batch == 0 || num_slots == 0) return GDR_OK;
     st = check_slab_pointers(slab);
     if (st != GDR_OK) return st;
@@ -1172,6 +1172,8 @@ gdr_status gdr_forward_packed(const gdr_problem *problem, const gdr_tensors *ten
     st = check_slab(slab);
     if (st != GDR_OK) return st;
     if (problem->num_slots < 1) return fail(GDR_E_INVALID, "a packed slab needs num_slots >= 1");
+    if (gdr::pack_blocks(problem->batch, problem->num_heads_v, problem->head_dim_v) > gdr::PACK_BLOCKS_MAX)
+        return fail(GDR_E_INVALID, "batch * num_heads_v * head_dim_v too large");
     if (tensors->initial_state || tensors->final_state)
         return fail(GDR_E_INVALID, "with a packed slab initial_state and final_state must be NULL");
     if (problem->batch == 0) return GDR_OK;  // slot_ids has no entries, and may be NULL

@@ -21,7 +21,10 @@ struct PackedParams {
     int32_t skip_empty;  // pack: requests without tokens keep their slots
 };
 
+// Workgroups of pack and unpack; a step takes no more.  A launch has fewer than
+// 2^32 threads, 256 a workgroup.
 int64_t pack_blocks(int batch, int heads, int dv);
+constexpr int64_t PACK_BLOCKS_MAX = (int64_t{1} << 24) - 1;
 
 hipError_t launch_pack(const PackedParams &a, hipStream_t s);
 hipError_t launch_unpack(const PackedParams &a, hipStream_t s);

@@ -237,9 +237,10 @@ __global__ __launch_bounds__(THREADS) void k_rotary(const RotaryParams p)
     }
 }
 
-// blockIdx.y: q or k.  A workgroup takes part.block tokens at a time; the weight's gradient stays in a lane's registers, as its
-// columns are the same for every row, and its sums over the workgroup's rows
-// and then over the workgroups have a fixed order.
+// blockIdx.y: q or k.  A workgroup takes part.block tokens at a time; the
+// weight's gradient stays in a lane's registers, as its columns are the same for
+// every row, and its sums over the workgroup's rows and then over the workgroups
+// have a fixed order.
 template <typename T, typename TW, int VEC, int LPR, int NV>
 __global__ __launch_bounds__(THREADS) void k_rotary_back(const RotaryParams p)
 {
@@ -448,6 +449,7 @@ hipError_t launch_rotary(const RotaryParams &params, hipStream_t s)
     const int64_t spread = (p.tokens + 511) / 512;  // few tokens: a workgroup each
     if (p.block > spread) p.block = (int)spread;
     const dim3 blocks((unsigned)((p.tokens + p.block - 1) / p.block));
+    if (blocks.x >= 1u << 24) return hipErrorInvalidConfiguration;  // a launch has fewer than 2^32 threads
     return by_types(p, [&](auto t, auto w) {
         using T = decltype(t);
         using TW = decltype(w);

@@ -374,16 +374,16 @@ gdr_status gdr_rms_norm_backward(int64_t rows, int32_t width, int32_t dtype, int
  * where a pair is columns (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with
  * interleaved; the other columns pass.  Several axes (time, height, width)
  * have a row of positions each.  The angle is the exact product of its int32
- * and fp32 factors to within 1e-6, at any position; arithmetic is in fp32 and
- * rounded to nearest once, on store.  An axis_of entry outside [0, axes) counts
- * as the nearest that is inside.  NaN and infinities stay in their heads (a
- * norm spreads them over the head).
+ * and fp32 factors to within 1e-6 up to 2^31 in magnitude (any position, at
+ * frequencies to 1); arithmetic is in fp32 and rounded to nearest once, on store.
+ * An axis_of entry outside [0, axes) counts as the nearest that is inside.  NaN
+ * and infinities stay in their heads (a norm spreads them over the head).
  *
  * q and k may be views of one projection's output: q_stride and k_stride count
  * elements from token to token (at least heads * head_dim; a token's heads lie
  * one after the other), and tensors need the alignment of their elements only. */
 typedef struct {
-    int64_t tokens;
+    int64_t tokens;             /* below 2^28 */
     int32_t heads_q, heads_k;   /* heads_q >= 1, heads_k >= 0, 65,536 at most */
     int32_t head_dim;           /* 2 to 256 */
     int32_t rotary_dim;         /* even, 2 to head_dim */
@@ -431,10 +431,11 @@ gdr_status gdr_qk_rotary_backward(const gdr_rotary *rotary, const void *d_q_out,
  * not below -100 (a row of zeros has that).  Values are rounded to nearest
  * even whenever a state is written.  fp16 holds magnitudes up to 65,504 (more
  * becomes an infinity); in e4m3 an infinity becomes NaN, a NaN stays in its
- * place, and what rounds to 2^128 (above 1.9375 * 2^127) reads as an infinity.  Each call that updates a state rounds it anew, by up to 2^-11 (fp16),
- * 2^-8 (bf16) or 2^-4 (e4m3) of a value; a decay a per token lets the errors of
- * about 1 / (1 - a^2) calls stand side by side, so 8 bits suit parked states
- * and heads that forget, 16 bits any decoding.
+ * place, and what rounds to 2^128 (above 1.9375 * 2^127) reads as an infinity.
+ * Each call that updates a state rounds it anew, by up to 2^-11 (fp16), 2^-8
+ * (bf16) or 2^-4 (e4m3) of a value; a decay a per token lets the errors of about
+ * 1 / (1 - a^2) calls stand side by side, so 8 bits suit parked states and heads
+ * that forget, 16 bits any decoding.
  * data and states are 16-byte aligned, slab, slot ids and their contract as in
  * gdr_forward. */
 typedef struct {
@@ -455,9 +456,10 @@ gdr_status gdr_state_unpack(int32_t batch, int32_t heads, int32_t dv, int32_t dk
  * slab's, tensors->slot_ids is required, tensors->initial_state and final_state
  * are NULL.  The states are read, updated in fp32 over all tokens of their
  * request and rounded once, on the way back; a request without tokens leaves
- * its states as they are.  Few tokens a request (8 on average) run in one
- * pass over the packed states, without workspace; longer requests (or algo
- * RECURRENT or CHUNKED) run gdr_forward's kernels on fp32 states in the workspace. */
+ * its states as they are.  An infinity that a token brings may make its rows'
+ * states NaN.  Few tokens a request (8 on average) run in one pass over the
+ * packed states, without workspace; longer requests (or algo RECURRENT or
+ * CHUNKED) run gdr_forward's kernels on fp32 states in the workspace. */
 gdr_status gdr_packed_workspace_size(const gdr_problem *problem, size_t *bytes);
 gdr_status gdr_forward_packed(const gdr_problem *problem, const gdr_tensors *tensors, const gdr_packed_slab *slab,
                               void *workspace, size_t workspace_bytes, void *stream);

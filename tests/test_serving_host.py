@@ -35,6 +35,7 @@ def _rotary(**over):
 
 BAD_ROTARY = [
     ("tokens", dict(tokens=-1), api.GDR_E_INVALID), ("tokens_past_32_bits", dict(tokens=2 ** 31), api.GDR_E_INVALID),
+    ("tokens_past_a_launch", dict(tokens=2 ** 28), api.GDR_E_INVALID),
     ("no_heads", dict(heads_q=0), api.GDR_E_INVALID), ("many_heads", dict(heads_q=65537), api.GDR_E_INVALID),
     ("dim", dict(head_dim=257), api.GDR_E_INVALID), ("odd_rotary", dict(rotary_dim=15), api.GDR_E_INVALID),
     ("no_rotary", dict(rotary_dim=0), api.GDR_E_INVALID), ("rotary_past_dim", dict(rotary_dim=34), api.GDR_E_INVALID),
@@ -143,7 +144,8 @@ def _pack(lib, slab, **over):
     (dict(dtype=api.F16), {}, api.GDR_E_INVALID), (dict(data=_fake(30) + 8), {}, api.GDR_E_INVALID),
     ({}, dict(batch=-1), api.GDR_E_INVALID), ({}, dict(heads=0), api.GDR_E_INVALID), ({}, dict(dk=257), api.GDR_E_INVALID),
     ({}, dict(dv=0), api.GDR_E_INVALID), ({}, dict(slots=-1), api.GDR_E_INVALID),
-    ({}, dict(batch=2 ** 30, heads=2 ** 20), api.GDR_E_INVALID), ({}, dict(states=None), api.GDR_E_INVALID),
+    ({}, dict(batch=2 ** 30, heads=2 ** 20), api.GDR_E_INVALID),
+    ({}, dict(batch=2 ** 19, heads=32), api.GDR_E_INVALID), ({}, dict(states=None), api.GDR_E_INVALID),
     ({}, dict(ids=None), api.GDR_E_INVALID), ({}, dict(states=_fake(32) + 4), api.GDR_E_INVALID),
     ({}, dict(states=_fake(30)), api.GDR_E_ALIAS), ({}, dict(states=_fake(31) - 4096), api.GDR_E_ALIAS),
     ({}, dict(batch=0), api.GDR_OK), ({}, dict(slots=0), api.GDR_OK),
@@ -186,6 +188,7 @@ def _step(problem=(), tensors=()):
     ("data_over_ids", (), dict(slot_ids=_fake(30)), {}, api.GDR_E_ALIAS),
     ("scales_over_data", (), (), dict(scale=_fake(30) + 64), api.GDR_E_ALIAS),
     ("decode_of_other_dims", dict(algo=2, head_dim_k=64), (), {}, api.GDR_E_UNSUPPORTED),
+    ("more_than_a_launch", dict(batch=2 ** 20, total_tokens=2 ** 20), (), {}, api.GDR_E_INVALID),
     ("no_workspace", dict(seq_len=9, total_tokens=36), (), {}, api.GDR_E_WORKSPACE),
 ])
 def test_forward_packed_refuses(lib, name, problem, tensors, slab, status):
