@@ -405,23 +405,27 @@ __device__ __forceinline__ f4v mfma(b8 a, b8 b, f4v c) { return __builtin_amdgcn
 template <typename T> struct Vec8 { using V = h8; };
 template <> struct Vec8<bf16_t> { using V = b8; };
 
-// Over a wave, to every lane.
-__device__ __forceinline__ float wave_sum(float x)
-{
-    x = sum16(x);
-    const auto past = [](float x, auto ctrl, auto rows) {  // other rows get 0
-        return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), ctrl(), rows(), 0xF, false));
-    };
-    x += past(x, std::integral_constant<int, 0x142>(), std::integral_constant<int, 0xA>());  // lane 15 of the row before
-    x += past(x, std::integral_constant<int, 0x143>(), std::integral_constant<int, 0xC>());  // lane 31
-    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
-}
-
-__device__ __forceinline__ float wave_max(float x)
+// Sixteen values over a wave: lane (c, any) gets the c-th.  At each step a lane
+// keeps half of its values, those that its place in 16 names, and gives its
+// partner the others: 45 operations where 16 reductions take 128.
+template <int N, int CTRL, typename Op> __device__ __forceinline__ void fold(float (&v)[16], bool upper, Op op)
 {
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) x = fmaxf(x, __shfl_xor(x, o));
-    return x;
+    for (int i = 0; i < N; ++i) {
+        const float keep = upper ? v[N + i] : v[i], give = upper ? v[i] : v[N + i];
+        v[i] = op(keep, dpp_mov<CTRL>(give));
+    }
+}
+
+template <typename Op> __device__ __forceinline__ float sixteen(float (&v)[16], int c, Op op)
+{
+    fold<8, 0x128>(v, c & 8, op);  // c ^ 8
+    fold<4, 0x141>(v, c & 4, op);  // i <-> 7 - i within 8
+    fold<2, 0x4E>(v, c & 2, op);   // c ^ 2
+    fold<1, 0xB1>(v, c & 1, op);   // c ^ 1
+    float x = v[0];
+    x = op(x, __shfl_xor(x, 16));
+    return op(x, __shfl_xor(x, 32));
 }
 
 // The power of two that brings `top` to [2^14, 2^15), and its inverse.
@@ -468,14 +472,14 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
     constexpr bool EIGHT = TYPE == CACHE_E4M3, BF = !GEN && std::is_same<TA, bf16_t>::value;
     constexpr int KS = DK / 32, NV = EIGHT ? KS / 2 : KS, T = 8, ROW = DK * (EIGHT ? 1 : 2);
     // type of the dots' operands, and planes of x
-    using TE = typename std::conditional<GEN, bf16_t, TA>::type;
+    using TE = typename std::conditional<GEN, half_t, TA>::type;
     using TC = typename std::conditional<EIGHT, TE, typename CacheType<TYPE>::T>::type;
     constexpr bool CB = std::is_same<TC, bf16_t>::value, SAME = !GEN && std::is_same<TC, TA>::value;
     constexpr int PX = GEN ? (CB ? 3 : 2) : SAME ? 1 : 2, PK = BF ? 1 : 2;
     using VA = typename Vec8<TA>::V;
     using VC = typename Vec8<TC>::V;
     // a wave's k by keys (and before it, where x does not come from memory, x)
-    constexpr int K_BYTES = PK * DK * T * 2, X_BYTES = GEN ? PX * 16 * DK * 2 : 0;
+    constexpr int K_BYTES = PK * DK * T * 2, XR = DK + 8, X_BYTES = GEN ? PX * 16 * XR * 2 : 0;  // (rows of x in different banks)
     __shared__ __align__(16) char s_kx4[4][K_BYTES > X_BYTES ? K_BYTES : X_BYTES];
     __shared__ __align__(16) float s_d4[4][T][16], s_all4[4][GEN ? DK : 4];
     const Params &p = a.p;
@@ -484,7 +488,7 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
     if (bh >= p.B * p.HV) return;
     const int b = bh / p.HV, h = bh - b * p.HV;
     auto &s_k = *reinterpret_cast<bf16_t (*)[PK][DK][T]>(s_kx4[wid]);
-    auto &s_x = *reinterpret_cast<TC (*)[PX][16][DK]>(s_kx4[wid]);
+    auto &s_x = *reinterpret_cast<TC (*)[PX][16][XR]>(s_kx4[wid]);
     auto &s_d = s_d4[wid];
     auto &s_all = s_all4[wid];
     const int slot = p.slot_ids[b];
@@ -541,98 +545,132 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
     s_d[4 + lane / 16][lane % 16] = 0.f;
 
     if constexpr (GEN) {
-        // Lane: keys lane, lane + 64.  With D_t the product of the decays up to token t,
+        // Lane: keys KL lane + m.  With D_t the product of the decays up to token t,
         // x_n is D_n o (e_n o k_n), D_n o q_n, and the rest is relative to a token.
         constexpr int KL = DK / 64;
-        const TA *q = static_cast<const TA *>(p.q), *k = static_cast<const TA *>(p.k);
-        float kv[T][KL], rv[T][KL], qv[T][KL], av[T][KL];
+        const auto plus = [](float x, float y) { return x + y; };
+        const int j0 = KL * lane;
+        // every token's values as they lie in memory, none waited for before the last is asked for
+        using Bits = typename std::conditional<sizeof(TA) == 4, uint32_t, uint16_t>::type;
+        const auto value = [](uint32_t x) {
+            if constexpr (sizeof(TA) == 4) return as_float(x);
+            else return to_f32(__builtin_bit_cast(TA, (uint16_t)x));
+        };
+        const bool wide_gate = p.gate_dt == 0;
+        uint32_t kw[T][KL], qw[T][KL], gw_[T][KL], ew[T][KL];
         each([&](auto t_) {
             constexpr int t = decltype(t_)::value;
             if (t < n) {
-                const size_t tq = ((size_t)(s + t) * p.H + qh) * DK, tv = (size_t)(s + t) * p.HV + h;
-                float qq = 0.f, kk = 0.f;
+                const size_t tq = ((size_t)(s + t) * p.H + qh) * DK + j0, tv = ((size_t)(s + t) * p.HV + h) * DK + j0;
 #pragma unroll
                 for (int m = 0; m < KL; ++m) {
-                    const int j = lane + 64 * m;
-                    kv[t][m] = to_f32(k[tq + j]);
-                    qv[t][m] = to_f32(q[tq + j]);
-                    av[t][m] = expf(per_key ? log_decay_key(p, tv, h, j) : decays ? log_decay(p, tv, h) : 0.f);
-                    rv[t][m] = p.erase ? p.erase[tv * DK + j] : 1.f;
-                    qq = fmaf(qv[t][m], qv[t][m], qq);
-                    kk = fmaf(kv[t][m], kv[t][m], kk);
+                    kw[t][m] = static_cast<const Bits *>(p.k)[tq + m];
+                    qw[t][m] = static_cast<const Bits *>(p.q)[tq + m];
+                    if (per_key) gw_[t][m] = wide_gate ? static_cast<const uint32_t *>(p.gate)[tv + m] : static_cast<const Bits *>(p.gate)[tv + m];
+                    if (p.erase) ew[t][m] = reinterpret_cast<const uint32_t *>(p.erase)[tv + m];
                 }
-                if (p.qk_l2_norm) {
-                    const float inq = 1.f / sqrtf(wave_sum(qq) + 1e-12f), ink = 1.f / sqrtf(wave_sum(kk) + 1e-12f);
-#pragma unroll
-                    for (int m = 0; m < KL; ++m) {
-                        qv[t][m] *= inq;
-                        kv[t][m] *= ink;
-                    }
-                }
-#pragma unroll
-                for (int m = 0; m < KL; ++m) rv[t][m] *= kv[t][m];
             }
         }, std::make_integer_sequence<int, T>());
-        float gone[KL];
+        const bool raw_gate = per_key && p.gate_qwen;
+        float bias[KL];
+#pragma unroll
+        for (int m = 0; m < KL; ++m) bias[m] = raw_gate ? p.dt_bias[(size_t)h * DK + j0 + m] : 0.f;
+        const float slope = raw_gate ? gate_scale(p, h) : 1.f;
+        const float alpha = decays && !per_key ? expf(log_decay(p, th, h)) : 1.f;  // of vector c's token
+        float kv[T][KL], rv[T][KL], qv[T][KL], av[T][KL], norm[16];
+        each([&](auto t_) {
+            constexpr int t = decltype(t_)::value;
+            norm[t] = norm[8 + t] = 0.f;
+            if (t < n) {
+                const float at = lane_of<t>(alpha);
+#pragma unroll
+                for (int m = 0; m < KL; ++m) {
+                    kv[t][m] = value(kw[t][m]);
+                    qv[t][m] = value(qw[t][m]);
+                    av[t][m] = at;
+                    if (per_key) {
+                        const float x = wide_gate ? as_float(gw_[t][m]) : value(gw_[t][m]);
+                        av[t][m] = expf(raw_gate ? slope * softplus_f32(x + bias[m]) : x);
+                    }
+                    rv[t][m] = p.erase ? as_float(ew[t][m]) : 1.f;
+                    norm[t] = fmaf(kv[t][m], kv[t][m], norm[t]);
+                    norm[8 + t] = fmaf(qv[t][m], qv[t][m], norm[8 + t]);
+                }
+            }
+        }, std::make_integer_sequence<int, T>());
+        const float inv = p.qk_l2_norm ? 1.f / sqrtf(sixteen(norm, c, plus) + 1e-12f) : 1.f;
+        float gone[KL], xr_[T][KL], xq_[T][KL], top[16];
 #pragma unroll
         for (int m = 0; m < KL; ++m) gone[m] = 1.f;
         each([&](auto t_) {
             constexpr int t = decltype(t_)::value;
+            top[t] = top[8 + t] = 0.f;
             if (t < n) {
-                float xr_[KL], xq_[KL], topr = 0.f, topq = 0.f, upr = 1.f, upq = 1.f, backr = 1.f, backq = 1.f;
+                const float ink = lane_of<t>(inv), inq = lane_of<8 + t>(inv);
 #pragma unroll
                 for (int m = 0; m < KL; ++m) {
+                    kv[t][m] *= ink;
+                    qv[t][m] *= inq;
+                    rv[t][m] *= kv[t][m];
                     gone[m] *= av[t][m];
-                    xr_[m] = gone[m] * rv[t][m];
-                    xq_[m] = gone[m] * qv[t][m];
-                    topr = fmaxf(topr, fabsf(xr_[m]));
-                    topq = fmaxf(topq, fabsf(xq_[m]));
+                    xr_[t][m] = gone[m] * rv[t][m];
+                    xq_[t][m] = gone[m] * qv[t][m];
+                    top[t] = fmaxf(top[t], fabsf(xr_[t][m]));
+                    top[8 + t] = fmaxf(top[8 + t], fabsf(xq_[t][m]));
                 }
-                if constexpr (!CB) {
-                    half_scale(wave_max(topr), upr, backr);
-                    half_scale(wave_max(topq), upq, backq);
-                    back = c == t ? backr : c == 8 + t ? backq : back;
-                }
+            }
+        }, std::make_integer_sequence<int, T>());
+        float up = 1.f;
+        if constexpr (!CB) half_scale(sixteen(top, c, [](float x, float y) { return fmaxf(x, y); }), up, back);
+        each([&](auto t_) {
+            constexpr int t = decltype(t_)::value;
+            if (t < n) {
+                float r[KL], w[KL];
+                const float upr = lane_of<t>(up), upq = lane_of<8 + t>(up);
 #pragma unroll
                 for (int m = 0; m < KL; ++m) {
-                    float r = xr_[m] * upr, w = xq_[m] * upq;
+                    r[m] = xr_[t][m] * upr;
+                    w[m] = xq_[t][m] * upq;
+                }
 #pragma unroll
-                    for (int x = 0; x < PX; ++x) {
-                        const TC hr = from_f32<TC>(r), hq = from_f32<TC>(w);
-                        s_x[x][t][lane + 64 * m] = hr;
-                        s_x[x][8 + t][lane + 64 * m] = hq;
-                        r -= to_f32(hr);
-                        w -= to_f32(hq);
+                for (int x = 0; x < PX; ++x) {
+                    const uint32_t hr = two_halves<TC>(r[0], r[KL - 1]), hq = two_halves<TC>(w[0], w[KL - 1]);
+                    if constexpr (KL == 2) {
+                        *reinterpret_cast<uint32_t *>(&s_x[x][t][j0]) = hr;
+                        *reinterpret_cast<uint32_t *>(&s_x[x][8 + t][j0]) = hq;
+                    } else {
+                        s_x[x][t][j0] = __builtin_bit_cast(TC, (uint16_t)hr);
+                        s_x[x][8 + t][j0] = __builtin_bit_cast(TC, (uint16_t)hq);
+                    }
+#pragma unroll
+                    for (int m = 0; m < KL; ++m) {
+                        r[m] -= half_of<TC>(hr, m);
+                        w[m] -= half_of<TC>(hq, m);
                     }
                 }
-                cl[t] = 0.f;
-                float since[KL];  // decays after token t
+                // what token t's write adds to the later dots
+                float since[KL], dots[16];  // since: decays after token t
 #pragma unroll
                 for (int m = 0; m < KL; ++m) since[m] = kv[t][m];
                 each([&](auto u_) {
                     constexpr int u = decltype(u_)::value;
+                    dots[u] = dots[8 + u] = 0.f;
                     if (u >= t && u < n) {
-                        float cr = 0.f, cq = 0.f;
 #pragma unroll
                         for (int m = 0; m < KL; ++m) {
                             if (u > t) since[m] *= av[u][m];
-                            cr = fmaf(since[m], rv[u][m], cr);
-                            cq = fmaf(since[m], qv[u][m], cq);
-                        }
-                        cq = wave_sum(cq);
-                        cl[t] = c == 8 + u ? cq : cl[t];
-                        if (u > t) {
-                            cr = wave_sum(cr);
-                            cl[t] = c == u ? cr : cl[t];
+                            if (u > t) dots[u] = fmaf(since[m], rv[u][m], dots[u]);
+                            dots[8 + u] = fmaf(since[m], qv[u][m], dots[8 + u]);
                         }
                     }
                 }, std::make_integer_sequence<int, T>());
+                cl[t] = sixteen(dots, c, plus);
 #pragma unroll
                 for (int m = 0; m < KL; ++m) kv[t][m] = since[m];
             }
         }, std::make_integer_sequence<int, T>());
 #pragma unroll
-        for (int m = 0; m < KL; ++m) s_all[lane + 64 * m] = gone[m];
+        for (int m = 0; m < KL; ++m) s_all[j0 + m] = gone[m];
         wave_sync();
 #pragma unroll
         for (int x = 0; x < PX; ++x)
@@ -648,8 +686,8 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
                 hi[t] = from_f32<bf16_t>(v);
                 mid[t] = from_f32<bf16_t>(v - to_f32(hi[t]));
             }
-            *reinterpret_cast<b8 *>(&s_k[0][lane + 64 * m][0]) = hi;
-            *reinterpret_cast<b8 *>(&s_k[PK - 1][lane + 64 * m][0]) = mid;
+            *reinterpret_cast<b8 *>(&s_k[0][j0 + m][0]) = hi;
+            *reinterpret_cast<b8 *>(&s_k[PK - 1][j0 + m][0]) = mid;
         }
         wave_sync();
     } else {
@@ -793,7 +831,7 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
             float vj[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                z[j] *= EIGHT ? scale_of(exr[i][j]) : back;
+                z[j] *= EIGHT ? scale_of(exr[i][j]) * back : back;
                 vj[j] = beta * to_f32(vr[i][j]);
             }
             fetch(i, tile + PRE * waves);
