@@ -381,10 +381,14 @@ __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packe
 // t's write enters a later x_n's dot by sum_j k_t (D_n / D_t) e_n k_n, and S by
 // d_t (D_T / D_t) o k_t: a lane forms these for its two keys, the quotients as
 // running products of the later decays, which do not overflow.  x_n in fp32 goes
-// in as planes (two of scaled fp16, three of bf16), k_t and d_t as two of bf16
-// each.  256 requests x 32 heads of 128, 4 tokens, vector units and this, in us: a
-// decay for each key on 16 and 8 bits 229 and 134, 210 and 124; fp32 activations
-// 211 and 130, 205 and 121.
+// in as planes (two of fp16 scaled as above, 2^-22 of its largest value; three
+// of bf16 beside a bf16 cache), k_t and d_t as two of bf16 each.  256 requests x
+// 32 heads of 128, 4 tokens, vector units and this, in us: a decay for each key
+// on 16 and 8 bits 229 and 118, 210 and 106; fp32 activations 211 and 113, 205
+// and 96; 64 requests x 32 heads of 256, a decay for each key, 243 and 123, 224
+// and 78.  8 bits wait for the vectors' own work: 7 tokens take 132 us, 64 of
+// them with 16 rows a state (96 with each token's values loaded when their turn
+// comes and every dot reduced by itself).
 //
 // A tile is 16 rows: lane (c, kb) of a wave holds row c, 8 keys of every 32 (with
 // codes 16 of 64) at the kb-th place, which is the first product's operand; the
@@ -599,7 +603,7 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
             }
         }, std::make_integer_sequence<int, T>());
         const float inv = p.qk_l2_norm ? 1.f / sqrtf(sixteen(norm, c, plus) + 1e-12f) : 1.f;
-        float gone[KL], xr_[T][KL], xq_[T][KL], top[16];
+        float gone[KL], top[16];  // gone: decays up to a token
 #pragma unroll
         for (int m = 0; m < KL; ++m) gone[m] = 1.f;
         each([&](auto t_) {
@@ -613,15 +617,15 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
                     qv[t][m] *= inq;
                     rv[t][m] *= kv[t][m];
                     gone[m] *= av[t][m];
-                    xr_[t][m] = gone[m] * rv[t][m];
-                    xq_[t][m] = gone[m] * qv[t][m];
-                    top[t] = fmaxf(top[t], fabsf(xr_[t][m]));
-                    top[8 + t] = fmaxf(top[8 + t], fabsf(xq_[t][m]));
+                    top[t] = fmaxf(top[t], fabsf(gone[m] * rv[t][m]));
+                    top[8 + t] = fmaxf(top[8 + t], fabsf(gone[m] * qv[t][m]));
                 }
             }
         }, std::make_integer_sequence<int, T>());
         float up = 1.f;
         if constexpr (!CB) half_scale(sixteen(top, c, [](float x, float y) { return fmaxf(x, y); }), up, back);
+#pragma unroll
+        for (int m = 0; m < KL; ++m) gone[m] = 1.f;
         each([&](auto t_) {
             constexpr int t = decltype(t_)::value;
             if (t < n) {
@@ -629,24 +633,22 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
                 const float upr = lane_of<t>(up), upq = lane_of<8 + t>(up);
 #pragma unroll
                 for (int m = 0; m < KL; ++m) {
-                    r[m] = xr_[t][m] * upr;
-                    w[m] = xq_[t][m] * upq;
+                    gone[m] *= av[t][m];
+                    r[m] = gone[m] * rv[t][m] * upr;
+                    w[m] = gone[m] * qv[t][m] * upq;
                 }
 #pragma unroll
                 for (int x = 0; x < PX; ++x) {
-                    const uint32_t hr = two_halves<TC>(r[0], r[KL - 1]), hq = two_halves<TC>(w[0], w[KL - 1]);
-                    if constexpr (KL == 2) {
-                        *reinterpret_cast<uint32_t *>(&s_x[x][t][j0]) = hr;
-                        *reinterpret_cast<uint32_t *>(&s_x[x][8 + t][j0]) = hq;
-                    } else {
-                        s_x[x][t][j0] = __builtin_bit_cast(TC, (uint16_t)hr);
-                        s_x[x][8 + t][j0] = __builtin_bit_cast(TC, (uint16_t)hq);
-                    }
+                    TC hr[KL], hq[KL];
 #pragma unroll
                     for (int m = 0; m < KL; ++m) {
-                        r[m] -= half_of<TC>(hr, m);
-                        w[m] -= half_of<TC>(hq, m);
+                        hr[m] = from_f32<TC>(r[m]);
+                        hq[m] = from_f32<TC>(w[m]);
+                        r[m] -= to_f32(hr[m]);
+                        w[m] -= to_f32(hq[m]);
                     }
+                    __builtin_memcpy(__builtin_assume_aligned(&s_x[x][t][j0], 2 * KL), hr, sizeof(hr));
+                    __builtin_memcpy(__builtin_assume_aligned(&s_x[x][8 + t][j0], 2 * KL), hq, sizeof(hq));
                 }
                 // what token t's write adds to the later dots
                 float since[KL], dots[16];  // since: decays after token t
@@ -945,11 +947,10 @@ hipError_t packed_step_at(const PackedParams &a, int rule, bool per_key, hipStre
     if (one)
         return keyed ? launch_step<TA, TYPE, DK, true, true>(a, rule, per_key, 1, s)
                      : launch_step<TA, TYPE, DK, false, true>(a, rule, per_key, 1, s);
-    // Up to 8 tokens on the matrix cores: 16-bit activations with one decay a head,
-    // or (to 128 keys, where its registers suffice) any.
-    constexpr bool PLAIN = DK >= 64 && sizeof(TA) == 2, ANY = DK >= 64 && DK <= 128;
+    // Up to 8 tokens on the matrix cores: 16-bit activations with one decay a head, or any.
+    constexpr bool ANY = DK >= 64, PLAIN = ANY && sizeof(TA) == 2;
     const bool plain = PLAIN && !keyed;
-    if (p.dk == DK && (plain || ANY)) {
+    if (ANY && p.dk == DK) {
         // Waves of a state: one, which spares the tokens' own work, until too few
         // states leave SIMDs idle: 2,048 waves, two a SIMD.  4 tokens, 32 heads of
         // 128, in us with 1,024, 2,048, 4,096 and 8,192 waves at least: 8-bit states of
