@@ -105,8 +105,11 @@ template <int TYPE, int DK, bool ONE> struct StepForm {
 
 // EXACT: p.dk is DK; else it is less, and a lane's vector that would pass the
 // row's end starts earlier: the columns that it then shares with another lane
-// count in that lane's sums only, and both write the same bytes.  Rows of under
-// 16 values have a lane each, which takes them value by value.
+// count in that lane's sums only, and both write the same bytes.  Such rows share
+// cache lines, which plain accesses keep for their next use (without: 256
+// requests x 32 heads of 56, 63 and 150 in 16 bits 37, 49 and 189 us instead of
+// 30, 40 and 167).  Rows of under 16 values have a lane each, which takes them
+// value by value.
 // Requests of fewer than `least` tokens are left alone.
 template <typename TA, int TYPE, int DK, bool VD, bool ONE, bool EXACT>
 __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packed_step(const PackedParams a, int rule,
@@ -201,7 +204,9 @@ __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packe
                     raw[g][n][i / PER] = (i % PER ? raw[g][n][i / PER] : 0) | v << (32 / PER * (i % PER));
                 }
             } else {
-                raw[g][n] = __builtin_nontemporal_load(reinterpret_cast<const Any4 *>(src + at[n] * (16 / VC)));
+                const Any4 *from = reinterpret_cast<const Any4 *>(src + at[n] * (16 / VC));
+                if constexpr (EXACT) raw[g][n] = __builtin_nontemporal_load(from);
+                else raw[g][n] = *from;
             }
         }
         ex[g] = EIGHT ? a.scale[head + from] : 0;
@@ -241,7 +246,9 @@ __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packe
                 for (int i = 0; i < VC; ++i)
                     if (at[n] + i < dk) reinterpret_cast<Code *>(dst)[at[n] + i] = (Code)(out[n][i / PER] >> (32 / PER * (i % PER)));
             } else if (EXACT || others[n] < VC) {
-                __builtin_nontemporal_store(out[n], reinterpret_cast<Any4 *>(dst + at[n] * (16 / VC)));
+                Any4 *to = reinterpret_cast<Any4 *>(dst + at[n] * (16 / VC));
+                if constexpr (EXACT) __builtin_nontemporal_store(out[n], to);
+                else *to = out[n];
             }
         }
         if (EIGHT && l == 0) a.scale[head + row] = (uint8_t)eo;
@@ -398,6 +405,7 @@ __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packe
 // with 8 lanes each and exchanging pieces between lanes c and c ^ 1 (without it
 // 4 tokens on 16 bits take 129 us).
 typedef float f4v __attribute__((ext_vector_type(4)));
+typedef float Any4f __attribute__((ext_vector_type(4), aligned(4)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 
@@ -470,11 +478,20 @@ __device__ __forceinline__ void exchange(w4 &x, w4 &y, bool odd)
 // itself (its LDS is its own), the next PRE of them on their way.  (At least two
 // waves a SIMD asked for: with one, products would accumulate in registers that
 // the vector units do not reach, 64 moves a tile.)
-template <typename TA, int TYPE, int DK, int PRE, bool GEN>
+// EXACT: p.dk is DK; else (GEN) it is over 16 and less, and a lane's 16 bytes of a
+// row that would pass its end start earlier: keys that they share with another
+// lane's count there in the dots (x is 0 here), and both write the same bytes, by
+// plain accesses as above.  256 requests x 32 heads, 2 and 4 tokens, vector units
+// and this, in us: heads of 56 in 16 bits 71, 111 and 33, 37, in 8 bits 55, 88 and
+// 32, 36; of 96 in 16 bits 128, 202 and 82, 90; of 150 361, 589 and 188, 202; of
+// 224 513, 840 and 388, 435.  (Of 255 in 16 bits, odd rows across each other's
+// lines, 622, 941 and 828, 899: behind at 2 tokens, ahead from 4.)
+template <typename TA, int TYPE, int DK, int PRE, bool GEN, bool EXACT>
 __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int rule, int per_key, int waves)
 {
     constexpr bool EIGHT = TYPE == CACHE_E4M3, BF = !GEN && std::is_same<TA, bf16_t>::value;
-    constexpr int KS = DK / 32, NV = EIGHT ? KS / 2 : KS, T = 8, ROW = DK * (EIGHT ? 1 : 2);
+    constexpr int KS = DK / 32, NV = EIGHT ? KS / 2 : KS, T = 8;
+    constexpr bool LINES = EXACT && NV > 1;
     // type of the dots' operands, and planes of x
     using TE = typename std::conditional<GEN, half_t, TA>::type;
     using TC = typename std::conditional<EIGHT, TE, typename CacheType<TYPE>::T>::type;
@@ -487,6 +504,7 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
     __shared__ __align__(16) char s_kx4[4][K_BYTES > X_BYTES ? K_BYTES : X_BYTES];
     __shared__ __align__(16) float s_d4[4][T][16], s_all4[4][GEN ? DK : 4];
     const Params &p = a.p;
+    const int dk = EXACT ? DK : p.dk, ROW = dk * (EIGHT ? 1 : 2);  // values and bytes of a row
     const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), gw = blockIdx.x * 4 + wid;
     const int bh = gw / waves, wave = gw - bh * waves;
     if (bh >= p.B * p.HV) return;
@@ -504,7 +522,13 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
     const int lane = threadIdx.x & 63, c = lane & 15, kb = lane >> 4;
     const int tiles = (p.dv + 15) / 16;
     const int qh = (int)(((int64_t)h * p.H) / p.HV);
-    const auto key = [](int f, int kb) { return EIGHT ? 64 * (f / 2) + 16 * kb + 8 * (f % 2) : 32 * f + 8 * kb; };
+    constexpr int VK = EIGHT ? 16 : 8;  // keys of 16 bytes
+    const auto wanted = [](int m, int kb) { return m * 4 * VK + kb * VK; };
+    const auto piece = [&](int m, int kb) {
+        const int at = wanted(m, kb);
+        return EXACT || at + VK <= dk ? at : dk - VK;
+    };
+    const auto key = [&](int f, int kb) { return EIGHT ? piece(f / 2, kb) + 8 * (f % 2) : piece(f, kb); };
 
     // vector c: k of token c, q of token c - 8
     const int own = c & 7, tt = own < n ? own : n - 1;
@@ -516,7 +540,7 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
         for (int f = 0; f < KS; ++f) xr[f] = *reinterpret_cast<const w4 *>(x + key(f, kb));
     }
     const size_t head = ((size_t)slot * p.HV + h) * p.dv;
-    char *const mat = static_cast<char *>(a.data) + head * DK * (EIGHT ? 1 : 2);
+    char *const mat = static_cast<char *>(a.data) + head * ROW;
     uint8_t *const scales = EIGHT ? a.scale + head : nullptr;
     const TA *const vv = static_cast<const TA *>(p.v) + th * p.dv;
     w4 raw[PRE][NV];
@@ -527,8 +551,12 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
         const int row = 16 * tile + c, at = row < p.dv ? row : p.dv - 1;
 #pragma unroll
         for (int m = 0; m < NV; ++m) {
-            const int r = NV > 1 ? 16 * tile + (c & ~1) + m % 2 : row, rr = r < p.dv ? r : p.dv - 1;
-            raw[j][m] = __builtin_nontemporal_load(reinterpret_cast<const w4 *>(mat + rr * ROW + m / 2 * 128 + (NV > 1 ? (c & 1) * 64 : 0) + kb * 16));
+            if constexpr (EXACT) {
+                const int r = LINES ? 16 * tile + (c & ~1) + m % 2 : row, rr = r < p.dv ? r : p.dv - 1;
+                raw[j][m] = __builtin_nontemporal_load(reinterpret_cast<const w4 *>(mat + rr * ROW + m / 2 * 128 + (LINES ? (c & 1) * 64 : 0) + kb * 16));
+            } else {
+                raw[j][m] = *reinterpret_cast<const Any4 *>(mat + at * ROW + piece(m, kb) * (16 / VK));
+            }
         }
         if (EIGHT) ex[j] = scales[at];
 #pragma unroll
@@ -565,9 +593,11 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
         each([&](auto t_) {
             constexpr int t = decltype(t_)::value;
             if (t < n) {
-                const size_t tq = ((size_t)(s + t) * p.H + qh) * DK + j0, tv = ((size_t)(s + t) * p.HV + h) * DK + j0;
+                const size_t tq = ((size_t)(s + t) * p.H + qh) * dk + j0, tv = ((size_t)(s + t) * p.HV + h) * dk + j0;
 #pragma unroll
                 for (int m = 0; m < KL; ++m) {
+                    kw[t][m] = qw[t][m] = gw_[t][m] = ew[t][m] = 0;  // past the row's end
+                    if (!EXACT && j0 + m >= dk) continue;
                     kw[t][m] = static_cast<const Bits *>(p.k)[tq + m];
                     qw[t][m] = static_cast<const Bits *>(p.q)[tq + m];
                     if (per_key) gw_[t][m] = wide_gate ? static_cast<const uint32_t *>(p.gate)[tv + m] : static_cast<const Bits *>(p.gate)[tv + m];
@@ -578,7 +608,7 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
         const bool raw_gate = per_key && p.gate_qwen;
         float bias[KL];
 #pragma unroll
-        for (int m = 0; m < KL; ++m) bias[m] = raw_gate ? p.dt_bias[(size_t)h * DK + j0 + m] : 0.f;
+        for (int m = 0; m < KL; ++m) bias[m] = raw_gate && (EXACT || j0 + m < dk) ? p.dt_bias[(size_t)h * dk + j0 + m] : 0.f;
         const float slope = raw_gate ? gate_scale(p, h) : 1.f;
         const float alpha = decays && !per_key ? expf(log_decay(p, th, h)) : 1.f;  // of vector c's token
         float kv[T][KL], rv[T][KL], qv[T][KL], av[T][KL], norm[16];
@@ -603,6 +633,13 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
             }
         }, std::make_integer_sequence<int, T>());
         const float inv = p.qk_l2_norm ? 1.f / sqrtf(sixteen(norm, c, plus) + 1e-12f) : 1.f;
+        // the columns of x in the order of the lanes' pieces: in the one that starts earlier, its own come last
+        int place[KL];
+#pragma unroll
+        for (int m = 0; m < KL; ++m) {
+            const int j = j0 + m, rest = dk % VK, last = dk - rest;
+            place[m] = EXACT || rest == 0 || j < last || j >= last + VK ? j : j < dk ? j + VK - rest : j - rest;
+        }
         float gone[KL], top[16];  // gone: decays up to a token
 #pragma unroll
         for (int m = 0; m < KL; ++m) gone[m] = 1.f;
@@ -647,8 +684,16 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
                         r[m] -= to_f32(hr[m]);
                         w[m] -= to_f32(hq[m]);
                     }
-                    __builtin_memcpy(__builtin_assume_aligned(&s_x[x][t][j0], 2 * KL), hr, sizeof(hr));
-                    __builtin_memcpy(__builtin_assume_aligned(&s_x[x][8 + t][j0], 2 * KL), hq, sizeof(hq));
+                    if constexpr (EXACT) {
+                        __builtin_memcpy(__builtin_assume_aligned(&s_x[x][t][j0], 2 * KL), hr, sizeof(hr));
+                        __builtin_memcpy(__builtin_assume_aligned(&s_x[x][8 + t][j0], 2 * KL), hq, sizeof(hq));
+                    } else {
+#pragma unroll
+                        for (int m = 0; m < KL; ++m) {
+                            s_x[x][t][place[m]] = hr[m];
+                            s_x[x][8 + t][place[m]] = hq[m];
+                        }
+                    }
                 }
                 // what token t's write adds to the later dots
                 float since[KL], dots[16];  // since: decays after token t
@@ -677,7 +722,8 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
 #pragma unroll
         for (int x = 0; x < PX; ++x)
 #pragma unroll
-            for (int f = 0; f < KS; ++f) y[x][f] = *reinterpret_cast<const VC *>(&s_x[x][c][key(f, kb)]);
+            for (int f = 0; f < KS; ++f)
+                y[x][f] = *reinterpret_cast<const VC *>(&s_x[x][c][EIGHT ? wanted(f / 2, kb) + 8 * (f % 2) : wanted(f, kb)]);
         wave_sync();
 #pragma unroll
         for (int m = 0; m < KL; ++m) {
@@ -772,7 +818,7 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
         for (int i = 0; i < PRE; ++i) {
             const int tile = t0 + i * waves;
             if (tile >= tiles) break;
-            if constexpr (NV > 1)
+            if constexpr (LINES)
 #pragma unroll
                 for (int m = 0; m < NV; m += 2) exchange(raw[i][m], raw[i][m + 1], c & 1);
             // dots of the states with every vector: rows 4 kb + j, column c
@@ -816,8 +862,9 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
             for (int f = 0; f < KS; ++f) {
                 f4v each_all[2];
                 if constexpr (GEN) {
-                    each_all[0] = *reinterpret_cast<const f4v *>(&s_all[key(f, kb)]);
-                    each_all[1] = *reinterpret_cast<const f4v *>(&s_all[key(f, kb) + 4]);
+                    using V = typename std::conditional<EXACT, f4v, Any4f>::type;
+                    each_all[0] = *reinterpret_cast<const V *>(&s_all[key(f, kb)]);
+                    each_all[1] = *reinterpret_cast<const V *>(&s_all[key(f, kb) + 4]);
                 }
                 if constexpr (EIGHT) {
                     from_codes(raw[i][f / 2][f % 2 * 2], scale_of(ex[i]), &S[f][0]);
@@ -913,13 +960,17 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
 #pragma unroll
                     for (int j = 0; j < 4; ++j) out[f][j] = two_halves<TC>(S[f][2 * j], S[f][2 * j + 1]);
             }
-            if constexpr (NV > 1)
+            if constexpr (LINES)
 #pragma unroll
                 for (int m = 0; m < NV; m += 2) exchange(out[m], out[m + 1], c & 1);
 #pragma unroll
             for (int m = 0; m < NV; ++m) {
-                const int r = NV > 1 ? 16 * tile + (c & ~1) + m % 2 : row;
-                if (r < p.dv) __builtin_nontemporal_store(out[m], reinterpret_cast<w4 *>(mat + r * ROW + m / 2 * 128 + (NV > 1 ? (c & 1) * 64 : 0) + kb * 16));
+                if constexpr (EXACT) {
+                    const int r = LINES ? 16 * tile + (c & ~1) + m % 2 : row;
+                    if (r < p.dv) __builtin_nontemporal_store(out[m], reinterpret_cast<w4 *>(mat + r * ROW + m / 2 * 128 + (LINES ? (c & 1) * 64 : 0) + kb * 16));
+                } else if (row < p.dv && wanted(m, kb) < dk) {
+                    *reinterpret_cast<Any4 *>(mat + row * ROW + piece(m, kb) * (16 / VK)) = out[m];
+                }
             }
             if (EIGHT && kb == 0 && row < p.dv) scales[row] = (uint8_t)eo;
         }
@@ -948,9 +999,7 @@ hipError_t packed_step_at(const PackedParams &a, int rule, bool per_key, hipStre
         return keyed ? launch_step<TA, TYPE, DK, true, true>(a, rule, per_key, 1, s)
                      : launch_step<TA, TYPE, DK, false, true>(a, rule, per_key, 1, s);
     // Up to 8 tokens on the matrix cores: 16-bit activations with one decay a head, or any.
-    constexpr bool ANY = DK >= 64, PLAIN = ANY && sizeof(TA) == 2;
-    const bool plain = PLAIN && !keyed;
-    if (ANY && p.dk == DK) {
+    if constexpr (DK >= 64) {
         // Waves of a state: one, which spares the tokens' own work, until too few
         // states leave SIMDs idle: 2,048 waves, two a SIMD.  4 tokens, 32 heads of
         // 128, in us with 1,024, 2,048, 4,096 and 8,192 waves at least: 8-bit states of
@@ -961,22 +1010,24 @@ hipError_t packed_step_at(const PackedParams &a, int rule, bool per_key, hipStre
         while (waves < 8 && waves * 16 < p.dv && states * waves < 2048) waves *= 2;
         const dim3 blocks((unsigned)((states * waves + 3) / 4)), threads(256);
         constexpr int PRE = TYPE == CACHE_E4M3 ? 2 : 1;
-        if constexpr (PLAIN) {
-            if (plain)
-                hipLaunchKernelGGL((k_packed_few<TA, TYPE, DK, PRE, false>), blocks, threads, 0, s, a, rule, 0, waves);
+        const bool exact = p.dk == DK;
+        if constexpr (sizeof(TA) == 2) {
+            if (exact && !keyed)
+                hipLaunchKernelGGL((k_packed_few<TA, TYPE, DK, PRE, false, true>), blocks, threads, 0, s, a, rule, 0, waves);
         }
-        if constexpr (ANY) {
-            if (!plain)
-                hipLaunchKernelGGL((k_packed_few<TA, TYPE, DK, PRE, true>), blocks, threads, 0, s, a, rule, (int)per_key, waves);
-        }
+        if (exact && (keyed || sizeof(TA) == 4))
+            hipLaunchKernelGGL((k_packed_few<TA, TYPE, DK, PRE, true, true>), blocks, threads, 0, s, a, rule, (int)per_key, waves);
+        if (DK == 256 && p.dk <= 192)
+            hipLaunchKernelGGL((k_packed_few<TA, TYPE, DK == 256 ? 192 : DK, PRE, true, false>), blocks, threads, 0, s, a, rule, (int)per_key, waves);
+        else if (!exact)
+            hipLaunchKernelGGL((k_packed_few<TA, TYPE, DK, PRE, true, false>), blocks, threads, 0, s, a, rule, (int)per_key, waves);
         hipError_t err = hipGetLastError();
         if (err != hipSuccess || (p.cu_seqlens ? p.T : p.L) <= 8) return err;
-        // requests of more than 8 tokens
-        return keyed ? launch_step<TA, TYPE, DK, true, false>(a, rule, per_key, 9, s)
-                     : launch_step<TA, TYPE, DK, false, false>(a, rule, false, 9, s);
     }
-    return keyed ? launch_step<TA, TYPE, DK, true, false>(a, rule, per_key, 1, s)
-                 : launch_step<TA, TYPE, DK, false, false>(a, rule, false, 1, s);
+    // requests of more than 8 tokens, or any of up to 16 keys
+    const int least = DK >= 64 ? 9 : 1;
+    return keyed ? launch_step<TA, TYPE, DK, true, false>(a, rule, per_key, least, s)
+                 : launch_step<TA, TYPE, DK, false, false>(a, rule, false, least, s);
 }
 
 template <typename TA, int TYPE>

@@ -296,7 +296,8 @@ def test_dims_heads_and_several_tokens(dtype, dk, dv, H, HV, L):
 @pytest.mark.parametrize("rule", [1, 6, 7])
 def test_several_tokens_with_per_key_factors(dtype, rule):
     for act, dim, L in (("bf16", 128, 5), (np.float16, 40, 3), (np.float32, 256, 2), ("bf16", 11, 2), (np.float32, 128, 8),
-                        (np.float16, 64, 8), ("bf16", 256, 7), (np.float16, 256, 4), (np.float32, 256, 8)):
+                        (np.float16, 64, 8), ("bf16", 256, 7), (np.float16, 256, 4), (np.float32, 256, 8),
+                         ("bf16", 17, 8), (np.float16, 73, 6), (np.float32, 120, 4), ("bf16", 250, 7)):
         case = workloads.random_case(60 + rule, rank4_batch=(2, L), H=2, HV=4, DK=dim, DV=dim, dtype=act, slots=(4,), **RULES[rule])
         step_and_check(case, dtype, tokens=L)
 
@@ -318,7 +319,7 @@ def test_tiny_and_huge_values_on_the_matrix_cores(dtype):
 
 @pytest.mark.parametrize("dtype", DT)
 @pytest.mark.parametrize("act", [np.float16, "bf16", np.float32])
-@pytest.mark.parametrize("dk,rule", [(128, 0), (64, 0), (256, 0), (40, 0), (128, 1), (64, 6), (9, 7), (256, 7)])
+@pytest.mark.parametrize("dk,rule", [(128, 0), (64, 0), (256, 0), (40, 0), (128, 1), (64, 6), (9, 7), (256, 7), (33, 6), (200, 1)])
 def test_nan_and_infinities_reach_later_tokens_only(dtype, act, dk, rule):
     """What a token brings does not reach the outputs before it, other requests,
     or, through v, other rows; what its q holds reaches its own output alone."""
