@@ -21,7 +21,7 @@ struct PackedParams {
     int32_t skip_empty;  // pack: requests without tokens keep their slots
 };
 
-// Workgroups of pack and unpack; a step takes no more.  A launch has fewer than
+// Workgroups of pack and unpack at most; a step takes no more.  A launch has fewer than
 // 2^32 threads, 256 a workgroup.
 int64_t pack_blocks(int batch, int heads, int dv);
 constexpr int64_t PACK_BLOCKS_MAX = (int64_t{1} << 24) - 1;

@@ -81,7 +81,7 @@ def ids(*values):
 
 @pytest.mark.parametrize("dtype", DT)
 @pytest.mark.parametrize("HV,dv,dk", [(1, 1, 1), (2, 128, 128), (3, 40, 72), (2, 33, 9), (1, 256, 256), (5, 7, 130), (4, 64, 64),
-                                      (1, 31, 255)])
+                                      (1, 31, 255), (2, 130, 30), (3, 65, 33), (1, 128, 3), (2, 129, 5), (1, 3, 4)])
 def test_pack_and_unpack(dtype, HV, dv, dk):
     from gated_delta_rule_token_amd import api
     g = torch.Generator().manual_seed(HV * dv + dk)
