@@ -739,78 +739,78 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
         }
         wave_sync();
     } else {
-    const float alpha = decays ? expf(log_decay(p, th, h)) : 1.f;
+        const float alpha = decays ? expf(log_decay(p, th, h)) : 1.f;
 
-    VA x[KS];
+        VA x[KS];
 #pragma unroll
-    for (int f = 0; f < KS; ++f) x[f] = __builtin_bit_cast(VA, xr[f]);
-    // k by keys, tokens together
-    if (c < 8) {
-#pragma unroll
-        for (int f = 0; f < KS; ++f)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float kf = c < n ? to_f32((TA)x[f][j]) : 0.f;
-                const bf16_t hi = from_f32<bf16_t>(kf);
-                s_k[0][key(f, kb) + j][c] = hi;
-                if constexpr (!BF) s_k[1][key(f, kb) + j][c] = from_f32<bf16_t>(kf - to_f32(hi));
-            }
-    }
-    f4v gram = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int f = 0; f < KS; ++f) gram = mfma(x[f], x[f], gram);
-    // x as operands of the cache's type
-    if constexpr (SAME) {
-#pragma unroll
-        for (int f = 0; f < KS; ++f) y[0][f] = __builtin_bit_cast(VC, xr[f]);
-    } else {
-        float up = 1.f;
-        if constexpr (BF) {  // bf16 in two fp16 planes: scaled to fp16's upper range
-            float top = 0.f;
+        for (int f = 0; f < KS; ++f) x[f] = __builtin_bit_cast(VA, xr[f]);
+        // k by keys, tokens together
+        if (c < 8) {
 #pragma unroll
             for (int f = 0; f < KS; ++f)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(to_f32((TA)x[f][j])));
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            half_scale(top, up, back);
+                for (int j = 0; j < 8; ++j) {
+                    const float kf = c < n ? to_f32((TA)x[f][j]) : 0.f;
+                    const bf16_t hi = from_f32<bf16_t>(kf);
+                    s_k[0][key(f, kb) + j][c] = hi;
+                    if constexpr (!BF) s_k[1][key(f, kb) + j][c] = from_f32<bf16_t>(kf - to_f32(hi));
+                }
         }
+        f4v gram = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int f = 0; f < KS; ++f)
+        for (int f = 0; f < KS; ++f) gram = mfma(x[f], x[f], gram);
+        // x as operands of the cache's type
+        if constexpr (SAME) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float v = to_f32((TA)x[f][j]) * up;
-                const TC hi = from_f32<TC>(v);
-                y[0][f][j] = hi;
-                y[1][f][j] = from_f32<TC>(v - to_f32(hi));
+            for (int f = 0; f < KS; ++f) y[0][f] = __builtin_bit_cast(VC, xr[f]);
+        } else {
+            float up = 1.f;
+            if constexpr (BF) {  // bf16 in two fp16 planes: scaled to fp16's upper range
+                float top = 0.f;
+#pragma unroll
+                for (int f = 0; f < KS; ++f)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(to_f32((TA)x[f][j])));
+                top = fmaxf(top, __shfl_xor(top, 16));
+                top = fmaxf(top, __shfl_xor(top, 32));
+                half_scale(top, up, back);
             }
-    }
-    // norms and the products of the tokens' vectors
-    float inv = 1.f;
-    if (p.qk_l2_norm) {
-        const float mine = c % 4 == 0 ? gram[0] : c % 4 == 1 ? gram[1] : c % 4 == 2 ? gram[2] : gram[3];
-        inv = 1.f / sqrtf(__shfl(mine, 16 * (c / 4) + c) + 1e-12f);
-    }
-    float later = 1.f;
-    each([&](auto t_) {
-        constexpr int t = decltype(t_)::value;
-        if (t < n) {
-            const float at = lane_of<t>(alpha), kt = lane_of<t>(inv), g = __shfl(gram[t % 4], 16 * (t / 4) + c);
-            const bool past = c >= 8 && t > c - 8;  // q of a token before t
-            al[t] = past ? 1.f : at;
-            cl[t] = past ? 0.f : kt * g;
-            all *= at;
-            if (t > own) later *= at;
+#pragma unroll
+            for (int f = 0; f < KS; ++f)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float v = to_f32((TA)x[f][j]) * up;
+                    const TC hi = from_f32<TC>(v);
+                    y[0][f][j] = hi;
+                    y[1][f][j] = from_f32<TC>(v - to_f32(hi));
+                }
         }
-    }, std::make_integer_sequence<int, T>());
-    const float put_own = later * inv;
-    oscale = p.scale * inv;
-    binv = retrieves ? beta * inv : 0.f;
-    each([&](auto t_) {
-        constexpr int t = decltype(t_)::value;
-        if (t < n) put[t] = lane_of<t>(put_own);
-    }, std::make_integer_sequence<int, T>());
-    wave_sync();
+        // norms and the products of the tokens' vectors
+        float inv = 1.f;
+        if (p.qk_l2_norm) {
+            const float mine = c % 4 == 0 ? gram[0] : c % 4 == 1 ? gram[1] : c % 4 == 2 ? gram[2] : gram[3];
+            inv = 1.f / sqrtf(__shfl(mine, 16 * (c / 4) + c) + 1e-12f);
+        }
+        float later = 1.f;
+        each([&](auto t_) {
+            constexpr int t = decltype(t_)::value;
+            if (t < n) {
+                const float at = lane_of<t>(alpha), kt = lane_of<t>(inv), g = __shfl(gram[t % 4], 16 * (t / 4) + c);
+                const bool past = c >= 8 && t > c - 8;  // q of a token before t
+                al[t] = past ? 1.f : at;
+                cl[t] = past ? 0.f : kt * g;
+                all *= at;
+                if (t > own) later *= at;
+            }
+        }, std::make_integer_sequence<int, T>());
+        const float put_own = later * inv;
+        oscale = p.scale * inv;
+        binv = retrieves ? beta * inv : 0.f;
+        each([&](auto t_) {
+            constexpr int t = decltype(t_)::value;
+            if (t < n) put[t] = lane_of<t>(put_own);
+        }, std::make_integer_sequence<int, T>());
+        wave_sync();
     }
 
     for (int t0 = wave; t0 < tiles; t0 += PRE * waves)

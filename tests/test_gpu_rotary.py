@@ -292,6 +292,15 @@ def test_gradients_over_many_workgroups():
     check_back(c, back(dev(c), *cuda(douts)), douts)
 
 
+@pytest.mark.parametrize("T,H,HK,d,R,dtype", [(3597, 10, 10, 128, 64, "bf16"), (613, 4, 20, 256, 256, "f32"), (700, 16, 2, 128, 128, "f16"),
+                                              (1013, 4, 1, 163, 146, "bf16"), (2600, 1, 9, 44, 12, "f16"), (9000, 1, 1, 13, 6, "f32")])
+def test_gradients_with_turns_of_every_length(T, H, HK, d, R, dtype):
+    c = make(T, T, H, HK, d, R, dtype, far=4096)
+    douts = d_outs(c)
+    check_back(c, back(dev(c), *cuda(douts)), douts)
+    check(c, call(dev(c)))
+
+
 def test_gradients_against_differences():
     """(f(x + h e) - f(x - h e)) / 2h of the calls themselves, in fp32 with
     h = 2^-6: the second-order term is h^2 times third derivatives of order 1
