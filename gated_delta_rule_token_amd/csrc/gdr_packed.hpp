@@ -1017,6 +1017,8 @@ hipError_t packed_step_at(const PackedParams &a, int rule, bool per_key, hipStre
         }
         if (exact && (keyed || sizeof(TA) == 4))
             hipLaunchKernelGGL((k_packed_few<TA, TYPE, DK, PRE, true, true>), blocks, threads, 0, s, a, rule, (int)per_key, waves);
+        // (to 192 keys with products over 192: 256 requests x 32 heads of 192, 2 tokens,
+        // 446 -> 313 us in 16 bits and 228 -> 188 in 8)
         if (DK == 256 && p.dk <= 192)
             hipLaunchKernelGGL((k_packed_few<TA, TYPE, DK == 256 ? 192 : DK, PRE, true, false>), blocks, threads, 0, s, a, rule, (int)per_key, waves);
         else if (!exact)
