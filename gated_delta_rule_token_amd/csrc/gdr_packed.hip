@@ -85,14 +85,11 @@ __global__ __launch_bounds__(256) void k_pack(const PackedParams a)
         const int row = r + STEP * i;
         uint32_t ex = 0;
         if constexpr (TYPE == CACHE_E4M3) {
-            float top = 0.f;
+            ex = scale_byte_of(reinterpret_cast<const float (&)[NV * VEC]>(x[i]), [](float top) {
 #pragma unroll
-            for (int n = 0; n < NV; ++n)
-#pragma unroll
-                for (int c = 0; c < VEC; ++c) top = fmaxf(top, fabsf(x[i][n][c]));
-#pragma unroll
-            for (int o = 1; o < LANES; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
-            ex = scale_byte(top);
+                for (int o = 1; o < LANES; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+                return top;
+            });
             if (row < w.rows && l == 0) a.scale[w.cache + row] = (uint8_t)ex;
         }
 #pragma unroll

@@ -10,8 +10,8 @@
 // byte a row.  The rows of a state evolve separately (gdr_device.hpp), so the
 // lanes that hold a row form its scale with one more reduction.  e is at least
 // -100: rows below 448 2^-100 lose their bits, and a row of zeros has a scale.
-// A NaN stays one and an infinity becomes one (e4m3 has none); the rest of the
-// row is held as ever.
+// A NaN stays one and an infinity becomes one (e4m3 has none); neither counts in
+// the largest value, so the rest of the row is held as ever.
 #pragma once
 
 #include "gdr_packed_launch.hpp"
@@ -40,6 +40,26 @@ __device__ __forceinline__ uint32_t scale_byte(float top)
 {
     const uint32_t e = (__builtin_bit_cast(uint32_t, top) + 0x1FFFFFu) >> 23;
     return e < SCALE_MIN + 8 ? SCALE_MIN : e - 8;
+}
+
+// The same for a lane's part of a row; reduce: the largest over the row's lanes.  An
+// infinite largest value, which would leave the others no bits, is formed again of
+// the finite ones (fmaxf leaves NaN out by itself).
+template <int N, typename Reduce>
+__device__ __forceinline__ uint32_t scale_byte_of(const float (&v)[N], Reduce reduce)
+{
+    constexpr float INF = __builtin_inff();
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) top = fmaxf(top, fabsf(v[i]));
+    top = reduce(top);
+    if (top == INF) {
+        top = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) top = fmaxf(top, fabsf(v[i]) < INF ? fabsf(v[i]) : 0.f);
+        top = reduce(top);
+    }
+    return scale_byte(top);
 }
 
 // Four values in one word of codes, and back.
@@ -225,10 +245,7 @@ __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packe
         w4 out[V];
         uint32_t eo = 0;
         if constexpr (EIGHT) {
-            float top = 0.f;
-#pragma unroll
-            for (int c = 0; c < C; ++c) top = fmaxf(top, fabsf(S[c]));
-            eo = scale_byte(row_reduce<LANES>(top, [](float x, float y) { return fmaxf(x, y); }));
+            eo = scale_byte_of(S, [](float top) { return row_reduce<LANES>(top, [](float x, float y) { return fmaxf(x, y); }); });
 #pragma unroll
             for (int n = 0; n < 4; ++n) out[0][n] = to_codes(&S[4 * n], scale_of(eo));
         } else {
@@ -941,14 +958,10 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
             w4 out[NV];
             uint32_t eo = 0;
             if constexpr (EIGHT) {
-                float top = 0.f;
-#pragma unroll
-                for (int f = 0; f < KS; ++f)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(S[f][j]));
-                top = fmaxf(top, __shfl_xor(top, 16));
-                top = fmaxf(top, __shfl_xor(top, 32));
-                eo = scale_byte(top);
+                eo = scale_byte_of(reinterpret_cast<const float (&)[8 * KS]>(S), [](float top) {
+                    top = fmaxf(top, __shfl_xor(top, 16));
+                    return fmaxf(top, __shfl_xor(top, 32));
+                });
 #pragma unroll
                 for (int f = 0; f < KS; ++f) {
                     out[f / 2][f % 2 * 2] = to_codes(&S[f][0], scale_of(eo));

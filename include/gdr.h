@@ -431,7 +431,8 @@ gdr_status gdr_qk_rotary_backward(const gdr_rotary *rotary, const void *d_q_out,
  * not below -100 (a row of zeros has that).  Values are rounded to nearest
  * even whenever a state is written.  fp16 holds magnitudes up to 65,504 (more
  * becomes an infinity); in e4m3 an infinity becomes NaN, a NaN stays in its
- * place, and what rounds to 2^128 (above 1.9375 * 2^127) reads as an infinity.
+ * place, neither counts in max |row|, and what rounds to 2^128 (above 1.9375 *
+ * 2^127) reads as an infinity.
  * Each call that updates a state rounds it anew, by up to 2^-11 (fp16), 2^-8
  * (bf16) or 2^-4 (e4m3) of a value; a decay a per token lets the errors of about
  * 1 / (1 - a^2) calls stand side by side, so 8 bits suit parked states and heads

@@ -1,0 +1,88 @@
+"""Edges of the norm and rotation of q and k and of the state cache in fewer
+bits, on an MI355X: values that are not finite, sizes at which a kernel changes
+its course, and bounds that a lost plane of an operand exceeds."""
+import numpy as np
+import pytest
+
+from gated_delta_rule_token_amd import workloads
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from gated_delta_rule_token_amd import api
+    api.load_library()
+
+
+DT = {"f16": torch.float16, "bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}
+
+
+def ids(*values):
+    return torch.tensor(values, dtype=torch.int32, device="cuda")
+
+
+def bits(t):
+    return t.view({1: torch.uint8, 2: torch.int16, 4: torch.int32}[t.element_size()])
+
+
+# ------------------------------------------------------------------ values that are not finite, in 8 bits
+
+@pytest.mark.parametrize("dk", [2, 3, 4, 30, 64, 128, 150, 256])
+def test_infinities_leave_the_rest_of_an_8_bit_row(dk):
+    """A row's scale is that of its finite values: with an infinity in place of a
+    zero every other code and the scale stay, and the infinity reads as NaN."""
+    from gated_delta_rule_token_amd import api
+    g = torch.Generator().manual_seed(dk)
+    x = torch.randn(2, 2, 37, dk, generator=g) * torch.exp(4 * torch.randn(2, 2, 37, 1, generator=g))
+    at = torch.randint(0, dk, (2, 2, 37, 1), generator=g)
+    x.scatter_(-1, at, 0.0)
+    bad = torch.tensor([float("inf"), -float("inf")]).repeat(74)[: 2 * 2 * 37].view(2, 2, 37, 1)
+    y = x.scatter(-1, at, bad)
+    y[1, 1, 5] = float("inf")  # nothing finite
+    got = []
+    for states in (x, y):
+        slab = api.packed_slab(3, 2, 37, dk, torch.float8_e4m3fn)
+        api.state_pack(states.cuda(), slab, ids(2, 0))
+        got.append((bits(slab.data).cpu(), bits(slab.scale).cpu(), api.state_unpack(slab, ids(2, 0)).cpu()))
+    (codes, scale, _), (codes_y, scale_y, read_y) = got
+    hit = torch.zeros(3, 2, 37, dk, dtype=torch.bool)
+    hit[[2, 0]] = torch.zeros(2, 2, 37, dk, dtype=torch.bool).scatter_(-1, at, True)
+    hit[0, 1, 5] = True
+    rows = torch.ones(3, 2, 37, dtype=torch.bool)
+    rows[0, 1, 5] = False
+    assert torch.equal(codes_y[~hit], codes[~hit]) and torch.equal(scale_y[rows], scale[rows])
+    assert torch.equal(read_y.isnan(), hit[[2, 0]])
+
+
+@pytest.mark.parametrize("act", [np.float16, "bf16", np.float32])
+@pytest.mark.parametrize("L", [1, 3, 10])
+@pytest.mark.parametrize("dk", [9, 64, 72, 128, 200, 256])
+def test_an_infinite_key_leaves_the_rest_of_an_8_bit_row(dk, L, act):
+    """Without retrieval a key channel's state is its own: an infinity there
+    (column 3 of the last token's k) leaves the others' codes and the rows' scales as
+    they are with a zero in its place."""
+    from gated_delta_rule_token_amd import api
+    packing = dict(lengths=[1, L]) if L > 8 else dict(rank4_batch=(2, L))
+    case = workloads.random_case(dk + L, H=1, HV=2, DK=dk, DV=40, dtype=act, slots=(4,), update_rule="linear", **packing)
+    cu = None if case["cu_seqlens"] is None else torch.from_numpy(case["cu_seqlens"]).cuda()
+    dt = {"float16": torch.float16, "float32": torch.float32}.get(getattr(act, "__name__", ""), torch.bfloat16)
+    q, k, v = (torch.from_numpy(np.asarray(case[n], np.float32)).to(dt).cuda() for n in "qkv")
+    k[..., 3] = 0
+    start = torch.from_numpy(np.asarray(case["slab"], np.float32))
+    start[..., 3] = 0
+    where = torch.from_numpy(case["slot_ids"]).cuda()
+    got = []
+    for value in (0.0, float("inf")):
+        slab = api.packed_slab(4, 2, 40, dk, torch.float8_e4m3fn)
+        api.state_pack(start.cuda(), slab, ids(0, 1, 2, 3))
+        k.flatten(0, -3)[-1, :, 3] = value
+        api.forward_packed(q, k, v, slab=slab, slot_ids=where, cu_seqlens=cu, update_rule="linear")
+        got.append((bits(slab.data).cpu(), bits(slab.scale).cpu(), slab.data.float().cpu()))
+    (codes, scale, _), (codes_y, scale_y, read_y) = got
+    rest = torch.arange(dk) != 3
+    assert torch.equal(codes_y[..., rest], codes[..., rest]) and torch.equal(scale_y, scale)
+    assert bool(read_y[int(where[1]), ..., 3].isnan().all()) and not bool(read_y[int(where[0])].isnan().any())
