@@ -6,7 +6,8 @@
 //   (y_0, y_1) = (h_0 cos a - h_1 sin a, h_1 cos a + h_0 sin a)
 // and backwards, with g the pairs of dy turned by -a, t = w g and n = x inv,
 //   dx = inv (t - n mean(t n)),   dw = sum over tokens and heads of g n
-// (the norm's statistics are formed again: a sum more, nothing kept).
+// (dx = t without the norm; its statistics are formed again: a sum more, nothing
+// kept).
 //
 // Bound by memory: a head's row lies in the registers of LPR lanes between its
 // load and its store.  A lane holds both values of its pairs: VEC elements
@@ -253,8 +254,9 @@ __global__ __launch_bounds__(THREADS) void k_rotary(const RotaryParams p)
 // weights kept in registers, 29,273 tokens x 16 + 16 heads of 128 in bf16 took 163
 // instead of 143 us.  A row's work has few branches: with one for every value of
 // lanes that hold nothing, a workgroup's two turns took 18 us, and 1,500 tokens 26
-// instead of 20.)
-template <typename T, typename TW, int VEC, int LPR, int NV>
+// instead of 20.  NORM is the call's: chosen value by value it took 58,000 tokens x
+// 32 heads of 64 from 140 to 149 us.)
+template <typename T, typename TW, int VEC, int LPR, int NV, bool NORM>
 __global__ __launch_bounds__(THREADS, 4) void k_rotary_back(const RotaryParams p)
 {
     __shared__ __align__(16) float s_cos[ANGLES], s_sin[ANGLES], s_w[ROTARY_MAX_DIM];
@@ -327,10 +329,12 @@ __global__ __launch_bounds__(THREADS, 4) void k_rotary_back(const RotaryParams p
             }
             if (token < n) fetch(token, head);
             float inv = 1.f, mean = 0.f;
-            if (p.norm) {
+            __builtin_amdgcn_sched_barrier(0);  // (the row's two halves mixed hold more than the registers)
+            if constexpr (NORM) {
                 inv = 1.f / sqrtf(row_sum<LPR>(sum) / (float)p.dim + p.eps);
                 mean = row_sum<LPR>(dot) * inv / (float)p.dim;
             }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
                 const Place<VEC> at(p, lane + LPR * v);
@@ -338,9 +342,9 @@ __global__ __launch_bounds__(THREADS, 4) void k_rotary_back(const RotaryParams p
                 weights(at, w);
 #pragma unroll
                 for (int i = 0; i < 2 * VEC; ++i) {
-                    const float nx = h[v][i] * inv;
+                    const float nx = h[v][i] * inv, t = g[v][i] * w[i];
                     dw[v][i] += g[v][i] * nx;
-                    g[v][i] = inv * (g[v][i] * w[i] - nx * mean);
+                    g[v][i] = NORM ? inv * (t - nx * mean) : t;  // (without: x, be it an infinity, has no part in it)
                 }
                 if (!at.on) continue;
                 store<T, VEC>(row + at.at[0], &g[v][0]);
@@ -519,8 +523,9 @@ hipError_t launch_rotary_backward(const RotaryParams &params, hipStream_t s)
                     for (RotaryPart &part : p.part) part.partial = part.heads ? part.d_weight : nullptr;
                 }
                 const dim3 blocks((unsigned)std::max(p.part[0].blocks, p.part[1].blocks), 2);
-                hipLaunchKernelGGL((k_rotary_back<T, TW, decltype(vec)::value, decltype(lpr)::value, decltype(nv)::value>),
-                                   blocks, dim3(THREADS), 0, s, p);
+                const auto kernel = p.norm ? k_rotary_back<T, TW, decltype(vec)::value, decltype(lpr)::value, decltype(nv)::value, true>
+                                           : k_rotary_back<T, TW, decltype(vec)::value, decltype(lpr)::value, decltype(nv)::value, false>;
+                hipLaunchKernelGGL(kernel, blocks, dim3(THREADS), 0, s, p);
                 return hipGetLastError();
             });
         });

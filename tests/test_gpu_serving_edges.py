@@ -86,3 +86,23 @@ def test_an_infinite_key_leaves_the_rest_of_an_8_bit_row(dk, L, act):
     rest = torch.arange(dk) != 3
     assert torch.equal(codes_y[..., rest], codes[..., rest]) and torch.equal(scale_y, scale)
     assert bool(read_y[int(where[1]), ..., 3].isnan().all()) and not bool(read_y[int(where[0])].isnan().any())
+
+
+# ------------------------------------------------------------------ the rotation
+
+@pytest.mark.parametrize("d,R,dtype,weight,inter", [(128, 128, "bf16", "bf16", False), (72, 40, "f16", None, False),
+                                                    (63, 30, "f32", "f32", True), (64, 64, "f32", None, False)])
+def test_gradients_without_the_norm_do_not_depend_on_x(d, R, dtype, weight, inter):
+    """d_x is weight * g then, whatever x holds; a weight's gradient sums x by column."""
+    from tests.test_gpu_rotary import back, cuda, d_outs, dev, make
+    c = make(31, 50, 3, 2, d, R, dtype, weight=weight)
+    douts = cuda(d_outs(c))
+    want = back(dev(c), *douts, inter, False)
+    c["q"][7, 1, 5], c["q"][20, 0, d - 1], c["k"][3, 1, 2] = float("inf"), float("nan"), -float("inf")
+    got = back(dev(c), *douts, inter, False)
+    assert torch.equal(got.q, want.q) and torch.equal(got.k, want.k)
+    if weight is not None:
+        for g, w, columns in ((got.q_weight, want.q_weight, [5, d - 1]), (got.k_weight, want.k_weight, [2])):
+            rest = torch.ones(d, dtype=torch.bool)
+            rest[columns] = False
+            assert torch.equal(g.cpu()[rest], w.cpu()[rest]) and not bool(g.cpu()[~rest].isfinite().any())
