@@ -134,7 +134,9 @@ __device__ __forceinline__ float row_sum(float x)
 // of a turn (their first terms left out are under 3e-8).
 __device__ __forceinline__ void sincos_turns(double turns, float &sn, float &cs)
 {
-    const float f = (float)(turns - rint(turns)), n = rintf(4.f * f), r = fmaf(n, -0.25f, f), y = r * r;
+    const double f = turns - rint(turns);
+    const float n = rintf(4.f * (float)f);
+    const float r = (float)fma((double)n, -0.25, f), y = r * r;  // (rounded before the quarters are off, it would lose two bits)
     const float s = r * fmaf(y, fmaf(y, fmaf(y, fmaf(y, 42.058693944897653f, -76.705859753061386f), 81.605249276075054f),
                                      -41.341702240399755f), 6.2831853071795865f);
     const float c = fmaf(y, fmaf(y, fmaf(y, fmaf(y, 60.244641371876664f, -85.456817206693732f), 64.939394022668291f),

@@ -106,3 +106,24 @@ def test_gradients_without_the_norm_do_not_depend_on_x(d, R, dtype, weight, inte
             rest = torch.ones(d, dtype=torch.bool)
             rest[columns] = False
             assert torch.equal(g.cpu()[rest], w.cpu()[rest]) and not bool(g.cpu()[~rest].isfinite().any())
+
+
+def test_sines_and_cosines_of_far_positions():
+    """Pairs (1, 0) turn into (cos, sin).  With u = 2^-24: the rest of the turn, at
+    most an eighth, is rounded by 2^-28, 2.4e-8 in the angle and 1.7e-8 in a sine of
+    0.707; its series loses 1.2 u on the last product's factor (up to 6.28, rounded by
+    2^-22 of at least 5.65), 0.3 u on its terms and u on the product, 2.5 u 0.707 =
+    1.05e-7 if all err to one side, and the terms left out 2e-8 at the ends alone (3e-9 in
+    the sine).  So each is within 1.3e-7 at most; a fraction of a whole turn rounded
+    to fp32 exceeds that by itself with 9.4e-8 in the angle."""
+    from gated_delta_rule_token_amd import api
+    T, half = 16384, 64
+    g = torch.Generator().manual_seed(5)
+    pos = torch.randint(-2000000, 2000000, (T,), generator=g).to(torch.int32)
+    freq = torch.exp(-9.2 * torch.rand(half, generator=g))
+    x = torch.cat([torch.ones(T, 1, half), torch.zeros(T, 1, half)], -1)
+    y = api.qk_rotary(x.cuda(), None, pos.cuda(), freq.cuda(), norm=False).q.cpu().double()
+    angle = pos.double()[:, None, None] * freq.double()
+    err = (y - torch.cat([torch.cos(angle), torch.sin(angle)], -1)).abs()
+    print("largest error %.3e" % float(err.max()))
+    assert float(err.max()) <= 1.3e-7
