@@ -182,7 +182,7 @@ __global__ __launch_bounds__(THREADS) void k_rotary(const RotaryParams p)
     constexpr int ROWS = THREADS / LPR;
     const int lane = threadIdx.x % LPR;
     const int heads = p.part[0].heads + p.part[1].heads;
-    const int64_t t0 = (int64_t)blockIdx.x * p.block;
+    const int64_t t0 = p.first + (int64_t)blockIdx.x * p.block;
     const int n = (int)(p.tokens - t0 < p.block ? p.tokens - t0 : p.block);
     const int step_t = ROWS / heads, step_h = ROWS - step_t * heads;
     int token = threadIdx.x / LPR / heads, head = threadIdx.x / LPR - token * heads;
@@ -487,11 +487,16 @@ hipError_t launch_rotary(const RotaryParams &params, hipStream_t s)
             p.block = token_block(p, heads, std::min(16384 / (p.dim * (int)sizeof(T)), 8 * THREADS / lpr()));
             const int64_t spread = (p.tokens + 511) / 512;  // few tokens: a workgroup each
             if (p.block > spread) p.block = (int)spread;
-            const dim3 blocks((unsigned)((p.tokens + p.block - 1) / p.block));
-            if (blocks.x >= 1u << 24) return hipErrorInvalidConfiguration;  // a launch has fewer than 2^32 threads
-            hipLaunchKernelGGL((k_rotary<T, TW, decltype(vec)::value, decltype(lpr)::value, decltype(nv)::value>),
-                               blocks, dim3(THREADS), 0, s, p);
-            return hipGetLastError();
+            // a launch has fewer than 2^32 threads: further tokens take another
+            const int64_t most = (int64_t)((1 << 24) - 1) * p.block;
+            for (; p.first < p.tokens; p.first += most) {
+                const dim3 blocks((unsigned)((std::min(most, p.tokens - p.first) + p.block - 1) / p.block));
+                hipLaunchKernelGGL((k_rotary<T, TW, decltype(vec)::value, decltype(lpr)::value, decltype(nv)::value>),
+                                   blocks, dim3(THREADS), 0, s, p);
+                hipError_t err = hipGetLastError();
+                if (err != hipSuccess) return err;
+            }
+            return hipSuccess;
         });
     });
 }

@@ -33,6 +33,7 @@ struct RotaryParams {
     int32_t dim, half, axes;        // half: pairs that are turned
     int32_t neighbours, norm, dt, weight_dt;
     int32_t block;                  // forward: tokens a workgroup takes
+    int64_t first;                  // forward: token of the launch's first workgroup
     float eps;
     const int32_t *positions, *axis_of;
     const float *freq;

@@ -127,3 +127,23 @@ def test_sines_and_cosines_of_far_positions():
     err = (y - torch.cat([torch.cos(angle), torch.sin(angle)], -1)).abs()
     print("largest error %.3e" % float(err.max()))
     assert float(err.max()) <= 1.3e-7
+
+
+def test_more_tokens_than_a_launch_has_workgroups():
+    """2^24 and more workgroups of a token each: rows at the ends and around the
+    2^24th against a call of those rows alone."""
+    from gated_delta_rule_token_amd import api
+    T, H = 2 ** 24 + 5, 128
+    at = torch.cat([torch.arange(0, 3), torch.arange(2 ** 24 - 4, T)]).cuda()
+    g = torch.Generator().manual_seed(6)
+    rows = torch.randn(at.shape[0], H, 2, generator=g).half().cuda()
+    p = torch.randint(-5000, 5000, (at.shape[0],), generator=g).to(torch.int32).cuda()
+    freq = torch.tensor([0.3], device="cuda")
+    q = torch.zeros(T, H, 2, dtype=torch.float16, device="cuda")
+    pos = torch.zeros(T, dtype=torch.int32, device="cuda")
+    q[at], pos[at] = rows, p
+    api.qk_rotary(q, None, pos, freq, out=(q, None))
+    assert torch.equal(q[at], api.qk_rotary(rows, None, p, freq).q)
+    assert not bool(q[3: 2 ** 24 - 4].any())
+    del q
+    torch.cuda.empty_cache()
