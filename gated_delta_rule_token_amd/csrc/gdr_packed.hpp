@@ -394,10 +394,12 @@ __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packe
 // z.  Vectors of the other 16-bit type go in as two planes, exact for fp16 in
 // bf16; bf16 in fp16 is scaled by a power of two that brings the largest to
 // [2^14, 2^15), where two planes hold 2^-39 of it.  d (fp32) goes into the
-// second product as bf16 planes: three, all 24 bits, beside a bf16 k; two (to
-// 2^-17, a sixty-fourth of fp16's rounding of the state) beside an fp16 k, which
-// takes two planes itself.  The planes share one product: its 32 inner places
-// hold 8 tokens of four plane pairs.
+// second product as three bf16 planes, all 24 bits: where a token replaces values,
+// d k takes away what is there, and what it is off by stays (with two planes, under
+// 2^-17, values 2^12 times smaller than those before them were off by eight of fp16's
+// steps).  An fp16 k takes two planes.  The 32 inner places of a product hold 8 tokens of
+// four plane pairs: one product beside a bf16 k, two beside others, of which the second,
+// of the small pairs, has the same operand k and no time of its own.
 //
 // Any other call (GEN: fp32 activations, a decay for each key, the erase gate)
 // takes the decays into the vectors.  With D_t the product of the decays up to
@@ -405,14 +407,14 @@ __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packe
 // t's write enters a later x_n's dot by sum_j k_t (D_n / D_t) e_n k_n, and S by
 // d_t (D_T / D_t) o k_t: a lane forms these for its two keys, the quotients as
 // running products of the later decays, which do not overflow.  x_n in fp32 goes
-// in as planes (two of fp16 scaled as above, 2^-22 of its largest value; three
-// of bf16 beside a bf16 cache), k_t and d_t as two of bf16 each.  256 requests x
+// in as planes (two of fp16 scaled as above, 2^-22 of its largest value, a third
+// would take 64 registers of 256 keys; three of bf16 beside a bf16 cache), k_t and
+// d_t as three of bf16 each.  256 requests x
 // 32 heads of 128, 4 tokens, vector units and this, in us: a decay for each key
-// on 16 and 8 bits 229 and 118, 210 and 106; fp32 activations 211 and 113, 205
-// and 96; 64 requests x 32 heads of 256, a decay for each key, 243 and 123, 224
-// and 78.  8 bits wait for the vectors' own work: 7 tokens take 132 us, 64 of
-// them with 16 rows a state (96 with each token's values loaded when their turn
-// comes and every dot reduced by itself).
+// on 16 and 8 bits 229 and 118, 210 and 96; fp32 activations 211 and 112, 205
+// and 90; 64 requests x 32 heads of 256, a decay for each key, 243 and 123, 224
+// and 79.  8 bits wait for the vectors' own work: 7 tokens take 119 us, 53 of
+// them with 16 rows a state.
 //
 // A tile is 16 rows: lane (c, kb) of a wave holds row c, 8 keys of every 32 (with
 // codes 16 of 64) at the kb-th place, which is the first product's operand; the
@@ -466,6 +468,16 @@ __device__ __forceinline__ void half_scale(float top, float &up, float &back)
     back = __builtin_bit_cast(float, (uint32_t)(127 + e) << 23);
 }
 
+// Planes of 8 bits: the upper half of an fp32 value is a bf16, what lies below it is
+// exact, and so three planes hold all 24 bits.  below: x without its bits in `mask`
+// (UPPER; 0: x; all: 0; NaN and infinities give NaN); uppers: two upper halves in a word.
+constexpr uint32_t UPPER = 0xFFFF0000u;
+__device__ __forceinline__ float below(float x, uint32_t mask) { return x - as_float(__builtin_bit_cast(uint32_t, x) & mask); }
+__device__ __forceinline__ uint32_t uppers(float a, float b)
+{
+    return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, a), 0x07060302);
+}
+
 // Orders a wave's own LDS accesses: writes of other lanes before it, reads after.
 __device__ __forceinline__ void wave_sync()
 {
@@ -499,10 +511,10 @@ __device__ __forceinline__ void exchange(w4 &x, w4 &y, bool odd)
 // row that would pass its end start earlier: keys that they share with another
 // lane's count there in the dots (x is 0 here), and both write the same bytes, by
 // plain accesses as above.  256 requests x 32 heads, 2 and 4 tokens, vector units
-// and this, in us: heads of 56 in 16 bits 71, 111 and 33, 37, in 8 bits 55, 88 and
-// 32, 36; of 96 in 16 bits 128, 202 and 82, 90; of 150 361, 589 and 188, 202; of
-// 224 513, 840 and 388, 435.  (Of 255 in 16 bits, odd rows across each other's
-// lines, 622, 941 and 828, 899: behind at 2 tokens, ahead from 4.)
+// and this, in us: heads of 56 in 16 bits 71, 111 and 31, 36, in 8 bits 55, 88 and
+// 32, 37; of 96 in 16 bits 128, 202 and 82, 90; of 150 361, 589 and 188, 202; of
+// 224 513, 840 and 387, 430.  (Of 255 in 16 bits, odd rows across each other's
+// lines, 622, 941 and 820, 895: behind at 2 tokens, ahead from 4.)
 template <typename TA, int TYPE, int DK, int PRE, bool GEN, bool EXACT>
 __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int rule, int per_key, int waves)
 {
@@ -513,7 +525,7 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
     using TE = typename std::conditional<GEN, half_t, TA>::type;
     using TC = typename std::conditional<EIGHT, TE, typename CacheType<TYPE>::T>::type;
     constexpr bool CB = std::is_same<TC, bf16_t>::value, SAME = !GEN && std::is_same<TC, TA>::value;
-    constexpr int PX = GEN ? (CB ? 3 : 2) : SAME ? 1 : 2, PK = BF ? 1 : 2;
+    constexpr int PX = GEN ? (CB ? 3 : 2) : SAME ? 1 : 2, PK = GEN ? 3 : BF ? 1 : 2;
     using VA = typename Vec8<TA>::V;
     using VC = typename Vec8<TC>::V;
     // a wave's k by keys (and before it, where x does not come from memory, x)
@@ -744,15 +756,19 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
         wave_sync();
 #pragma unroll
         for (int m = 0; m < KL; ++m) {
-            b8 hi, mid;
+            w4 planes[3];
 #pragma unroll
-            for (int t = 0; t < T; ++t) {
-                const float v = t < n ? kv[t][m] : 0.f;
-                hi[t] = from_f32<bf16_t>(v);
-                mid[t] = from_f32<bf16_t>(v - to_f32(hi[t]));
+            for (int t = 0; t < T; t += 2) {
+                float v0 = t < n ? kv[t][m] : 0.f, v1 = t + 1 < n ? kv[t + 1][m] : 0.f;
+#pragma unroll
+                for (int x = 0; x < 3; ++x) {
+                    planes[x][t / 2] = uppers(v0, v1);
+                    v0 = below(v0, UPPER);
+                    v1 = below(v1, UPPER);
+                }
             }
-            *reinterpret_cast<b8 *>(&s_k[0][j0 + m][0]) = hi;
-            *reinterpret_cast<b8 *>(&s_k[PK - 1][j0 + m][0]) = mid;
+#pragma unroll
+            for (int x = 0; x < PK; ++x) *reinterpret_cast<w4 *>(&s_k[x][j0 + m][0]) = planes[x];
         }
         wave_sync();
     } else {
@@ -927,30 +943,36 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
                     if (16 * tile + 4 * kb + j < p.dv) o[j] = from_f32<TA>(oscale * z[j]);
             }
             wave_sync();
-            // d of row c in planes: hi, mid, lo (and k is exact), or hi, mid for both planes of k
-            const bool plane1 = BF ? kb > 0 : (kb & 1), plane2 = kb > 1;
-            b8 dv8;
+            // d of row c in planes hi, mid, lo, beside k's at the same inner places: by kb, hi
+            // mid lo - (k is exact), or lo - lo - and then hi mid hi mid beside k's hi hi mid mid, or
+            // lo - mid - and then hi mid hi hi beside hi hi mid lo
+            float d[T];
 #pragma unroll
-            for (int t = 0; t < T; ++t) {
-                dv8[t] = from_f32<bf16_t>(0.f);
-                if (t < n) {
-                    float d = GEN ? s_d[t][c] : s_d[t][c] * put[t];
-                    d -= plane1 ? to_f32(from_f32<bf16_t>(d)) : 0.f;
-                    if constexpr (BF) {
-                        d -= plane2 ? to_f32(from_f32<bf16_t>(d)) : 0.f;
-                        d = kb == 3 ? 0.f : d;
-                    }
-                    dv8[t] = from_f32<bf16_t>(d);
-                }
-            }
+            for (int t = 0; t < T; ++t) d[t] = GEN ? s_d[t][c] : t < n ? s_d[t][c] * put[t] : 0.f;  // 0 past the tokens
             wave_sync();
+            const auto planes = [&](uint32_t first, uint32_t second) {
+                w4 d8;
+#pragma unroll
+                for (int t = 0; t < T; t += 2)
+                    d8[t / 2] = uppers(below(below(d[t], first), second), below(below(d[t + 1], first), second));
+                return __builtin_bit_cast(b8, d8);
+            };
+            b8 d8, low8;
+            if constexpr (BF) {
+                d8 = planes(kb == 0 ? 0 : UPPER, kb < 2 ? 0 : kb == 2 ? UPPER : ~0u);
+            } else {
+                d8 = planes(kb == 1 || (!GEN && kb == 3) ? UPPER : 0, 0);
+                low8 = planes(UPPER, kb & 1 ? ~0u : GEN && kb == 2 ? 0 : UPPER);
+            }
+            const int k_plane = BF || kb == 0 ? 0 : GEN ? kb - 1 : kb >> 1;
 #pragma unroll
             for (int f = 0; f < KS; ++f)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const b8 k8 = *reinterpret_cast<const b8 *>(&s_k[BF ? 0 : kb >> 1][key(f, c / 4) + 4 * j + c % 4][0]);
+                    const b8 k8 = *reinterpret_cast<const b8 *>(&s_k[k_plane][key(f, c / 4) + 4 * j + c % 4][0]);
                     f4v acc = {S[f][4 * j], S[f][4 * j + 1], S[f][4 * j + 2], S[f][4 * j + 3]};
-                    acc = mfma(k8, dv8, acc);
+                    if constexpr (!BF) acc = mfma(k8, low8, acc);
+                    acc = mfma(k8, d8, acc);
 #pragma unroll
                     for (int m = 0; m < 4; ++m) S[f][4 * j + m] = acc[m];
                 }
@@ -1022,20 +1044,22 @@ hipError_t packed_step_at(const PackedParams &a, int rule, bool per_key, hipStre
         int waves = 1;
         while (waves < 8 && waves * 16 < p.dv && states * waves < 2048) waves *= 2;
         const dim3 blocks((unsigned)((states * waves + 3) / 4)), threads(256);
-        constexpr int PRE = TYPE == CACHE_E4M3 ? 2 : 1;
+        // Tiles ahead: two in 8 bits, but one where two would spill (GEN, 256 keys) or leave two
+        // waves a SIMD instead of three (other dims: 4 tokens, heads of 96 in 8 bits 83 and 68 us).
+        constexpr int PRE = TYPE == CACHE_E4M3 ? 2 : 1, PRE_GEN = DK > 192 ? 1 : PRE;
         const bool exact = p.dk == DK;
         if constexpr (sizeof(TA) == 2) {
             if (exact && !keyed)
                 hipLaunchKernelGGL((k_packed_few<TA, TYPE, DK, PRE, false, true>), blocks, threads, 0, s, a, rule, 0, waves);
         }
         if (exact && (keyed || sizeof(TA) == 4))
-            hipLaunchKernelGGL((k_packed_few<TA, TYPE, DK, PRE, true, true>), blocks, threads, 0, s, a, rule, (int)per_key, waves);
+            hipLaunchKernelGGL((k_packed_few<TA, TYPE, DK, PRE_GEN, true, true>), blocks, threads, 0, s, a, rule, (int)per_key, waves);
         // (to 192 keys with products over 192: 256 requests x 32 heads of 192, 2 tokens,
         // 446 -> 313 us in 16 bits and 228 -> 188 in 8)
         if (DK == 256 && p.dk <= 192)
             hipLaunchKernelGGL((k_packed_few<TA, TYPE, DK == 256 ? 192 : DK, PRE, true, false>), blocks, threads, 0, s, a, rule, (int)per_key, waves);
         else if (!exact)
-            hipLaunchKernelGGL((k_packed_few<TA, TYPE, DK, PRE, true, false>), blocks, threads, 0, s, a, rule, (int)per_key, waves);
+            hipLaunchKernelGGL((k_packed_few<TA, TYPE, DK, 1, true, false>), blocks, threads, 0, s, a, rule, (int)per_key, waves);
         hipError_t err = hipGetLastError();
         if (err != hipSuccess || (p.cu_seqlens ? p.T : p.L) <= 8) return err;
     }

@@ -457,10 +457,13 @@ gdr_status gdr_state_unpack(int32_t batch, int32_t heads, int32_t dv, int32_t dk
  * slab's, tensors->slot_ids is required, tensors->initial_state and final_state
  * are NULL.  The states are read, updated in fp32 over all tokens of their
  * request and rounded once, on the way back; a request without tokens leaves
- * its states as they are.  An infinity that a token brings may make its rows'
- * states NaN.  Few tokens a request (8 on average) run in one pass over the
- * packed states, without workspace; longer requests (or algo RECURRENT or
- * CHUNKED) run gdr_forward's kernels on fp32 states in the workspace. */
+ * its states as they are.  (Two to eight tokens a request with fp32 activations,
+ * a decay for each key or the erase gate: the vectors that multiply fp16 or e4m3
+ * states count to 2^-22 of their largest value.)  An infinity that a token
+ * brings may make its rows' states NaN.  Few tokens a request (8 on average) run
+ * in one pass over the packed states, without workspace; longer requests (or
+ * algo RECURRENT or CHUNKED) run gdr_forward's kernels on fp32 states in the
+ * workspace. */
 gdr_status gdr_packed_workspace_size(const gdr_problem *problem, size_t *bytes);
 gdr_status gdr_forward_packed(const gdr_problem *problem, const gdr_tensors *tensors, const gdr_packed_slab *slab,
                               void *workspace, size_t workspace_bytes, void *stream);

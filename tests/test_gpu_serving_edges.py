@@ -147,3 +147,76 @@ def test_more_tokens_than_a_launch_has_workgroups():
     assert not bool(q[3: 2 ** 24 - 4].any())
     del q
     torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------------ steps of several tokens
+
+FORMS = {"plain": dict(update_rule="delta"), "per_key": dict(update_rule="gated_delta", per_key=True),
+         "erase": dict(update_rule="gated_delta_v2")}
+
+
+@pytest.mark.parametrize("cache", DT)
+@pytest.mark.parametrize("act", [np.float16, "bf16", np.float32])
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dk,L", [(128, 1), (128, 3), (64, 8), (256, 5), (72, 4), (200, 7), (15, 3), (128, 12)])
+def test_values_that_replace_far_larger_ones(cache, act, form, dk, L):
+    """Each token has a key channel of its own, k = c there, and a rate (or an
+    erase) of 1 / c^2: what stays of the old value S is v / c, up to 2^-14 times
+    smaller, so the arithmetic's share of S shows: every product of the update
+    takes part in 32 bits.  With u = 2^-24 and M = |S| + 2 |v|, which bounds
+    every term: S k by planes 4 u, the difference from v and its factors 4 u, the
+    planes of that and of k and their products 6 u, the sum with S u: 16 u M.  Two planes
+    of 8 bits instead of three would add 64 u M."""
+    from gated_delta_rule_token_amd import api
+    from tests.test_gpu_packed import HALF, LEAST, gpu_tensors, oracle_step, read, slab_of
+    from tests.test_gpu_packed import bits as code_bits
+    far = {"f16": 2.0 ** 12, "bf16": 2.0 ** 15, "e4m3": 2.0 ** 18}[cache]
+    if act == np.float16 and far > 2.0 ** 15:
+        far = 2.0 ** 15  # (v times a power of two below)
+    packing = dict(lengths=[1, L]) if L > 8 else dict(rank4_batch=(2, L))
+    case = workloads.random_case(7 * dk + L, H=1, HV=2, DK=dk, DV=72, dtype=act, slots=(3,), **packing, **FORMS[form])
+    rng = np.random.default_rng(dk + L)
+    lead = case["q"].shape[:-2]
+    T = int(np.prod(lead))
+    narrow = {np.float16: lambda x: x.astype(np.float16), "bf16": lambda x: torch.from_numpy(x).bfloat16().float().numpy(),
+              np.float32: lambda x: x}[act]
+    column = np.concatenate([rng.permutation(dk)[:n] for n in ([1, L] if L > 8 else [L, L])])
+    c = narrow(rng.uniform(0.5, 1.0, T).astype(np.float32))
+    k, q = np.zeros((T, 1, dk), c.dtype), np.zeros((T, 1, dk), c.dtype)
+    k[np.arange(T), 0, column] = c
+    q[np.arange(T), 0, column] = narrow(rng.uniform(0.5, 1.0, T).astype(np.float32))
+    case["k"], case["q"] = k.reshape(case["k"].shape), q.reshape(case["q"].shape)
+    case["v"] = narrow((rng.uniform(0.5, 1.0, case["v"].shape) * rng.choice([-1, 1], case["v"].shape)).astype(np.float32))
+    rate = (1 / c.astype(np.float64) ** 2).astype(np.float32)
+    if case["gate"] is not None:
+        case["gate"] = np.zeros_like(case["gate"])
+    if case["beta"] is not None:
+        case["beta"] = np.broadcast_to(rate.reshape(lead + (1,)), case["beta"].shape).astype(np.float32).copy()
+    if case["erase"] is not None:
+        case["erase"] = np.broadcast_to(rate.reshape(lead + (1, 1)), case["erase"].shape).astype(np.float32).copy()
+    start = np.zeros_like(case["slab"])
+    first = 0
+    for b, n in enumerate([1, L] if L > 8 else [L, L]):
+        mine = column[first: first + n]
+        start[int(case["slot_ids"][b])][..., mine] = far * rng.uniform(0.5, 1.0, (2, 72, n)) * rng.choice([-1, 1], (2, 72, n))
+        first += n
+    case["slab"] = start
+    slab = slab_of(start, cache)
+    old = read(slab.data, slab.scale).numpy()
+    d, args = gpu_tensors(case)
+    o = api.forward_packed(d["q"], d["k"], d["v"], slab=slab, **args)
+    ro, rs = oracle_step(case, old)
+    got = read(slab.data, slab.scale).numpy()
+    live = case["slot_ids"]
+    M = np.abs(old[live]).max() + 2 * np.abs(np.asarray(case["v"], np.float64)).max()
+    least = LEAST[cache] * (1 if cache != "e4m3" else np.exp2(code_bits(slab.scale).cpu().double().numpy()[live] - 127)[..., None])
+    slack = 2.0 ** -20 * M
+    bound = HALF[cache] * (np.abs(rs[live]) + slack) + least + slack
+    err = np.abs(got[live] - rs[live])
+    print("state: %.3f of the bound" % float((err / bound).max()))
+    assert (err <= bound).all()
+    out_half = {"float32": 2.0 ** -24, "float16": 2.0 ** -11, "bfloat16": 2.0 ** -8}[str(o.dtype)[6:]]
+    err = np.abs(o.double().cpu().numpy() - ro)
+    bound = out_half * np.abs(ro) + slack / np.sqrt(dk) * 1.01 + 2.0 ** -25
+    print("outputs: %.3f of the bound" % float((err / bound).max()))
+    assert (err <= bound).all()
