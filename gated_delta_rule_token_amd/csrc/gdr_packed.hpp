@@ -651,7 +651,7 @@ __global__ __launch_bounds__(256, 2) void k_packed_few(const PackedParams a, int
                     kv[t][m] = value(kw[t][m]);
                     qv[t][m] = value(qw[t][m]);
                     av[t][m] = at;
-                    if (per_key) {
+                    if (per_key && (EXACT || j0 + m < dk)) {  // (past the row's end a decay of 1: no 0 x infinity)
                         const float x = wide_gate ? as_float(gw_[t][m]) : value(gw_[t][m]);
                         av[t][m] = expf(raw_gate ? slope * softplus_f32(x + bias[m]) : x);
                     }

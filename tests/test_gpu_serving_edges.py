@@ -220,3 +220,18 @@ def test_values_that_replace_far_larger_ones(cache, act, form, dk, L):
     bound = out_half * np.abs(ro) + slack / np.sqrt(dk) * 1.01 + 2.0 ** -25
     print("outputs: %.3f of the bound" % float((err / bound).max()))
     assert (err <= bound).all()
+
+
+@pytest.mark.parametrize("act", [np.float16, np.float32])
+@pytest.mark.parametrize("dk", [72, 120, 150, 200, 250])
+def test_a_growing_gate_stays_in_its_row(dk, act):
+    """gate_scale = 300 and biases that take the softplus to 1e-20: decays of 1.  The
+    lanes past a row's end, which have no bias, would see e^208."""
+    from tests.test_gpu_packed import step_and_check
+    case = workloads.random_case(dk, rank4_batch=(2, 3), H=1, HV=2, DK=dk, DV=24, dtype=act, slots=(3,), qk_l2_norm=1,
+                                 update_rule="gated_delta", per_key=True, gate_activation="qwen", folded_scale=True)
+    case["gate_scale"][:] = 300.0
+    case["gate"][:] = 0
+    case["dt_bias"][:] = -46.0
+    for cache in DT:
+        step_and_check(case, cache, tokens=3)
