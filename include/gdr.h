@@ -463,7 +463,9 @@ gdr_status gdr_state_unpack(int32_t batch, int32_t heads, int32_t dv, int32_t dk
  * brings may make its rows' states NaN.  Few tokens a request (8 on average) run
  * in one pass over the packed states, without workspace; longer requests (or
  * algo RECURRENT or CHUNKED) run gdr_forward's kernels on fp32 states in the
- * workspace. */
+ * workspace.  Which kernel takes a request is chosen by the shapes: a token
+ * spelled (B, 1) and the same token in cu_seqlens, alone or beside longer requests,
+ * give results that differ by rounding. */
 gdr_status gdr_packed_workspace_size(const gdr_problem *problem, size_t *bytes);
 gdr_status gdr_forward_packed(const gdr_problem *problem, const gdr_tensors *tensors, const gdr_packed_slab *slab,
                               void *workspace, size_t workspace_bytes, void *stream);
