@@ -235,3 +235,155 @@ def test_a_growing_gate_stays_in_its_row(dk, act):
     case["dt_bias"][:] = -46.0
     for cache in DT:
         step_and_check(case, cache, tokens=3)
+
+
+@pytest.mark.parametrize("cache", DT)
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("act", [torch.float16, torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dk,dv,L", [(128, 128, 4), (64, 200, 7), (256, 130, 2), (96, 256, 3), (200, 120, 8)])
+def test_many_states_give_what_few_do(cache, form, act, dk, dv, L):
+    """64 requests of 32 heads fill the GPU with a wave for each state, which walks
+    all its rows 16 at a time with the next ones on their way; four requests have up to 8
+    waves a state, each with a part of its rows.  The same bits."""
+    from gated_delta_rule_token_amd import api
+    B, H, HV = 64, 16, 32
+    g = torch.Generator("cuda").manual_seed(dk + dv)
+    n = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    x = dict(q=n(B, L, H, dk).to(act), k=n(B, L, H, dk).to(act), v=n(B, L, HV, dv).to(act))
+    rule = {"update_rule": FORMS[form]["update_rule"] if form != "plain" else "gated_delta"}
+    if rule["update_rule"] != "delta":
+        x["gate"] = -0.2 * n(B, L, HV, *((dk,) if form == "per_key" else ())).abs()
+    if form == "erase":
+        x["erase"] = torch.sigmoid(n(B, L, HV, dk))
+    else:
+        x["beta"] = torch.sigmoid(n(B, L, HV))
+    states = n(B, HV, dv, dk) * torch.exp(2 * n(B, HV, dv, 1))
+    where = torch.randperm(B, generator=g, device="cuda").to(torch.int32)
+    start = api.packed_slab(B, HV, dv, dk, DT[cache])
+    api.state_pack(states, start, where)
+    big = api.PackedSlab(start.data.clone(), None if start.scale is None else start.scale.clone())
+
+    def run(slab, rows):
+        y = {name: t[rows].contiguous() for name, t in x.items()}
+        return api.forward_packed(y.pop("q"), y.pop("k"), y.pop("v"), slab=slab, slot_ids=where[rows].contiguous(),
+                                  qk_l2_norm=True, **y, **rule)
+
+    o = run(big, slice(0, B))
+    parts = torch.cat([run(start, slice(b, b + 4)) for b in range(0, B, 4)])
+    assert torch.equal(o, parts) and bool(o.isfinite().all()) and torch.equal(bits(big.data), bits(start.data))
+    assert start.scale is None or torch.equal(bits(big.scale), bits(start.scale))
+
+
+@pytest.mark.parametrize("cache", DT)
+@pytest.mark.parametrize("act", [torch.float16, torch.bfloat16])
+def test_each_step_of_a_run_from_the_states_it_found(cache, act):
+    """A prompt and six single tokens with positions; each call against 64 bits from
+    what the cache held before it, so that no call's rounding hides the next one's work.
+    With u = 2^-24, a dot of 128 products in fp32 is off by 128 u of its magnitudes and
+    the norms, the rate and the decay add under 32 u: 160 u of sum |S| |k| and sum
+    |S| |q|, and with the token's own part of |v|.  The prompt's states: the chunked form's
+    bar, 2e-3 of the largest."""
+    from gated_delta_rule_token_amd import api
+    from tests.test_gpu_packed import HALF, LEAST, read
+    from tests.test_gpu_serving import D, H, HV, inputs, recurrence, unit
+    lens, steps, u = [150, 1, 70], 6, 2.0 ** -24
+    c = inputs(lens, steps, act, 17)
+    B, T0 = len(lens), sum(lens)
+    slab = api.packed_slab(6, HV, D, D, DT[cache])
+    slots = [4, 0, 5]
+    dev = {n: t.cuda() for n, t in c.items()}
+    d = {n: t.double() for n, t in c.items()}
+    start = torch.tensor([0] + lens).cumsum(0)
+
+    def call(rows, pos, **kw):
+        n = rows.stop - rows.start
+        wide = dev["qk"][rows]
+        r = api.qk_rotary(wide[:, : H * D].view(n, H, D), wide[:, H * D:].view(n, H, D), pos.to(torch.int32).cuda(),
+                          dev["freq"], q_weight=dev["qw"], k_weight=dev["kw"])
+        v, a, b = (dev[name][rows].clone() for name in "vab")
+        o = api.forward_packed(r.q, r.k, v, slab=slab, slot_ids=ids(*slots), gate=a, beta=b, gate_activation="qwen",
+                               beta_activation="sigmoid", qk_l2_norm=True, a_log=dev["a_log"], dt_bias=dev["dt_bias"], **kw)
+        q, k = (unit(t.cpu().double()).repeat_interleave(HV // H, 1) for t in r)
+        g = -torch.exp(d["a_log"]) * torch.nn.functional.softplus(d["a"][rows] + d["dt_bias"])
+        return o.cpu().double(), q, k, d["v"][rows], g, torch.sigmoid(d["b"][rows])
+
+    def state():
+        return read(slab.data, slab.scale)[slots]
+
+    def check_states(want, slack):
+        least = LEAST[cache] if cache != "e4m3" else \
+            LEAST[cache] * torch.exp2(slab.scale.view(torch.uint8).cpu()[slots].double() - 127)[..., None]
+        bound = HALF[cache] * (want.abs() + slack) + least + slack
+        err = (state() - want).abs()
+        assert bool((err <= bound).all()), float((err / bound).max())
+
+    _, *x = call(slice(0, T0), torch.cat([torch.arange(n) for n in lens]), cu_seqlens=start.to(torch.int32).cuda())
+    want = torch.stack([recurrence(*(t[start[b]: start[b + 1]] for t in x), torch.zeros(HV, D, D).double())[1] for b in range(B)])
+    check_states(want, 2e-3 * float(want.abs().max()))
+    for i in range(steps):
+        before = state()
+        o, q, k, v, g, beta = call(slice(T0 + i * B, T0 + (i + 1) * B), torch.tensor([n + i for n in lens]))
+        S = before * torch.exp(g)[..., None, None]
+        put = beta[..., None] * (v - (S * k[..., None, :]).sum(-1))
+        new = S + put[..., None] * k[..., None, :]
+        # magnitudes of the sums behind `put` (one a row) and behind an output
+        around = beta[..., None] * (v.abs() + (S.abs() * k[..., None, :].abs()).sum(-1))
+        check_states(new, 160 * u * (S.abs() + around[..., None] * k[..., None, :].abs()))
+        ref = (new * q[..., None, :]).sum(-1) / D ** 0.5
+        reach = ((S.abs() * q[..., None, :].abs()).sum(-1) + around * (q * k).abs().sum(-1)[..., None]) / D ** 0.5
+        bound = torch.finfo(act).eps / 2 * ref.abs() + 2 * 160 * u * reach + 2.0 ** -25
+        assert bool(((o - ref).abs() <= bound).all()), (i, float(((o - ref).abs() / bound).max()))
+        assert float(ref.abs().max()) > 20 * float(bound.max())
+
+
+@pytest.mark.parametrize("cache", DT)
+@pytest.mark.parametrize("act", [np.float16, "bf16", np.float32])
+@pytest.mark.parametrize("rule", [dict(update_rule="gated_delta"), dict(update_rule="gated_delta", per_key=True),
+                                  dict(update_rule="gated_delta_v2", per_key=True)], ids=["plain", "per_key", "erase"])
+@pytest.mark.parametrize("dk,L", [(128, 1), (128, 4), (64, 8), (256, 7), (72, 5), (200, 3), (13, 6)])
+def test_several_tokens_within_their_arithmetic(cache, act, rule, dk, L):
+    """Bounds that run along with the recurrence.  A holds the magnitudes that went
+    into a state, E what it may be off by; with u = 2^-24 a dot of dk products in
+    fp32 is off by dk u of its magnitudes, and planes, decays (up to 8 in a product, 3 u
+    each), norms and rates by under 64 u: c = dk + 64.  So a new value is off by
+    e = beta (c u sum A |k| + sum E |k|) + 4 u |put|, the state by E <- a E + e |k| +
+    c u |put| |k| + 32 u A, an output by c u sum A |q| + sum E |q| and its rounding.  (That
+    these bounds say something is asserted of the inputs: their median is under a
+    hundredth of an output's.)"""
+    from gated_delta_rule_token_amd import api
+    from tests.test_gpu_packed import HALF, LEAST, gpu_tensors, read, slab_of
+    case = workloads.random_case(3 * dk + L, rank4_batch=(2, L), H=2, HV=4, DK=dk, DV=40, dtype=act, slots=(3,), qk_l2_norm=1, **rule)
+    slab = slab_of(case["slab"], cache)
+    S = read(slab.data, slab.scale).numpy()[case["slot_ids"]]
+    d, args = gpu_tensors(case)
+    o = api.forward_packed(d["q"], d["k"], d["v"], slab=slab, **args)
+    got, out = read(slab.data, slab.scale).numpy()[case["slot_ids"]], o.double().cpu().numpy()
+    half_out = {"float32": 2.0 ** -24, "float16": 2.0 ** -11, "bfloat16": 2.0 ** -8}[str(o.dtype)[6:]]
+    q, k, v = (np.asarray(case[n], np.float64) for n in "qkv")
+    q, k = (np.repeat(x / np.sqrt((x * x).sum(-1, keepdims=True) + 1e-12), 2, 2) for x in (q, k))
+    cu, u = (dk + 64) * 2.0 ** -24, 2.0 ** -24
+    A, E = np.abs(S), np.zeros_like(S)
+    for t in range(L):
+        a = np.exp(case["gate"][:, t].astype(np.float64))
+        a = a[..., None, :] if rule.get("per_key") else a[..., None, None]
+        beta = np.ones((2, 4, 1)) if case["beta"] is None else case["beta"][:, t].astype(np.float64)[..., None]
+        kr = k[:, t] if case["erase"] is None else k[:, t] * case["erase"][:, t].astype(np.float64)
+        S, A, E = a * S, a * A, a * E
+        dot = lambda M, x: (M * np.abs(x)[..., None, :]).sum(-1)  # noqa: E731
+        put = beta * (v[:, t] - (S * kr[..., None, :]).sum(-1))
+        most = beta * (np.abs(v[:, t]) + dot(A, kr))
+        e = beta * (cu * dot(A, kr) + dot(E, kr)) + 4 * u * most
+        outer = lambda x: x[..., None] * np.abs(k[:, t])[..., None, :]  # noqa: E731
+        S = S + put[..., None] * k[:, t][..., None, :]
+        E = E + outer(e) + cu * outer(most) + 32 * u * A
+        A = A + outer(most)
+        ref = (S * q[:, t][..., None, :]).sum(-1) / np.sqrt(dk)
+        bound = half_out * np.abs(ref) + (cu * dot(A, q[:, t]) + dot(E, q[:, t])) / np.sqrt(dk) + 2.0 ** -25
+        err = np.abs(out[:, t] - ref)
+        assert (err <= bound).all(), (t, float((err / bound).max()))
+        if act == np.float32:
+            assert np.median(bound) < 1e-2 * np.median(np.abs(ref))
+    least = LEAST[cache] * (1 if cache != "e4m3" else
+                            np.exp2(slab.scale.view(torch.uint8).cpu().double().numpy()[case["slot_ids"]] - 127)[..., None])
+    err, bound = np.abs(got - S), HALF[cache] * (np.abs(S) + E) + least + E
+    assert (err <= bound).all(), float((err / bound).max())
