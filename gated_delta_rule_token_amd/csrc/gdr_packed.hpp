@@ -113,10 +113,10 @@ template <> struct CacheType<CACHE_BF16> { using T = bf16_t; };
 // keys).  A wave holds G times 64 / LANES rows.  With single tokens (ONE) each row
 // group is widened, stepped and rounded by itself, so few registers are live beside
 // the packed values; more tokens keep all groups in fp32 between them.
-// Bound by memory for single tokens (256 requests x 32 heads of 128): 8 bits
-// 60 us for 283 MB, 16 bits 96 us for 547 MB.  Waves and rows, in us for 8 and
-// 16 bits: 2 waves of 64 rows 60 and 109, 4 of 32 rows 63 and 104, 4 of 16 rows
-// 73 and 96; as the form for more tokens 68 and 102.
+// Bound by memory for single tokens (256 requests x 32 heads of 128): 8 bits 57
+// to 60 us for 277 MB, 16 bits 97 us for 543 MB, fp32 activations the same.  Waves
+// and rows, in us for 8 and 16 bits: 2 waves of 64 rows 60 and 109, 4 of 32 rows 63
+// and 104, 4 of 16 rows 73 and 96; as the form for more tokens 68 and 102.
 template <int TYPE, int DK, bool ONE> struct StepForm {
     static constexpr bool EIGHT = TYPE == CACHE_E4M3;
     static constexpr int WAVES = DK == 16 ? 1 : ONE && EIGHT ? 2 : 4;
@@ -396,10 +396,11 @@ __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packe
 // [2^14, 2^15), where two planes hold 2^-39 of it.  d (fp32) goes into the
 // second product as three bf16 planes, all 24 bits: where a token replaces values,
 // d k takes away what is there, and what it is off by stays (with two planes, under
-// 2^-17, values 2^12 times smaller than those before them were off by eight of fp16's
+// 2^-17, values 2^12 times smaller than those before them were off by several of fp16's
 // steps).  An fp16 k takes two planes.  The 32 inner places of a product hold 8 tokens of
 // four plane pairs: one product beside a bf16 k, two beside others, of which the second,
-// of the small pairs, has the same operand k and no time of its own.
+// of the small pairs, has the same operand k (fp16 activations, 4 tokens: 117 us on
+// 16 bits with and without it, 84 and 87 on 8).
 //
 // Any other call (GEN: fp32 activations, a decay for each key, the erase gate)
 // takes the decays into the vectors.  With D_t the product of the decays up to
@@ -407,13 +408,12 @@ __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packe
 // t's write enters a later x_n's dot by sum_j k_t (D_n / D_t) e_n k_n, and S by
 // d_t (D_T / D_t) o k_t: a lane forms these for its two keys, the quotients as
 // running products of the later decays, which do not overflow.  x_n in fp32 goes
-// in as planes (two of fp16 scaled as above, 2^-22 of its largest value, a third
-// would take 64 registers of 256 keys; three of bf16 beside a bf16 cache), k_t and
-// d_t as three of bf16 each.  256 requests x
-// 32 heads of 128, 4 tokens, vector units and this, in us: a decay for each key
-// on 16 and 8 bits 229 and 118, 210 and 96; fp32 activations 211 and 112, 205
-// and 90; 64 requests x 32 heads of 256, a decay for each key, 243 and 123, 224
-// and 79.  8 bits wait for the vectors' own work: 7 tokens take 119 us, 53 of
+// in as planes (two of fp16 scaled as above, 2^-22 of its largest value; a third
+// would take 32 registers of 256 keys; three of bf16 beside a bf16 cache), k_t and
+// d_t as three of bf16 each.  256 requests x 32 heads of 128, 4 tokens, vector
+// units and this, in us: a decay for each key on 16 and 8 bits 229 and 118, 210 and
+// 96; fp32 activations 211 and 112, 205 and 90; 64 requests x 32 heads of 256, a
+// decay for each key, 243 and 123, 224 and 79.  8 bits wait for the vectors' own work: 7 tokens take 119 us, 53 of
 // them with 16 rows a state.
 //
 // A tile is 16 rows: lane (c, kb) of a wave holds row c, 8 keys of every 32 (with

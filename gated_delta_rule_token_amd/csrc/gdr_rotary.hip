@@ -413,8 +413,8 @@ hipError_t by_form(const RotaryParams &p, F &&f)
     const auto lanes = [&](auto vec) {
         const int vectors = p.dim / (2 * vec());
         // Three vectors a lane where they fill more lanes (29,273 tokens, 32 heads of 72,
-        // 72 and 36 columns turned, in fp16 86 -> 74 and 114 -> 82 us; of 80 with 20
-        // 117 -> 97, gradients 198 -> 147; but gradients of 72 with 72 131 -> 159).
+        // 72 and 36 columns turned, in fp16 86 -> 71 and 114 -> 80 us; of 80 with 20
+        // 117 -> 97, gradients 198 -> 142; but gradients of 72 with 72 114 -> 253).
         if constexpr (vec() < V && (!BACK || vec() <= 2)) {
             if (vectors > 8 && vectors <= 12) return f(vec, integral_constant<int, 4>(), integral_constant<int, 3>());
             if (vectors > 16 && vectors <= 24) return f(vec, integral_constant<int, 8>(), integral_constant<int, 3>());
