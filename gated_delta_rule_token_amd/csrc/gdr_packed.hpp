@@ -413,8 +413,8 @@ __global__ __launch_bounds__((64 * StepForm<TYPE, DK, ONE>::WAVES)) void k_packe
 // d_t as three of bf16 each.  256 requests x 32 heads of 128, 4 tokens, vector
 // units and this, in us: a decay for each key on 16 and 8 bits 229 and 118, 210 and
 // 96; fp32 activations 211 and 112, 205 and 90; 64 requests x 32 heads of 256, a
-// decay for each key, 243 and 123, 224 and 79.  8 bits wait for the vectors' own work: 7 tokens take 119 us, 53 of
-// them with 16 rows a state.
+// decay for each key, 243 and 123, 224 and 79.  8 bits wait for the vectors' own
+// work: 7 tokens take 119 us, 53 of them with 16 rows a state.
 //
 // A tile is 16 rows: lane (c, kb) of a wave holds row c, 8 keys of every 32 (with
 // codes 16 of 64) at the kb-th place, which is the first product's operand; the
